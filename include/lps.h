@@ -464,6 +464,106 @@ int attention_decode_noalloc_status(void* stream);
  * device. Launches nothing. */
 long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max_pos);
 
+/* ---- operators over a caller-owned cache -------------------------------------- */
+
+/* Like the allocation-free attention above, these run without a model, on
+ * device memory of the caller: the attention of whole prompts of different
+ * lengths, the attention of a TREE of drafted tokens over a cache (of which one
+ * drafted token is an ordinary decode step), and the two row moves between
+ * them. Together they are the attention side of speculative decoding: a prompt
+ * (or a draft) is attended and appended, drafts are verified in one pass over
+ * the cache, and the accepted path's rows are moved behind the committed ones.
+ * The staged runtime on the pages has no counterpart to them (its verify rows
+ * are consecutive positions of one sequence: LPS_FLAG_VERIFY).
+ *
+ * Common rules:
+ *   - elements are bf16 or fp16 (LPS_TYPE_*), q, k, v, caches and out of a call
+ *     alike; scores, softmax statistics and sums are fp32, each result is
+ *     rounded once; the softmax weights are rounded to the element type for
+ *     the product with V;
+ *   - a cache is [batch][n_kv_heads][max_ctx][head_dim], dense (one layer), the
+ *     layout of attention_decode_noalloc; head_dim is 64 or 128; q head h reads
+ *     kv head h / (n_q_heads / n_kv_heads), 1 to 16 q heads per kv head;
+ *   - device pointers are 16-byte aligned; strides are in elements, multiples
+ *     of 8 and at least head_dim; out overlaps no input;
+ *   - host arrays are read during the call and travel with the launch: a
+ *     captured call replays with the values it was captured with;
+ *   - a call runs on the calling thread's current device, in `stream` (NULL:
+ *     the default stream), returns once enqueued and allocates nothing. Calls
+ *     may overlap as long as their outputs and workspaces do not;
+ *   - an error is LPS_EINVAL (nothing enqueued) or LPS_ECUDA, with
+ *     last_error_string() naming it. */
+#define LPS_TYPE_BF16 0
+#define LPS_TYPE_FP16 1
+
+/* Causal attention of n_seqs whole prompts packed one after another: sequence s
+ * holds the tokens offsets[s] .. offsets[s + 1] - 1, token t of it sees the
+ * tokens [0, t] of the same sequence:
+ *     out[t][h] = sum_j p_j v[j], p = softmax_j(scale * q[t][h] . k[j]).
+ *   q, out   device [tokens][n_q_heads][head_dim]
+ *   k, v     device [tokens][n_kv_heads][head_dim]
+ *   offsets  host int32[n_seqs + 1], offsets[0] >= 0, not descending; empty
+ *            sequences are fine. Rows outside [offsets[0], offsets[n_seqs]) are
+ *            neither used nor written; a key a token does not see changes
+ *            nothing, whatever it holds
+ *   strides  host int64[8]: token and head stride of q, k, v and out; NULL: dense
+ *   scale    > 0, or 0 for 1/sqrt(head_dim)
+ * LPS_EINVAL for bad types, head counts, offsets, strides, alignment or scale. */
+int attention_prompt_packed(const void* q, const void* k, const void* v, void* out, int type, int n_seqs,
+                            const int32_t* offsets, int n_q_heads, int n_kv_heads, int head_dim,
+                            const int64_t* strides, float scale, void* stream);
+
+/* Attention of drafted trees over a cache. Sequence b has pos[b] committed rows
+ * and rows[b] drafted tokens, whose keys and values the caller has stored in
+ * the cache rows pos[b] .. pos[b] + rows[b] - 1 (kv_rows_append). Draft t hangs
+ * from draft parents[b][t] < t, or from the last committed token when that is
+ * -1; it sees the cache rows [0, pos[b]), itself and its chain of parents.
+ *   q, out   device [batch][width][n_q_heads][head_dim]; rows t >= rows[b] are
+ *            neither read nor written
+ *   pos, rows  host int32[batch]: 0 <= rows[b] <= width, pos[b] + rows[b] <= max_ctx
+ *   parents  device int32[batch][width]; the drafts of a chain that holds a
+ *            parent outside [-1, t) get zeros
+ *   strides  host int64[6]: batch, token and head stride of q, then of out; NULL: dense
+ *   workspace  device memory of attention_tree_workspace_bytes() bytes for the
+ *            same arguments, 16-byte aligned, used until the call's work has run
+ * batch is 1..256, width 1..64. rows of 1 with a parent of -1 is a decode step.
+ * Cache rows at and after pos[b] + rows[b] change nothing, whatever they hold.
+ * LPS_EINVAL for bad arguments or a workspace that is too small. */
+int attention_tree_verify(const void* q, const void* k_cache, const void* v_cache, void* out, int type, int batch,
+                          int width, const int32_t* pos, const int32_t* rows, const int32_t* parents, int n_q_heads,
+                          int n_kv_heads, int head_dim, int max_ctx, const int64_t* strides, float scale,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The workspace attention_tree_verify needs for these arguments on the current
+ * device (0 where it needs none), or -1 for arguments it refuses or without a
+ * device. Launches nothing. */
+long long attention_tree_workspace_bytes(int batch, int width, const int32_t* pos, const int32_t* rows, int n_q_heads,
+                                         int n_kv_heads, int head_dim);
+
+/* Key and value rows of packed tokens into the cache: token i of sequence s
+ * (tokens offsets[s] .. offsets[s + 1] - 1) goes to row start[s] + i of cache
+ * sequence s, for every kv head. No other row changes. Elements of 2 bytes.
+ *   k, v     device [tokens][n_kv_heads][head_dim]
+ *   caches   device [n_seqs][n_kv_heads][max_ctx][head_dim]
+ *   offsets  host int32[n_seqs + 1], start host int32[n_seqs]:
+ *            start[s] + length <= max_ctx
+ *   strides  host int64[4]: token and head stride of k, then of v; NULL: dense */
+int kv_rows_append(const void* k, const void* v, int n_seqs, const int32_t* offsets, void* k_cache, void* v_cache,
+                   const int32_t* start, int n_kv_heads, int head_dim, int max_ctx, const int64_t* strides,
+                   void* stream);
+
+/* The accepted path of a drafted tree, moved in place behind the committed
+ * rows: for i < accepted[b], cache row pos[b] + path[b][i] goes to row
+ * pos[b] + i, in every layer, for keys and values.
+ *   caches   device [n_layers][batch][n_kv_heads][max_ctx][head_dim], elements of 2 bytes
+ *   pos      host int32[batch], 0..max_ctx
+ *   path     device int32[batch][width], strictly ascending draft rows (parents
+ *            come before their children); accepted: device int32[batch], 0..width
+ * A sequence whose accepted count or path breaks these rules, or reaches past
+ * max_ctx, is left as it was. width is 1..64, batch 1..256. */
+int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_kv_heads, int head_dim, int max_ctx,
+                   const int32_t* pos, int width, const int32_t* path, const int32_t* accepted, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,27 +22,19 @@ from . import _capi
 from ._capi import (KERNELS, LPS_EBUSY, LPS_ECUDA, LPS_EINVAL, LPS_ENOMEM, LPS_ETIMEDOUT,  # noqa: F401
                     LPS_FLAG_KEEP_ATTN_OUT, LPS_FLAG_SERIAL_STEPS, LPS_FLAG_SINGLE_STREAM, LPS_FLAG_VERIFY, LPS_FLAG_PERSISTENT, LPS_FLAG_GRAPH,
                     LPS_NOALLOC_SCRATCH_BYTES,
-                    LPS_OK)
+                    LPS_OK, LPS_TYPE_BF16, LPS_TYPE_FP16)
+from ._capi import LpsError
+from ._capi import check as _check
+from .ops import attention_prompt_packed, attention_tree_verify, kv_rows_accept, kv_rows_append
 
 __all__ = ["LpsError", "StagePlan", "Model", "Pending", "stage_plan_create", "stage_plan_from_counts",
            "stage_plan_solve", "model_stage_bytes", "model_bind", "decode_step", "decode_step_deferred",
-           "pending_wait", "pending_free", "decode_step_device", "load"]
-
-
-class LpsError(RuntimeError):
-    def __init__(self, code: int, msg: str):
-        super().__init__(f"[{code}] {msg}")
-        self.code = code
+           "pending_wait", "pending_free", "decode_step_device", "load", "attention_prompt_packed",
+           "attention_tree_verify", "kv_rows_append", "kv_rows_accept"]
 
 
 def load():
     return _capi.load()
-
-
-def _check(rc: int) -> int:
-    if rc < 0:
-        raise LpsError(rc, _capi.load().last_error_string().decode())
-    return rc
 
 
 def _ptr(a: np.ndarray | None) -> int | None:

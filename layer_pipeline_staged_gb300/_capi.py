@@ -17,6 +17,8 @@ LPS_EBUSY = -5
 LPS_WEIGHT_BF16 = 0
 LPS_WEIGHT_INT8_ROWSCALE = 1
 LPS_KV_BF16 = 0
+LPS_TYPE_BF16 = 0
+LPS_TYPE_FP16 = 1
 LPS_NOALLOC_SCRATCH_BYTES = 8 << 20
 LPS_FLAG_SINGLE_STREAM = 1
 LPS_FLAG_KEEP_ATTN_OUT = 2
@@ -37,7 +39,8 @@ EXPORTS = (
     "model_time_kernel", "model_kernel_time", "model_set_serial_steps", "attention_decode_noalloc", "attention_decode_noalloc_error",
     "attention_decode_noalloc_scratch_bytes", "model_trace_enable", "model_trace_read", "model_trace_disable",
     "stage_plan_solve", "model_stage_bytes", "model_set_wait_limit", "attention_decode_noalloc_status",
-    "model_prefill",
+    "model_prefill", "attention_prompt_packed", "attention_tree_verify", "attention_tree_workspace_bytes",
+    "kv_rows_append", "kv_rows_accept",
 )
 
 
@@ -95,7 +98,7 @@ def load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it first (python -m layer_pipeline_staged_gb300.build)")
     L = ctypes.CDLL(path)
-    vp, i, pp = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p)
+    vp, i, pp, f = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p), ctypes.c_float
     sig = {
         "stage_plan_create": (i, [i, vp, i, pp]),
         "stage_plan_from_counts": (i, [vp, i, pp]),
@@ -129,13 +132,30 @@ def load(path: str = LIB_PATH):
         "attention_decode_noalloc_error": (ctypes.c_char_p, []),
         "attention_decode_noalloc_status": (i, [vp]),
         "attention_decode_noalloc_scratch_bytes": (ctypes.c_longlong, [i, i, i, i, i]),
+        "attention_prompt_packed": (i, [vp, vp, vp, vp, i, i, vp, i, i, i, vp, f, vp]),
+        "attention_tree_verify": (i, [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, vp, f, vp, ctypes.c_size_t, vp]),
+        "attention_tree_workspace_bytes": (ctypes.c_longlong, [i, i, vp, vp, i, i, i]),
+        "kv_rows_append": (i, [vp, vp, i, vp, vp, vp, vp, i, i, i, vp, vp]),
+        "kv_rows_accept": (i, [vp, vp, i, i, i, i, i, vp, i, vp, vp, vp]),
         "stage_plan_solve": (i, [i, i, vp, vp, vp, vp, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_int64)]),
         "model_stage_bytes": (i, [ctypes.POINTER(ModelDesc), vp, vp, ctypes.POINTER(ctypes.c_uint64),
                                   ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
     }
     for name, (res, args) in sig.items():
-        f = getattr(L, name)
-        f.restype = res
-        f.argtypes = args
+        fn = getattr(L, name)
+        fn.restype = res
+        fn.argtypes = args
     _lib = L
     return L
+
+
+class LpsError(RuntimeError):
+    def __init__(self, code: int, msg: str):
+        super().__init__(f"[{code}] {msg}")
+        self.code = code
+
+
+def check(rc: int) -> int:
+    if rc < 0:
+        raise LpsError(rc, load().last_error_string().decode())
+    return rc

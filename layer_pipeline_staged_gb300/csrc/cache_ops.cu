@@ -1,0 +1,234 @@
+// Entry points of the operators over a caller-owned cache: argument checks,
+// tensor maps and launches. Nothing here synchronises, allocates device memory
+// or keeps anything between calls. Lengths, offsets and positions are host
+// arrays that travel in the kernel parameters (so a captured launch keeps the
+// values it was captured with); a tree's parents and an accepted path are
+// device arrays, as a drafter and a sampler on the GPU leave them, and the
+// kernels check them.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <exception>
+#include <string>
+
+#include "cache_ops.h"
+#include "kernels.h"
+#include "lps.h"
+
+namespace lps {
+int host_fail(int code, const char* fn, const std::string& why);
+}  // namespace lps
+
+namespace {
+
+using namespace lps;
+
+// Runs the body of an entry point; no exception leaves the C boundary.
+template <class F>
+int guarded(const char* fn, F&& body) {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    try {
+      return host_fail(LPS_ENOMEM, fn, e.what());
+    } catch (...) {
+      return LPS_ENOMEM;
+    }
+  } catch (...) {
+    return LPS_ENOMEM;
+  }
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+int check_heads(const char* fn, int type, int nq, int nkv, int hd) {
+  if (type != LPS_TYPE_BF16 && type != LPS_TYPE_FP16) return host_fail(LPS_EINVAL, fn, "type must be LPS_TYPE_BF16 or LPS_TYPE_FP16");
+  if (hd != 64 && hd != 128) return host_fail(LPS_EINVAL, fn, "head_dim must be 64 or 128");
+  if (nkv < 1 || nkv > 65535 || nq < 1 || nq % nkv || nq / nkv > kMaxGroup || nq > 65535)
+    return host_fail(LPS_EINVAL, fn, "n_q_heads must be 1 to 16 times n_kv_heads (each at most 65535)");
+  return LPS_OK;
+}
+
+int check_scale(const char* fn, float scale) {
+  if (!(scale >= 0.f) || std::isinf(scale)) return host_fail(LPS_EINVAL, fn, "scale must be finite and >= 0 (0: 1/sqrt(head_dim))");
+  return LPS_OK;
+}
+
+// Element strides of a tensor's outer axes: whole 16-byte units, at least one
+// row apart, and inside what a tensor map can hold.
+int check_strides(const char* fn, const int64_t* st, int n, int hd) {
+  for (int i = 0; i < n; ++i)
+    if (st[i] < hd || st[i] % 8 || st[i] >= (1ll << 38))
+      return host_fail(LPS_EINVAL, fn, "strides must be multiples of 8 elements, at least head_dim and below 2^38");
+  return LPS_OK;
+}
+
+int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
+  if (offsets[0] < 0) return host_fail(LPS_EINVAL, fn, "offsets[0] must be >= 0");
+  for (int s = 0; s < n_seqs; ++s)
+    if (offsets[s + 1] < offsets[s]) return host_fail(LPS_EINVAL, fn, "offsets must not descend");
+  return LPS_OK;
+}
+
+}  // namespace
+
+extern "C" int attention_prompt_packed(const void* q, const void* k, const void* v, void* out, int type, int n_seqs,
+                                       const int32_t* offsets, int n_q_heads, int n_kv_heads, int head_dim,
+                                       const int64_t* strides, float scale, void* stream) {
+  static const char* FN = "attention_prompt_packed";
+  return guarded(FN, [&]() -> int {
+    if (!q || !k || !v || !out || !offsets) return host_fail(LPS_EINVAL, FN, "q, k, v, out and offsets are required");
+    if (n_seqs < 1) return host_fail(LPS_EINVAL, FN, "n_seqs must be >= 1");
+    int rc = check_heads(FN, type, n_q_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if ((rc = check_scale(FN, scale)) || (rc = check_offsets(FN, n_seqs, offsets))) return rc;
+    const int64_t q_dense = static_cast<int64_t>(n_q_heads) * head_dim, k_dense = static_cast<int64_t>(n_kv_heads) * head_dim;
+    const int64_t dense[8] = {q_dense, head_dim, k_dense, head_dim, k_dense, head_dim, q_dense, head_dim};
+    const int64_t* st = strides ? strides : dense;
+    if ((rc = check_strides(FN, st, 8, head_dim))) return rc;
+    if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(out))
+      return host_fail(LPS_EINVAL, FN, "q, k, v and out must be 16-byte aligned");
+
+    for (int s0 = 0; s0 < n_seqs; s0 += kOpSeqs) {
+      TileAttnParams p{};
+      p.n_seqs = n_seqs - s0 < kOpSeqs ? n_seqs - s0 : kOpSeqs;
+      p.q = q, p.k = k, p.v = v, p.out = out;
+      p.q_tok = st[0], p.q_head = st[1], p.k_row = st[2], p.k_head = st[3];
+      p.v_row = st[4], p.v_head = st[5], p.o_tok = st[6], p.o_head = st[7];
+      p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+      p.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+      for (int s = 0; s < p.n_seqs; ++s) {
+        p.tok0[s] = offsets[s0 + s];
+        p.len[s] = offsets[s0 + s + 1] - offsets[s0 + s];
+      }
+      const cudaError_t e = launch_tile_attn(p, type == LPS_TYPE_BF16, head_dim, false, static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
+    }
+    return LPS_OK;
+  });
+}
+
+namespace {
+int check_tree(const char* fn, int batch, int width, const int32_t* pos, const int32_t* rows, int max_ctx) {
+  if (batch < 1 || batch > kOpSeqs) return host_fail(LPS_EINVAL, fn, "batch must be in 1..256");
+  if (width < 1 || width > kTreeMax) return host_fail(LPS_EINVAL, fn, "width must be in 1..64");
+  if (max_ctx < 1) return host_fail(LPS_EINVAL, fn, "max_ctx must be >= 1");
+  for (int b = 0; b < batch; ++b) {
+    if (pos[b] < 0 || rows[b] < 0 || rows[b] > width) return host_fail(LPS_EINVAL, fn, "need pos >= 0 and 0 <= rows <= width");
+    if (pos[b] > max_ctx - rows[b]) return host_fail(LPS_EINVAL, fn, "pos + rows must stay within max_ctx");
+  }
+  return LPS_OK;
+}
+}  // namespace
+
+extern "C" long long attention_tree_workspace_bytes(int batch, int width, const int32_t* pos, const int32_t* rows,
+                                                    int n_q_heads, int n_kv_heads, int head_dim) {
+  static const char* FN = "attention_tree_workspace_bytes";
+  if (!pos || !rows || check_heads(FN, LPS_TYPE_BF16, n_q_heads, n_kv_heads, head_dim) ||
+      check_tree(FN, batch, width, pos, rows, 0x7fffffff))
+    return -1;
+  return 0;
+}
+
+extern "C" int attention_tree_verify(const void* q, const void* k_cache, const void* v_cache, void* out, int type,
+                                     int batch, int width, const int32_t* pos, const int32_t* rows,
+                                     const int32_t* parents, int n_q_heads, int n_kv_heads, int head_dim, int max_ctx,
+                                     const int64_t* strides, float scale, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  static const char* FN = "attention_tree_verify";
+  return guarded(FN, [&]() -> int {
+    if (!q || !k_cache || !v_cache || !out || !pos || !rows || !parents)
+      return host_fail(LPS_EINVAL, FN, "q, the caches, out, pos, rows and parents are required");
+    int rc = check_heads(FN, type, n_q_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if ((rc = check_tree(FN, batch, width, pos, rows, max_ctx)) || (rc = check_scale(FN, scale))) return rc;
+    const int64_t tok = static_cast<int64_t>(n_q_heads) * head_dim;
+    const int64_t dense[6] = {width * tok, tok, head_dim, width * tok, tok, head_dim};
+    const int64_t* st = strides ? strides : dense;
+    if ((rc = check_strides(FN, st, 6, head_dim))) return rc;
+    if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out))
+      return host_fail(LPS_EINVAL, FN, "q, the caches and out must be 16-byte aligned");
+    (void)workspace;
+    (void)workspace_bytes;
+    TileAttnParams p{};
+    p.n_seqs = batch;
+    p.q = q, p.k = k_cache, p.v = v_cache, p.out = out;
+    p.q_seq = st[0], p.q_tok = st[1], p.q_head = st[2], p.o_seq = st[3], p.o_tok = st[4], p.o_head = st[5];
+    p.k_row = p.v_row = head_dim;
+    p.k_head = p.v_head = static_cast<long long>(max_ctx) * head_dim;
+    p.k_seq = p.v_seq = p.k_head * n_kv_heads;
+    p.parents = parents;
+    p.width = width;
+    p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+    p.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+    for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
+    const cudaError_t e = launch_tile_attn(p, type == LPS_TYPE_BF16, head_dim, true, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
+    return LPS_OK;
+  });
+}
+
+extern "C" int kv_rows_append(const void* k, const void* v, int n_seqs, const int32_t* offsets, void* k_cache,
+                              void* v_cache, const int32_t* start, int n_kv_heads, int head_dim, int max_ctx,
+                              const int64_t* strides, void* stream) {
+  static const char* FN = "kv_rows_append";
+  return guarded(FN, [&]() -> int {
+    if (!k || !v || !offsets || !k_cache || !v_cache || !start)
+      return host_fail(LPS_EINVAL, FN, "k, v, offsets, the caches and start are required");
+    if (n_seqs < 1) return host_fail(LPS_EINVAL, FN, "n_seqs must be >= 1");
+    int rc = check_heads(FN, LPS_TYPE_BF16, n_kv_heads, n_kv_heads, head_dim);
+    if (rc || (rc = check_offsets(FN, n_seqs, offsets))) return rc;
+    if (max_ctx < 1) return host_fail(LPS_EINVAL, FN, "max_ctx must be >= 1");
+    for (int s = 0; s < n_seqs; ++s)
+      if (start[s] < 0 || start[s] > max_ctx || offsets[s + 1] - offsets[s] > max_ctx - start[s])
+        return host_fail(LPS_EINVAL, FN, "start + the sequence's length must stay within [0, max_ctx]");
+    const int64_t kd = static_cast<int64_t>(n_kv_heads) * head_dim;
+    const int64_t dense[4] = {kd, head_dim, kd, head_dim};
+    const int64_t* st = strides ? strides : dense;
+    if ((rc = check_strides(FN, st, 4, head_dim))) return rc;
+    if (misaligned(k) || misaligned(v) || misaligned(k_cache) || misaligned(v_cache))
+      return host_fail(LPS_EINVAL, FN, "k, v and the caches must be 16-byte aligned");
+    const long long seq_units = static_cast<long long>(n_kv_heads) * max_ctx * (head_dim / 8);
+    for (int s0 = 0; s0 < n_seqs; s0 += kOpSeqs) {
+      AppendParams p{};
+      p.n_seqs = n_seqs - s0 < kOpSeqs ? n_seqs - s0 : kOpSeqs;
+      p.k = static_cast<const uint4*>(k), p.v = static_cast<const uint4*>(v);
+      p.kc = static_cast<uint4*>(k_cache) + s0 * seq_units, p.vc = static_cast<uint4*>(v_cache) + s0 * seq_units;
+      p.k_tok = st[0] / 8, p.k_head = st[1] / 8, p.v_tok = st[2] / 8, p.v_head = st[3] / 8;
+      p.nkv = n_kv_heads, p.chunks = head_dim / 8, p.max_ctx = max_ctx;
+      for (int s = 0; s < p.n_seqs; ++s) p.off[s] = offsets[s0 + s], p.start[s] = start[s0 + s];
+      p.off[p.n_seqs] = offsets[s0 + p.n_seqs];
+      const cudaError_t e = launch_append(p, static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
+    }
+    return LPS_OK;
+  });
+}
+
+extern "C" int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_kv_heads, int head_dim,
+                              int max_ctx, const int32_t* pos, int width, const int32_t* path,
+                              const int32_t* accepted, void* stream) {
+  static const char* FN = "kv_rows_accept";
+  return guarded(FN, [&]() -> int {
+    if (!k_cache || !v_cache || !pos || !path || !accepted)
+      return host_fail(LPS_EINVAL, FN, "the caches, pos, path and accepted are required");
+    if (n_layers < 1 || n_layers > 65535) return host_fail(LPS_EINVAL, FN, "n_layers must be in 1..65535");
+    if (batch < 1 || batch > kOpSeqs) return host_fail(LPS_EINVAL, FN, "batch must be in 1..256");
+    if (width < 1 || width > kTreeMax) return host_fail(LPS_EINVAL, FN, "width must be in 1..64");
+    const int rc = check_heads(FN, LPS_TYPE_BF16, n_kv_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if (max_ctx < 1) return host_fail(LPS_EINVAL, FN, "max_ctx must be >= 1");
+    for (int b = 0; b < batch; ++b)
+      if (pos[b] < 0 || pos[b] > max_ctx) return host_fail(LPS_EINVAL, FN, "pos out of [0, max_ctx]");
+    if (misaligned(k_cache) || misaligned(v_cache)) return host_fail(LPS_EINVAL, FN, "the caches must be 16-byte aligned");
+    AcceptParams p{};
+    p.kc = static_cast<uint4*>(k_cache), p.vc = static_cast<uint4*>(v_cache);
+    p.path = path, p.accepted = accepted;
+    p.layers = n_layers, p.batch = batch, p.nkv = n_kv_heads, p.max_ctx = max_ctx, p.chunks = head_dim / 8, p.width = width;
+    for (int b = 0; b < batch; ++b) p.pos[b] = pos[b];
+    const cudaError_t e = launch_accept(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
+    return LPS_OK;
+  });
+}
