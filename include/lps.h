@@ -564,6 +564,12 @@ int kv_rows_append(const void* k, const void* v, int n_seqs, const int32_t* offs
 int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_kv_heads, int head_dim, int max_ctx,
                    const int32_t* pos, int width, const int32_t* path, const int32_t* accepted, void* stream);
 
+/* Synchronize `stream` and read the status word that the two attention kernels
+ * set on the current device when one of their bounded waits gives up. LPS_OK:
+ * none has since the last check. LPS_ECUDA: at least one call's `out` is
+ * invalid; the word is then cleared. It is shared by all calls on the device. */
+int cache_ops_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

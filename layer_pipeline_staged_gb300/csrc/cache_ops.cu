@@ -6,6 +6,7 @@
 // device arrays, as a drafter and a sampler on the GPU leave them, and the
 // kernels check them.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -64,6 +65,51 @@ int check_strides(const char* fn, const int64_t* st, int n, int hd) {
   return LPS_OK;
 }
 
+// The driver's tensor-map encoder, looked up once per process.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [n3][n2][n1][hd] of 2-byte elements with element strides s1..s3, in boxes of
+// 64 elements x b1 x b2 with the 128-byte swizzle. The stride of an axis of one
+// entry is never used and set to one row.
+bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long long (&n)[3], const long long (&st)[3],
+             int b1, int b2) {
+  if (!encoder()) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(n[0]), static_cast<cuuint64_t>(n[1]),
+                        static_cast<cuuint64_t>(n[2])};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? st[i] : hd) * 2;
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The current device's SM count, or -1.
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return n;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
 int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
   if (offsets[0] < 0) return host_fail(LPS_EINVAL, fn, "offsets[0] must be >= 0");
   for (int s = 0; s < n_seqs; ++s)
@@ -97,12 +143,21 @@ extern "C" int attention_prompt_packed(const void* q, const void* k, const void*
       p.q_tok = st[0], p.q_head = st[1], p.k_row = st[2], p.k_head = st[3];
       p.v_row = st[4], p.v_head = st[5], p.o_tok = st[6], p.o_head = st[7];
       p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
-      p.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+      p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
       for (int s = 0; s < p.n_seqs; ++s) {
         p.tok0[s] = offsets[s0 + s];
         p.len[s] = offsets[s0 + s + 1] - offsets[s0 + s];
       }
-      const cudaError_t e = launch_tile_attn(p, type == LPS_TYPE_BF16, head_dim, false, static_cast<cudaStream_t>(stream));
+      const long long ctas = tile_prompt_plan(p);
+      if (ctas == 0) continue;
+      if (ctas > 0x7fffffffll) return host_fail(LPS_EINVAL, FN, "too many tokens for one launch");
+      const bool bf16 = type == LPS_TYPE_BF16;
+      const long long tokens = offsets[n_seqs];
+      if (!encode4(&p.tmap_q, bf16, q, head_dim, {n_q_heads, tokens, 1}, {st[1], st[0], 0}, p.group, p.tpt) ||
+          !encode4(&p.tmap_k, bf16, k, head_dim, {tokens, n_kv_heads, 1}, {st[2], st[3], 0}, 128, 1) ||
+          !encode4(&p.tmap_v, bf16, v, head_dim, {tokens, n_kv_heads, 1}, {st[4], st[5], 0}, 128, 1))
+        return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
+      const cudaError_t e = launch_tile_attn(p, ctas, bf16, head_dim, false, static_cast<cudaStream_t>(stream));
       if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     }
     return LPS_OK;
@@ -120,6 +175,13 @@ int check_tree(const char* fn, int batch, int width, const int32_t* pos, const i
   }
   return LPS_OK;
 }
+
+void tree_shape(TileAttnParams& p, int batch, int width, const int32_t* pos, const int32_t* rows, int nq, int nkv) {
+  p.n_seqs = batch;
+  p.width = width;
+  p.nq = nq, p.nkv = nkv, p.group = nq / nkv;
+  for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
+}
 }  // namespace
 
 extern "C" long long attention_tree_workspace_bytes(int batch, int width, const int32_t* pos, const int32_t* rows,
@@ -128,7 +190,11 @@ extern "C" long long attention_tree_workspace_bytes(int batch, int width, const 
   if (!pos || !rows || check_heads(FN, LPS_TYPE_BF16, n_q_heads, n_kv_heads, head_dim) ||
       check_tree(FN, batch, width, pos, rows, 0x7fffffff))
     return -1;
-  return 0;
+  const int sms = num_sms();
+  if (sms < 1) return -1;
+  TileAttnParams p{};
+  tree_shape(p, batch, width, pos, rows, n_q_heads, n_kv_heads);
+  return static_cast<long long>(tile_tree_workspace(p, tile_tree_plan(p, sms), head_dim));
 }
 
 extern "C" int attention_tree_verify(const void* q, const void* k_cache, const void* v_cache, void* out, int type,
@@ -149,21 +215,31 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     if ((rc = check_strides(FN, st, 6, head_dim))) return rc;
     if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out))
       return host_fail(LPS_EINVAL, FN, "q, the caches and out must be 16-byte aligned");
-    (void)workspace;
-    (void)workspace_bytes;
+    const int sms = num_sms();
+    if (sms < 1) return host_fail(LPS_ECUDA, FN, "no usable current device");
     TileAttnParams p{};
-    p.n_seqs = batch;
+    tree_shape(p, batch, width, pos, rows, n_q_heads, n_kv_heads);
+    const long long ctas = tile_tree_plan(p, sms);
+    const size_t need = tile_tree_workspace(p, ctas, head_dim);
+    if (need && (!workspace || workspace_bytes < need || misaligned(workspace)))
+      return host_fail(LPS_EINVAL, FN, "needs a 16-byte aligned workspace of " + std::to_string(need) + " bytes");
+    if (ctas == 0) return LPS_OK;
+    if (ctas > 0x7fffffffll) return host_fail(LPS_EINVAL, FN, "too many rows for one launch");
+    if (need) tile_tree_set_workspace(p, ctas, workspace);
     p.q = q, p.k = k_cache, p.v = v_cache, p.out = out;
     p.q_seq = st[0], p.q_tok = st[1], p.q_head = st[2], p.o_seq = st[3], p.o_tok = st[4], p.o_head = st[5];
     p.k_row = p.v_row = head_dim;
     p.k_head = p.v_head = static_cast<long long>(max_ctx) * head_dim;
     p.k_seq = p.v_seq = p.k_head * n_kv_heads;
     p.parents = parents;
-    p.width = width;
-    p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
-    p.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
-    for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
-    const cudaError_t e = launch_tile_attn(p, type == LPS_TYPE_BF16, head_dim, true, static_cast<cudaStream_t>(stream));
+    p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
+    const bool bf16 = type == LPS_TYPE_BF16;
+    const long long kv_n[3] = {max_ctx, n_kv_heads, batch}, kv_st[3] = {p.k_row, p.k_head, p.k_seq};
+    if (!encode4(&p.tmap_q, bf16, q, head_dim, {n_q_heads, width, batch}, {st[2], st[1], st[0]}, p.group, p.tpt) ||
+        !encode4(&p.tmap_k, bf16, k_cache, head_dim, kv_n, kv_st, 128, 1) ||
+        !encode4(&p.tmap_v, bf16, v_cache, head_dim, kv_n, kv_st, 128, 1))
+      return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
+    const cudaError_t e = launch_tile_attn(p, ctas, bf16, head_dim, true, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     return LPS_OK;
   });
@@ -230,5 +306,16 @@ extern "C" int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int ba
     const cudaError_t e = launch_accept(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     return LPS_OK;
+  });
+}
+
+extern "C" int cache_ops_status(void* stream) {
+  static const char* FN = "cache_ops_status";
+  return guarded(FN, [&]() -> int {
+    int st[2] = {0, 0};
+    const cudaError_t e = tile_attn_status(st, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, cudaGetErrorString(e));
+    if (!st[0] && !st[1]) return LPS_OK;
+    return host_fail(LPS_ECUDA, FN, "an earlier call's output is invalid: " + describe_status(st[0], st[1]));
   });
 }

@@ -32,6 +32,7 @@ enum : int {
   kKidTcGemm = 9,      // prefill-chunk GEMM on tcgen05
   kKidChunkAttn = 10,  // prefill-chunk attention (and its merge)
   kKidPrep = 11,       // prefill-chunk RMSNorm / split of the activations
+  kKidTileAttn = 12,   // packed-prompt and drafted-tree attention
   kKidSkinnyBit = 1 << 12,
 };
 

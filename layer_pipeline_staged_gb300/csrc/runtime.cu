@@ -73,7 +73,8 @@ std::string describe_status(int kinds, int first) {
                                          "persistent stage kernel",
                                          "prefill GEMM (tcgen05)",
                                          "prefill chunk attention",
-                                         "prefill RMSNorm / activation split"};
+                                         "prefill RMSNorm / activation split",
+                                         "packed-prompt / drafted-tree attention"};
   const int kid = (first >> 8) & 0xf;
   std::string what;
   const int k = first & 0xff ? first & 0xff : kinds;
@@ -83,7 +84,7 @@ std::string describe_status(int kinds, int first) {
   if (k & 8) what += "a kernel argument was out of range; ";
   if (k & 16) what += "a grid-wide barrier wait timed out; ";
   if (what.empty()) what = "unknown error; ";
-  std::string name = kKernels[kid < 12 ? kid : 0];
+  std::string name = kKernels[kid < 13 ? kid : 0];
   if (first & 0x1000) name += " (batch > 1 tensor-core GEMM)";
   char buf[96];
   std::snprintf(buf, sizeof buf, "(status 0x%x, first report 0x%x, detail %d)", kinds, first,

@@ -1,21 +1,194 @@
-// Attention of packed prompts (causal) and of drafted trees over a cache.
-// One warp per (token, query head): the lanes share the head dimension, keys
-// are walked in order with the running maximum and sum of the softmax.
+// Attention of packed prompts (causal) and of drafted trees over a cache, on
+// the fifth-generation tensor cores.
+//
+// For a query row q and the keys it sees, o = sum_j p_j v_j / sum_j p_j with
+// p_j = 2^(x_j - m), x_j = scale log2(e) q.k_j, in one pass over the keys: a
+// row keeps the exponent's base m, the sum l of its weights and the unscaled
+// o; the base follows the running maximum only when that has grown by more
+// than 2^8 (kStale), because o and l carry any common factor exactly as well,
+// so o is rescaled a few times per row instead of once per 128 keys.
+//
+// A tile is 128 rows = the `group` query heads of one kv head x 128 / group
+// consecutive tokens, so every key and value fetched serves the whole group,
+// and a short sequence still fills the matrix instruction with its heads. A
+// CTA runs two such accumulators (slots) at once, so that one slot's softmax
+// runs under the other's matrix products:
+//   - paired: two neighbouring tiles over the same key blocks (prompts, and
+//     trees of more than 128 rows);
+//   - solo (trees of up to 128 rows): the one tile over the even and over the
+//     odd key blocks; the two halves are joined like any two key chunks.
+// Per 128-key block and slot: S = Q.K^T (both operands in shared memory,
+// 128-byte swizzle, as TMA wrote them) into 128 TMEM columns; four warps read
+// a row per thread, make the weights, and write them back over S as the A
+// operand of O += P.V, whose B operand is the V block as it lies, keys as rows.
+// TMEM: S0 S1 O0 O1.
+//
+// Warps 0-3 and 4-7: softmax and epilogue of slot 0 and 1. Warp 8: TMA. Warp
+// 9: the MMAs. Warp 10: V blocks that some row does not see whole are made
+// safe before the MMA reads them, as 0 x inf is not 0: rows past the last key
+// become zero, and so do infinities and NaNs, which the epilogue then adds to
+// the rows that do see them (a path that finite inputs never take).
+//
+// Trees split the keys into chunks of `cs` blocks, one CTA each, which leave
+// (o, m, l) in the workspace for the merge kernel; prompts are whole.
+// Every sum has one order given by the shapes, so equal calls give equal bits.
+// Waits are bounded and report through the status word.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "cache_ops.h"
+#include "kernels.h"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace lps {
 namespace {
 
-constexpr int kWarps = 8;
+using namespace tc;
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* o) { *o = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* o) { *o = __float2half_rn(x); }
+constexpr int kRows = 128;        // rows of a tile (MMA M) and keys of a block (MMA N)
+constexpr int kThreads = 352;
+constexpr int kMaxStages = 8;
+constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
+constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
+constexpr int kKid = kKidTileAttn << 8;
+
+__device__ int g_status[2];       // sticky: error kinds, first report
+
+template <int HD>
+struct Shape {
+  static constexpr int kTile = kRows * HD * 2;  // bytes of a Q tile, a K block or a V block
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTile + 1024 + 1024;  // + alignment + barriers and flags
+};
+
+// ---- building blocks ---------------------------------------------------------------
+
+__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B, B in shared memory.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 fp32 columns of this thread's TMEM lane; tmem_wait_ld before they are used.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Wait for this thread's loads; v's uses stay behind the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Descriptor of an operand whose rows run along K (V: one key per 128-byte
+// row, 64 head dimensions wide): 8-key groups 1024 bytes apart (the stride
+// byte offset), the next 64 dimensions one [128 keys][128 bytes] panel on (the
+// leading byte offset).
+__device__ __forceinline__ uint64_t sw128_desc_rows(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>((kRows * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// Instruction descriptor as idesc_bf16, for either type, with B's rows along
+// K when b_rows (bit 16).
+__host__ __device__ constexpr uint32_t idesc_of(bool bf16, int n, bool b_rows) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_rows ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r.v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// x * 0 + acc: acc becomes NaN where x holds an infinity or a NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t probe(uint32_t x, uint32_t acc) {
+  uint32_t r;
+  if (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ bool nonfinite(uint32_t half) {  // the low 16 bits
+  constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+  return (half & kExp) == kExp;
+}
+template <bool BF16>
+__device__ __forceinline__ float widen(uint16_t x) {
+  if (BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
+  return __half2float(__ushort_as_half(x));
+}
 
 // The drafted rows that row t sees, as bits; 0 for a chain that leaves its
 // range (a parent outside [-1, child)).
@@ -30,59 +203,665 @@ __device__ __forceinline__ unsigned long long tree_mask(const int* parents, int 
   return m;
 }
 
-template <class T, int HD, bool TREE>
-__global__ void __launch_bounds__(kWarps * 32) tile_attn_kernel(const __grid_constant__ TileAttnParams p) {
+// ---- one CTA's work --------------------------------------------------------------
+
+struct Item {
+  int s, g;          // sequence, kv head
+  int t0;            // first token of slot 0's tile
+  int b0, nblk;      // key blocks [b0, b0 + nblk) of this CTA
+  int n[2];          // of which each slot works through so many (solo: every other one)
+  int tiles;         // tiles with rows (1 or 2)
+  int clean;         // keys [0, clean) are seen by every row of the item
+  int kend;          // keys at and after kend are seen by none
+  bool direct;       // out is written here (else: a partial)
+};
+
+template <bool TREE>
+__device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
+  Item it;
+  const int w = idx / p.nkv;
+  it.g = idx - w * p.nkv;
+  int lo = 0, hi = p.n_seqs - 1;  // the last s with item0[s] <= w
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.item0[mid] <= w) lo = mid; else hi = mid - 1;
+  }
+  it.s = lo;
+  const int len = p.len[lo], off = w - p.item0[lo], span = 2 * p.tpt;
+  if (!TREE) {
+    const int pairs = (len + span - 1) / span;
+    it.t0 = (pairs - 1 - off) * span;  // the last tokens, which see the most keys, first
+    const int endA = min(it.t0 + p.tpt, len), endB = min(it.t0 + span, len);
+    it.b0 = 0;
+    it.n[0] = (endA + kRows - 1) / kRows;
+    it.n[1] = endB > endA ? (endB + kRows - 1) / kRows : 0;
+    it.nblk = max(it.n[0], it.n[1]);
+    it.tiles = endB > endA ? 2 : 1;
+    it.clean = it.t0 + 1;
+    it.kend = endB;
+    it.direct = true;
+  } else {
+    const int all = (p.pos[lo] + len + kRows - 1) / kRows, chunks = (all + p.cs - 1) / p.cs;
+    const int pair = off / chunks, c = off - pair * chunks;
+    it.t0 = pair * span;
+    it.b0 = c * p.cs;
+    it.nblk = min(p.cs, all - it.b0);
+    it.tiles = !p.solo && it.t0 + p.tpt < len ? 2 : 1;
+    it.n[0] = p.solo ? (it.nblk + 1) / 2 : it.nblk;
+    it.n[1] = p.solo ? it.nblk / 2 : it.tiles == 2 ? it.nblk : 0;
+    it.clean = p.pos[lo];
+    it.kend = p.pos[lo] + len;
+    it.direct = p.solo ? all == 1 : chunks == 1;
+  }
+  return it;
+}
+
+// Which 32 keys from kw on a row sees, as bits. Prompt: the keys [0, lim]; tree:
+// the keys [0, lim] and the drafts of anc, whose bit 0 is key lim + 1.
+template <bool TREE>
+__device__ __forceinline__ uint32_t seen32(int kw, int lim, unsigned long long anc) {
+  const int n = lim - kw + 1;
+  uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  if (TREE) {
+    const int d = -n;  // the draft that key kw holds
+    if (d >= 0) {
+      if (d < 64) bits |= static_cast<uint32_t>(anc >> d);
+    } else if (d > -32) {
+      bits |= static_cast<uint32_t>(anc << -d);
+    }
+  }
+  return bits;
+}
+
+template <bool BF16, int HD, bool TREE>
+__global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_constant__ TileAttnParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  constexpr int kTile = Shape<HD>::kTile, NS = Shape<HD>::kStages, kPanels = HD / 64, kPanel = kRows * 128;
+  static_assert(NS <= kMaxStages, "ring");
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem;
+  uint8_t* ring = smem + 2 * kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + NS * kTile);
+  uint64_t* empty = full + NS;
+  uint64_t* qfull = empty + NS;
+  uint64_t* sfull = qfull + 1;     // [2]: S of the slot is ready (and its earlier P.V is done)
+  uint64_t* pfull = sfull + 2;     // [2]: P of the slot is written (and O rescaled)
+  uint64_t* ofull = pfull + 2;     // [2]: the slot's last P.V is done
+  uint64_t* vfix = ofull + 2;      // [kMaxFix]: the V block is safe to multiply
+  uint64_t* vissued = vfix + kMaxFix;  // [kMaxFix]: its copy has been issued (its stage's phase is the current one)
+  uint64_t* mma_done = vissued + kMaxFix;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* dirty = reinterpret_cast<int*>(tmem_base + 1);
+  int* parents = reinterpret_cast<int*>(tmem_base + 2);  // [kTreeMax]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Item it = item_of<TREE>(p, blockIdx.x);
+  const bool solo = TREE && p.solo;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(qfull, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&ofull[i], 1);
+    }
+    for (int i = 0; i < kMaxFix; ++i) {
+      mbar_init(&vfix[i], 1);
+      mbar_init(&vissued[i], 1);
+    }
+    mbar_init(mma_done, 1);
+    *dirty = 0;
+    fence_mbar_init();
+  }
+  if (TREE)
+    for (int i = tid; i < p.len[it.s]; i += kThreads) parents[i] = p.parents[static_cast<size_t>(it.s) * p.width + i];
+  if (warp == 9) {
+    tmem_alloc(tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_base;
+  const uint32_t tS[2] = {tbase, tbase + 128}, tO[2] = {tbase + 256, tbase + 256 + HD};
+  if (TREE) pdl_launch_dependents();
+
+  // first block that some row does not see whole
+  const int fix0 = max(it.b0, it.clean / kRows);
+  // place in the load order of V block j (counted from b0); K blocks are ahead of their V
+  auto v_at = [&](int j) { return !solo ? 2 * j + 1 : j <= it.nblk - 2 ? 2 * j + 2 : 2 * it.nblk - 1; };
+
+  if (warp == 8) {
+    // ---------------- TMA ----------------
+    if (lane == 0) {
+      const int tb = p.tok0[it.s], seq = TREE ? it.s : 0;
+      const uint32_t qbytes = static_cast<uint32_t>(p.group * p.tpt) * 128u * kPanels;
+      mbar_arrive_expect_tx(qfull, qbytes * it.tiles);
+      for (int t = 0; t < it.tiles; ++t)
+        for (int c = 0; c < kPanels; ++c)
+          tma_4d(qs + t * kTile + c * kPanel, &p.tmap_q, c * 64, it.g * p.group, tb + it.t0 + t * p.tpt, seq, qfull);
+      int n = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int j) {
+        const int st = n % NS;
+        if (ok && n >= NS && !mbar_wait(&empty[st], static_cast<uint32_t>((n / NS - 1) & 1))) {
+          report_error(g_status, kErrWaitEmpty | kKid);
+          ok = false;
+        }
+        if (!ok) return;
+        mbar_arrive_expect_tx(&full[st], kTile);
+        for (int c = 0; c < kPanels; ++c)
+          tma_4d(ring + st * kTile + c * kPanel, map, c * 64, tb + (it.b0 + j) * kRows, it.g, seq, &full[st]);
+        ++n;
+      };
+      load(&p.tmap_k, 0);
+      if (solo && it.nblk > 1) load(&p.tmap_k, 1);
+      const int ahead = solo ? 2 : 1;
+      for (int j = 0; j < it.nblk && ok; ++j) {
+        load(&p.tmap_v, j);
+        if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[it.b0 + j - fix0]);
+        if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
+      }
+      // every copy issued lands before the CTA may end
+      bool landed = mbar_wait(qfull, 0, kDrainLimitCycles);
+      for (int m = max(n - NS, 0); m < n; ++m) landed &= mbar_wait(&full[m % NS], static_cast<uint32_t>((m / NS) & 1), kDrainLimitCycles);
+      if (!landed) report_error(g_status, kErrDrain | kKid);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_of(BF16, kRows, false), id_pv = idesc_of(BF16, HD, true);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
+        if (ok && !mbar_wait(bar, parity)) {
+          report_error(g_status, kErrWaitFull | kKid | (what << 13));
+          ok = false;
+        }
+      };
+      auto wait_stage = [&](int n) { wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1), 1); };
+      auto stage = [&](int n) { return smem_u32(ring + (n % NS) * kTile); };
+      auto qk = [&](int slot, int n) {
+        const uint64_t a = sw128_desc(smem_u32(qs + (solo ? 0 : slot) * kTile)), b = sw128_desc(stage(n));
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t adv = static_cast<uint64_t>((kk / 4) * (kPanel >> 4) + (kk % 4) * 2);
+          umma_bf16(tS[slot], a + adv, b + adv, id_qk, kk > 0);
+        }
+        umma_commit(&sfull[slot]);
+      };
+      auto pv = [&](int slot, int n, bool first) {
+        const uint64_t b = sw128_desc_rows(stage(n));
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)  // 16 keys on: 8 columns of P, 2048 bytes of V
+          umma_ts(tO[slot], tS[slot] + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv, !first || kk > 0);
+      };
+      wait(qfull, 0, 2);
+      if (!solo) {
+        // K0 V0 K1 V1 ..
+        wait_stage(0);
+        if (ok) {
+          tc_fence_after();
+          for (int s = 0; s < 2; ++s)
+            if (it.n[s] > 0) qk(s, 0);
+          umma_commit(&empty[0]);
+        }
+        for (int j = 0; j < it.nblk && ok; ++j) {
+          wait_stage(2 * j + 1);
+          if (it.b0 + j >= fix0) wait(&vfix[it.b0 + j - fix0], 0, 3);
+          bool have_k = false;
+          for (int s = 0; s < 2 && ok; ++s) {
+            if (j >= it.n[s]) continue;
+            wait(&pfull[s], static_cast<uint32_t>(j & 1), 4);
+            if (!ok) break;
+            tc_fence_after();
+            pv(s, 2 * j + 1, j == 0);
+            if (j + 1 < it.n[s]) {
+              if (!have_k) wait_stage(2 * j + 2);
+              have_k = true;
+              if (!ok) break;
+              tc_fence_after();
+              qk(s, 2 * j + 2);
+            } else {
+              umma_commit(&ofull[s]);
+            }
+          }
+          umma_commit(&empty[(2 * j + 1) % NS]);
+          if (j + 1 < it.nblk) {
+            if (!have_k) wait_stage(2 * j + 2);
+            umma_commit(&empty[(2 * j + 2) % NS]);
+          }
+        }
+      } else {
+        // K0 K1 V0 K2 V1 K3 ..; slot j & 1 takes block j
+        int n = 0;
+        for (int j = 0; j < 2 && j < it.nblk && ok; ++j, ++n) {
+          wait_stage(n);
+          if (!ok) break;
+          tc_fence_after();
+          qk(j, n);
+          umma_commit(&empty[n % NS]);
+        }
+        for (int j = 0; j < it.nblk && ok; ++j) {
+          const int s = j & 1;
+          wait_stage(n);
+          if (it.b0 + j >= fix0) wait(&vfix[it.b0 + j - fix0], 0, 3);
+          wait(&pfull[s], static_cast<uint32_t>((j >> 1) & 1), 4);
+          if (!ok) break;
+          tc_fence_after();
+          pv(s, n, j < 2);
+          umma_commit(&empty[n % NS]);
+          ++n;
+          if (j + 2 < it.nblk) {
+            wait_stage(n);
+            if (!ok) break;
+            tc_fence_after();
+            qk(s, n);
+            umma_commit(&empty[n % NS]);
+            ++n;
+          } else {
+            umma_commit(&ofull[s]);
+          }
+        }
+      }
+      // every MMA has completed before TMEM is freed
+      umma_commit(mma_done);
+      if (!mbar_wait(mma_done, 0, kDrainLimitCycles)) report_error(g_status, kErrDrain | kKid | (1 << 13));
+    }
+  } else if (warp == 10) {
+    // ---------------- V blocks made safe ----------------
+    for (int kb = fix0; kb < it.b0 + it.nblk; ++kb) {
+      const int n = v_at(kb - it.b0);
+      if (!__all_sync(0xffffffffu, mbar_wait(&vissued[kb - fix0], 0) &&
+                                       mbar_wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1)))) {
+        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (5 << 13));
+        break;
+      }
+      uint8_t* v = ring + (n % NS) * kTile;
+      const int rows = max(0, min(kRows, it.kend - kb * kRows));  // rows that hold keys
+      uint32_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kPanels; ++c) {
+        uint8_t* panel = v + c * kPanel;
+        for (int i = lane + rows * 8; i < kRows * 8; i += 32) reinterpret_cast<uint4*>(panel)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int i = lane; i < rows * 8; i += 32) {
+          const uint4 x = reinterpret_cast<const uint4*>(panel)[i];
+          acc[0] = probe<BF16>(x.x, acc[0]);
+          acc[1] = probe<BF16>(x.y, acc[1]);
+          acc[2] = probe<BF16>(x.z, acc[2]);
+          acc[3] = probe<BF16>(x.w, acc[3]);
+        }
+      }
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bad |= nonfinite<BF16>(acc[i]) || nonfinite<BF16>(acc[i] >> 16);
+      if (__any_sync(0xffffffffu, bad)) {
+        for (int c = 0; c < kPanels; ++c)
+          for (int i = lane; i < rows * 32; i += 32) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(v + c * kPanel) + i;
+            uint32_t x = *w;
+            if (nonfinite<BF16>(x)) x &= 0xffff0000u;
+            if (nonfinite<BF16>(x >> 16)) x &= 0xffffu;
+            *w = x;
+          }
+        if (lane == 0) *dirty = 1;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&vfix[kb - fix0]);
+    }
+  } else {
+    // ---------------- softmax and epilogue of slot `slot` ----------------
+    const int slot = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tS[slot] + lane_off, o_addr = tO[slot] + lane_off;
+    const int len = p.len[it.s];
+    const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + r / p.group;
+    const bool row_ok = r < p.group * p.tpt && tok < len;
+    const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+    const unsigned long long anc = TREE && row_ok ? tree_mask(parents, tok) : 0;
+    const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
+    const float sl2 = p.scale_log2;
+    const int nb = it.n[slot];
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nb; ++i) {
+      const int kb = it.b0 + (solo ? 2 * i + slot : i);
+      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(i & 1)))) {
+        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (warp_ok) {
+        float x[kRows];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, x + c * 32);
+        tmem_wait_ld<kRows>(x);
+        if (kb >= fix0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = seen32<TREE>(kb * kRows + c * 32, lim, anc);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((bits >> e) & 1u)) x[c * 32 + e] = -INFINITY;
+          }
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int e = 4; e < kRows; e += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], e + 4 + q < kRows ? x[e + 4 + q] : x[e + q]);
+        }
+        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        if (i == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, row_ok && (top - m) * sl2 > kStale)) {  // rows without a query have no say
+          // O holds the blocks before this one, whole: S of this block was
+          // issued behind their P.V
+          const float f = top > m ? ex2((m - top) * sl2) : 1.0f;
+          l *= f;
+          m = top;
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+            tmem_st16(o_addr + c + 16, reinterpret_cast<const uint32_t*>(o) + 16);
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m * sl2;
+        const F2 sl = pack2(sl2, sl2), ng = pack2(neg, neg);
+        F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, b;
+            unpack2(fma2(pack2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), sl, ng), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+            w[e] = pack16<BF16>(a, b);
+          }
+          tmem_st16(s_addr + c * 16, w);
+        }
+        float a, b;
+        unpack2(add2(sum[0], sum[1]), a, b);
+        l += a + b;
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[slot]);
+    }
+    if (ok && nb > 0) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&ofull[slot], 0))) {
+        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (7 << 13));
+        ok = false;
+      }
+    }
+    tc_fence_after();
+    const bool seen = row_ok && (!TREE || anc != 0);  // a draft of a broken chain sees nothing
+    const bool fix = ok && *dirty != 0;
+    // 32 columns of o from c on, with the infinities and NaNs of the V blocks made safe
+    auto load_o = [&](int c, float* o) {
+      tmem_ld32(o_addr + c, o);
+      tmem_wait_ld<32>(o);
+      if (fix && seen) {
+        const uint16_t* v = static_cast<const uint16_t*>(p.v) + (TREE ? it.s * p.v_seq : 0) + p.tok0[it.s] * p.v_row + it.g * p.v_head + c;
+        for (int i = 0; i < nb; ++i) {
+          const int kb = it.b0 + (solo ? 2 * i + slot : i);
+          if (kb < fix0) continue;
+          for (int key = kb * kRows; key < min(kb * kRows + kRows, it.kend); ++key) {
+            if (!(seen32<TREE>(key, lim, anc) & 1u)) continue;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint16_t w = v[key * p.v_row + e];
+              if (nonfinite<BF16>(w)) o[e] += widen<BF16>(w);
+            }
+          }
+        }
+      }
+    };
+    if (ok && warp_ok && it.direct) {
+      if (nb > 0) {
+        // rows to shared memory (the slot's Q tile is no longer read), 16-byte
+        // units swizzled by the row, then whole rows to global memory
+        const float inv = seen ? 1.0f / l : 0.f;
+        uint8_t* st = qs + slot * kTile;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          load_o(c, o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = seen ? pack16<BF16>(o[u * 8 + 2 * e] * inv, o[u * 8 + 2 * e + 1] * inv) : 0u;
+            *reinterpret_cast<uint4*>(st + r * (HD * 2) + (((c / 8 + u) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+        constexpr int U = HD / 8, RW = 32 / U;  // units per row, rows per pass of the warp
+        uint16_t* out = static_cast<uint16_t*>(p.out) + (TREE ? it.s * p.o_seq : 0);
+        for (int i = 0; i < 32; i += RW) {
+          const int rr = quarter * 32 + i + lane / U, u = lane % U;
+          const int t = it.t0 + (solo ? 0 : slot * p.tpt) + rr / p.group;
+          if (rr < p.group * p.tpt && t < len) {
+            const uint4 w = *reinterpret_cast<const uint4*>(st + rr * (HD * 2) + ((u ^ (rr & 7)) << 4));
+            *reinterpret_cast<uint4*>(out + (p.tok0[it.s] + t) * p.o_tok + (it.g * p.group + rr % p.group) * p.o_head + u * 8) = w;
+          }
+        }
+      }
+    } else if (TREE && ok && warp_ok) {
+      // partial of this CTA and slot: (m log2-scaled, l) per row, then o
+      const size_t slab = (static_cast<size_t>(blockIdx.x) * 2 + slot) * kRows + r;
+      if (row_ok) p.part_ml[slab] = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
+      if (nb > 0) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          load_o(c, o);
+          if (seen) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + slab * HD + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ---- joining the key chunks of a tree ---------------------------------------------
+
+constexpr int kMergeWarps = 8;
+
+// One warp per (drafted row, query head): o = sum_c w_c o_c / sum_c w_c l_c over
+// the row's partials in chunk order, w_c = 2^(m_c - max m).
+template <bool BF16, int HD>
+__global__ void __launch_bounds__(kMergeWarps * 32) tile_merge_kernel(const __grid_constant__ TileAttnParams p) {
   constexpr int E = HD / 32;
   const int lane = threadIdx.x & 31;
-  const int s = blockIdx.z, h = blockIdx.y, g = h / p.group;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= p.len[s]) return;
-  const T* q = static_cast<const T*>(p.q) + s * p.q_seq + (p.tok0[s] + t) * p.q_tok + h * p.q_head + lane * E;
-  const T* k = static_cast<const T*>(p.k) + s * p.k_seq + p.tok0[s] * p.k_row + g * p.k_head + lane * E;
-  const T* v = static_cast<const T*>(p.v) + s * p.v_seq + p.tok0[s] * p.v_row + g * p.v_head + lane * E;
-  T* o = static_cast<T*>(p.out) + s * p.o_seq + (p.tok0[s] + t) * p.o_tok + h * p.o_head + lane * E;
-  const unsigned long long tm = TREE ? tree_mask(p.parents + static_cast<size_t>(s) * p.width, t) : 0;
-  const int pos = TREE ? p.pos[s] : 0;
-  const int nkeys = TREE ? (tm ? pos + t + 1 : 0) : t + 1;
-  float qf[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    qf[e] = to_f(q[e]) * p.scale;
-    acc[e] = 0.f;
+  const int s = blockIdx.z, t = blockIdx.y, head = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (t >= p.len[s] || head >= p.nq) return;
+  const int all = (p.pos[s] + p.len[s] + kRows - 1) / kRows, chunks = (all + p.cs - 1) / p.cs;
+  if (p.solo ? all == 1 : chunks == 1) return;  // written directly
+  const int g = head / p.group, pair = t / (2 * p.tpt), slots = p.solo ? 2 : 1;
+  const int slot0 = p.solo ? 0 : (t / p.tpt) & 1;
+  const int r = (t - (p.solo ? 0 : (2 * pair + slot0) * p.tpt)) * p.group + head % p.group;
+  const int w0 = p.item0[s] + pair * chunks, n = chunks * slots;
+  auto slab = [&](int c) {
+    const int chunk = c / slots, slot = slot0 + c % slots;
+    return ((static_cast<size_t>(w0 + chunk) * p.nkv + g) * 2 + slot) * kRows + r;
+  };
+  pdl_wait();
+  float top = -INFINITY;
+  for (int c = lane; c < n; c += 32) {
+    const float2 ml = p.part_ml[slab(c)];
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
   }
-  for (int j = 0; j < nkeys; ++j) {
-    if (TREE && j >= pos && !((tm >> (j - pos)) & 1)) continue;
-    float x = 0.f;
-    for (int e = 0; e < E; ++e) x = fmaf(qf[e], to_f(k[j * p.k_row + e]), x);
-    x = warp_sum(x);
-    const float mn = fmaxf(m, x);
-    const float a = m == mn ? 1.f : expf(m - mn), w = expf(x - mn);
-    l = fmaf(l, a, w);
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], a, w * to_f(v[j * p.v_row + e]));
-    m = mn;
+  top = warp_max(top);
+  float l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    float wl = 0.f, ll = 0.f;
+    if (c0 + lane < n) {
+      const float2 ml = p.part_ml[slab(c0 + lane)];
+      ll = ml.y;
+      if (ll != 0.f) wl = ex2(top == -INFINITY ? 0.f : ml.x - top);
+    }
+#pragma unroll 4
+    for (int c = 0; c < min(32, n - c0); ++c) {
+      const float w = __shfl_sync(0xffffffffu, wl, c), lc = __shfl_sync(0xffffffffu, ll, c);
+      if (lc == 0.f) continue;
+      const float* src = p.part_o + slab(c0 + c) * HD + lane * E;
+      l = fmaf(w, lc, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+    }
   }
-  const float inv = nkeys ? 1.0f / l : 0.f;
-  for (int e = 0; e < E; ++e) from_f(acc[e] * inv, o + e);
+  const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
+  uint16_t* out = static_cast<uint16_t*>(p.out) + s * p.o_seq + t * p.o_tok + head * p.o_head + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack16<BF16>(o[e] * inv, o[e + 1] * inv);
 }
 
-template <class T, int HD, bool TREE>
-cudaError_t launch_t(const TileAttnParams& p, cudaStream_t s) {
-  int longest = 0;
-  for (int i = 0; i < p.n_seqs; ++i) longest = p.len[i] > longest ? p.len[i] : longest;
-  if (longest == 0) return cudaSuccess;
-  tile_attn_kernel<T, HD, TREE><<<dim3((longest + kWarps - 1) / kWarps, p.nq, p.n_seqs), kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+template <bool BF16, int HD, bool TREE>
+cudaError_t launch_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
+  auto kern = tile_attn_kernel<BF16, HD, TREE>;
+  static std::atomic<int> smem_set[kMaxDevices];
+  cudaError_t e = set_smem_attr(kern, Shape<HD>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(ctas), kThreads, Shape<HD>::kSmem, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !TREE || !p.partials) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.nq + kMergeWarps - 1) / kMergeWarps, p.width, p.n_seqs);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<BF16, HD>, p);
 }
 
-template <class T>
-cudaError_t launch_hd(const TileAttnParams& p, int hd, bool tree, cudaStream_t s) {
-  if (hd == 128) return tree ? launch_t<T, 128, true>(p, s) : launch_t<T, 128, false>(p, s);
-  return tree ? launch_t<T, 64, true>(p, s) : launch_t<T, 64, false>(p, s);
+template <bool BF16>
+cudaError_t launch_hd(const TileAttnParams& p, long long ctas, int hd, bool tree, cudaStream_t s) {
+  if (hd == 128) return tree ? launch_t<BF16, 128, true>(p, ctas, s) : launch_t<BF16, 128, false>(p, ctas, s);
+  return tree ? launch_t<BF16, 64, true>(p, ctas, s) : launch_t<BF16, 64, false>(p, ctas, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tile_attn(const TileAttnParams& p, bool bf16, int hd, bool tree, cudaStream_t s) {
-  return bf16 ? launch_hd<__nv_bfloat16>(p, hd, tree, s) : launch_hd<__half>(p, hd, tree, s);
+// Workspace of a tree launch: per CTA and slot, (m, l) and o of 128 rows.
+size_t tile_tree_workspace(const TileAttnParams& p, long long ctas, int hd) {
+  return p.partials ? static_cast<size_t>(ctas) * 2 * kRows * (sizeof(float2) + hd * sizeof(float)) : 0;
+}
+void tile_tree_set_workspace(TileAttnParams& p, long long ctas, void* ws) {
+  p.part_ml = static_cast<float2*>(ws);
+  p.part_o = reinterpret_cast<float*>(p.part_ml + ctas * 2 * kRows);
+}
+
+// Work items of a prompt launch: sequences longest first, each from its last
+// tokens (which see the most keys) to its first, so that the launch ends on
+// small items.
+long long tile_prompt_plan(TileAttnParams& p) {
+  int order[kOpSeqs], tok0[kOpSeqs], len[kOpSeqs];
+  for (int s = 0; s < p.n_seqs; ++s) order[s] = s, tok0[s] = p.tok0[s], len[s] = p.len[s];
+  std::stable_sort(order, order + p.n_seqs, [&](int a, int b) { return len[a] > len[b]; });
+  p.tpt = kRows / p.group;
+  long long items = 0;
+  for (int s = 0; s < p.n_seqs; ++s) {
+    p.tok0[s] = tok0[order[s]];
+    p.len[s] = len[order[s]];
+    p.item0[s] = static_cast<int>(items);
+    items += (p.len[s] + 2 * p.tpt - 1) / (2 * p.tpt);
+  }
+  return items * p.nkv;
+}
+
+// Work items of a tree launch: keys in chunks of cs blocks, for the shortest
+// modelled time. A CTA takes its blocks and about two blocks' time of start,
+// ramp and epilogue (kCtaCost); the SMs share the CTAs' total, and the whole
+// chunks come in rounds.
+long long tile_tree_plan(TileAttnParams& p, int num_sms) {
+  constexpr int kCtaCost = 2;
+  p.tpt = kRows / p.group;
+  int most_rows = 0, most = 1, blocks[kOpSeqs];
+  for (int s = 0; s < p.n_seqs; ++s) {
+    most_rows = std::max(most_rows, p.len[s]);
+    blocks[s] = p.len[s] ? (p.pos[s] + p.len[s] + kRows - 1) / kRows : 0;
+    most = std::max(most, blocks[s]);
+  }
+  p.solo = most_rows <= p.tpt;
+  auto pairs_of = [&](int s) -> long long { return p.solo ? 1 : (p.len[s] + 2 * p.tpt - 1) / (2 * p.tpt); };
+  long long total = 0;
+  for (int s = 0; s < p.n_seqs; ++s) total += pairs_of(s) * blocks[s] * p.nkv;
+  // chunks of the longest sequence: past two CTAs per SM no split pays
+  const long long most_chunks = std::min<long long>(most, 2ll * num_sms * most / std::max(total, 1ll) + 1);
+  long long best = -1;
+  p.cs = most;
+  for (int c = 1, last = 0; c <= most_chunks; ++c) {
+    const int cs = (most + c - 1) / c;
+    if (cs == last) continue;
+    last = cs;
+    long long ctas = 0, whole = 0;
+    for (int s = 0; s < p.n_seqs; ++s) {
+      ctas += pairs_of(s) * ((blocks[s] + cs - 1) / cs);
+      whole += pairs_of(s) * (blocks[s] / cs);
+    }
+    const long long rounds = (whole * p.nkv + num_sms - 1) / num_sms;
+    const long long shared = (total + kCtaCost * ctas * p.nkv + num_sms - 1) / num_sms;
+    const long long cost = std::max(rounds * (cs + kCtaCost), shared);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.cs = cs;
+    }
+  }
+  long long items = 0;
+  p.partials = 0;
+  for (int s = 0; s < p.n_seqs; ++s) {
+    p.item0[s] = static_cast<int>(items);
+    items += pairs_of(s) * ((blocks[s] + p.cs - 1) / p.cs);
+    if (p.solo ? blocks[s] > 1 : blocks[s] > p.cs) p.partials = 1;
+  }
+  return items * p.nkv;
+}
+
+cudaError_t launch_tile_attn(const TileAttnParams& p, long long ctas, bool bf16, int hd, bool tree, cudaStream_t s) {
+  if (ctas <= 0) return cudaSuccess;
+  return bf16 ? launch_hd<true>(p, ctas, hd, tree, s) : launch_hd<false>(p, ctas, hd, tree, s);
+}
+
+cudaError_t tile_attn_status(int* status, cudaStream_t s) {
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(status, g_status, 2 * sizeof(int));
+  if (e != cudaSuccess || (!status[0] && !status[1])) return e;
+  const int zero[2] = {0, 0};
+  return cudaMemcpyToSymbol(g_status, zero, sizeof zero);
 }
 
 }  // namespace lps
