@@ -29,6 +29,12 @@
 // become zero, and so do infinities and NaNs, which the epilogue then adds to
 // the rows that do see them (a path that finite inputs never take).
 //
+// A CTA stays on its SM: once the copies of its item are issued, its TMA lane
+// takes over the next CTA of the grid that has not started
+// (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first
+// S is made, while the last item's softmax and epilogue still run. The grid is
+// ordered from the largest item to the smallest.
+//
 // Trees split the keys into chunks of `cs` blocks, one CTA each, which leave
 // (o, m, l) in the workspace for the merge kernel; prompts are whole.
 // Every sum has one order given by the shapes, so equal calls give equal bits.
@@ -49,7 +55,9 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;        // rows of a tile (MMA M) and keys of a block (MMA N)
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;     // two softmax warpgroups; TMA, MMA and repair warps, one idle
+constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168, what the block is launched with
+constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
@@ -190,17 +198,47 @@ __device__ __forceinline__ float widen(uint16_t x) {
   return __half2float(__ushort_as_half(x));
 }
 
-// The drafted rows that row t sees, as bits; 0 for a chain that leaves its
-// range (a parent outside [-1, child)).
-__device__ __forceinline__ unsigned long long tree_mask(const int* parents, int t) {
+// The drafted rows that row t sees, as bits, from parents in [-1, child) or -2
+// where that was not so; 0 for a chain that holds a -2.
+__device__ __forceinline__ unsigned long long tree_mask(const int8_t* parents, int t) {
   unsigned long long m = 0;
   while (t >= 0) {
     m |= 1ull << t;
-    const int up = parents[t];
-    if (up < -1 || up >= t) return 0;
-    t = up;
+    t = parents[t];
   }
-  return m;
+  return t == -1 ? m : 0;
+}
+
+// Ask for a CTA of this grid that has not started; 16 bytes of answer complete on `bar`.
+__device__ __forceinline__ void take_next(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The index of the CTA taken, or -1 when none is left.
+__device__ __forceinline__ int taken(const void* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before a later answer is written there
+  return ok ? static_cast<int>(x) : -1;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---- one CTA's work --------------------------------------------------------------
@@ -281,44 +319,48 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem;
   uint8_t* ring = smem + 2 * kTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + NS * kTile);
+  uint8_t* answer = ring + NS * kTile;                      // [2][16]: the items taken over
+  uint64_t* next_full = reinterpret_cast<uint64_t*>(answer + 32);  // [2]: an answer is there
+  uint64_t* next_empty = next_full + 2;  // [2]: every role has read it
+  uint64_t* full = next_empty + 2;
   uint64_t* empty = full + NS;
-  uint64_t* qfull = empty + NS;
-  uint64_t* sfull = qfull + 1;     // [2]: S of the slot is ready (and its earlier P.V is done)
-  uint64_t* pfull = sfull + 2;     // [2]: P of the slot is written (and O rescaled)
-  uint64_t* ofull = pfull + 2;     // [2]: the slot's last P.V is done
+  uint64_t* qfull = empty + NS;    // [2]: a Q tile is there
+  uint64_t* qempty = qfull + 2;    // [2]: its last S is made
+  uint64_t* sfull = qempty + 2;    // [2]: S of the slot is ready (and its earlier P.V is done)
+  uint64_t* pfull = sfull + 2;     // [2]: P of the slot is written (and O rescaled, and the last item's O read)
+  uint64_t* ofull = pfull + 2;     // [2]: the slot's last P.V of the item is done
   uint64_t* vfix = ofull + 2;      // [kMaxFix]: the V block is safe to multiply
   uint64_t* vissued = vfix + kMaxFix;  // [kMaxFix]: its copy has been issued (its stage's phase is the current one)
   uint64_t* mma_done = vissued + kMaxFix;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(mma_done + 1);
-  volatile int* dirty = reinterpret_cast<int*>(tmem_base + 1);
-  int* parents = reinterpret_cast<int*>(tmem_base + 2);  // [kTreeMax]
+  volatile int* dirty = reinterpret_cast<int*>(tmem_base + 1);  // [2]: 1 + the last item of that parity with repaired values
+  int8_t* parents = reinterpret_cast<int8_t*>(tmem_base + 4);   // [8][kTreeMax], a copy per softmax warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Item it = item_of<TREE>(p, blockIdx.x);
   const bool solo = TREE && p.solo;
 
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    mbar_init(qfull, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&next_full[i], 1);
+      mbar_init(&next_empty[i], 10);  // eight softmax warps, MMA, repair
+      mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
       mbar_init(&ofull[i], 1);
+      dirty[i] = 0;
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kMaxFix; ++i) {
       mbar_init(&vfix[i], 1);
       mbar_init(&vissued[i], 1);
     }
     mbar_init(mma_done, 1);
-    *dirty = 0;
     fence_mbar_init();
   }
-  if (TREE)
-    for (int i = tid; i < p.len[it.s]; i += kThreads) parents[i] = p.parents[static_cast<size_t>(it.s) * p.width + i];
   if (warp == 9) {
     tmem_alloc(tmem_base, 512);
     tmem_relinquish();
@@ -330,356 +372,430 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   const uint32_t tS[2] = {tbase, tbase + 128}, tO[2] = {tbase + 256, tbase + 256 + HD};
   if (TREE) pdl_launch_dependents();
 
-  // first block that some row does not see whole
-  const int fix0 = max(it.b0, it.clean / kRows);
-  // place in the load order of V block j (counted from b0); K blocks are ahead of their V
-  auto v_at = [&](int j) { return !solo ? 2 * j + 1 : j <= it.nblk - 2 ? 2 * j + 2 : 2 * it.nblk - 1; };
+  // first block of an item that some row does not see whole
+  auto fix0_of = [](const Item& it) { return max(it.b0, it.clean / kRows); };
+  // the item after item number `no`, for a role that reads the answers (lane 0 of its warp arrives)
+  auto next_item = [&](int no) -> int {
+    const int slot = no & 1;
+    int idx = -2;  // a wait that gave up
+    if (__all_sync(0xffffffffu, mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + slot * 16);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&next_empty[slot]);
+    return idx;
+  };
 
-  if (warp == 8) {
-    // ---------------- TMA ----------------
-    if (lane == 0) {
-      const int tb = p.tok0[it.s], seq = TREE ? it.s : 0;
-      const uint32_t qbytes = static_cast<uint32_t>(p.group * p.tpt) * 128u * kPanels;
-      mbar_arrive_expect_tx(qfull, qbytes * it.tiles);
-      for (int t = 0; t < it.tiles; ++t)
-        for (int c = 0; c < kPanels; ++c)
-          tma_4d(qs + t * kTile + c * kPanel, &p.tmap_q, c * 64, it.g * p.group, tb + it.t0 + t * p.tpt, seq, qfull);
-      int n = 0;
-      bool ok = true;
-      auto load = [&](const CUtensorMap* map, int j) {
-        const int st = n % NS;
-        if (ok && n >= NS && !mbar_wait(&empty[st], static_cast<uint32_t>((n / NS - 1) & 1))) {
-          report_error(g_status, kErrWaitEmpty | kKid);
-          ok = false;
+  if (warp >= 8) {
+    regs_dec<kOtherRegs>();
+    if (warp == 8) {
+      // ---------------- TMA ----------------
+      if (lane == 0) {
+        int n = 0, nq[2] = {0, 0}, nf = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity)) {
+            report_error(g_status, kErrWaitEmpty | kKid);
+            ok = false;
+          }
+        };
+        for (int idx = blockIdx.x, no = 0; idx >= 0 && ok; ++no) {
+          const Item it = item_of<TREE>(p, idx);
+          const int fix0 = fix0_of(it);
+          const int tb = p.tok0[it.s], seq = TREE ? it.s : 0;
+          auto load = [&](const CUtensorMap* map, int j) {
+            const int st = n % NS;
+            if (n >= NS) wait(&empty[st], static_cast<uint32_t>((n / NS - 1) & 1));
+            if (!ok) return;
+            mbar_arrive_expect_tx(&full[st], kTile);
+            for (int c = 0; c < kPanels; ++c)
+              tma_4d(ring + st * kTile + c * kPanel, map, c * 64, tb + (it.b0 + j) * kRows, it.g, seq, &full[st]);
+            ++n;
+          };
+          for (int t = 0; t < it.tiles; ++t) {
+            if (nq[t] > 0) wait(&qempty[t], static_cast<uint32_t>((nq[t] - 1) & 1));
+            if (!ok) break;
+            ++nq[t];
+            mbar_arrive_expect_tx(&qfull[t], static_cast<uint32_t>(p.group * p.tpt) * 128u * kPanels);
+            for (int c = 0; c < kPanels; ++c)
+              tma_4d(qs + t * kTile + c * kPanel, &p.tmap_q, c * 64, it.g * p.group, tb + it.t0 + t * p.tpt, seq, &qfull[t]);
+            if (t == 0) load(&p.tmap_k, 0);
+          }
+          if (solo && it.nblk > 1) load(&p.tmap_k, 1);
+          const int ahead = solo ? 2 : 1;
+          for (int j = 0; j < it.nblk && ok; ++j) {
+            load(&p.tmap_v, j);
+            if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[nf++ % kMaxFix]);
+            if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
+          }
+          if (!ok) break;
+          const int slot = no & 1;
+          if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
+          if (!ok) break;
+          mbar_arrive_expect_tx(&next_full[slot], 16);
+          take_next(answer + slot * 16, &next_full[slot]);
+          wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1));
+          idx = ok ? taken(answer + slot * 16) : -1;
         }
-        if (!ok) return;
-        mbar_arrive_expect_tx(&full[st], kTile);
-        for (int c = 0; c < kPanels; ++c)
-          tma_4d(ring + st * kTile + c * kPanel, map, c * 64, tb + (it.b0 + j) * kRows, it.g, seq, &full[st]);
-        ++n;
-      };
-      load(&p.tmap_k, 0);
-      if (solo && it.nblk > 1) load(&p.tmap_k, 1);
-      const int ahead = solo ? 2 : 1;
-      for (int j = 0; j < it.nblk && ok; ++j) {
-        load(&p.tmap_v, j);
-        if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[it.b0 + j - fix0]);
-        if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
+        // every copy issued lands before the CTA may end
+        bool landed = true;
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) landed &= mbar_wait(&qfull[t], static_cast<uint32_t>((nq[t] - 1) & 1), kDrainLimitCycles);
+        for (int m = max(n - NS, 0); m < n; ++m)
+          landed &= mbar_wait(&full[m % NS], static_cast<uint32_t>((m / NS) & 1), kDrainLimitCycles);
+        if (!landed) report_error(g_status, kErrDrain | kKid);
       }
-      // every copy issued lands before the CTA may end
-      bool landed = mbar_wait(qfull, 0, kDrainLimitCycles);
-      for (int m = max(n - NS, 0); m < n; ++m) landed &= mbar_wait(&full[m % NS], static_cast<uint32_t>((m / NS) & 1), kDrainLimitCycles);
-      if (!landed) report_error(g_status, kErrDrain | kKid);
-    }
-  } else if (warp == 9) {
-    // ---------------- MMA ----------------
-    if (lane == 0) {
+    } else if (warp == 9) {
+      // ---------------- MMA ----------------
       constexpr uint32_t id_qk = idesc_of(BF16, kRows, false), id_pv = idesc_of(BF16, HD, true);
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-        if (ok && !mbar_wait(bar, parity)) {
-          report_error(g_status, kErrWaitFull | kKid | (what << 13));
-          ok = false;
-        }
-      };
-      auto wait_stage = [&](int n) { wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1), 1); };
-      auto stage = [&](int n) { return smem_u32(ring + (n % NS) * kTile); };
-      auto qk = [&](int slot, int n) {
-        const uint64_t a = sw128_desc(smem_u32(qs + (solo ? 0 : slot) * kTile)), b = sw128_desc(stage(n));
+      int n0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, nf = 0;  // stages, Q tiles, P blocks and repaired blocks so far
+      for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
+        const Item it = item_of<TREE>(p, idx);
+        if (lane == 0 && ok) {
+          const int fix0 = fix0_of(it);
+          auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
+            if (ok && !mbar_wait(bar, parity)) {
+              report_error(g_status, kErrWaitFull | kKid | (what << 13));
+              ok = false;
+            }
+          };
+          auto wait_stage = [&](int n) { wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1), 1); };
+          auto wait_q = [&](int t) { wait(&qfull[t], static_cast<uint32_t>(nq[t]++ & 1), 2); };
+          auto wait_p = [&](int s) { wait(&pfull[s], static_cast<uint32_t>(np[s]++ & 1), 4); };
+          auto wait_fix = [&](int j) {
+            if (it.b0 + j < fix0) return;
+            wait(&vfix[nf % kMaxFix], static_cast<uint32_t>((nf / kMaxFix) & 1), 3);
+            ++nf;
+          };
+          auto stage = [&](int n) { return smem_u32(ring + (n % NS) * kTile); };
+          auto qk = [&](int slot, int n) {
+            const uint64_t a = sw128_desc(smem_u32(qs + (solo ? 0 : slot) * kTile)), b = sw128_desc(stage(n));
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t adv = static_cast<uint64_t>((kk / 4) * (kPanel >> 4) + (kk % 4) * 2);
-          umma_bf16(tS[slot], a + adv, b + adv, id_qk, kk > 0);
-        }
-        umma_commit(&sfull[slot]);
-      };
-      auto pv = [&](int slot, int n, bool first) {
-        const uint64_t b = sw128_desc_rows(stage(n));
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint64_t adv = static_cast<uint64_t>((kk / 4) * (kPanel >> 4) + (kk % 4) * 2);
+              umma_bf16(tS[slot], a + adv, b + adv, id_qk, kk > 0);
+            }
+            umma_commit(&sfull[slot]);
+          };
+          auto pv = [&](int slot, int n, bool first) {
+            const uint64_t b = sw128_desc_rows(stage(n));
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)  // 16 keys on: 8 columns of P, 2048 bytes of V
-          umma_ts(tO[slot], tS[slot] + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv, !first || kk > 0);
-      };
-      wait(qfull, 0, 2);
-      if (!solo) {
-        // K0 V0 K1 V1 ..
-        wait_stage(0);
-        if (ok) {
-          tc_fence_after();
-          for (int s = 0; s < 2; ++s)
-            if (it.n[s] > 0) qk(s, 0);
-          umma_commit(&empty[0]);
-        }
-        for (int j = 0; j < it.nblk && ok; ++j) {
-          wait_stage(2 * j + 1);
-          if (it.b0 + j >= fix0) wait(&vfix[it.b0 + j - fix0], 0, 3);
-          bool have_k = false;
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (j >= it.n[s]) continue;
-            wait(&pfull[s], static_cast<uint32_t>(j & 1), 4);
-            if (!ok) break;
-            tc_fence_after();
-            pv(s, 2 * j + 1, j == 0);
-            if (j + 1 < it.n[s]) {
-              if (!have_k) wait_stage(2 * j + 2);
-              have_k = true;
+            for (int kk = 0; kk < kRows / 16; ++kk)  // 16 keys on: 8 columns of P, 2048 bytes of V
+              umma_ts(tO[slot], tS[slot] + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv, !first || kk > 0);
+          };
+          if (!solo) {
+            // K0 V0 K1 V1 ..
+            for (int s = 0; s < it.tiles && ok; ++s) {
+              wait_q(s);
+              if (s == 0) wait_stage(n0);
               if (!ok) break;
               tc_fence_after();
-              qk(s, 2 * j + 2);
-            } else {
-              umma_commit(&ofull[s]);
+              qk(s, n0);
+              if (it.n[s] == 1) umma_commit(&qempty[s]);
             }
-          }
-          umma_commit(&empty[(2 * j + 1) % NS]);
-          if (j + 1 < it.nblk) {
-            if (!have_k) wait_stage(2 * j + 2);
-            umma_commit(&empty[(2 * j + 2) % NS]);
-          }
-        }
-      } else {
-        // K0 K1 V0 K2 V1 K3 ..; slot j & 1 takes block j
-        int n = 0;
-        for (int j = 0; j < 2 && j < it.nblk && ok; ++j, ++n) {
-          wait_stage(n);
-          if (!ok) break;
-          tc_fence_after();
-          qk(j, n);
-          umma_commit(&empty[n % NS]);
-        }
-        for (int j = 0; j < it.nblk && ok; ++j) {
-          const int s = j & 1;
-          wait_stage(n);
-          if (it.b0 + j >= fix0) wait(&vfix[it.b0 + j - fix0], 0, 3);
-          wait(&pfull[s], static_cast<uint32_t>((j >> 1) & 1), 4);
-          if (!ok) break;
-          tc_fence_after();
-          pv(s, n, j < 2);
-          umma_commit(&empty[n % NS]);
-          ++n;
-          if (j + 2 < it.nblk) {
-            wait_stage(n);
-            if (!ok) break;
-            tc_fence_after();
-            qk(s, n);
-            umma_commit(&empty[n % NS]);
-            ++n;
+            if (ok) umma_commit(&empty[n0 % NS]);
+            for (int j = 0; j < it.nblk && ok; ++j) {
+              const int nv = n0 + 2 * j + 1, nk = nv + 1;
+              wait_stage(nv);
+              wait_fix(j);
+              bool have_k = false;
+              for (int s = 0; s < 2 && ok; ++s) {
+                if (j >= it.n[s]) continue;
+                wait_p(s);
+                if (!ok) break;
+                tc_fence_after();
+                pv(s, nv, j == 0);
+                if (j + 1 < it.n[s]) {
+                  if (!have_k) wait_stage(nk);
+                  have_k = true;
+                  if (!ok) break;
+                  tc_fence_after();
+                  qk(s, nk);
+                  if (j + 2 == it.n[s]) umma_commit(&qempty[s]);
+                } else {
+                  umma_commit(&ofull[s]);
+                }
+              }
+              if (!ok) break;
+              umma_commit(&empty[nv % NS]);
+              if (j + 1 < it.nblk) umma_commit(&empty[nk % NS]);
+            }
+            n0 += 2 * it.nblk;
           } else {
-            umma_commit(&ofull[s]);
-          }
-        }
-      }
-      // every MMA has completed before TMEM is freed
-      umma_commit(mma_done);
-      if (!mbar_wait(mma_done, 0, kDrainLimitCycles)) report_error(g_status, kErrDrain | kKid | (1 << 13));
-    }
-  } else if (warp == 10) {
-    // ---------------- V blocks made safe ----------------
-    for (int kb = fix0; kb < it.b0 + it.nblk; ++kb) {
-      const int n = v_at(kb - it.b0);
-      if (!__all_sync(0xffffffffu, mbar_wait(&vissued[kb - fix0], 0) &&
-                                       mbar_wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1)))) {
-        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (5 << 13));
-        break;
-      }
-      uint8_t* v = ring + (n % NS) * kTile;
-      const int rows = max(0, min(kRows, it.kend - kb * kRows));  // rows that hold keys
-      uint32_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < kPanels; ++c) {
-        uint8_t* panel = v + c * kPanel;
-        for (int i = lane + rows * 8; i < kRows * 8; i += 32) reinterpret_cast<uint4*>(panel)[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int i = lane; i < rows * 8; i += 32) {
-          const uint4 x = reinterpret_cast<const uint4*>(panel)[i];
-          acc[0] = probe<BF16>(x.x, acc[0]);
-          acc[1] = probe<BF16>(x.y, acc[1]);
-          acc[2] = probe<BF16>(x.z, acc[2]);
-          acc[3] = probe<BF16>(x.w, acc[3]);
-        }
-      }
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bad |= nonfinite<BF16>(acc[i]) || nonfinite<BF16>(acc[i] >> 16);
-      if (__any_sync(0xffffffffu, bad)) {
-        for (int c = 0; c < kPanels; ++c)
-          for (int i = lane; i < rows * 32; i += 32) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(v + c * kPanel) + i;
-            uint32_t x = *w;
-            if (nonfinite<BF16>(x)) x &= 0xffff0000u;
-            if (nonfinite<BF16>(x >> 16)) x &= 0xffffu;
-            *w = x;
-          }
-        if (lane == 0) *dirty = 1;
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&vfix[kb - fix0]);
-    }
-  } else {
-    // ---------------- softmax and epilogue of slot `slot` ----------------
-    const int slot = warp >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tS[slot] + lane_off, o_addr = tO[slot] + lane_off;
-    const int len = p.len[it.s];
-    const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + r / p.group;
-    const bool row_ok = r < p.group * p.tpt && tok < len;
-    const bool warp_ok = __any_sync(0xffffffffu, row_ok);
-    const unsigned long long anc = TREE && row_ok ? tree_mask(parents, tok) : 0;
-    const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
-    const float sl2 = p.scale_log2;
-    const int nb = it.n[slot];
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int i = 0; i < nb; ++i) {
-      const int kb = it.b0 + (solo ? 2 * i + slot : i);
-      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(i & 1)))) {
-        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (warp_ok) {
-        float x[kRows];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, x + c * 32);
-        tmem_wait_ld<kRows>(x);
-        if (kb >= fix0) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = seen32<TREE>(kb * kRows + c * 32, lim, anc);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((bits >> e) & 1u)) x[c * 32 + e] = -INFINITY;
-          }
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int e = 4; e < kRows; e += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], e + 4 + q < kRows ? x[e + 4 + q] : x[e + q]);
-        }
-        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        if (i == 0) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, row_ok && (top - m) * sl2 > kStale)) {  // rows without a query have no say
-          // O holds the blocks before this one, whole: S of this block was
-          // issued behind their P.V
-          const float f = top > m ? ex2((m - top) * sl2) : 1.0f;
-          l *= f;
-          m = top;
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            tmem_ld32(o_addr + c, o);
-            tmem_wait_ld<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
-            tmem_st16(o_addr + c + 16, reinterpret_cast<const uint32_t*>(o) + 16);
-          }
-        }
-        const float neg = m == -INFINITY ? 0.f : -m * sl2;
-        const F2 sl = pack2(sl2, sl2), ng = pack2(neg, neg);
-        F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a, b;
-            unpack2(fma2(pack2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), sl, ng), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            sum[e & 1] = add2(sum[e & 1], pack2(a, b));
-            w[e] = pack16<BF16>(a, b);
-          }
-          tmem_st16(s_addr + c * 16, w);
-        }
-        float a, b;
-        unpack2(add2(sum[0], sum[1]), a, b);
-        l += a + b;
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[slot]);
-    }
-    if (ok && nb > 0) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&ofull[slot], 0))) {
-        if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (7 << 13));
-        ok = false;
-      }
-    }
-    tc_fence_after();
-    const bool seen = row_ok && (!TREE || anc != 0);  // a draft of a broken chain sees nothing
-    const bool fix = ok && *dirty != 0;
-    // 32 columns of o from c on, with the infinities and NaNs of the V blocks made safe
-    auto load_o = [&](int c, float* o) {
-      tmem_ld32(o_addr + c, o);
-      tmem_wait_ld<32>(o);
-      if (fix && seen) {
-        const uint16_t* v = static_cast<const uint16_t*>(p.v) + (TREE ? it.s * p.v_seq : 0) + p.tok0[it.s] * p.v_row + it.g * p.v_head + c;
-        for (int i = 0; i < nb; ++i) {
-          const int kb = it.b0 + (solo ? 2 * i + slot : i);
-          if (kb < fix0) continue;
-          for (int key = kb * kRows; key < min(kb * kRows + kRows, it.kend); ++key) {
-            if (!(seen32<TREE>(key, lim, anc) & 1u)) continue;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint16_t w = v[key * p.v_row + e];
-              if (nonfinite<BF16>(w)) o[e] += widen<BF16>(w);
+            // K0 K1 V0 K2 V1 K3 ..; slot j & 1 takes block j
+            int n = n0;
+            wait_q(0);
+            for (int j = 0; j < 2 && j < it.nblk && ok; ++j, ++n) {
+              wait_stage(n);
+              if (!ok) break;
+              tc_fence_after();
+              qk(j, n);
+              umma_commit(&empty[n % NS]);
+              if (j + 1 == it.nblk) umma_commit(&qempty[0]);
             }
-          }
-        }
-      }
-    };
-    if (ok && warp_ok && it.direct) {
-      if (nb > 0) {
-        // rows to shared memory (the slot's Q tile is no longer read), 16-byte
-        // units swizzled by the row, then whole rows to global memory
-        const float inv = seen ? 1.0f / l : 0.f;
-        uint8_t* st = qs + slot * kTile;
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          load_o(c, o);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = seen ? pack16<BF16>(o[u * 8 + 2 * e] * inv, o[u * 8 + 2 * e + 1] * inv) : 0u;
-            *reinterpret_cast<uint4*>(st + r * (HD * 2) + (((c / 8 + u) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < it.nblk && ok; ++j) {
+              const int s = j & 1;
+              wait_stage(n);
+              wait_fix(j);
+              wait_p(s);
+              if (!ok) break;
+              tc_fence_after();
+              pv(s, n, j < 2);
+              umma_commit(&empty[n % NS]);
+              ++n;
+              if (j + 2 < it.nblk) {
+                wait_stage(n);
+                if (!ok) break;
+                tc_fence_after();
+                qk(s, n);
+                umma_commit(&empty[n % NS]);
+                if (j + 3 == it.nblk) umma_commit(&qempty[0]);
+                ++n;
+              } else {
+                umma_commit(&ofull[s]);
+              }
+            }
+            n0 += 2 * it.nblk;
           }
         }
         __syncwarp();
-        constexpr int U = HD / 8, RW = 32 / U;  // units per row, rows per pass of the warp
-        uint16_t* out = static_cast<uint16_t*>(p.out) + (TREE ? it.s * p.o_seq : 0);
-        for (int i = 0; i < 32; i += RW) {
-          const int rr = quarter * 32 + i + lane / U, u = lane % U;
-          const int t = it.t0 + (solo ? 0 : slot * p.tpt) + rr / p.group;
-          if (rr < p.group * p.tpt && t < len) {
-            const uint4 w = *reinterpret_cast<const uint4*>(st + rr * (HD * 2) + ((u ^ (rr & 7)) << 4));
-            *reinterpret_cast<uint4*>(out + (p.tok0[it.s] + t) * p.o_tok + (it.g * p.group + rr % p.group) * p.o_head + u * 8) = w;
-          }
-        }
+        idx = next_item(no);
       }
-    } else if (TREE && ok && warp_ok) {
-      // partial of this CTA and slot: (m log2-scaled, l) per row, then o
-      const size_t slab = (static_cast<size_t>(blockIdx.x) * 2 + slot) * kRows + r;
-      if (row_ok) p.part_ml[slab] = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
-      if (nb > 0) {
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          load_o(c, o);
-          if (seen) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + slab * HD + c);
+      // every MMA has completed before TMEM is freed
+      if (lane == 0) {
+        umma_commit(mma_done);
+        if (!mbar_wait(mma_done, 0, kDrainLimitCycles)) report_error(g_status, kErrDrain | kKid | (1 << 13));
+      }
+    } else if (warp == 10) {
+      // ---------------- V blocks made safe ----------------
+      bool ok = true;
+      int n0 = 0, nf = 0;
+      for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
+        const Item it = item_of<TREE>(p, idx);
+        const int fix0 = fix0_of(it);
+        for (int kb = fix0; kb < it.b0 + it.nblk && ok; ++kb, ++nf) {
+          // place in the load order of V block j of the item: K blocks are ahead of their V
+          const int j = kb - it.b0;
+          const int n = n0 + (!solo ? 2 * j + 1 : j <= it.nblk - 2 ? 2 * j + 2 : 2 * it.nblk - 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&vissued[nf % kMaxFix], static_cast<uint32_t>((nf / kMaxFix) & 1)) &&
+                                           mbar_wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1)));
+          if (!ok) {
+            if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (5 << 13));
+            break;
+          }
+          uint8_t* v = ring + (n % NS) * kTile;
+          const int rows = max(0, min(kRows, it.kend - kb * kRows));  // rows that hold keys
+          uint32_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int c = 0; c < kPanels; ++c) {
+            uint8_t* panel = v + c * kPanel;
+            for (int i = lane + rows * 8; i < kRows * 8; i += 32) reinterpret_cast<uint4*>(panel)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
+            for (int i = lane; i < rows * 8; i += 32) {
+              const uint4 x = reinterpret_cast<const uint4*>(panel)[i];
+              acc[0] = probe<BF16>(x.x, acc[0]);
+              acc[1] = probe<BF16>(x.y, acc[1]);
+              acc[2] = probe<BF16>(x.z, acc[2]);
+              acc[3] = probe<BF16>(x.w, acc[3]);
+            }
+          }
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= nonfinite<BF16>(acc[i]) || nonfinite<BF16>(acc[i] >> 16);
+          if (__any_sync(0xffffffffu, bad)) {
+            for (int c = 0; c < kPanels; ++c)
+              for (int i = lane; i < rows * 32; i += 32) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(v + c * kPanel) + i;
+                uint32_t x = *w;
+                if (nonfinite<BF16>(x)) x &= 0xffff0000u;
+                if (nonfinite<BF16>(x >> 16)) x &= 0xffffu;
+                *w = x;
+              }
+            if (lane == 0) dirty[no & 1] = no + 1;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads through the async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vfix[nf % kMaxFix]);
+        }
+        n0 += 2 * it.nblk;
+        idx = next_item(no);
+      }
+    }
+  } else {
+    // ---------------- softmax and epilogue of slot `slot` ----------------
+    regs_inc<kSoftRegs>();
+    const int slot = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int row_tok = r / p.group, row_head = r % p.group;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tS[slot] + lane_off, o_addr = tO[slot] + lane_off;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
+    for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
+      const Item it = item_of<TREE>(p, idx);
+      const int fix0 = fix0_of(it);
+      const int len = p.len[it.s];
+      const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + row_tok;
+      const bool row_ok = row_tok < p.tpt && tok < len;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      unsigned long long anc = 0;
+      if (TREE) {
+        int8_t* mine = parents + warp * kTreeMax;
+        __syncwarp();  // the last item's copy has been read
+        for (int t = lane; t < len; t += 32) {
+          const int up = p.parents[static_cast<size_t>(it.s) * p.width + t];
+          mine[t] = static_cast<int8_t>(up >= -1 && up < t ? up : -2);
+        }
+        __syncwarp();
+        if (row_ok) anc = tree_mask(mine, tok);
+      }
+      const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
+      const int nb = it.n[slot];
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < nb && ok; ++i, ++ns) {
+        const int kb = it.b0 + (solo ? 2 * i + slot : i);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
+        if (!ok) {
+          if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
+          break;
+        }
+        tc_fence_after();
+        if (warp_ok) {
+          float x[kRows];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, x + c * 32);
+          tmem_wait_ld<kRows>(x);
+          if (kb >= fix0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = seen32<TREE>(kb * kRows + c * 32, lim, anc);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[c * 32 + e] = -INFINITY;
+            }
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int e = 4; e < kRows; e += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], e + 4 + q < kRows ? x[e + 4 + q] : x[e + q]);
+          }
+          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (i == 0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, row_ok && (top - m) * sl2 > kStale)) {  // rows without a query have no say
+            // O holds the blocks before this one, whole: S of this block was
+            // issued behind their P.V
+            const float f = top > m ? ex2((m - top) * sl2) : 1.0f;
+            l *= f;
+            m = top;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              tmem_ld32(o_addr + c, o);
+              tmem_wait_ld<32>(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st16(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+              tmem_st16(o_addr + c + 16, reinterpret_cast<const uint32_t*>(o) + 16);
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m * sl2;
+          const F2 sl = pack2(sl2, sl2), ng = pack2(neg, neg);
+          F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              unpack2(fma2(pack2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), sl, ng), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+              w[e] = pack16<BF16>(a, b);
+            }
+            tmem_st16(s_addr + c * 16, w);
+          }
+          float a, b;
+          unpack2(add2(sum[0], sum[1]), a, b);
+          l += a + b;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[slot]);
+      }
+      if (nb > 0 && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot], static_cast<uint32_t>(no_o & 1)));
+        if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (7 << 13));
+        ++no_o;
+        tc_fence_after();
+      }
+      const bool seen = row_ok && (!TREE || anc != 0);  // a draft of a broken chain sees nothing
+      const bool fix = dirty[no & 1] == no + 1;
+      // 32 columns of o from c on, with the infinities and NaNs of the V blocks made safe
+      auto load_o = [&](int c, float* o) {
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld<32>(o);
+        if (fix && seen) {
+          const uint16_t* v =
+              static_cast<const uint16_t*>(p.v) + (TREE ? it.s * p.v_seq : 0) + p.tok0[it.s] * p.v_row + it.g * p.v_head + c;
+          for (int i = 0; i < nb; ++i) {
+            const int kb = it.b0 + (solo ? 2 * i + slot : i);
+            if (kb < fix0) continue;
+            for (int key = kb * kRows; key < min(kb * kRows + kRows, it.kend); ++key) {
+              if (!(seen32<TREE>(key, lim, anc) & 1u)) continue;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint16_t w = v[key * p.v_row + e];
+                if (nonfinite<BF16>(w)) o[e] += widen<BF16>(w);
+              }
+            }
+          }
+        }
+      };
+      if (ok && warp_ok && it.direct) {
+        if (nb > 0) {
+          // a thread writes its row, 16 bytes at a time
+          const float inv = seen ? 1.0f / l : 0.f;
+          uint16_t* out = static_cast<uint16_t*>(p.out) + (TREE ? it.s * p.o_seq : 0) + (p.tok0[it.s] + tok) * p.o_tok +
+                          (it.g * p.group + row_head) * p.o_head;
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            load_o(c, o);
+            if (row_ok) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = seen ? pack16<BF16>(o[u * 8 + 2 * e] * inv, o[u * 8 + 2 * e + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+        }
+      } else if (TREE && ok && warp_ok) {
+        // partial of this item and slot: (m log2-scaled, l) per row, then o
+        const size_t slab = (static_cast<size_t>(idx) * 2 + slot) * kRows + r;
+        if (row_ok) p.part_ml[slab] = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
+        if (nb > 0) {
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            load_o(c, o);
+            if (seen) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + slab * HD + c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
           }
         }
       }
+      tc_fence_before();  // O has been read before the next item's first P allows its P.V
+      idx = next_item(no);
     }
   }
 
@@ -693,16 +809,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 
 // ---- joining the key chunks of a tree ---------------------------------------------
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
 
-// One warp per (drafted row, query head): o = sum_c w_c o_c / sum_c w_c l_c over
-// the row's partials in chunk order, w_c = 2^(m_c - max m).
+// One block per (drafted row, query head): o = sum_c w_c o_c / sum_c w_c l_c
+// over the row's partials, w_c = 2^(m_c - max m). Warp w adds the partials w,
+// w + kMergeWarps, .. in order, then the warps' sums are added in order: the
+// partials' loads are independent, so a row costs a few trips to L2.
 template <bool BF16, int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32) tile_merge_kernel(const __grid_constant__ TileAttnParams p) {
   constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int s = blockIdx.z, t = blockIdx.y, head = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  if (t >= p.len[s] || head >= p.nq) return;
+  __shared__ float so[kMergeWarps][HD], sl[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.z, t = blockIdx.y, head = blockIdx.x;
+  if (t >= p.len[s]) return;
   const int all = (p.pos[s] + p.len[s] + kRows - 1) / kRows, chunks = (all + p.cs - 1) / p.cs;
   if (p.solo ? all == 1 : chunks == 1) return;  // written directly
   const int g = head / p.group, pair = t / (2 * p.tpt), slots = p.solo ? 2 : 1;
@@ -720,25 +839,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tile_merge_kernel(const __gr
     if (ml.y != 0.f) top = fmaxf(top, ml.x);
   }
   top = warp_max(top);
+  if (top == -INFINITY) top = 0.f;
   float l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int c0 = 0; c0 < n; c0 += 32) {
-    float wl = 0.f, ll = 0.f;
-    if (c0 + lane < n) {
-      const float2 ml = p.part_ml[slab(c0 + lane)];
-      ll = ml.y;
-      if (ll != 0.f) wl = ex2(top == -INFINITY ? 0.f : ml.x - top);
-    }
 #pragma unroll 4
-    for (int c = 0; c < min(32, n - c0); ++c) {
-      const float w = __shfl_sync(0xffffffffu, wl, c), lc = __shfl_sync(0xffffffffu, ll, c);
-      if (lc == 0.f) continue;
-      const float* src = p.part_o + slab(c0 + c) * HD + lane * E;
-      l = fmaf(w, lc, l);
+  for (int c = warp; c < n; c += kMergeWarps) {
+    const size_t at = slab(c);
+    const float2 ml = p.part_ml[at];
+    if (ml.y == 0.f) continue;  // nothing seen: o was not written
+    const float w = ex2(ml.x - top);
+    l = fmaf(w, ml.y, l);
+    const float* src = p.part_o + at * HD + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
-    }
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+  if (lane == 0) sl[warp] = l;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    l += sl[w];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += so[w][lane * E + e];
   }
   const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
   uint16_t* out = static_cast<uint16_t*>(p.out) + s * p.o_seq + t * p.o_tok + head * p.o_head + lane * E;
@@ -752,11 +877,17 @@ cudaError_t launch_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
   static std::atomic<int> smem_set[kMaxDevices];
   cudaError_t e = set_smem_attr(kern, Shape<HD>::kSmem, smem_set);
   if (e != cudaSuccess) return e;
+  // the register split draws on what the block is launched with
+  static const int regs = [&] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
   kern<<<static_cast<unsigned>(ctas), kThreads, Shape<HD>::kSmem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !TREE || !p.partials) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.nq + kMergeWarps - 1) / kMergeWarps, p.width, p.n_seqs);
+  cfg.gridDim = dim3(p.nq, p.width, p.n_seqs);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
