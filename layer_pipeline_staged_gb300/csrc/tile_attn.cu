@@ -23,8 +23,8 @@
 // operand of O += P.V, whose B operand is the V block as it lies, keys as rows.
 // TMEM: S0 S1 O0 O1.
 //
-// Warps 0-3 and 4-7: softmax and epilogue of slot 0 and 1. Warp 8: TMA. Warp
-// 9: the MMAs. Warp 10: V blocks that some row does not see whole are made
+// Warps 0-3 and 4-7: softmax and epilogue of slot 0 and 1. Warp 8: TMA. Warps
+// 9 and 11: the MMAs of slot 0 and 1. Warp 10: V blocks that some row does not see whole are made
 // safe before the MMA reads them, as 0 x inf is not 0: rows past the last key
 // become zero, and so do infinities and NaNs, which the epilogue then adds to
 // the rows that do see them (a path that finite inputs never take).
@@ -55,7 +55,7 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;        // rows of a tile (MMA M) and keys of a block (MMA N)
-constexpr int kThreads = 384;     // two softmax warpgroups; TMA, MMA and repair warps, one idle
+constexpr int kThreads = 384;     // two softmax warpgroups; TMA, two MMA and repair warps
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168, what the block is launched with
 constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   uint64_t* next_full = reinterpret_cast<uint64_t*>(answer + 32);  // [2]: an answer is there
   uint64_t* next_empty = next_full + 2;  // [2]: every role has read it
   uint64_t* full = next_empty + 2;
-  uint64_t* empty = full + NS;
+  uint64_t* empty = full + NS;     // both MMA warps are through with the stage
   uint64_t* qfull = empty + NS;    // [2]: a Q tile is there
   uint64_t* qempty = qfull + 2;    // [2]: its last S is made
   uint64_t* sfull = qempty + 2;    // [2]: S of the slot is ready (and its earlier P.V is done)
@@ -331,8 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   uint64_t* ofull = pfull + 2;     // [2]: the slot's last P.V of the item is done
   uint64_t* vfix = ofull + 2;      // [kMaxFix]: the V block is safe to multiply
   uint64_t* vissued = vfix + kMaxFix;  // [kMaxFix]: its copy has been issued (its stage's phase is the current one)
-  uint64_t* mma_done = vissued + kMaxFix;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* mma_done = vissued + kMaxFix;  // [2]
+  uint64_t* turn = mma_done + 2;       // [2]: the slot's turn at the tensor core
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* dirty = reinterpret_cast<int*>(tmem_base + 1);  // [2]: 1 + the last item of that parity with repaired values
   int8_t* parents = reinterpret_cast<int8_t*>(tmem_base + 4);   // [8][kTreeMax], a copy per softmax warp
 
@@ -342,9 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&next_full[i], 1);
-      mbar_init(&next_empty[i], 10);  // eight softmax warps, MMA, repair
+      mbar_init(&next_empty[i], 11);  // eight softmax warps, two MMA, repair
       mbar_init(&qfull[i], 1);
-      mbar_init(&qempty[i], 1);
+      mbar_init(&qempty[i], solo ? 2 : 1);
+      mbar_init(&mma_done[i], 1);
+      mbar_init(&turn[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
       mbar_init(&ofull[i], 1);
@@ -352,13 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);
     }
     for (int i = 0; i < kMaxFix; ++i) {
       mbar_init(&vfix[i], 1);
       mbar_init(&vissued[i], 1);
     }
-    mbar_init(mma_done, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -443,118 +445,116 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           landed &= mbar_wait(&full[m % NS], static_cast<uint32_t>((m / NS) & 1), kDrainLimitCycles);
         if (!landed) report_error(g_status, kErrDrain | kKid);
       }
-    } else if (warp == 9) {
-      // ---------------- MMA ----------------
+    } else if (warp == 9 || warp == 11) {
+      // ---------------- MMA, one warp per slot ----------------
+      // Waits and commits cost an issuing thread hundreds of cycles in a row;
+      // with a warp per slot they pass under the other slot's products.
+      const int slot = warp == 11;
       constexpr uint32_t id_qk = idesc_of(BF16, kRows, false), id_pv = idesc_of(BF16, HD, true);
       bool ok = true;
-      int n0 = 0, nq[2] = {0, 0}, np[2] = {0, 0}, nf = 0;  // stages, Q tiles, P blocks and repaired blocks so far
+      int st = 0, nq = 0, np = 0, nf = 0, nt = 0;  // ring stage; Q tiles, P blocks, repaired blocks and turns so far
+      uint32_t ph = 0;                     // the stage's phase
       for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
         const Item it = item_of<TREE>(p, idx);
         if (lane == 0 && ok) {
-          const int fix0 = fix0_of(it);
+          const int fix0 = fix0_of(it), mine = it.n[slot];
           auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
             if (ok && !mbar_wait(bar, parity)) {
               report_error(g_status, kErrWaitFull | kKid | (what << 13));
               ok = false;
             }
           };
-          auto wait_stage = [&](int n) { wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1), 1); };
-          auto wait_q = [&](int t) { wait(&qfull[t], static_cast<uint32_t>(nq[t]++ & 1), 2); };
-          auto wait_p = [&](int s) { wait(&pfull[s], static_cast<uint32_t>(np[s]++ & 1), 4); };
+          auto advance = [&] {
+            if (++st == NS) st = 0, ph ^= 1;
+          };
+          auto wait_p = [&] { wait(&pfull[slot], static_cast<uint32_t>(np++ & 1), 4); };
           auto wait_fix = [&](int j) {
             if (it.b0 + j < fix0) return;
             wait(&vfix[nf % kMaxFix], static_cast<uint32_t>((nf / kMaxFix) & 1), 3);
             ++nf;
           };
-          auto stage = [&](int n) { return smem_u32(ring + (n % NS) * kTile); };
-          auto qk = [&](int slot, int n) {
-            const uint64_t a = sw128_desc(smem_u32(qs + (solo ? 0 : slot) * kTile)), b = sw128_desc(stage(n));
+          auto skip = [&] {  // a stage that this slot does not use
+            wait(&full[st], ph, 1);
+            if (ok) mbar_arrive(&empty[st]);
+            advance();
+          };
+          auto qk = [&](int stage, bool both) {
+            const uint64_t a = sw128_desc(smem_u32(qs + (solo ? 0 : slot) * kTile)), b = sw128_desc(smem_u32(ring + stage * kTile));
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
               const uint64_t adv = static_cast<uint64_t>((kk / 4) * (kPanel >> 4) + (kk % 4) * 2);
               umma_bf16(tS[slot], a + adv, b + adv, id_qk, kk > 0);
+              if (kk == HD / 32 - 1 && both) mbar_arrive(&turn[slot ^ 1]);
             }
             umma_commit(&sfull[slot]);
           };
-          auto pv = [&](int slot, int n, bool first) {
-            const uint64_t b = sw128_desc_rows(stage(n));
+          auto pv = [&](int stage, bool first) {
+            const uint64_t b = sw128_desc_rows(smem_u32(ring + stage * kTile));
 #pragma unroll
             for (int kk = 0; kk < kRows / 16; ++kk)  // 16 keys on: 8 columns of P, 2048 bytes of V
               umma_ts(tO[slot], tS[slot] + kk * 8, b + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv, !first || kk > 0);
           };
-          if (!solo) {
-            // K0 V0 K1 V1 ..
-            for (int s = 0; s < it.tiles && ok; ++s) {
-              wait_q(s);
-              if (s == 0) wait_stage(n0);
-              if (!ok) break;
-              tc_fence_after();
-              qk(s, n0);
-              if (it.n[s] == 1) umma_commit(&qempty[s]);
+          // Loads come as K0 V0 K1 V1 .. (paired: every slot takes every block) or
+          // K0 K1 V0 K2 V1 K3 .. (solo: slot j & 1 takes block j).
+          const int lead = solo ? 2 : 1;
+          int done = 0;  // of this slot's blocks, those whose S is under way
+          if (solo || mine > 0) wait(&qfull[solo ? 0 : slot], static_cast<uint32_t>(nq++ & 1), 2);
+          for (int j = 0; j < lead && j < it.nblk && ok; ++j) {
+            if (solo ? j != slot : mine == 0) {
+              skip();
+              continue;
             }
-            if (ok) umma_commit(&empty[n0 % NS]);
-            for (int j = 0; j < it.nblk && ok; ++j) {
-              const int nv = n0 + 2 * j + 1, nk = nv + 1;
-              wait_stage(nv);
-              wait_fix(j);
-              bool have_k = false;
-              for (int s = 0; s < 2 && ok; ++s) {
-                if (j >= it.n[s]) continue;
-                wait_p(s);
-                if (!ok) break;
-                tc_fence_after();
-                pv(s, nv, j == 0);
-                if (j + 1 < it.n[s]) {
-                  if (!have_k) wait_stage(nk);
-                  have_k = true;
-                  if (!ok) break;
-                  tc_fence_after();
-                  qk(s, nk);
-                  if (j + 2 == it.n[s]) umma_commit(&qempty[s]);
-                } else {
-                  umma_commit(&ofull[s]);
-                }
-              }
-              if (!ok) break;
-              umma_commit(&empty[nv % NS]);
-              if (j + 1 < it.nblk) umma_commit(&empty[nk % NS]);
+            wait(&full[st], ph, 1);
+            if (!ok) break;
+            tc_fence_after();
+            qk(st, false);
+            umma_commit(&empty[st]);
+            advance();
+            if (++done == mine) umma_commit(&qempty[solo ? 0 : slot]);
+          }
+          if (solo && mine == 0 && ok) mbar_arrive(&qempty[0]);
+          for (int j = 0; j < it.nblk && ok; ++j) {
+            const bool has_k = j + lead < it.nblk;
+            if (solo ? (j & 1) != slot : j >= mine) {
+              skip();
+              if (it.b0 + j >= fix0) ++nf;
+              if (has_k) skip();
+              continue;
             }
-            n0 += 2 * it.nblk;
-          } else {
-            // K0 K1 V0 K2 V1 K3 ..; slot j & 1 takes block j
-            int n = n0;
-            wait_q(0);
-            for (int j = 0; j < 2 && j < it.nblk && ok; ++j, ++n) {
-              wait_stage(n);
-              if (!ok) break;
-              tc_fence_after();
-              qk(j, n);
-              umma_commit(&empty[n % NS]);
-              if (j + 1 == it.nblk) umma_commit(&qempty[0]);
+            const int sv = st;
+            wait(&full[st], ph, 1);
+            wait_fix(j);
+            advance();
+            const bool more = done < mine;  // another S of this slot behind this P.V
+            const int sk = st;
+            if (more) {
+              wait(&full[st], ph, 1);
+              advance();
             }
-            for (int j = 0; j < it.nblk && ok; ++j) {
-              const int s = j & 1;
-              wait_stage(n);
-              wait_fix(j);
-              wait_p(s);
-              if (!ok) break;
-              tc_fence_after();
-              pv(s, n, j < 2);
-              umma_commit(&empty[n % NS]);
-              ++n;
-              if (j + 2 < it.nblk) {
-                wait_stage(n);
-                if (!ok) break;
-                tc_fence_after();
-                qk(s, n);
-                umma_commit(&empty[n % NS]);
-                if (j + 3 == it.nblk) umma_commit(&qempty[0]);
-                ++n;
-              } else {
-                umma_commit(&ofull[s]);
-              }
+            wait_p();
+            // The slots take turns at the tensor core, so that they stay half an
+            // iteration apart: left to themselves they fall into step, both
+            // in their softmax, then both waiting for it. The turn is handed
+            // on in the middle of S, to cover the time it takes to arrive.
+            const bool both = !solo && j < it.n[slot ^ 1];
+            if (both) {
+              if (slot == 1 || nt > 0) wait(&turn[slot], static_cast<uint32_t>((slot == 1 ? nt : nt - 1) & 1), 8);
+              ++nt;
             }
-            n0 += 2 * it.nblk;
+            if (!ok) break;
+            tc_fence_after();
+            pv(sv, j < lead);
+            if (more) {
+              qk(sk, both);
+              if (++done == mine) umma_commit(&qempty[solo ? 0 : slot]);
+              umma_commit(&empty[sv]);
+              umma_commit(&empty[sk]);
+            } else {
+              if (both) mbar_arrive(&turn[slot ^ 1]);
+              umma_commit(&ofull[slot]);
+              umma_commit(&empty[sv]);
+              if (has_k) skip();
+            }
           }
         }
         __syncwarp();
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       }
       // every MMA has completed before TMEM is freed
       if (lane == 0) {
-        umma_commit(mma_done);
-        if (!mbar_wait(mma_done, 0, kDrainLimitCycles)) report_error(g_status, kErrDrain | kKid | (1 << 13));
+        umma_commit(&mma_done[slot]);
+        if (!mbar_wait(&mma_done[slot], 0, kDrainLimitCycles)) report_error(g_status, kErrDrain | kKid | (1 << 13));
       }
     } else if (warp == 10) {
       // ---------------- V blocks made safe ----------------
