@@ -490,7 +490,7 @@ long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n
  *     captured call replays with the values it was captured with;
  *   - a call runs on the calling thread's current device, in `stream` (NULL:
  *     the default stream), returns once enqueued and allocates nothing. Calls
- *     may overlap as long as their outputs and workspaces do not;
+ *     may overlap as long as their outputs do not;
  *   - an error is LPS_EINVAL (nothing enqueued) or LPS_ECUDA, with
  *     last_error_string() naming it. */
 #define LPS_TYPE_BF16 0
@@ -524,21 +524,13 @@ int attention_prompt_packed(const void* q, const void* k, const void* v, void* o
  *   parents  device int32[batch][width]; the drafts of a chain that holds a
  *            parent outside [-1, t) get zeros
  *   strides  host int64[6]: batch, token and head stride of q, then of out; NULL: dense
- *   workspace  device memory of attention_tree_workspace_bytes() bytes for the
- *            same arguments, 16-byte aligned, used until the call's work has run
  * batch is 1..256, width 1..64. rows of 1 with a parent of -1 is a decode step.
  * Cache rows at and after pos[b] + rows[b] change nothing, whatever they hold.
- * LPS_EINVAL for bad arguments or a workspace that is too small. */
+ * LPS_EINVAL for bad arguments. */
 int attention_tree_verify(const void* q, const void* k_cache, const void* v_cache, void* out, int type, int batch,
                           int width, const int32_t* pos, const int32_t* rows, const int32_t* parents, int n_q_heads,
                           int n_kv_heads, int head_dim, int max_ctx, const int64_t* strides, float scale,
-                          void* workspace, size_t workspace_bytes, void* stream);
-
-/* The workspace attention_tree_verify needs for these arguments on the current
- * device (0 where it needs none), or -1 for arguments it refuses or without a
- * device. Launches nothing. */
-long long attention_tree_workspace_bytes(int batch, int width, const int32_t* pos, const int32_t* rows, int n_q_heads,
-                                         int n_kv_heads, int head_dim);
+                          void* stream);
 
 /* Key and value rows of packed tokens into the cache: token i of sequence s
  * (tokens offsets[s] .. offsets[s + 1] - 1) goes to row start[s] + i of cache

@@ -39,7 +39,7 @@ EXPORTS = (
     "model_time_kernel", "model_kernel_time", "model_set_serial_steps", "attention_decode_noalloc", "attention_decode_noalloc_error",
     "attention_decode_noalloc_scratch_bytes", "model_trace_enable", "model_trace_read", "model_trace_disable",
     "stage_plan_solve", "model_stage_bytes", "model_set_wait_limit", "attention_decode_noalloc_status",
-    "model_prefill", "attention_prompt_packed", "attention_tree_verify", "attention_tree_workspace_bytes",
+    "model_prefill", "attention_prompt_packed", "attention_tree_verify",
     "kv_rows_append", "kv_rows_accept", "cache_ops_status",
 )
 
@@ -133,8 +133,7 @@ def load(path: str = LIB_PATH):
         "attention_decode_noalloc_status": (i, [vp]),
         "attention_decode_noalloc_scratch_bytes": (ctypes.c_longlong, [i, i, i, i, i]),
         "attention_prompt_packed": (i, [vp, vp, vp, vp, i, i, vp, i, i, i, vp, f, vp]),
-        "attention_tree_verify": (i, [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, vp, f, vp, ctypes.c_size_t, vp]),
-        "attention_tree_workspace_bytes": (ctypes.c_longlong, [i, i, vp, vp, i, i, i]),
+        "attention_tree_verify": (i, [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, vp, f, vp]),
         "kv_rows_append": (i, [vp, vp, i, vp, vp, vp, vp, i, i, i, vp, vp]),
         "cache_ops_status": (i, [vp]),
         "kv_rows_accept": (i, [vp, vp, i, i, i, i, i, vp, i, vp, vp, vp]),

@@ -98,16 +98,6 @@ bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device's SM count, or -1.
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  return n;
-}
-
 constexpr float kLog2e = 1.44269504088896340736f;
 
 int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
@@ -157,7 +147,7 @@ extern "C" int attention_prompt_packed(const void* q, const void* k, const void*
           !encode4(&p.tmap_k, bf16, k, head_dim, {tokens, n_kv_heads, 1}, {st[2], st[3], 0}, 128, 1) ||
           !encode4(&p.tmap_v, bf16, v, head_dim, {tokens, n_kv_heads, 1}, {st[4], st[5], 0}, 128, 1))
         return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
-      const cudaError_t e = launch_tile_attn(p, ctas, bf16, head_dim, false, static_cast<cudaStream_t>(stream));
+      const cudaError_t e = launch_tile_prompt(p, ctas, bf16, head_dim, static_cast<cudaStream_t>(stream));
       if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     }
     return LPS_OK;
@@ -175,33 +165,12 @@ int check_tree(const char* fn, int batch, int width, const int32_t* pos, const i
   }
   return LPS_OK;
 }
-
-void tree_shape(TileAttnParams& p, int batch, int width, const int32_t* pos, const int32_t* rows, int nq, int nkv) {
-  p.n_seqs = batch;
-  p.width = width;
-  p.nq = nq, p.nkv = nkv, p.group = nq / nkv;
-  for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
-}
 }  // namespace
-
-extern "C" long long attention_tree_workspace_bytes(int batch, int width, const int32_t* pos, const int32_t* rows,
-                                                    int n_q_heads, int n_kv_heads, int head_dim) {
-  static const char* FN = "attention_tree_workspace_bytes";
-  if (!pos || !rows || check_heads(FN, LPS_TYPE_BF16, n_q_heads, n_kv_heads, head_dim) ||
-      check_tree(FN, batch, width, pos, rows, 0x7fffffff))
-    return -1;
-  const int sms = num_sms();
-  if (sms < 1) return -1;
-  TileAttnParams p{};
-  tree_shape(p, batch, width, pos, rows, n_q_heads, n_kv_heads);
-  return static_cast<long long>(tile_tree_workspace(p, tile_tree_plan(p, sms), head_dim));
-}
 
 extern "C" int attention_tree_verify(const void* q, const void* k_cache, const void* v_cache, void* out, int type,
                                      int batch, int width, const int32_t* pos, const int32_t* rows,
                                      const int32_t* parents, int n_q_heads, int n_kv_heads, int head_dim, int max_ctx,
-                                     const int64_t* strides, float scale, void* workspace, size_t workspace_bytes,
-                                     void* stream) {
+                                     const int64_t* strides, float scale, void* stream) {
   static const char* FN = "attention_tree_verify";
   return guarded(FN, [&]() -> int {
     if (!q || !k_cache || !v_cache || !out || !pos || !rows || !parents)
@@ -215,17 +184,17 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     if ((rc = check_strides(FN, st, 6, head_dim))) return rc;
     if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out))
       return host_fail(LPS_EINVAL, FN, "q, the caches and out must be 16-byte aligned");
-    const int sms = num_sms();
-    if (sms < 1) return host_fail(LPS_ECUDA, FN, "no usable current device");
+    const bool bf16 = type == LPS_TYPE_BF16;
     TileAttnParams p{};
-    tree_shape(p, batch, width, pos, rows, n_q_heads, n_kv_heads);
-    const long long ctas = tile_tree_plan(p, sms);
-    const size_t need = tile_tree_workspace(p, ctas, head_dim);
-    if (need && (!workspace || workspace_bytes < need || misaligned(workspace)))
-      return host_fail(LPS_EINVAL, FN, "needs a 16-byte aligned workspace of " + std::to_string(need) + " bytes");
+    p.n_seqs = batch;
+    p.width = width;
+    p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+    for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
+    long long ctas = 0;
+    cudaError_t e = tile_tree_plan(p, bf16, head_dim, &ctas);
+    if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("plan: ") + cudaGetErrorString(e));
     if (ctas == 0) return LPS_OK;
     if (ctas > 0x7fffffffll) return host_fail(LPS_EINVAL, FN, "too many rows for one launch");
-    if (need) tile_tree_set_workspace(p, ctas, workspace);
     p.q = q, p.k = k_cache, p.v = v_cache, p.out = out;
     p.q_seq = st[0], p.q_tok = st[1], p.q_head = st[2], p.o_seq = st[3], p.o_tok = st[4], p.o_head = st[5];
     p.k_row = p.v_row = head_dim;
@@ -233,13 +202,12 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     p.k_seq = p.v_seq = p.k_head * n_kv_heads;
     p.parents = parents;
     p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
-    const bool bf16 = type == LPS_TYPE_BF16;
     const long long kv_n[3] = {max_ctx, n_kv_heads, batch}, kv_st[3] = {p.k_row, p.k_head, p.k_seq};
     if (!encode4(&p.tmap_q, bf16, q, head_dim, {n_q_heads, width, batch}, {st[2], st[1], st[0]}, p.group, p.tpt) ||
         !encode4(&p.tmap_k, bf16, k_cache, head_dim, kv_n, kv_st, 128, 1) ||
         !encode4(&p.tmap_v, bf16, v_cache, head_dim, kv_n, kv_st, 128, 1))
       return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
-    const cudaError_t e = launch_tile_attn(p, ctas, bf16, head_dim, true, static_cast<cudaStream_t>(stream));
+    e = launch_tile_tree(p, ctas, bf16, head_dim, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     return LPS_OK;
   });

@@ -39,18 +39,15 @@ struct TileAttnParams {
   // set by the plan
   int tpt;             // tokens of a tile: 128 / group
   int solo;            // tree: one tile, its key blocks dealt to the two slots
-  int cs;              // tree: key blocks per CTA
-  int partials;        // tree: some sequence goes through the workspace
-  float2* part_ml;     // [CTAs][2][128] (log2-domain base, sum of weights)
-  float* part_o;       // [CTAs][2][128][hd]
-  int item0[kOpSeqs];  // first work item of each sequence; an item is nkv CTAs
+  int cluster;         // tree: CTAs that share a sequence's keys
+  int item0[kOpSeqs];  // first work item of each sequence; an item is nkv CTAs (tree: clusters)
 };
-// Set the plan and return the launch's CTAs (0: nothing to do).
+// Set the plan (which puts the longest sequences first) and the launch's CTAs
+// (0: nothing to do). A tree's tok0 becomes the sequences' places in the batch.
 long long tile_prompt_plan(TileAttnParams& p);
-long long tile_tree_plan(TileAttnParams& p, int num_sms);
-size_t tile_tree_workspace(const TileAttnParams& p, long long ctas, int hd);
-void tile_tree_set_workspace(TileAttnParams& p, long long ctas, void* ws);
-cudaError_t launch_tile_attn(const TileAttnParams& p, long long ctas, bool bf16, int hd, bool tree, cudaStream_t s);
+cudaError_t tile_tree_plan(TileAttnParams& p, bool bf16, int hd, long long* ctas);
+cudaError_t launch_tile_prompt(const TileAttnParams& p, long long ctas, bool bf16, int hd, cudaStream_t s);
+cudaError_t launch_tile_tree(const TileAttnParams& p, long long ctas, bool bf16, int hd, cudaStream_t s);
 // Synchronize the stream, then read and clear the kernels' status words.
 cudaError_t tile_attn_status(int* status, cudaStream_t s);
 

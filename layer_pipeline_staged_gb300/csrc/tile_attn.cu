@@ -16,7 +16,7 @@
 //   - paired: two neighbouring tiles over the same key blocks (prompts, and
 //     trees of more than 128 rows);
 //   - solo (trees of up to 128 rows): the one tile over the even and over the
-//     odd key blocks; the two halves are joined like any two key chunks.
+//     odd key blocks; the two halves are joined at the end.
 // Per 128-key block and slot: S = Q.K^T (both operands in shared memory,
 // 128-byte swizzle, as TMA wrote them) into 128 TMEM columns; four warps read
 // a row per thread, make the weights, and write them back over S as the A
@@ -29,14 +29,14 @@
 // become zero, and so do infinities and NaNs, which the epilogue then adds to
 // the rows that do see them (a path that finite inputs never take).
 //
-// A CTA stays on its SM: once the copies of its item are issued, its TMA lane
+// A prompt's CTA stays on its SM: once the copies of its item are issued, its TMA lane
 // takes over the next CTA of the grid that has not started
 // (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first
 // S is made, while the last item's softmax and epilogue still run. The grid is
 // ordered from the largest item to the smallest.
 //
-// Trees split the keys into chunks of `cs` blocks, one CTA each, which leave
-// (o, m, l) in the workspace for the merge kernel; prompts are whole.
+// A tree's keys are shared out over a thread-block cluster, whose CTAs join
+// their (o, m, l) through distributed shared memory; a prompt tile's are not.
 // Every sum has one order given by the shapes, so equal calls give equal bits.
 // Waits are bounded and report through the status word.
 #include <cuda_bf16.h>
@@ -60,6 +60,8 @@ constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168, what
 constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
+constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
+constexpr int kMaxCluster = 1 << (kClusterSizes - 1);
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
 constexpr int kKid = kKidTileAttn << 8;
 
@@ -80,6 +82,10 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x,
           "r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // D[tmem] (+)= A[tmem] . B, B in shared memory.
@@ -232,6 +238,24 @@ __device__ __forceinline__ int taken(const void* answer) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before a later answer is written there
   return ok ? static_cast<int>(x) : -1;
 }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 peer_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -251,14 +275,14 @@ struct Item {
   int tiles;         // tiles with rows (1 or 2)
   int clean;         // keys [0, clean) are seen by every row of the item
   int kend;          // keys at and after kend are seen by none
-  bool direct;       // out is written here (else: a partial)
 };
 
 template <bool TREE>
 __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
   Item it;
-  const int w = idx / p.nkv;
-  it.g = idx - w * p.nkv;
+  const int rank = TREE ? idx % p.cluster : 0, unit = TREE ? idx / p.cluster : idx;
+  const int w = unit / p.nkv;
+  it.g = unit - w * p.nkv;
   int lo = 0, hi = p.n_seqs - 1;  // the last s with item0[s] <= w
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -277,19 +301,16 @@ __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
     it.tiles = endB > endA ? 2 : 1;
     it.clean = it.t0 + 1;
     it.kend = endB;
-    it.direct = true;
   } else {
-    const int all = (p.pos[lo] + len + kRows - 1) / kRows, chunks = (all + p.cs - 1) / p.cs;
-    const int pair = off / chunks, c = off - pair * chunks;
-    it.t0 = pair * span;
-    it.b0 = c * p.cs;
-    it.nblk = min(p.cs, all - it.b0);
-    it.tiles = !p.solo && it.t0 + p.tpt < len ? 2 : 1;
+    const int all = (p.pos[lo] + len + kRows - 1) / kRows;  // fewer than 2^24, so rank * all fits
+    it.t0 = off * span;
+    it.b0 = rank * all / p.cluster;
+    it.nblk = (rank + 1) * all / p.cluster - it.b0;  // may be none
+    it.tiles = it.nblk == 0 ? 0 : !p.solo && it.t0 + p.tpt < len ? 2 : 1;
     it.n[0] = p.solo ? (it.nblk + 1) / 2 : it.nblk;
     it.n[1] = p.solo ? it.nblk / 2 : it.tiles == 2 ? it.nblk : 0;
     it.clean = p.pos[lo];
     it.kend = p.pos[lo] + len;
-    it.direct = p.solo ? all == 1 : chunks == 1;
   }
   return it;
 }
@@ -309,6 +330,58 @@ __device__ __forceinline__ uint32_t seen32(int kw, int lim, unsigned long long a
     }
   }
   return bits;
+}
+
+// The weight of a part with (base, sum of weights) ml in a join whose largest
+// base is top: 0 where the part saw nothing, NaN where its sum is NaN.
+__device__ __forceinline__ float weight_of(float2 ml, float top) {
+  if (ml.y == 0.f) return 0.f;
+  return ml.y != ml.y ? ml.y : ex2(ml.x - top);
+}
+
+// One row's join over a cluster's C CTAs in order, 8 columns (a unit) at a time
+// from unit u0 on: o = sum_c w_c o_c / sum_c w_c l_c, w_c = 2^(m_c - max m). All
+// loads of a unit are issued before the first is used: a trip to another CTA's
+// shared memory takes some 200 ns, and one per part and unit in turn took 3.5
+// of a call's 14 us.
+template <bool BF16, int HD, int C>
+__device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t* out, int u0, int step) {
+  float2 ml[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) ml[c] = peer_ld2(peer_smem(ml_at, c));
+  for (int u = u0; u < HD / 8; u += step) {
+    float4 x[C], y[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t at = peer_smem(o_at + 2 * u * kRows * 16, c);
+      x[c] = peer_ld4(at);
+      y[c] = peer_ld4(at + kRows * 16);
+    }
+    float top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (ml[c].y != 0.f) top = fmaxf(top, ml[c].x);
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float w = weight_of(ml[c], top);
+      if (w != 0.f) {  // a part that saw nothing has left no o
+        l = fmaf(w, ml[c].y, l);
+        o[0] = fmaf(w, x[c].x, o[0]);
+        o[1] = fmaf(w, x[c].y, o[1]);
+        o[2] = fmaf(w, x[c].z, o[2]);
+        o[3] = fmaf(w, x[c].w, o[3]);
+        o[4] = fmaf(w, y[c].x, o[4]);
+        o[5] = fmaf(w, y[c].y, o[5]);
+        o[6] = fmaf(w, y[c].z, o[6]);
+        o[7] = fmaf(w, y[c].w, o[7]);
+      }
+    }
+    const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
+    *reinterpret_cast<uint4*>(out + u * 8) =
+        make_uint4(pack16<BF16>(o[0] * inv, o[1] * inv), pack16<BF16>(o[2] * inv, o[3] * inv),
+                   pack16<BF16>(o[4] * inv, o[5] * inv), pack16<BF16>(o[6] * inv, o[7] * inv));
+  }
 }
 
 template <bool BF16, int HD, bool TREE>
@@ -340,6 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool solo = TREE && p.solo;
 
+  if (tid == 32 * 8) {
+    prefetch_map(&p.tmap_q);
+    prefetch_map(&p.tmap_k);
+    prefetch_map(&p.tmap_v);
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&next_full[i], 1);
@@ -372,7 +450,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tbase = *tmem_base;
   const uint32_t tS[2] = {tbase, tbase + 128}, tO[2] = {tbase + 256, tbase + 256 + HD};
-  if (TREE) pdl_launch_dependents();
+  // A tree's result is joined over its cluster (and over the two slots).
+  const bool joined = TREE && (solo || p.cluster > 1);
+  // After the last product the ring holds what is joined: o [tile][HD / 4][128]
+  // float4 columns of rows, the slots' exchange in the second tile's place, and
+  // (log2-scaled base, sum of weights) of each slot and of each tile's joined row.
+  float4* const join_o = reinterpret_cast<float4*>(ring);
+  float4* const swap_o = join_o + HD / 4 * kRows;
+  float2* const swap_ml = reinterpret_cast<float2*>(ring + 2 * kRows * HD * 4);
+  float2* const join_ml = swap_ml + 2 * kRows;
+  static_assert(2 * kRows * HD * 4 + 4 * kRows * 8 <= NS * kTile, "the join fits the ring");
 
   // first block of an item that some row does not see whole
   auto fix0_of = [](const Item& it) { return max(it.b0, it.clean / kRows); };
@@ -402,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         for (int idx = blockIdx.x, no = 0; idx >= 0 && ok; ++no) {
           const Item it = item_of<TREE>(p, idx);
           const int fix0 = fix0_of(it);
-          const int tb = p.tok0[it.s], seq = TREE ? it.s : 0;
+          const int tb = TREE ? 0 : p.tok0[it.s], seq = TREE ? p.tok0[it.s] : 0;
           auto load = [&](const CUtensorMap* map, int j) {
             const int st = n % NS;
             if (n >= NS) wait(&empty[st], static_cast<uint32_t>((n / NS - 1) & 1));
@@ -428,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[nf++ % kMaxFix]);
             if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
           }
-          if (!ok) break;
+          if (TREE || !ok) break;
           const int slot = no & 1;
           if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
           if (!ok) break;
@@ -498,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           // K0 K1 V0 K2 V1 K3 .. (solo: slot j & 1 takes block j).
           const int lead = solo ? 2 : 1;
           int done = 0;  // of this slot's blocks, those whose S is under way
-          if (solo || mine > 0) wait(&qfull[solo ? 0 : slot], static_cast<uint32_t>(nq++ & 1), 2);
+          if (it.tiles > (solo ? 0 : slot)) wait(&qfull[solo ? 0 : slot], static_cast<uint32_t>(nq++ & 1), 2);
           for (int j = 0; j < lead && j < it.nblk && ok; ++j) {
             if (solo ? j != slot : mine == 0) {
               skip();
@@ -558,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           }
         }
         __syncwarp();
-        idx = next_item(no);
+        idx = TREE ? -1 : next_item(no);
       }
       // every MMA has completed before TMEM is freed
       if (lane == 0) {
@@ -617,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&vfix[nf % kMaxFix]);
         }
         n0 += 2 * it.nblk;
-        idx = next_item(no);
+        idx = TREE ? -1 : next_item(no);
       }
     }
   } else {
@@ -643,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         int8_t* mine = parents + warp * kTreeMax;
         __syncwarp();  // the last item's copy has been read
         for (int t = lane; t < len; t += 32) {
-          const int up = p.parents[static_cast<size_t>(it.s) * p.width + t];
+          const int up = p.parents[static_cast<size_t>(p.tok0[it.s]) * p.width + t];
           mine[t] = static_cast<int8_t>(up >= -1 && up < t ? up : -2);
         }
         __syncwarp();
@@ -740,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         tmem_wait_ld<32>(o);
         if (fix && seen) {
           const uint16_t* v =
-              static_cast<const uint16_t*>(p.v) + (TREE ? it.s * p.v_seq : 0) + p.tok0[it.s] * p.v_row + it.g * p.v_head + c;
+              static_cast<const uint16_t*>(p.v) + p.tok0[it.s] * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head + c;
           for (int i = 0; i < nb; ++i) {
             const int kb = it.b0 + (solo ? 2 * i + slot : i);
             if (kb < fix0) continue;
@@ -755,11 +842,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           }
         }
       };
-      if (ok && warp_ok && it.direct) {
+      if (ok && warp_ok && !joined) {
         if (nb > 0) {
           // a thread writes its row, 16 bytes at a time
           const float inv = seen ? 1.0f / l : 0.f;
-          uint16_t* out = static_cast<uint16_t*>(p.out) + (TREE ? it.s * p.o_seq : 0) + (p.tok0[it.s] + tok) * p.o_tok +
+          uint16_t* out = static_cast<uint16_t*>(p.out) + p.tok0[it.s] * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
 #pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
@@ -777,26 +864,93 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             }
           }
         }
-      } else if (TREE && ok && warp_ok) {
-        // partial of this item and slot: (m log2-scaled, l) per row, then o
-        const size_t slab = (static_cast<size_t>(idx) * 2 + slot) * kRows + r;
-        if (row_ok) p.part_ml[slab] = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
-        if (nb > 0) {
+      } else if (TREE && joined) {
+        // the ring is free once the other slot's products are done too
+        if (ok && it.n[slot ^ 1] > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot ^ 1], 0));
+          if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
+        }
+        const bool here = ok && warp_ok && nb > 0;  // this warp has sums
+        const float2 ml = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
+        if (!solo) {
+          join_ml[slot * kRows + r] = ml;
+          if (here) {
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            load_o(c, o);
-            if (seen) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + slab * HD + c);
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              load_o(c, o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 8; ++e)
+                join_o[(slot * (HD / 4) + c / 4 + e) * kRows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        } else {
+          // each slot joins one half of the columns and hands the other half over
+          swap_ml[slot * kRows + r] = ml;
+          const int mine = slot * (HD / 2), other = HD / 2 - mine;
+          if (here) {
+#pragma unroll 1
+            for (int c = 0; c < HD / 2; c += 32) {
+              float o[32];
+              load_o(other + c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                swap_o[((other + c) / 4 + e) * kRows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          named_bar_sync(1, 256);
+          const float2 to = swap_ml[(slot ^ 1) * kRows + r];
+          const float top = fmaxf(ml.y != 0.f ? ml.x : -INFINITY, to.y != 0.f ? to.x : -INFINITY);
+          const float fm = weight_of(ml, top), ft = weight_of(to, top);
+          if (slot == 0) join_ml[r] = make_float2(top, fm * ml.y + ft * to.y);
+          if (ok && warp_ok) {
+#pragma unroll 1
+            for (int c = 0; c < HD / 2; c += 32) {
+              float o[32];
+              if (nb > 0) load_o(mine + c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int at = ((mine + c) / 4 + e) * kRows + r;
+                float4 x = ft != 0.f ? swap_o[at] : make_float4(0.f, 0.f, 0.f, 0.f);
+                x.x = fm != 0.f ? fmaf(fm, o[4 * e], ft * x.x) : ft * x.x;
+                x.y = fm != 0.f ? fmaf(fm, o[4 * e + 1], ft * x.y) : ft * x.y;
+                x.z = fm != 0.f ? fmaf(fm, o[4 * e + 2], ft * x.z) : ft * x.z;
+                x.w = fm != 0.f ? fmaf(fm, o[4 * e + 3], ft * x.w) : ft * x.w;
+                join_o[at] = x;
+              }
             }
           }
         }
       }
       tc_fence_before();  // O has been read before the next item's first P allows its P.V
-      idx = next_item(no);
+      idx = TREE ? -1 : next_item(no);
     }
+  }
+
+  if (TREE && joined) {
+    // every CTA of the cluster joins its share of the columns
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8) {
+      const Item it = item_of<TREE>(p, blockIdx.x);
+      const int half = tid >> 7, r = tid & 127, tile = solo ? 0 : half;
+      const int tok = it.t0 + tile * p.tpt + r / p.group;
+      if (r / p.group < p.tpt && tok < p.len[it.s]) {
+        const uint32_t ml_at = smem_u32(join_ml + tile * kRows + r), o_at = smem_u32(join_o + tile * (HD / 4) * kRows + r);
+        uint16_t* out = static_cast<uint16_t*>(p.out) + p.tok0[it.s] * p.o_seq + tok * p.o_tok +
+                        (it.g * p.group + r % p.group) * p.o_head;
+        const int u0 = blockIdx.x % p.cluster + (solo ? half * p.cluster : 0), step = solo ? 2 * p.cluster : p.cluster;
+        switch (p.cluster) {
+          case 1: join_row<BF16, HD, 1>(ml_at, o_at, out, u0, step); break;
+          case 2: join_row<BF16, HD, 2>(ml_at, o_at, out, u0, step); break;
+          case 4: join_row<BF16, HD, 4>(ml_at, o_at, out, u0, step); break;
+          case 8: join_row<BF16, HD, 8>(ml_at, o_at, out, u0, step); break;
+          default: join_row<BF16, HD, 16>(ml_at, o_at, out, u0, step); break;
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the cluster's shared memory has been read
   }
 
   tc_fence_before();
@@ -807,72 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   }
 }
 
-// ---- joining the key chunks of a tree ---------------------------------------------
-
-constexpr int kMergeWarps = 4;
-
-// One block per (drafted row, query head): o = sum_c w_c o_c / sum_c w_c l_c
-// over the row's partials, w_c = 2^(m_c - max m). Warp w adds the partials w,
-// w + kMergeWarps, .. in order, then the warps' sums are added in order: the
-// partials' loads are independent, so a row costs a few trips to L2.
-template <bool BF16, int HD>
-__global__ void __launch_bounds__(kMergeWarps * 32) tile_merge_kernel(const __grid_constant__ TileAttnParams p) {
-  constexpr int E = HD / 32;
-  __shared__ float so[kMergeWarps][HD], sl[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = blockIdx.z, t = blockIdx.y, head = blockIdx.x;
-  if (t >= p.len[s]) return;
-  const int all = (p.pos[s] + p.len[s] + kRows - 1) / kRows, chunks = (all + p.cs - 1) / p.cs;
-  if (p.solo ? all == 1 : chunks == 1) return;  // written directly
-  const int g = head / p.group, pair = t / (2 * p.tpt), slots = p.solo ? 2 : 1;
-  const int slot0 = p.solo ? 0 : (t / p.tpt) & 1;
-  const int r = (t - (p.solo ? 0 : (2 * pair + slot0) * p.tpt)) * p.group + head % p.group;
-  const int w0 = p.item0[s] + pair * chunks, n = chunks * slots;
-  auto slab = [&](int c) {
-    const int chunk = c / slots, slot = slot0 + c % slots;
-    return ((static_cast<size_t>(w0 + chunk) * p.nkv + g) * 2 + slot) * kRows + r;
-  };
-  pdl_wait();
-  float top = -INFINITY;
-  for (int c = lane; c < n; c += 32) {
-    const float2 ml = p.part_ml[slab(c)];
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
-  }
-  top = warp_max(top);
-  if (top == -INFINITY) top = 0.f;
-  float l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int c = warp; c < n; c += kMergeWarps) {
-    const size_t at = slab(c);
-    const float2 ml = p.part_ml[at];
-    if (ml.y == 0.f) continue;  // nothing seen: o was not written
-    const float w = ex2(ml.x - top);
-    l = fmaf(w, ml.y, l);
-    const float* src = p.part_o + at * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-  if (lane == 0) sl[warp] = l;
-  __syncthreads();
-  if (warp) return;
-#pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) {
-    l += sl[w];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += so[w][lane * E + e];
-  }
-  const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
-  uint16_t* out = static_cast<uint16_t*>(p.out) + s * p.o_seq + t * p.o_tok + head * p.o_head + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack16<BF16>(o[e] * inv, o[e + 1] * inv);
-}
-
 template <bool BF16, int HD, bool TREE>
-cudaError_t launch_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
+cudaError_t prepare_t() {
   auto kern = tile_attn_kernel<BF16, HD, TREE>;
   static std::atomic<int> smem_set[kMaxDevices];
   cudaError_t e = set_smem_attr(kern, Shape<HD>::kSmem, smem_set);
@@ -882,108 +972,163 @@ cudaError_t launch_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
     cudaFuncAttributes a{};
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
-  if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  kern<<<static_cast<unsigned>(ctas), kThreads, Shape<HD>::kSmem, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !TREE || !p.partials) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.nq, p.width, p.n_seqs);
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<BF16, HD>, p);
+  return regs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
 }
 
-template <bool BF16>
-cudaError_t launch_hd(const TileAttnParams& p, long long ctas, int hd, bool tree, cudaStream_t s) {
-  if (hd == 128) return tree ? launch_t<BF16, 128, true>(p, ctas, s) : launch_t<BF16, 128, false>(p, ctas, s);
-  return tree ? launch_t<BF16, 64, true>(p, ctas, s) : launch_t<BF16, 64, false>(p, ctas, s);
+template <bool BF16, int HD>
+cudaLaunchConfig_t tree_config(int cluster, long long ctas, cudaStream_t s, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<HD>::kSmem;
+  cfg.stream = s;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of 2^i CTAs that run at once on the current device (0: none do).
+template <bool BF16, int HD>
+cudaError_t active_t(const int** out) {
+  static int active[kMaxDevices][kClusterSizes];
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!known[dev].load(std::memory_order_acquire)) {
+    auto kern = tile_attn_kernel<BF16, HD, true>;
+    if ((e = prepare_t<BF16, HD, true>()) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+    int got[kClusterSizes];
+    for (int i = 0; i < kClusterSizes; ++i) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t cfg = tree_config<BF16, HD>(1 << i, 1 << i, nullptr, &attr);
+      got[i] = 0;
+      if (cudaOccupancyMaxActiveClusters(&got[i], kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        got[i] = 0;
+      }
+    }
+    for (int i = 0; i < kClusterSizes; ++i) active[dev][i] = got[i];  // equal values, whoever writes them
+    known[dev].store(1, std::memory_order_release);
+  }
+  *out = active[dev];
+  return cudaSuccess;
+}
+
+template <bool BF16, int HD>
+cudaError_t launch_prompt_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
+  const cudaError_t e = prepare_t<BF16, HD, false>();
+  if (e != cudaSuccess) return e;
+  tile_attn_kernel<BF16, HD, false><<<static_cast<unsigned>(ctas), kThreads, Shape<HD>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool BF16, int HD>
+cudaError_t launch_tree_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = tree_config<BF16, HD>(p.cluster, ctas, s, &attr);
+  return cudaLaunchKernelEx(&cfg, tile_attn_kernel<BF16, HD, true>, p);
 }
 
 }  // namespace
 
-// Workspace of a tree launch: per CTA and slot, (m, l) and o of 128 rows.
-size_t tile_tree_workspace(const TileAttnParams& p, long long ctas, int hd) {
-  return p.partials ? static_cast<size_t>(ctas) * 2 * kRows * (sizeof(float2) + hd * sizeof(float)) : 0;
-}
-void tile_tree_set_workspace(TileAttnParams& p, long long ctas, void* ws) {
-  p.part_ml = static_cast<float2*>(ws);
-  p.part_o = reinterpret_cast<float*>(p.part_ml + ctas * 2 * kRows);
+// Sequences longest first: their positions in p.len / p.pos / p.tok0 move.
+static void longest_first(TileAttnParams& p, const int* keys) {
+  int order[kOpSeqs], tok0[kOpSeqs], len[kOpSeqs], pos[kOpSeqs];
+  for (int s = 0; s < p.n_seqs; ++s) order[s] = s, tok0[s] = p.tok0[s], len[s] = p.len[s], pos[s] = p.pos[s];
+  std::sort(order, order + p.n_seqs, [&](int a, int b) { return keys[a] != keys[b] ? keys[a] > keys[b] : a < b; });
+  for (int s = 0; s < p.n_seqs; ++s) p.tok0[s] = tok0[order[s]], p.len[s] = len[order[s]], p.pos[s] = pos[order[s]];
 }
 
 // Work items of a prompt launch: sequences longest first, each from its last
 // tokens (which see the most keys) to its first, so that the launch ends on
 // small items.
 long long tile_prompt_plan(TileAttnParams& p) {
-  int order[kOpSeqs], tok0[kOpSeqs], len[kOpSeqs];
-  for (int s = 0; s < p.n_seqs; ++s) order[s] = s, tok0[s] = p.tok0[s], len[s] = p.len[s];
-  std::stable_sort(order, order + p.n_seqs, [&](int a, int b) { return len[a] > len[b]; });
+  int keys[kOpSeqs];
+  for (int s = 0; s < p.n_seqs; ++s) keys[s] = p.len[s];
+  longest_first(p, keys);
   p.tpt = kRows / p.group;
   long long items = 0;
   for (int s = 0; s < p.n_seqs; ++s) {
-    p.tok0[s] = tok0[order[s]];
-    p.len[s] = len[order[s]];
     p.item0[s] = static_cast<int>(items);
     items += (p.len[s] + 2 * p.tpt - 1) / (2 * p.tpt);
   }
   return items * p.nkv;
 }
 
-// Work items of a tree launch: keys in chunks of cs blocks, for the shortest
-// modelled time. A CTA takes its blocks and about two blocks' time of start,
-// ramp and epilogue (kCtaCost); the SMs share the CTAs' total, and the whole
-// chunks come in rounds.
-long long tile_tree_plan(TileAttnParams& p, int num_sms) {
-  constexpr int kCtaCost = 2;
-  p.tpt = kRows / p.group;
-  int most_rows = 0, most = 1, blocks[kOpSeqs];
-  for (int s = 0; s < p.n_seqs; ++s) {
-    most_rows = std::max(most_rows, p.len[s]);
-    blocks[s] = p.len[s] ? (p.pos[s] + p.len[s] + kRows - 1) / kRows : 0;
-    most = std::max(most, blocks[s]);
-  }
-  p.solo = most_rows <= p.tpt;
-  auto pairs_of = [&](int s) -> long long { return p.solo ? 1 : (p.len[s] + 2 * p.tpt - 1) / (2 * p.tpt); };
-  long long total = 0;
-  for (int s = 0; s < p.n_seqs; ++s) total += pairs_of(s) * blocks[s] * p.nkv;
-  // chunks of the longest sequence: past two CTAs per SM no split pays
-  const long long most_chunks = std::min<long long>(most, 2ll * num_sms * most / std::max(total, 1ll) + 1);
-  long long best = -1;
-  p.cs = most;
-  for (int c = 1, last = 0; c <= most_chunks; ++c) {
-    const int cs = (most + c - 1) / c;
-    if (cs == last) continue;
-    last = cs;
-    long long ctas = 0, whole = 0;
-    for (int s = 0; s < p.n_seqs; ++s) {
-      ctas += pairs_of(s) * ((blocks[s] + cs - 1) / cs);
-      whole += pairs_of(s) * (blocks[s] / cs);
-    }
-    const long long rounds = (whole * p.nkv + num_sms - 1) / num_sms;
-    const long long shared = (total + kCtaCost * ctas * p.nkv + num_sms - 1) / num_sms;
-    const long long cost = std::max(rounds * (cs + kCtaCost), shared);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.cs = cs;
-    }
-  }
-  long long items = 0;
-  p.partials = 0;
-  for (int s = 0; s < p.n_seqs; ++s) {
-    p.item0[s] = static_cast<int>(items);
-    items += pairs_of(s) * ((blocks[s] + p.cs - 1) / p.cs);
-    if (p.solo ? blocks[s] > 1 : blocks[s] > p.cs) p.partials = 1;
-  }
-  return items * p.nkv;
+cudaError_t launch_tile_prompt(const TileAttnParams& p, long long ctas, bool bf16, int hd, cudaStream_t s) {
+  if (bf16) return hd == 128 ? launch_prompt_t<true, 128>(p, ctas, s) : launch_prompt_t<true, 64>(p, ctas, s);
+  return hd == 128 ? launch_prompt_t<false, 128>(p, ctas, s) : launch_prompt_t<false, 64>(p, ctas, s);
 }
 
-cudaError_t launch_tile_attn(const TileAttnParams& p, long long ctas, bool bf16, int hd, bool tree, cudaStream_t s) {
-  if (ctas <= 0) return cudaSuccess;
-  return bf16 ? launch_hd<true>(p, ctas, hd, tree, s) : launch_hd<false>(p, ctas, hd, tree, s);
+static long long blocks_of(const TileAttnParams& p, int s) {
+  return p.len[s] ? (p.pos[s] + p.len[s] + kRows - 1) / kRows : 0;
+}
+
+// Work items of a tree launch: one cluster per (sequence, pair of tiles, kv
+// head), which shares out the sequence's key blocks. The cluster's size is the
+// one with the shortest modelled time in units of a block: the longest CTA, two
+// in a row, or all clusters' work over those that run at once, whichever is
+// most; a CTA costs about kStart blocks to start and finish, and kJoin more
+// where it is joined.
+cudaError_t tile_tree_plan(TileAttnParams& p, bool bf16, int hd, long long* ctas) {
+  constexpr long long kStart = 4, kJoin = 2;
+  p.tpt = kRows / p.group;
+  int blocks[kOpSeqs], most_rows = 0;
+  for (int s = 0; s < p.n_seqs; ++s) {
+    p.tok0[s] = s;
+    most_rows = std::max(most_rows, p.len[s]);
+    blocks[s] = p.len[s] ? (p.pos[s] + p.len[s] + kRows - 1) / kRows : 0;
+  }
+  longest_first(p, blocks);
+  p.solo = most_rows <= p.tpt;
+  long long clusters = 0;
+  for (int s = 0; s < p.n_seqs; ++s) {
+    p.item0[s] = static_cast<int>(clusters);
+    clusters += p.len[s] == 0 ? 0 : p.solo ? 1 : (p.len[s] + 2 * p.tpt - 1) / (2 * p.tpt);
+  }
+  *ctas = 0;
+  if (clusters == 0) return cudaSuccess;
+  const int* active = nullptr;
+  const cudaError_t e = bf16 ? (hd == 128 ? active_t<true, 128>(&active) : active_t<true, 64>(&active))
+                             : (hd == 128 ? active_t<false, 128>(&active) : active_t<false, 64>(&active));
+  if (e != cudaSuccess) return e;
+  long long best = -1;
+  for (int i = 0; i < kClusterSizes; ++i) {
+    if (active[i] < 1) continue;
+    const int size = 1 << i;
+    const long long fixed = kStart + (p.solo || size > 1 ? kJoin : 0);
+    // clusters come longest first: past the first `active` of them, one runs
+    // behind another of at least its own length
+    long long total = 0, longest = 0, seen = 0, second = 0;
+    for (int s = 0; s < p.n_seqs; ++s) {
+      if (!p.len[s]) continue;
+      const long long each = (blocks_of(p, s) + size - 1) / size + fixed;
+      const long long n = ((s + 1 < p.n_seqs ? p.item0[s + 1] : clusters) - p.item0[s]) * p.nkv;
+      longest = std::max(longest, each);
+      total += n * each;
+      if (seen <= active[i] && seen + n > active[i]) second = 2 * each;
+      seen += n;
+    }
+    const long long cost = std::max(std::max(longest, second), (total + active[i] - 1) / active[i]);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.cluster = size;
+    }
+  }
+  if (best < 0) return cudaErrorInvalidConfiguration;
+  *ctas = clusters * p.nkv * p.cluster;
+  return cudaSuccess;
+}
+
+cudaError_t launch_tile_tree(const TileAttnParams& p, long long ctas, bool bf16, int hd, cudaStream_t s) {
+  if (bf16) return hd == 128 ? launch_tree_t<true, 128>(p, ctas, s) : launch_tree_t<true, 64>(p, ctas, s);
+  return hd == 128 ? launch_tree_t<false, 128>(p, ctas, s) : launch_tree_t<false, 64>(p, ctas, s);
 }
 
 cudaError_t tile_attn_status(int* status, cudaStream_t s) {

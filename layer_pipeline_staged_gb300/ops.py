@@ -23,15 +23,16 @@ __all__ = ["attention_prompt_packed", "attention_tree_verify", "kv_rows_append",
 
 _S4, _S6, _S8 = (struct.Struct(f"{n}q").pack for n in (4, 6, 8))
 _int32 = np.dtype(np.int32)
-_torch = _types = _stream_of = _current = None
+_torch = _types = _stream_of = _current = _dense = None
 
 
 def _need_torch() -> None:
     """The parts of torch the calls use, looked up once (the package itself does not need torch)."""
-    global _torch, _types, _stream_of, _current
+    global _torch, _types, _stream_of, _current, _dense
     import torch
     _types = {torch.bfloat16: _capi.LPS_TYPE_BF16, torch.float16: _capi.LPS_TYPE_FP16}
     _stream_of, _current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _dense = torch.contiguous_format
     _torch = torch
 
 
@@ -121,7 +122,7 @@ def attention_prompt_packed(q, k, v, offsets, out=None, scale: float = 0.0):
         raise ValueError("k and v must be [tokens, kv heads, head_dim] of q's tokens and head_dim")
     if out is None:
         kind, dev = _alike((q, k, v))
-        out = q.new_empty(shape)
+        out = _torch.empty_like(q, memory_format=_dense)
     else:
         kind, dev = _alike((q, k, v, out))
         if out.shape != shape:
@@ -157,7 +158,7 @@ def attention_tree_verify(q, k_cache, v_cache, parents, pos, rows, out=None, sca
         raise ValueError("the caches must be [batch, kv heads, max_ctx, head_dim] of q's batch and head_dim")
     if out is None:
         kind, dev = _alike((q, k_cache, v_cache))
-        out = q.new_empty(shape)
+        out = _torch.empty_like(q, memory_format=_dense)
     else:
         kind, dev = _alike((q, k_cache, v_cache, out))
         if out.shape != shape:
@@ -172,20 +173,8 @@ def attention_tree_verify(q, k_cache, v_cache, parents, pos, rows, out=None, sca
         if d != 1:
             raise ValueError("the head dimension must be contiguous")
         st += (a if batch > 1 else width * nq * hd), (b if width > 1 else nq * hd), (c if nq > 1 else hd)
-    L = _capi.load()
-    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), kind, batch, width, p, r,
-            parents.data_ptr(), nq, nkv, hd, max_ctx, _S6(*st), scale)
-    here = _current()
-    if here != dev:
-        with _torch.cuda.device(dev):
-            need = L.attention_tree_workspace_bytes(batch, width, p, r, nq, nkv, hd)
-    else:
-        need = L.attention_tree_workspace_bytes(batch, width, p, r, nq, nkv, hd)
-    if need > 0:
-        ws = q.new_empty(need >> 1)  # elements of 2 bytes; the allocator keeps it until the stream has passed the call
-        _call(L.attention_tree_verify, dev, *args, ws.data_ptr(), need)
-    else:
-        _call(L.attention_tree_verify, dev, *args, None, 0)
+    _call(_capi.load().attention_tree_verify, dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+          kind, batch, width, p, r, parents.data_ptr(), nq, nkv, hd, max_ctx, _S6(*st), scale)
     return out
 
 

@@ -43,10 +43,10 @@ def prompt(q=Q, k=K, v=V, out=OUT, type=0, n=2, offsets=(0, 5, 9), nq=32, nkv=8,
 
 
 def tree(q=Q, k=K, v=V, out=OUT, type=0, batch=2, width=8, pos=(3, 4), rows=(8, 1), parents=DEV, nq=32, nkv=8, hd=128,
-         max_ctx=64, strides=None, scale=0.0, ws=None, ws_bytes=0):
+         max_ctx=64, strides=None, scale=0.0):
     return _capi.load().attention_tree_verify(q, k, v, out, type, batch, width, None if pos is None else _i32(pos),
                                               None if rows is None else _i32(rows), parents, nq, nkv, hd, max_ctx,
-                                              _i64(strides), scale, ws, ws_bytes, None)
+                                              _i64(strides), scale, None)
 
 
 def append(k=K, v=V, n=2, offsets=(0, 5, 9), kc=OUT, vc=Q, start=(0, 60), nkv=8, hd=128, max_ctx=64, strides=None):
@@ -96,14 +96,6 @@ def test_refused_before_the_device(call, kw, what):
     assert call(**kw) == lps.LPS_EINVAL
     err = _capi.load().last_error_string().decode()
     assert what in err, err
-
-
-def test_workspace_query_refuses():
-    L = _capi.load()
-    for args in [(0, 8, (1,), (1,), 32, 8, 128), (1, 65, (1,), (1,), 32, 8, 128), (1, 8, (1,), (1,), 32, 5, 128),
-                 (1, 8, (1,), (1,), 32, 8, 100), (1, 8, (-1,), (1,), 32, 8, 128), (1, 8, (1,), (9,), 32, 8, 128)]:
-        b, w, p, r, *rest = args
-        assert L.attention_tree_workspace_bytes(b, w, _i32(p), _i32(r), *rest) == -1, args
 
 
 def test_wrappers_refuse_cpu_tensors():
