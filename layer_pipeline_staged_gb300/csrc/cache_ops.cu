@@ -11,6 +11,7 @@
 
 #include <cmath>
 #include <exception>
+#include <initializer_list>
 #include <string>
 
 #include "cache_ops.h"
@@ -39,6 +40,14 @@ int guarded(const char* fn, F&& body) {
   } catch (...) {
     return LPS_ENOMEM;
   }
+}
+
+// Whether every row of an output starts on 32 bytes.
+bool wide(const void* p, std::initializer_list<int64_t> strides) {
+  if (reinterpret_cast<uintptr_t>(p) & 31) return false;
+  for (int64_t s : strides)
+    if (s % 16) return false;
+  return true;
 }
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
@@ -133,6 +142,7 @@ extern "C" int attention_prompt_packed(const void* q, const void* k, const void*
       p.q_tok = st[0], p.q_head = st[1], p.k_row = st[2], p.k_head = st[3];
       p.v_row = st[4], p.v_head = st[5], p.o_tok = st[6], p.o_head = st[7];
       p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+      p.wide_out = wide(out, {st[6], st[7]});
       p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
       for (int s = 0; s < p.n_seqs; ++s) {
         p.tok0[s] = offsets[s0 + s];
@@ -201,6 +211,7 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     p.k_head = p.v_head = static_cast<long long>(max_ctx) * head_dim;
     p.k_seq = p.v_seq = p.k_head * n_kv_heads;
     p.parents = parents;
+    p.wide_out = wide(out, {st[3], st[4], st[5]});
     p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
     const long long kv_n[3] = {max_ctx, n_kv_heads, batch}, kv_st[3] = {p.k_row, p.k_head, p.k_seq};
     if (!encode4(&p.tmap_q, bf16, q, head_dim, {n_q_heads, width, batch}, {st[2], st[1], st[0]}, p.group, p.tpt) ||

@@ -35,6 +35,7 @@ struct TileAttnParams {
   int width;
   int nq, nkv, group, n_seqs;
   float scale_log2;    // scale * log2(e)
+  int wide_out;        // out's rows are 32-byte aligned
   int tok0[kOpSeqs], len[kOpSeqs], pos[kOpSeqs];
   // set by the plan
   int tpt;             // tokens of a tile: 128 / group

@@ -29,8 +29,8 @@
 // become zero, and so do infinities and NaNs, which the epilogue then adds to
 // the rows that do see them (a path that finite inputs never take).
 //
-// A prompt's CTA stays on its SM: once the copies of its item are issued, its TMA lane
-// takes over the next CTA of the grid that has not started
+// A prompt's CTA stays on its SM: shortly before the copies of its item are all
+// issued, its TMA lane takes over the next CTA of the grid that has not started
 // (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first
 // S is made, while the last item's softmax and epilogue still run. The grid is
 // ordered from the largest item to the smallest.
@@ -59,9 +59,9 @@ constexpr int kThreads = 384;     // two softmax warpgroups; TMA, two MMA and re
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168, what the block is launched with
 constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
+constexpr int kAskAhead = 3;      // the next item is asked for this many blocks before the copies end
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
 constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
-constexpr int kMaxCluster = 1 << (kClusterSizes - 1);
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
 constexpr int kKid = kKidTileAttn << 8;
 
@@ -181,6 +181,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ void st_global32(void* at, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // x * 0 + acc: acc becomes NaN where x holds an infinity or a NaN.
@@ -463,13 +469,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 
   // first block of an item that some row does not see whole
   auto fix0_of = [](const Item& it) { return max(it.b0, it.clean / kRows); };
-  // the item after item number `no`, for a role that reads the answers (lane 0 of its warp arrives)
+  // the item after item number `no` (-1: none, -2: a wait gave up), read by one
+  // lane of a role's warp, or by the whole warp
   auto next_item = [&](int no) -> int {
     const int slot = no & 1;
-    int idx = -2;  // a wait that gave up
-    if (__all_sync(0xffffffffu, mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + slot * 16);
+    const int idx = mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)) ? taken(answer + slot * 16) : -2;
+    mbar_arrive(&next_empty[slot]);
+    return idx;
+  };
+  auto next_item_warp = [&](int no) -> int {
+    int idx = -2;
+    if (__all_sync(0xffffffffu, mbar_wait(&next_full[no & 1], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + (no & 1) * 16);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&next_empty[slot]);
+    if (lane == 0) mbar_arrive(&next_empty[no & 1]);
     return idx;
   };
 
@@ -510,17 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           }
           if (solo && it.nblk > 1) load(&p.tmap_k, 1);
           const int ahead = solo ? 2 : 1;
+          const int slot = no & 1;
           for (int j = 0; j < it.nblk && ok; ++j) {
+            if (!TREE && j == max(it.nblk - kAskAhead, 0)) {
+              if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
+              if (!ok) break;
+              mbar_arrive_expect_tx(&next_full[slot], 16);
+              take_next(answer + slot * 16, &next_full[slot]);
+            }
             load(&p.tmap_v, j);
             if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[nf++ % kMaxFix]);
             if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
           }
           if (TREE || !ok) break;
-          const int slot = no & 1;
-          if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
-          if (!ok) break;
-          mbar_arrive_expect_tx(&next_full[slot], 16);
-          take_next(answer + slot * 16, &next_full[slot]);
           wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1));
           idx = ok ? taken(answer + slot * 16) : -1;
         }
@@ -541,8 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       bool ok = true;
       int st = 0, nq = 0, np = 0, nf = 0, nt = 0;  // ring stage; Q tiles, P blocks, repaired blocks and turns so far
       uint32_t ph = 0;                     // the stage's phase
+      Item it = item_of<TREE>(p, blockIdx.x);
       for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-        const Item it = item_of<TREE>(p, idx);
+        Item following{};
+        bool ahead = false;  // the next item is known
         if (lane == 0 && ok) {
           const int fix0 = fix0_of(it), mine = it.n[slot];
           auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
@@ -618,6 +634,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
               wait(&full[st], ph, 1);
               advance();
             }
+            // finding the next item takes some 1500 cycles: before the last P is there
+            if (!TREE && !more) {
+              idx = next_item(no);
+              if (idx >= 0) following = item_of<TREE>(p, idx);
+              ahead = true;
+            }
             wait_p();
             // The slots take turns at the tensor core, so that they stay half an
             // iteration apart: left to themselves they fall into step, both
@@ -644,8 +666,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             }
           }
         }
-        __syncwarp();
-        idx = TREE ? -1 : next_item(no);
+        if (TREE) break;
+        if (lane == 0 && !ahead) {
+          idx = next_item(no);
+          if (idx >= 0) following = item_of<TREE>(p, idx);
+        }
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        it = following;
       }
       // every MMA has completed before TMEM is freed
       if (lane == 0) {
@@ -704,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&vfix[nf % kMaxFix]);
         }
         n0 += 2 * it.nblk;
-        idx = TREE ? -1 : next_item(no);
+        idx = TREE ? -1 : next_item_warp(no);
       }
     }
   } else {
@@ -718,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     const float sl2 = p.scale_log2;
     bool ok = true;
     int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
+    Item it = item_of<TREE>(p, blockIdx.x);
     for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-      const Item it = item_of<TREE>(p, idx);
+      Item following{};
       const int fix0 = fix0_of(it);
       const int len = p.len[it.s];
       const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + row_tok;
@@ -741,6 +769,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nb && ok; ++i, ++ns) {
         const int kb = it.b0 + (solo ? 2 * i + slot : i);
+        if (!TREE && i == nb - 1) {  // finding the next item takes some 1500 cycles: before the last S is there
+          idx = next_item_warp(no);
+          if (idx >= 0) following = item_of<TREE>(p, idx);
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
         if (!ok) {
           if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
@@ -844,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       };
       if (ok && warp_ok && !joined) {
         if (nb > 0) {
-          // a thread writes its row, 16 bytes at a time
+          // a thread writes its row, whole 32-byte sectors at a time where out
+          // is so aligned: a warp's store goes out sector by sector
           const float inv = seen ? 1.0f / l : 0.f;
           uint16_t* out = static_cast<uint16_t*>(p.out) + p.tok0[it.s] * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
@@ -853,13 +886,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             float o[32];
             load_o(c, o);
             if (row_ok) {
+              uint32_t w[16];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                uint32_t w[4];
+              for (int e = 0; e < 16; ++e) w[e] = seen ? pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+              if (p.wide_out) {
+                st_global32(out + c, w);
+                st_global32(out + c + 16, w + 8);
+              } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = seen ? pack16<BF16>(o[u * 8 + 2 * e] * inv, o[u * 8 + 2 * e + 1] * inv) : 0u;
-                *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int u = 0; u < 4; ++u)
+                  *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
               }
             }
           }
@@ -923,7 +959,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         }
       }
       tc_fence_before();  // O has been read before the next item's first P allows its P.V
-      idx = TREE ? -1 : next_item(no);
+      if (TREE) break;
+      if (nb == 0) {
+        idx = next_item_warp(no);
+        if (idx >= 0) following = item_of<TREE>(p, idx);
+      }
+      it = following;
     }
   }
 
