@@ -29,8 +29,8 @@
 // become zero, and so do infinities and NaNs, which the epilogue then adds to
 // the rows that do see them (a path that finite inputs never take).
 //
-// A prompt's CTA stays on its SM: shortly before the copies of its item are all
-// issued, its TMA lane takes over the next CTA of the grid that has not started
+// A prompt's CTA stays on its SM: once the copies of its item are issued, its TMA lane
+// takes over the next CTA of the grid that has not started
 // (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first
 // S is made, while the last item's softmax and epilogue still run. The grid is
 // ordered from the largest item to the smallest.
@@ -59,7 +59,6 @@ constexpr int kThreads = 384;     // two softmax warpgroups; TMA, two MMA and re
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 2 * 208 + 88 = 3 * 168, what the block is launched with
 constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
-constexpr int kAskAhead = 3;      // the next item is asked for this many blocks before the copies end
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
 constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
@@ -275,6 +274,7 @@ __device__ __forceinline__ void regs_dec() {
 
 struct Item {
   int s, g;          // sequence, kv head
+  int len, tok0;     // p.len[s], p.tok0[s]
   int t0;            // first token of slot 0's tile
   int b0, nblk;      // key blocks [b0, b0 + nblk) of this CTA
   int n[2];          // of which each slot works through so many (solo: every other one)
@@ -295,7 +295,9 @@ __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
     if (p.item0[mid] <= w) lo = mid; else hi = mid - 1;
   }
   it.s = lo;
-  const int len = p.len[lo], off = w - p.item0[lo], span = 2 * p.tpt;
+  it.len = p.len[lo];
+  it.tok0 = p.tok0[lo];
+  const int len = it.len, off = w - p.item0[lo], span = 2 * p.tpt;
   if (!TREE) {
     const int pairs = (len + span - 1) / span;
     it.t0 = (pairs - 1 - off) * span;  // the last tokens, which see the most keys, first
@@ -352,38 +354,48 @@ __device__ __forceinline__ float weight_of(float2 ml, float top) {
 // of a call's 14 us.
 template <bool BF16, int HD, int C>
 __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t* out, int u0, int step) {
-  float2 ml[C];
+  constexpr int G = C < 8 ? C : 8;  // parts whose loads are under way at once
+  float w[C], top = -INFINITY, l = 0.f;
+  {
+    float2 ml[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) ml[c] = peer_ld2(peer_smem(ml_at, c));
-  for (int u = u0; u < HD / 8; u += step) {
-    float4 x[C], y[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint32_t at = peer_smem(o_at + 2 * u * kRows * 16, c);
-      x[c] = peer_ld4(at);
-      y[c] = peer_ld4(at + kRows * 16);
-    }
-    float top = -INFINITY, l = 0.f;
+    for (int c = 0; c < C; ++c) ml[c] = peer_ld2(peer_smem(ml_at, c));
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (ml[c].y != 0.f) top = fmaxf(top, ml[c].x);
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float w = weight_of(ml[c], top);
-      if (w != 0.f) {  // a part that saw nothing has left no o
-        l = fmaf(w, ml[c].y, l);
-        o[0] = fmaf(w, x[c].x, o[0]);
-        o[1] = fmaf(w, x[c].y, o[1]);
-        o[2] = fmaf(w, x[c].z, o[2]);
-        o[3] = fmaf(w, x[c].w, o[3]);
-        o[4] = fmaf(w, y[c].x, o[4]);
-        o[5] = fmaf(w, y[c].y, o[5]);
-        o[6] = fmaf(w, y[c].z, o[6]);
-        o[7] = fmaf(w, y[c].w, o[7]);
+      w[c] = weight_of(ml[c], top);
+      if (w[c] != 0.f) l = fmaf(w[c], ml[c].y, l);
+    }
+  }
+  const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
+  for (int u = u0; u < HD / 8; u += step) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < C; g += G) {
+      float4 x[G], y[G];
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        const uint32_t at = peer_smem(o_at + 2 * u * kRows * 16, g + c);
+        x[c] = peer_ld4(at);
+        y[c] = peer_ld4(at + kRows * 16);
+      }
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        const float f = w[g + c];
+        if (f != 0.f) {  // a part that saw nothing has left no o
+          o[0] = fmaf(f, x[c].x, o[0]);
+          o[1] = fmaf(f, x[c].y, o[1]);
+          o[2] = fmaf(f, x[c].z, o[2]);
+          o[3] = fmaf(f, x[c].w, o[3]);
+          o[4] = fmaf(f, y[c].x, o[4]);
+          o[5] = fmaf(f, y[c].y, o[5]);
+          o[6] = fmaf(f, y[c].z, o[6]);
+          o[7] = fmaf(f, y[c].w, o[7]);
+        }
       }
     }
-    const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
     *reinterpret_cast<uint4*>(out + u * 8) =
         make_uint4(pack16<BF16>(o[0] * inv, o[1] * inv), pack16<BF16>(o[2] * inv, o[3] * inv),
                    pack16<BF16>(o[4] * inv, o[5] * inv), pack16<BF16>(o[6] * inv, o[7] * inv));
@@ -469,19 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 
   // first block of an item that some row does not see whole
   auto fix0_of = [](const Item& it) { return max(it.b0, it.clean / kRows); };
-  // the item after item number `no` (-1: none, -2: a wait gave up), read by one
-  // lane of a role's warp, or by the whole warp
+  // the item after item number `no`, for a role that reads the answers (lane 0 of its warp arrives)
   auto next_item = [&](int no) -> int {
     const int slot = no & 1;
-    const int idx = mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)) ? taken(answer + slot * 16) : -2;
-    mbar_arrive(&next_empty[slot]);
-    return idx;
-  };
-  auto next_item_warp = [&](int no) -> int {
-    int idx = -2;
-    if (__all_sync(0xffffffffu, mbar_wait(&next_full[no & 1], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + (no & 1) * 16);
+    int idx = -2;  // a wait that gave up
+    if (__all_sync(0xffffffffu, mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + slot * 16);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&next_empty[no & 1]);
+    if (lane == 0) mbar_arrive(&next_empty[slot]);
     return idx;
   };
 
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         for (int idx = blockIdx.x, no = 0; idx >= 0 && ok; ++no) {
           const Item it = item_of<TREE>(p, idx);
           const int fix0 = fix0_of(it);
-          const int tb = TREE ? 0 : p.tok0[it.s], seq = TREE ? p.tok0[it.s] : 0;
+          const int tb = TREE ? 0 : it.tok0, seq = TREE ? it.tok0 : 0;
           auto load = [&](const CUtensorMap* map, int j) {
             const int st = n % NS;
             if (n >= NS) wait(&empty[st], static_cast<uint32_t>((n / NS - 1) & 1));
@@ -522,19 +528,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           }
           if (solo && it.nblk > 1) load(&p.tmap_k, 1);
           const int ahead = solo ? 2 : 1;
-          const int slot = no & 1;
           for (int j = 0; j < it.nblk && ok; ++j) {
-            if (!TREE && j == max(it.nblk - kAskAhead, 0)) {
-              if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
-              if (!ok) break;
-              mbar_arrive_expect_tx(&next_full[slot], 16);
-              take_next(answer + slot * 16, &next_full[slot]);
-            }
             load(&p.tmap_v, j);
             if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[nf++ % kMaxFix]);
             if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
           }
           if (TREE || !ok) break;
+          const int slot = no & 1;
+          if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
+          if (!ok) break;
+          mbar_arrive_expect_tx(&next_full[slot], 16);
+          take_next(answer + slot * 16, &next_full[slot]);
           wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1));
           idx = ok ? taken(answer + slot * 16) : -1;
         }
@@ -555,10 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       bool ok = true;
       int st = 0, nq = 0, np = 0, nf = 0, nt = 0;  // ring stage; Q tiles, P blocks, repaired blocks and turns so far
       uint32_t ph = 0;                     // the stage's phase
-      Item it = item_of<TREE>(p, blockIdx.x);
       for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-        Item following{};
-        bool ahead = false;  // the next item is known
+        const Item it = item_of<TREE>(p, idx);
         if (lane == 0 && ok) {
           const int fix0 = fix0_of(it), mine = it.n[slot];
           auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
@@ -634,12 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
               wait(&full[st], ph, 1);
               advance();
             }
-            // finding the next item takes some 1500 cycles: before the last P is there
-            if (!TREE && !more) {
-              idx = next_item(no);
-              if (idx >= 0) following = item_of<TREE>(p, idx);
-              ahead = true;
-            }
             wait_p();
             // The slots take turns at the tensor core, so that they stay half an
             // iteration apart: left to themselves they fall into step, both
@@ -666,13 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             }
           }
         }
-        if (TREE) break;
-        if (lane == 0 && !ahead) {
-          idx = next_item(no);
-          if (idx >= 0) following = item_of<TREE>(p, idx);
-        }
-        idx = __shfl_sync(0xffffffffu, idx, 0);
-        it = following;
+        __syncwarp();
+        idx = TREE ? -1 : next_item(no);
       }
       // every MMA has completed before TMEM is freed
       if (lane == 0) {
@@ -731,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&vfix[nf % kMaxFix]);
         }
         n0 += 2 * it.nblk;
-        idx = TREE ? -1 : next_item_warp(no);
+        idx = TREE ? -1 : next_item(no);
       }
     }
   } else {
@@ -745,11 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     const float sl2 = p.scale_log2;
     bool ok = true;
     int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
-    Item it = item_of<TREE>(p, blockIdx.x);
     for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-      Item following{};
+      const Item it = item_of<TREE>(p, idx);
       const int fix0 = fix0_of(it);
-      const int len = p.len[it.s];
+      const int len = it.len;
       const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + row_tok;
       const bool row_ok = row_tok < p.tpt && tok < len;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -758,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         int8_t* mine = parents + warp * kTreeMax;
         __syncwarp();  // the last item's copy has been read
         for (int t = lane; t < len; t += 32) {
-          const int up = p.parents[static_cast<size_t>(p.tok0[it.s]) * p.width + t];
+          const int up = p.parents[static_cast<size_t>(it.tok0) * p.width + t];
           mine[t] = static_cast<int8_t>(up >= -1 && up < t ? up : -2);
         }
         __syncwarp();
@@ -769,10 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nb && ok; ++i, ++ns) {
         const int kb = it.b0 + (solo ? 2 * i + slot : i);
-        if (!TREE && i == nb - 1) {  // finding the next item takes some 1500 cycles: before the last S is there
-          idx = next_item_warp(no);
-          if (idx >= 0) following = item_of<TREE>(p, idx);
-        }
         ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
         if (!ok) {
           if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
@@ -859,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         tmem_wait_ld<32>(o);
         if (fix && seen) {
           const uint16_t* v =
-              static_cast<const uint16_t*>(p.v) + p.tok0[it.s] * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head + c;
+              static_cast<const uint16_t*>(p.v) + it.tok0 * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head + c;
           for (int i = 0; i < nb; ++i) {
             const int kb = it.b0 + (solo ? 2 * i + slot : i);
             if (kb < fix0) continue;
@@ -877,9 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       if (ok && warp_ok && !joined) {
         if (nb > 0) {
           // a thread writes its row, whole 32-byte sectors at a time where out
-          // is so aligned: a warp's store goes out sector by sector
+          // is so aligned: a warp's store goes out row by row
           const float inv = seen ? 1.0f / l : 0.f;
-          uint16_t* out = static_cast<uint16_t*>(p.out) + p.tok0[it.s] * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
+          uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
 #pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
@@ -959,12 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         }
       }
       tc_fence_before();  // O has been read before the next item's first P allows its P.V
-      if (TREE) break;
-      if (nb == 0) {
-        idx = next_item_warp(no);
-        if (idx >= 0) following = item_of<TREE>(p, idx);
-      }
-      it = following;
+      idx = TREE || !ok ? -1 : next_item(no);
     }
   }
 
@@ -976,9 +957,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       const Item it = item_of<TREE>(p, blockIdx.x);
       const int half = tid >> 7, r = tid & 127, tile = solo ? 0 : half;
       const int tok = it.t0 + tile * p.tpt + r / p.group;
-      if (r / p.group < p.tpt && tok < p.len[it.s]) {
+      if (r / p.group < p.tpt && tok < it.len) {
         const uint32_t ml_at = smem_u32(join_ml + tile * kRows + r), o_at = smem_u32(join_o + tile * (HD / 4) * kRows + r);
-        uint16_t* out = static_cast<uint16_t*>(p.out) + p.tok0[it.s] * p.o_seq + tok * p.o_tok +
+        uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * p.o_seq + tok * p.o_tok +
                         (it.g * p.group + r % p.group) * p.o_head;
         const int u0 = blockIdx.x % p.cluster + (solo ? half * p.cluster : 0), step = solo ? 2 * p.cluster : p.cluster;
         switch (p.cluster) {
