@@ -502,7 +502,7 @@ long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n
  *     out[t][h] = sum_j p_j v[j], p = softmax_j(scale * q[t][h] . k[j]).
  *   q, out   device [tokens][n_q_heads][head_dim]
  *   k, v     device [tokens][n_kv_heads][head_dim]
- *   offsets  host int32[n_seqs + 1], offsets[0] >= 0, not descending; empty
+ *   offsets  host int32[n_seqs + 1], in [0, 2^31 - 2^16], not descending; empty
  *            sequences are fine. Rows outside [offsets[0], offsets[n_seqs]) are
  *            neither used nor written; a key a token does not see changes
  *            nothing, whatever it holds

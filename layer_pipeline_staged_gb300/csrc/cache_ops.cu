@@ -109,8 +109,11 @@ bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long l
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// Rows and tokens are counted in 32 bits, a block of keys past the last one included.
+constexpr int32_t kMaxRows = 0x7fff0000;
+
 int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
-  if (offsets[0] < 0) return host_fail(LPS_EINVAL, fn, "offsets[0] must be >= 0");
+  if (offsets[0] < 0 || offsets[n_seqs] > kMaxRows) return host_fail(LPS_EINVAL, fn, "offsets must lie in [0, 2^31 - 2^16]");
   for (int s = 0; s < n_seqs; ++s)
     if (offsets[s + 1] < offsets[s]) return host_fail(LPS_EINVAL, fn, "offsets must not descend");
   return LPS_OK;
@@ -168,7 +171,7 @@ namespace {
 int check_tree(const char* fn, int batch, int width, const int32_t* pos, const int32_t* rows, int max_ctx) {
   if (batch < 1 || batch > kOpSeqs) return host_fail(LPS_EINVAL, fn, "batch must be in 1..256");
   if (width < 1 || width > kTreeMax) return host_fail(LPS_EINVAL, fn, "width must be in 1..64");
-  if (max_ctx < 1) return host_fail(LPS_EINVAL, fn, "max_ctx must be >= 1");
+  if (max_ctx < 1 || max_ctx > kMaxRows) return host_fail(LPS_EINVAL, fn, "max_ctx must be in [1, 2^31 - 2^16]");
   for (int b = 0; b < batch; ++b) {
     if (pos[b] < 0 || rows[b] < 0 || rows[b] > width) return host_fail(LPS_EINVAL, fn, "need pos >= 0 and 0 <= rows <= width");
     if (pos[b] > max_ctx - rows[b]) return host_fail(LPS_EINVAL, fn, "pos + rows must stay within max_ctx");
@@ -234,7 +237,8 @@ extern "C" int kv_rows_append(const void* k, const void* v, int n_seqs, const in
     if (n_seqs < 1) return host_fail(LPS_EINVAL, FN, "n_seqs must be >= 1");
     int rc = check_heads(FN, LPS_TYPE_BF16, n_kv_heads, n_kv_heads, head_dim);
     if (rc || (rc = check_offsets(FN, n_seqs, offsets))) return rc;
-    if (max_ctx < 1) return host_fail(LPS_EINVAL, FN, "max_ctx must be >= 1");
+    if (max_ctx < 1 || max_ctx > kMaxRows) return host_fail(LPS_EINVAL, FN, "max_ctx must be in [1, 2^31 - 2^16]");
+    if (k_cache == v_cache) return host_fail(LPS_EINVAL, FN, "the two caches must differ");
     for (int s = 0; s < n_seqs; ++s)
       if (start[s] < 0 || start[s] > max_ctx || offsets[s + 1] - offsets[s] > max_ctx - start[s])
         return host_fail(LPS_EINVAL, FN, "start + the sequence's length must stay within [0, max_ctx]");
@@ -268,12 +272,13 @@ extern "C" int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int ba
   return guarded(FN, [&]() -> int {
     if (!k_cache || !v_cache || !pos || !path || !accepted)
       return host_fail(LPS_EINVAL, FN, "the caches, pos, path and accepted are required");
-    if (n_layers < 1 || n_layers > 65535) return host_fail(LPS_EINVAL, FN, "n_layers must be in 1..65535");
+    if (n_layers < 1 || n_layers > 32767) return host_fail(LPS_EINVAL, FN, "n_layers must be in 1..32767");
     if (batch < 1 || batch > kOpSeqs) return host_fail(LPS_EINVAL, FN, "batch must be in 1..256");
     if (width < 1 || width > kTreeMax) return host_fail(LPS_EINVAL, FN, "width must be in 1..64");
     const int rc = check_heads(FN, LPS_TYPE_BF16, n_kv_heads, n_kv_heads, head_dim);
     if (rc) return rc;
-    if (max_ctx < 1) return host_fail(LPS_EINVAL, FN, "max_ctx must be >= 1");
+    if (max_ctx < 1 || max_ctx > kMaxRows) return host_fail(LPS_EINVAL, FN, "max_ctx must be in [1, 2^31 - 2^16]");
+    if (k_cache == v_cache) return host_fail(LPS_EINVAL, FN, "the two caches must differ");
     for (int b = 0; b < batch; ++b)
       if (pos[b] < 0 || pos[b] > max_ctx) return host_fail(LPS_EINVAL, FN, "pos out of [0, max_ctx]");
     if (misaligned(k_cache) || misaligned(v_cache)) return host_fail(LPS_EINVAL, FN, "the caches must be 16-byte aligned");

@@ -23,16 +23,15 @@ __all__ = ["attention_prompt_packed", "attention_tree_verify", "kv_rows_append",
 
 _S4, _S6, _S8 = (struct.Struct(f"{n}q").pack for n in (4, 6, 8))
 _int32 = np.dtype(np.int32)
-_torch = _types = _stream_of = _current = _dense = None
+_torch = _types = _stream_of = _current = None
 
 
 def _need_torch() -> None:
     """The parts of torch the calls use, looked up once (the package itself does not need torch)."""
-    global _torch, _types, _stream_of, _current, _dense
+    global _torch, _types, _stream_of, _current
     import torch
     _types = {torch.bfloat16: _capi.LPS_TYPE_BF16, torch.float16: _capi.LPS_TYPE_FP16}
     _stream_of, _current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-    _dense = torch.contiguous_format
     _torch = torch
 
 
@@ -122,7 +121,7 @@ def attention_prompt_packed(q, k, v, offsets, out=None, scale: float = 0.0):
         raise ValueError("k and v must be [tokens, kv heads, head_dim] of q's tokens and head_dim")
     if out is None:
         kind, dev = _alike((q, k, v))
-        out = _torch.empty_like(q, memory_format=_dense)
+        out = _torch.empty(shape, dtype=q.dtype, device=q.device)
     else:
         kind, dev = _alike((q, k, v, out))
         if out.shape != shape:
@@ -158,7 +157,7 @@ def attention_tree_verify(q, k_cache, v_cache, parents, pos, rows, out=None, sca
         raise ValueError("the caches must be [batch, kv heads, max_ctx, head_dim] of q's batch and head_dim")
     if out is None:
         kind, dev = _alike((q, k_cache, v_cache))
-        out = _torch.empty_like(q, memory_format=_dense)
+        out = _torch.empty(shape, dtype=q.dtype, device=q.device)
     else:
         kind, dev = _alike((q, k_cache, v_cache, out))
         if out.shape != shape:

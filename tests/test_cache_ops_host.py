@@ -65,7 +65,7 @@ CASES = [(prompt, kw, what) for kw, what in [
     (dict(offsets=None), "required"), (dict(n=0), "n_seqs"), (dict(n=-1), "n_seqs"), (dict(type=2), "type"),
     (dict(type=-1), "type"), (dict(hd=96), "head_dim"), (dict(nkv=0), "n_q_heads"), (dict(nq=0), "n_q_heads"),
     (dict(nq=12), "n_q_heads"), (dict(nq=34, nkv=2), "n_q_heads"), (dict(nq=70000, nkv=70000), "n_q_heads"),
-    (dict(offsets=(-1, 5, 9)), "offsets"), (dict(offsets=(0, 5, 4)), "offsets"), (dict(scale=-0.5), "scale"),
+    (dict(offsets=(-1, 5, 9)), "offsets"), (dict(offsets=(0, 5, 4)), "offsets"), (dict(offsets=(0, 5, 2**31 - 1)), "offsets"), (dict(scale=-0.5), "scale"),
     (dict(scale=float("inf")), "scale"), (dict(scale=float("nan")), "scale"),
     (dict(q=Q + 2), "aligned"), (dict(k=K + 8), "aligned"), (dict(v=V + 1), "aligned"), (dict(out=OUT + 4), "aligned"),
     *[(dict(strides=D8[:i] + (bad,) + D8[i + 1:]), "strides") for i in range(8) for bad in (0, -128, 132, 64, 1 << 40)],
@@ -75,19 +75,19 @@ CASES = [(prompt, kw, what) for kw, what in [
     (dict(nq=24, nkv=16), "n_q_heads"), (dict(batch=0), "batch"), (dict(batch=257, pos=(0,) * 257, rows=(1,) * 257), "batch"),
     (dict(width=0), "width"), (dict(width=65), "width"), (dict(max_ctx=0), "max_ctx"), (dict(pos=(-1, 0)), "pos"),
     (dict(rows=(9, 1)), "rows"), (dict(rows=(1, -1)), "rows"), (dict(pos=(57, 0)), "max_ctx"),
-    (dict(pos=(0, 2**31 - 1)), "max_ctx"), (dict(scale=-1.0), "scale"), (dict(k=K + 2), "aligned"),
+    (dict(pos=(0, 2**31 - 1)), "max_ctx"), (dict(max_ctx=2**31 - 1), "max_ctx"), (dict(scale=-1.0), "scale"), (dict(k=K + 2), "aligned"),
     (dict(strides=(4096, 4096, 100, 32768, 4096, 128)), "strides"), (dict(strides=(0, 4096, 128, 32768, 4096, 128)), "strides"),
 ]] + [(append, kw, what) for kw, what in [
     (dict(k=None), "required"), (dict(kc=None), "required"), (dict(start=None), "required"), (dict(n=0), "n_seqs"),
     (dict(offsets=(3, 2, 9)), "offsets"), (dict(start=(0, 61)), "start"), (dict(start=(-1, 0)), "start"),
     (dict(start=(65, 0), offsets=(0, 0, 1)), "start"), (dict(start=(0, 2**31 - 1)), "start"), (dict(hd=80), "head_dim"),
-    (dict(nkv=0), "n_q_heads"), (dict(max_ctx=0), "max_ctx"), (dict(kc=OUT + 2), "aligned"),
+    (dict(nkv=0), "n_q_heads"), (dict(max_ctx=0), "max_ctx"), (dict(kc=OUT + 2), "aligned"), (dict(vc=OUT), "differ"),
     (dict(strides=(1024, 128, 1024, 4)), "strides"),
 ]] + [(accept, kw, what) for kw, what in [
     (dict(kc=None), "required"), (dict(path=None), "required"), (dict(accepted=None), "required"), (dict(pos=None), "required"),
-    (dict(layers=0), "n_layers"), (dict(layers=65536), "n_layers"), (dict(batch=0), "batch"), (dict(width=65), "width"),
+    (dict(layers=0), "n_layers"), (dict(layers=32768), "n_layers"), (dict(batch=0), "batch"), (dict(width=65), "width"),
     (dict(width=0), "width"), (dict(pos=(0, 65)), "pos"), (dict(pos=(-1, 0)), "pos"), (dict(hd=256), "head_dim"),
-    (dict(vc=V + 4), "aligned"),
+    (dict(vc=V + 4), "aligned"), (dict(vc=K), "differ"), (dict(max_ctx=2**31 - 1), "max_ctx"),
 ]]
 
 

@@ -174,6 +174,39 @@ def test_prompt_extreme_scores(dtype):
         check_prompt(q, k, v, off, lps.attention_prompt_packed(q, k, v, off, scale=scale), scale)
 
 
+def test_prompt_more_items_than_sms():
+    """Enough tiles that every CTA takes over others, long and short ones, of one tile and of two."""
+    off, g = offsets_of([1500, 33, 0, 700, 129, 64, 65, 1, 1000, 200]), _gen(17)
+    n, nq, nkv, hd = int(off[-1]), 32, 8, 128
+    q, k, v = (_randn(g, n, h, hd, dtype=torch.bfloat16) for h in (nq, nkv, nkv))
+    out = lps.attention_prompt_packed(q, k, v, off)
+    check_prompt(q, k, v, off, out)
+    for _ in range(3):
+        assert torch.equal(lps.attention_prompt_packed(q, k, v, off), out)
+    # repaired values in one item leave the items around it as they were
+    v2 = v.clone()
+    v2[1400, 3, 40] = float("inf")
+    got = lps.attention_prompt_packed(q, k, v2, off)
+    assert (got[1400:1500, 12:16, 40] == float("inf")).all()
+    got[1400:1500, 12:16, 40] = out[1400:1500, 12:16, 40]
+    assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("shift", [8, 16])
+def test_prompt_output_alignment(shift):
+    """Output rows on 16 and on 32 bytes: the same bits, and nothing between them touched."""
+    off, g, nq, nkv, hd = offsets_of([70, 130]), _gen(19), 4, 2, 64
+    n = int(off[-1])
+    q, k, v = (_randn(g, n, h, hd, dtype=torch.float16) for h in (nq, nkv, nkv))
+    ref = lps.attention_prompt_packed(q, k, v, off)
+    buf = torch.full((n, nq * (hd + shift) + shift), 3.0, device="cuda", dtype=torch.float16)
+    out = buf[:, shift:].view(n, nq, hd + shift)[:, :, :hd]
+    lps.attention_prompt_packed(q, k, v, off, out=out)
+    assert torch.equal(out, ref)
+    out.fill_(3.0)
+    assert (buf == 3.0).all()
+
+
 def test_prompt_many_sequences():
     """More sequences than one launch carries."""
     rng = np.random.default_rng(1)
@@ -308,6 +341,28 @@ def test_tree_strided_q_and_out():
     assert torch.equal(out, ref)
 
 
+@pytest.mark.parametrize("nq,nkv,width", [(8, 2, 16), (16, 4, 64), (5, 1, 33)])
+def test_tree_of_many_sequences(nq, nkv, width):
+    """More clusters than run at once, of very different lengths, and sequences without drafts among them."""
+    rng = np.random.default_rng(6)
+    batch = 256 if nq == 8 else 90
+    pos = np.concatenate([[3000, 2900], rng.integers(0, 500, batch - 2)]).astype(np.int32)
+    rows = rng.integers(0, width + 1, batch).astype(np.int32)
+    q, kc, vc, parents, pos, rows = tree_case(23, pos, rows, width, nq, nkv, 64, torch.bfloat16)
+    out = lps.attention_tree_verify(q, kc, vc, torch.from_numpy(parents).cuda(), pos, rows, out=torch.full_like(q, 2.0))
+    check_tree(q, kc, vc, parents, pos, rows, out, torch.full_like(q, 2.0))
+
+
+def test_tree_scores_far_apart():
+    """One key far above all others, in the first, a middle and the last part of the cache: every part but
+    one has weights next to nothing in the join."""
+    for at in (0, 2000, 4090):
+        q, kc, vc, parents, pos, rows = tree_case(25, [4095], [3], 3, 4, 2, 128, torch.bfloat16)
+        kc[:, :, at] = (q[:, 0, :, :].view(1, 2, 2, 128).float().mean(2) * 8).to(torch.bfloat16)
+        out = lps.attention_tree_verify(q, kc, vc, torch.from_numpy(parents).cuda(), pos, rows)
+        check_tree(q, kc, vc, parents, pos, rows, out)
+
+
 def test_tree_cache_past_32_bits():
     """A cache of more than 2^32 bytes and 2^31 elements, read at its last head and sequence."""
     batch, nkv, ctx, hd = 2, 8, 1 << 20, 128
@@ -356,6 +411,73 @@ def test_tree_streams_and_graphs():
         graphs[1].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[0], refs[0]) and torch.equal(outs[1], refs[1])
+
+
+def test_prompt_and_moves_in_a_graph():
+    """The other operators captured and replayed on new values: the eager calls' bits."""
+    nq, nkv, hd, off, ctx = 8, 2, 64, offsets_of([100, 40, 257]), 300
+    n = int(off[-1])
+    q, k, v = (torch.zeros(n, h, hd, device="cuda", dtype=torch.bfloat16) for h in (nq, nkv, nkv))
+    kc, vc = (torch.zeros(2, 3, nkv, ctx, hd, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    path = torch.zeros(3, 4, device="cuda", dtype=torch.int32)
+    taken = torch.zeros(3, device="cuda", dtype=torch.int32)
+
+    def step(out):
+        lps.attention_prompt_packed(q, k, v, off, out=out)
+        lps.kv_rows_append(k, v, off, kc[1], vc[1], [0, 10, 43])
+        lps.kv_rows_accept(kc, vc, [100, 50, 296], path, taken)
+        return out
+
+    out, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    step(out)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(out)
+    for seed in (1, 2):
+        g = _gen(seed)
+        for t in (q, k, v, kc, vc):
+            t.normal_(generator=g)
+        path.copy_(torch.tensor([[0, 2, 3, 0], [1, 3, 0, 0], [3, 0, 0, 0]], dtype=torch.int32))
+        taken.copy_(torch.tensor([3, 2, 1], dtype=torch.int32))
+        before = kc.clone(), vc.clone()
+        want = step(torch.zeros_like(q)).clone(), kc.clone(), vc.clone()
+        kc.copy_(before[0]), vc.copy_(before[1]), out.zero_()
+        graph.replay()
+        for got, w in zip((out, kc, vc), want):
+            assert torch.equal(got, w)
+
+
+def test_calls_from_two_threads():
+    """Two host threads, each on a stream of its own: each call's own result, and messages that stay apart."""
+    import threading
+    cases, got, errors = [tree_case(50 + i, [900 + 300 * i, 20], [9, 26], 26, 8, 2, 128, torch.bfloat16) for i in range(2)], {}, []
+    refs = [lps.attention_tree_verify(*c[:3], torch.from_numpy(c[3]).cuda(), c[4], c[5], out=torch.zeros_like(c[0])) for c in cases]
+    pds = [torch.from_numpy(c[3]).cuda() for c in cases]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            q, kc, vc, _, p, r = cases[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    got[i] = lps.attention_tree_verify(q, kc, vc, pds[i], p, r, out=torch.zeros_like(q))
+                try:
+                    lps.attention_tree_verify(q, kc, vc, pds[i], [-1 - i, 0], r)
+                    errors.append("not refused")
+                except lps.LpsError as e:
+                    assert e.code == lps.LPS_EINVAL
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        assert torch.equal(got[i], refs[i])
 
 
 # ---- row moves -----------------------------------------------------------------------------------
@@ -514,6 +636,7 @@ def test_refusals_of_tensors():
     for pos, rows in (([1, 14], [1, 3]), ([-1, 0], [1, 1]), ([0, 0], [4, 1])):
         with pytest.raises(lps.LpsError):
             lps.attention_tree_verify(tq, kc, kc, par, pos, rows)
-    with pytest.raises(lps.LpsError):
-        lps.kv_rows_append(k, k, [0, 2, 4], kc, kc, [0, 15])
-    torch.cuda.synchronize()
+    for vc, start in ((kc.clone(), [0, 15]), (kc, [0, 0])):
+        with pytest.raises(lps.LpsError):
+            lps.kv_rows_append(k, k, [0, 2, 4], kc, vc, start)
+    assert _capi.load().cache_ops_status(torch.cuda.current_stream().cuda_stream) == lps.LPS_OK
