@@ -641,7 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             // iteration apart: left to themselves they fall into step, both
             // in their softmax, then both waiting for it. The turn is handed
             // on in the middle of S, to cover the time it takes to arrive.
-            const bool both = !solo && j < it.n[slot ^ 1];
+            // In a paired item they have block j one after the other, in a solo
+            // one block j and block j + 1.
+            const bool both = solo ? it.nblk > 1 : j < it.n[slot ^ 1], give = solo ? j + 1 < it.nblk : both;
             if (both) {
               if (slot == 1 || nt > 0) wait(&turn[slot], static_cast<uint32_t>((slot == 1 ? nt : nt - 1) & 1), 8);
               ++nt;
@@ -650,12 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             tc_fence_after();
             pv(sv, j < lead);
             if (more) {
-              qk(sk, both);
+              qk(sk, give);
               if (++done == mine) umma_commit(&qempty[solo ? 0 : slot]);
               umma_commit(&empty[sv]);
               umma_commit(&empty[sk]);
             } else {
-              if (both) mbar_arrive(&turn[slot ^ 1]);
+              if (give) mbar_arrive(&turn[slot ^ 1]);
               umma_commit(&ofull[slot]);
               umma_commit(&empty[sv]);
               if (has_k) skip();
