@@ -70,7 +70,7 @@ template <int HD>
 struct Shape {
   static constexpr int kTile = kRows * HD * 2;  // bytes of a Q tile, a K block or a V block
   static constexpr int kStages = HD == 128 ? 5 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024 + 1024;  // + alignment + barriers and flags
+  static constexpr int kSmem = (2 + kStages) * kTile + 1024 + (HD == 128 ? 1024 : 1280);  // + alignment + barriers, items and flags
 };
 
 // ---- building blocks ---------------------------------------------------------------
@@ -240,7 +240,7 @@ __device__ __forceinline__ int taken(const void* answer) {
       : "=r"(ok), "=r"(x)
       : "r"(smem_u32(answer))
       : "memory");
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before a later answer is written there
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before a later answer is written over it
   return ok ? static_cast<int>(x) : -1;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -273,11 +273,12 @@ __device__ __forceinline__ void regs_dec() {
 // ---- one CTA's work --------------------------------------------------------------
 
 struct Item {
+  int idx;           // its CTA in the grid; -1: none is left
   int s, g;          // sequence, kv head
   int len, tok0;     // p.len[s], p.tok0[s]
   int t0;            // first token of slot 0's tile
   int b0, nblk;      // key blocks [b0, b0 + nblk) of this CTA
-  int n[2];          // of which each slot works through so many (solo: every other one)
+  int n0, n1;        // of which slots 0 and 1 work through so many (solo: every other one)
   int tiles;         // tiles with rows (1 or 2)
   int clean;         // keys [0, clean) are seen by every row of the item
   int kend;          // keys at and after kend are seen by none
@@ -286,6 +287,7 @@ struct Item {
 template <bool TREE>
 __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
   Item it;
+  it.idx = idx;
   const int rank = TREE ? idx % p.cluster : 0, unit = TREE ? idx / p.cluster : idx;
   const int w = unit / p.nkv;
   it.g = unit - w * p.nkv;
@@ -303,9 +305,9 @@ __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
     it.t0 = (pairs - 1 - off) * span;  // the last tokens, which see the most keys, first
     const int endA = min(it.t0 + p.tpt, len), endB = min(it.t0 + span, len);
     it.b0 = 0;
-    it.n[0] = (endA + kRows - 1) / kRows;
-    it.n[1] = endB > endA ? (endB + kRows - 1) / kRows : 0;
-    it.nblk = max(it.n[0], it.n[1]);
+    it.n0 = (endA + kRows - 1) / kRows;
+    it.n1 = endB > endA ? (endB + kRows - 1) / kRows : 0;
+    it.nblk = max(it.n0, it.n1);
     it.tiles = endB > endA ? 2 : 1;
     it.clean = it.t0 + 1;
     it.kend = endB;
@@ -315,8 +317,8 @@ __device__ __forceinline__ Item item_of(const TileAttnParams& p, int idx) {
     it.b0 = rank * all / p.cluster;
     it.nblk = (rank + 1) * all / p.cluster - it.b0;  // may be none
     it.tiles = it.nblk == 0 ? 0 : !p.solo && it.t0 + p.tpt < len ? 2 : 1;
-    it.n[0] = p.solo ? (it.nblk + 1) / 2 : it.nblk;
-    it.n[1] = p.solo ? it.nblk / 2 : it.tiles == 2 ? it.nblk : 0;
+    it.n0 = p.solo ? (it.nblk + 1) / 2 : it.nblk;
+    it.n1 = p.solo ? it.nblk / 2 : it.tiles == 2 ? it.nblk : 0;
     it.clean = p.pos[lo];
     it.kend = p.pos[lo] + len;
   }
@@ -410,10 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qs = smem;
   uint8_t* ring = smem + 2 * kTile;
-  uint8_t* answer = ring + NS * kTile;                      // [2][16]: the items taken over
-  uint64_t* next_full = reinterpret_cast<uint64_t*>(answer + 32);  // [2]: an answer is there
-  uint64_t* next_empty = next_full + 2;  // [2]: every role has read it
-  uint64_t* full = next_empty + 2;
+  uint8_t* answer = ring + NS * kTile;                 // [16]: the CTA taken over
+  Item* items = reinterpret_cast<Item*>(answer + 16);  // [2]: item number no in place no & 1
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(items + 2);  // [2]: the item is there
+  uint64_t* item_done = item_full + 2;   // [2]: every role is through with it
+  uint64_t* asked = item_done + 2;       // the answer is there
+  uint64_t* full = asked + 1;
   uint64_t* empty = full + NS;     // both MMA warps are through with the stage
   uint64_t* qfull = empty + NS;    // [2]: a Q tile is there
   uint64_t* qempty = qfull + 2;    // [2]: its last S is made
@@ -438,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&next_full[i], 1);
-      mbar_init(&next_empty[i], 11);  // eight softmax warps, two MMA, repair
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_done[i], 11);  // eight softmax warps, two MMA, repair
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], solo ? 2 : 1);
       mbar_init(&mma_done[i], 1);
@@ -457,6 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       mbar_init(&vfix[i], 1);
       mbar_init(&vissued[i], 1);
     }
+    mbar_init(asked, 1);
+    items[0] = item_of<TREE>(p, blockIdx.x);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -481,14 +487,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 
   // first block of an item that some row does not see whole
   auto fix0_of = [](const Item& it) { return max(it.b0, it.clean / kRows); };
-  // the item after item number `no`, for a role that reads the answers (lane 0 of its warp arrives)
-  auto next_item = [&](int no) -> int {
-    const int slot = no & 1;
-    int idx = -2;  // a wait that gave up
-    if (__all_sync(0xffffffffu, mbar_wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1)))) idx = taken(answer + slot * 16);
+  auto blocks_of = [](const Item& it, int slot) { return slot ? it.n1 : it.n0; };
+  // Whether there is an item number `no`, which the TMA lane has left in its
+  // place (each role for itself would take 1500 cycles to work it out).
+  auto item_there = [&](int no) -> bool {
+    if (no == 0) return true;
+    if (TREE) return false;
+    return __all_sync(0xffffffffu, mbar_wait(&item_full[no & 1], static_cast<uint32_t>(((no - 1) >> 1) & 1))) &&
+           items[no & 1].idx >= 0;
+  };
+  auto through_with = [&](int no) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&next_empty[slot]);
-    return idx;
+    if (lane == 0) mbar_arrive(&item_done[no & 1]);
   };
 
   if (warp >= 8) {
@@ -504,8 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             ok = false;
           }
         };
-        for (int idx = blockIdx.x, no = 0; idx >= 0 && ok; ++no) {
-          const Item it = item_of<TREE>(p, idx);
+        for (int no = 0; ok; ++no) {
+          const Item it = items[no & 1];
+          if (it.idx < 0) break;
           const int fix0 = fix0_of(it);
           const int tb = TREE ? 0 : it.tok0, seq = TREE ? it.tok0 : 0;
           auto load = [&](const CUtensorMap* map, int j) {
@@ -533,14 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             if (ok && it.b0 + j >= fix0) mbar_arrive(&vissued[nf++ % kMaxFix]);
             if (j + ahead < it.nblk) load(&p.tmap_k, j + ahead);
           }
-          if (TREE || !ok) break;
-          const int slot = no & 1;
-          if (no >= 2) wait(&next_empty[slot], static_cast<uint32_t>(((no >> 1) - 1) & 1));
-          if (!ok) break;
-          mbar_arrive_expect_tx(&next_full[slot], 16);
-          take_next(answer + slot * 16, &next_full[slot]);
-          wait(&next_full[slot], static_cast<uint32_t>((no >> 1) & 1));
-          idx = ok ? taken(answer + slot * 16) : -1;
+          if (TREE) break;
+          const int place = (no + 1) & 1;  // of the next item; the last but this one was there
+          if (ok) {
+            mbar_arrive_expect_tx(asked, 16);
+            take_next(answer, asked);
+            wait(asked, static_cast<uint32_t>(no & 1));
+          }
+          if (no >= 1) wait(&item_done[place], static_cast<uint32_t>(((no - 1) >> 1) & 1));
+          const int idx = ok ? taken(answer) : -1;
+          if (idx >= 0) items[place] = item_of<TREE>(p, idx);
+          else items[place].idx = -1;
+          mbar_arrive(&item_full[place]);
         }
         // every copy issued lands before the CTA may end
         bool landed = true;
@@ -559,10 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       bool ok = true;
       int st = 0, nq = 0, np = 0, nf = 0, nt = 0;  // ring stage; Q tiles, P blocks, repaired blocks and turns so far
       uint32_t ph = 0;                     // the stage's phase
-      for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-        const Item it = item_of<TREE>(p, idx);
+      for (int no = 0; item_there(no); ++no) {
         if (lane == 0 && ok) {
-          const int fix0 = fix0_of(it), mine = it.n[slot];
+          const Item it = items[no & 1];
+          const int fix0 = fix0_of(it), mine = blocks_of(it, slot), others = blocks_of(it, slot ^ 1);
           auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
             if (ok && !mbar_wait(bar, parity)) {
               report_error(g_status, kErrWaitFull | kKid | (what << 13));
@@ -643,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             // on in the middle of S, to cover the time it takes to arrive.
             // In a paired item they have block j one after the other, in a solo
             // one block j and block j + 1.
-            const bool both = solo ? it.nblk > 1 : j < it.n[slot ^ 1], give = solo ? j + 1 < it.nblk : both;
+            const bool both = solo ? it.nblk > 1 : j < others, give = solo ? j + 1 < it.nblk : both;
             if (both) {
               if (slot == 1 || nt > 0) wait(&turn[slot], static_cast<uint32_t>((slot == 1 ? nt : nt - 1) & 1), 8);
               ++nt;
@@ -664,8 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             }
           }
         }
-        __syncwarp();
-        idx = TREE ? -1 : next_item(no);
+        through_with(no);
       }
       // every MMA has completed before TMEM is freed
       if (lane == 0) {
@@ -676,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       // ---------------- V blocks made safe ----------------
       bool ok = true;
       int n0 = 0, nf = 0;
-      for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-        const Item it = item_of<TREE>(p, idx);
+      for (int no = 0; item_there(no); ++no) {
+        const Item it = items[no & 1];
         const int fix0 = fix0_of(it);
         for (int kb = fix0; kb < it.b0 + it.nblk && ok; ++kb, ++nf) {
           // place in the load order of V block j of the item: K blocks are ahead of their V
@@ -724,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&vfix[nf % kMaxFix]);
         }
         n0 += 2 * it.nblk;
-        idx = TREE ? -1 : next_item(no);
+        through_with(no);
       }
     }
   } else {
@@ -738,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     const float sl2 = p.scale_log2;
     bool ok = true;
     int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
-    for (int idx = blockIdx.x, no = 0; idx >= 0; ++no) {
-      const Item it = item_of<TREE>(p, idx);
-      const int fix0 = fix0_of(it);
+    for (int no = 0; ok && item_there(no); ++no) {
+      const Item& it = items[no & 1];
+      const int fix0 = fix0_of(it), b0 = it.b0;
       const int len = it.len;
       const int tok = it.t0 + (solo ? 0 : slot * p.tpt) + row_tok;
       const bool row_ok = row_tok < p.tpt && tok < len;
@@ -757,10 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         if (row_ok) anc = tree_mask(mine, tok);
       }
       const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
-      const int nb = it.n[slot];
+      const int nb = blocks_of(it, slot);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < nb && ok; ++i, ++ns) {
-        const int kb = it.b0 + (solo ? 2 * i + slot : i);
+        const int kb = b0 + (solo ? 2 * i + slot : i);
         ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
         if (!ok) {
           if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
@@ -890,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         }
       } else if (TREE && joined) {
         // the ring is free once the other slot's products are done too
-        if (ok && it.n[slot ^ 1] > 0) {
+        if (ok && blocks_of(it, slot ^ 1) > 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot ^ 1], 0));
           if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
         }
@@ -947,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         }
       }
       tc_fence_before();  // O has been read before the next item's first P allows its P.V
-      idx = TREE || !ok ? -1 : next_item(no);
+      through_with(no);
     }
   }
 
@@ -956,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     __syncwarp();
     cluster_sync();
     if (warp < 8) {
-      const Item it = item_of<TREE>(p, blockIdx.x);
+      const Item& it = items[0];
       const int half = tid >> 7, r = tid & 127, tile = solo ? 0 : half;
       const int tok = it.t0 + tile * p.tpt + r / p.group;
       if (r / p.group < p.tpt && tok < it.len) {
