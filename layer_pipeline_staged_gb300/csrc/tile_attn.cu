@@ -23,26 +23,44 @@
 // operand of O += P.V, whose B operand is the V block as it lies, keys as rows.
 // TMEM: S0 S1 O0 O1.
 //
-// Warps 0-3 and 4-7: softmax and epilogue of slot 0 and 1. Warp 8: TMA. Warps
-// 9 and 11: the MMAs of slot 0 and 1. Warp 10: V blocks that some row does not see whole are made
-// safe before the MMA reads them, as 0 x inf is not 0: rows past the last key
-// become zero, and so do infinities and NaNs, which the epilogue then adds to
-// the rows that do see them (a path that finite inputs never take).
+// Warps 0-3 and 4-7: softmax and epilogue of slot 0 and 1. Warp 8: TMA. Warps 9
+// and 11: the MMAs of slot 0 and 1. Warp 10: V blocks that some row does not see
+// whole are made safe before the MMA reads them, as 0 x inf is not 0: rows past
+// the last key become zero, and so do infinities and NaNs, which the epilogue
+// then adds to the rows that do see them (a path that finite inputs never take).
 //
-// A prompt's CTA stays on its SM: once the copies of its item are issued, its TMA lane
-// takes over the next CTA of the grid that has not started
-// (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first
-// S is made, while the last item's softmax and epilogue still run. The grid is
+// A prompt's CTA stays on its SM: once the copies of its item are issued, its
+// TMA lane takes over the next CTA of the grid that has not started
+// (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first S
+// is made, while the last item's softmax and epilogue still run. The grid is
 // ordered from the largest item to the smallest.
 //
 // A tree's keys are shared out over a thread-block cluster, whose CTAs join
 // their (o, m, l) through distributed shared memory; a prompt tile's are not.
 // Every sum has one order given by the shapes, so equal calls give equal bits.
 // Waits are bounded and report through the status word.
+//
+// What bounds it, on one GB300 (cuBLAS bf16 1865 TFLOP/s, copy 6793 GB/s):
+//   - an 8184-token prompt, 32/8 heads of 128: 375 us, 1465 TFLOP/s. A paired
+//     iteration (two tiles x 128 keys) is 2048 cycles of products at the tensor
+//     core's rate and takes 2900 to 3300: a block's softmax is 1160 cycles (the
+//     hardware's exp2 alone 512), hand-overs between the warps 250 to 300 each,
+//     as the products keep shared memory busy (256 KB an iteration at 128 bytes a
+//     cycle), and an item's end about 6000 (its last P.V, and 32 rows a warp
+//     stored row by row);
+//   - 26 drafts over 8176 rows, 8 kv heads (33.5 MB): 16.3 us, of which 2.2 until
+//     the first S, 6.7 for the blocks, 5 for the join and its barriers.
+// Tried and slower: one warp for all MMAs (its waits and commits leave the tensor
+// core idle, 428 us), two without turns (they fall into step, 495), P in two halves
+// (413), two threads a row (a row's exp2 is bound to its quarter of the SM either
+// way, 399), hardware barriers instead of mbarriers (389), output warps of their
+// own (too few registers left for the softmax, 410), one key chunk per CTA with
+// partials in global memory and a merge kernel (tree of 26: 22 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "cache_ops.h"
 #include "kernels.h"
@@ -1031,28 +1049,27 @@ cudaLaunchConfig_t tree_config(int cluster, long long ctas, cudaStream_t s, cuda
 // Clusters of 2^i CTAs that run at once on the current device (0: none do).
 template <bool BF16, int HD>
 cudaError_t active_t(const int** out) {
+  static std::mutex mu;
   static int active[kMaxDevices][kClusterSizes];
-  static std::atomic<int> known[kMaxDevices];
+  static bool known[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!known[dev].load(std::memory_order_acquire)) {
+  std::lock_guard<std::mutex> lock(mu);
+  if (!known[dev]) {
     auto kern = tile_attn_kernel<BF16, HD, true>;
     if ((e = prepare_t<BF16, HD, true>()) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    int got[kClusterSizes];
     for (int i = 0; i < kClusterSizes; ++i) {
       cudaLaunchAttribute attr;
       const cudaLaunchConfig_t cfg = tree_config<BF16, HD>(1 << i, 1 << i, nullptr, &attr);
-      got[i] = 0;
-      if (cudaOccupancyMaxActiveClusters(&got[i], kern, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&active[dev][i], kern, &cfg) != cudaSuccess) {
         cudaGetLastError();
-        got[i] = 0;
+        active[dev][i] = 0;
       }
     }
-    for (int i = 0; i < kClusterSizes; ++i) active[dev][i] = got[i];  // equal values, whoever writes them
-    known[dev].store(1, std::memory_order_release);
+    known[dev] = true;
   }
   *out = active[dev];
   return cudaSuccess;
