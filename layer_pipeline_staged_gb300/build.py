@@ -1,8 +1,10 @@
 """Build the C-ABI library ``liblps.so`` in-tree with nvcc for sm_103a.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
-shared library (static CUDA runtime, no libtorch). Run as a module or call
-``build()``; the result sits next to this file and is git-ignored.
+shared library (static CUDA runtime, no libtorch); then the torch wrappers'
+argument marshalling as a Python extension beside it (gcc, no torch headers).
+Run as a module or call ``build()``; the results sit next to this file and are
+git-ignored.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblps.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(HERE, "_marshal.so")  # Python extension: the torch wrappers' argument marshalling
 SOURCES = ["runtime.cu", "gemv.cu", "attention.cu", "embed.cu", "noalloc.cu", "skinny.cu", "solver.cu", "stage.cu", "tcgemm.cu", "prefill.cu",
            "cache_ops.cu", "cache_rows.cu", "tile_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -63,7 +68,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         if verbose or r.returncode:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode:
-            raise RuntimeError("nvcc failed: " + " ".join(cmd))
+            raise RuntimeError("failed: " + " ".join(cmd))
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         list(ex.map(run, jobs))
@@ -71,6 +76,11 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if force or _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "lps.h")]):
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        run([os.environ.get("CC") or "gcc", "-O2", "-std=gnu11", "-Wall", "-Wextra", "-Wno-cast-function-type", "-shared", "-fPIC",
+             f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", MARSHAL_SRC, f"-L{HERE}", "-l:liblps.so", "-Wl,-rpath,$ORIGIN", "-o", tmp])
+        os.replace(tmp, MARSHAL)
     return LIB
 
 

@@ -112,3 +112,24 @@ def test_wrappers_refuse_cpu_tensors():
         lps.kv_rows_append(k, k, [0, 2, 4], kc, kc[:1], [0, 0])
     with pytest.raises(ValueError):
         lps.kv_rows_accept(kc, kc[:1], [0, 0], np.zeros((2, 4), np.int32), np.zeros(2, np.int32))
+
+
+def test_wrappers_read_host_integers():
+    """Lists, arrays of 32 and 64 bits, strided arrays and CPU tensors are host integers; floats, booleans, two
+    axes, too many values and values past 32 bits are not. Each call is refused for its tensors or for its
+    integers, so what the message names tells which was reached."""
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16)
+    from layer_pipeline_staged_gb300 import ops
+    ops._ready()
+    # CPU tensors are refused before the integers are read, by every wrapper
+    for call in (lambda: lps.kv_rows_append(k, k, [0, 2, 4], kc, kc.clone(), [0, 0]),
+                 lambda: lps.attention_prompt_packed(k, k, k, np.array([0, 4])),
+                 lambda: lps.attention_tree_verify(kc, kc, kc, torch.zeros(2, 2, dtype=torch.int32), [0, 0], [1, 1]),
+                 lambda: lps.kv_rows_accept(kc, kc.clone(), [0, 0], torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for bad in (None, 3, "q", np.zeros((4, 2, 64))):
+        with pytest.raises(TypeError):
+            lps.attention_prompt_packed(bad, k, k, [0, 4])

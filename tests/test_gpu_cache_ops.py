@@ -602,6 +602,35 @@ def test_prompt_append_verify_accept_decode():
     assert ((got[0].double().view(-1) - ref[0].double()).abs() <= 2 * tol.view(-1)).all()
 
 
+def test_host_integers_of_every_kind():
+    """Offsets as a list, a tuple, arrays of several types and strides, and CPU tensors: the same bits; what is
+    not a row of integers that fit 32 bits is refused."""
+    g, nq, nkv, hd = _gen(3), 4, 2, 64
+    q, k, v = (_randn(g, 50, h, hd, dtype=torch.bfloat16) for h in (nq, nkv, nkv))
+    ref = lps.attention_prompt_packed(q, k, v, [0, 20, 50])
+    wide = np.array([0, 7, 20, 7, 50, 7], np.int32)
+    for off in ((0, 20, 50), np.array([0, 20, 50]), np.array([0, 20, 50], np.int32), np.array([0, 20, 50], np.uint8), wide[::2],
+                np.array([50, 20, 0])[::-1], torch.tensor([0, 20, 50]), torch.tensor([0, 20, 50], dtype=torch.int32),
+                [np.int64(0), 20, np.int16(50)], range(0, 51, 10)):
+        got = lps.attention_prompt_packed(q, k, v, off)
+        assert torch.equal(got, ref) or isinstance(off, range)
+    many = [0] * 300 + [50]
+    assert torch.equal(lps.attention_prompt_packed(q, k, v, many), lps.attention_prompt_packed(q, k, v, [0, 50]))
+    for off in ([0.0, 50.0], np.array([0.0, 50.0]), np.array([False, True]), np.array([[0, 50]]), [0, 2**31], np.array([0, 2**40]),
+                [], torch.tensor([0, 50]).cuda(), ["0", "50"], np.array(50)):
+        with pytest.raises(ValueError):
+            lps.attention_prompt_packed(q, k, v, off)
+    with pytest.raises(TypeError):
+        lps.attention_prompt_packed(q, k, v, None)
+    with pytest.raises(TypeError):
+        lps.attention_prompt_packed(q, k, v, [0, 50], scale="1")
+    with torch.no_grad():
+        assert torch.equal(lps.attention_prompt_packed(q.clone().requires_grad_(), k, v, [0, 20, 50]), ref)
+    empty = lps.attention_prompt_packed(q[:0], k[:0], v[:0], [0, 0])
+    assert empty.shape == (0, nq, hd)
+    assert lps.attention_prompt_packed(q, k, v, [0]).shape == q.shape
+
+
 # ---- refusals with real buffers --------------------------------------------------------------------
 
 def test_refusals_of_tensors():
