@@ -3,6 +3,7 @@
 // (accept). Both only move bytes, so both are bound by HBM when they are large
 // and by the launch when they are small.
 #include "cache_ops.h"
+#include "ptx.cuh"
 
 namespace lps {
 namespace {
@@ -16,6 +17,7 @@ constexpr int kThreads = 256;
 // a 64-bit division each took 17.8 us.
 template <int UNITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  pdl_launch_dependents();
   constexpr int kLanes = UNITS < kThreads ? UNITS : kThreads;  // threads of one token
   constexpr int kWays = kThreads / kLanes, kEach = 4;
   const int units = p.nkv * p.chunks;
@@ -26,6 +28,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int tok0 = p.off[0] + static_cast<int>(blockIdx.x) * (kWays * kEach) + static_cast<int>(threadIdx.x) / kLanes;
   uint4 k[kEach], v[kEach];
   size_t dst[kEach];
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int tok = tok0 + i * kWays;
@@ -61,6 +64,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 constexpr int kAhead = 8;
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ AcceptParams p) {
   __shared__ int path[kTreeMax];
+  pdl_launch_dependents();
+  pdl_wait();
   const int b = blockIdx.x, l = blockIdx.y >> 1;
   const int t = threadIdx.x;
   const int n = p.accepted[b], pos = p.pos[b];
@@ -86,16 +91,31 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   }
 }
 
+// Launched so that its start runs under the stream's last kernel; the kernels
+// touch global memory behind the dependency wait.
+template <class Kern, class Params>
+cudaError_t launch(Kern kern, dim3 grid, const Params& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int UNITS>
 cudaError_t launch_append_t(const AppendParams& p, cudaStream_t s) {
   constexpr int kLanes = UNITS < kThreads ? UNITS : kThreads;
   constexpr int kTokens = kThreads / kLanes * 4;
   const int tokens = p.off[p.n_seqs] - p.off[0];
   const int units = p.nkv * p.chunks;
-  append_kernel<UNITS><<<dim3(static_cast<unsigned>((static_cast<long long>(tokens) + kTokens - 1) / kTokens),
-                              (units + kLanes - 1) / kLanes),
-                         kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch(append_kernel<UNITS>,
+                dim3(static_cast<unsigned>((static_cast<long long>(tokens) + kTokens - 1) / kTokens), (units + kLanes - 1) / kLanes),
+                p, s);
 }
 
 }  // namespace
@@ -115,8 +135,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
 
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s) {
   const int units = p.nkv * p.chunks;
-  accept_kernel<<<dim3(p.batch, 2 * p.layers, (units + kThreads - 1) / kThreads), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch(accept_kernel, dim3(p.batch, 2 * p.layers, (units + kThreads - 1) / kThreads), p, s);
 }
 
 }  // namespace lps

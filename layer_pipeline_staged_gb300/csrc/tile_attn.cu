@@ -79,6 +79,10 @@ constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
 constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
+// A launch of up to so many CTAs starts under the stream's last kernel (18 tokens,
+// call after call: 5.6 -> 4.6 us); of more, its early CTAs only wait on SMs that
+// the last one's could use (7 prompts, 296 CTAs: 22.15 us so, 22.5 started early).
+constexpr int kEarlyCtas = 128;
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
 constexpr int kKid = kKidTileAttn << 8;
 
@@ -453,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool solo = TREE && p.solo;
 
+  pdl_launch_dependents();
   if (tid == 32 * 8) {
     prefetch_map(&p.tmap_q);
     prefetch_map(&p.tmap_k);
@@ -487,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     tmem_alloc(tmem_base, 512);
     tmem_relinquish();
   }
+  pdl_wait();  // the set-up above runs under the stream's last kernel; all global memory is behind this
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1031,18 +1037,21 @@ cudaError_t prepare_t() {
   return regs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidKernelImage;
 }
 
-template <bool BF16, int HD>
-cudaLaunchConfig_t tree_config(int cluster, long long ctas, cudaStream_t s, cudaLaunchAttribute* attr) {
+// attr: two attributes; a cluster of 1 is none.
+template <int HD>
+cudaLaunchConfig_t config_of(int cluster, long long ctas, cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<HD>::kSmem;
   cfg.stream = s;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = cluster;
-  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = cluster > 1 || ctas <= kEarlyCtas;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cfg;
 }
 
@@ -1062,8 +1071,10 @@ cudaError_t active_t(const int** out) {
     if ((e = prepare_t<BF16, HD, true>()) != cudaSuccess) return e;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
     for (int i = 0; i < kClusterSizes; ++i) {
-      cudaLaunchAttribute attr;
-      const cudaLaunchConfig_t cfg = tree_config<BF16, HD>(1 << i, 1 << i, nullptr, &attr);
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = config_of<HD>(1 << i, 1 << i, nullptr, attr);
+      cfg.attrs = attr + 1;  // the cluster alone
+      cfg.numAttrs = 1;
       if (cudaOccupancyMaxActiveClusters(&active[dev][i], kern, &cfg) != cudaSuccess) {
         cudaGetLastError();
         active[dev][i] = 0;
@@ -1079,14 +1090,15 @@ template <bool BF16, int HD>
 cudaError_t launch_prompt_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
   const cudaError_t e = prepare_t<BF16, HD, false>();
   if (e != cudaSuccess) return e;
-  tile_attn_kernel<BF16, HD, false><<<static_cast<unsigned>(ctas), kThreads, Shape<HD>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config_of<HD>(1, ctas, s, attr);
+  return cudaLaunchKernelEx(&cfg, tile_attn_kernel<BF16, HD, false>, p);
 }
 
 template <bool BF16, int HD>
 cudaError_t launch_tree_t(const TileAttnParams& p, long long ctas, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = tree_config<BF16, HD>(p.cluster, ctas, s, &attr);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config_of<HD>(p.cluster, ctas, s, attr);
   return cudaLaunchKernelEx(&cfg, tile_attn_kernel<BF16, HD, true>, p);
 }
 
