@@ -331,6 +331,15 @@ static int argc_is(Py_ssize_t n, Py_ssize_t want) {
   return -1;
 }
 
+/* A library call without the interpreter lock: a launch waits while the stream's
+ * queue is full, and what the queue waits for may need the lock. */
+#define UNLOCKED(call)                     \
+  __extension__({                          \
+    int rc_;                               \
+    Py_BEGIN_ALLOW_THREADS rc_ = (call);   \
+    Py_END_ALLOW_THREADS rc_;              \
+  })
+
 /* ---- the calls --------------------------------------------------------------------- */
 
 /* prompt(q, k, v, offsets, out, scale) -> out */
@@ -363,8 +372,8 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (out && off.n > 1 && q->shape[0] > 0) {
     const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[3].stride[0], t[3].stride[1]};
     if (enter(&at, q->device) ||
-        leave(&at, attention_prompt_packed(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)(off.n - 1), off.v, (int)q->shape[1],
-                                           (int)k->shape[1], (int)q->shape[2], st, (float)scale, at.stream)))
+        leave(&at, UNLOCKED(attention_prompt_packed(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)(off.n - 1), off.v, (int)q->shape[1],
+                                           (int)k->shape[1], (int)q->shape[2], st, (float)scale, at.stream))))
       Py_CLEAR(out);
   }
   ints_free(&off);
@@ -405,9 +414,9 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
       (out = output_like(args[6], q, &t[3]))) {
     const int64_t st[6] = {q->stride[0], q->stride[1], q->stride[2], t[3].stride[0], t[3].stride[1], t[3].stride[2]};
     if (enter(&at, q->device) ||
-        leave(&at, attention_tree_verify(q->ptr, kc->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, (int)width, pos.v, rows.v, par.ptr,
+        leave(&at, UNLOCKED(attention_tree_verify(q->ptr, kc->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, (int)width, pos.v, rows.v, par.ptr,
                                          (int)q->shape[2], (int)kc->shape[1], (int)q->shape[3], (int)kc->shape[2], st, (float)scale,
-                                         at.stream)))
+                                         at.stream))))
       Py_CLEAR(out);
   }
   ints_free(&pos);
@@ -445,8 +454,8 @@ static PyObject *append(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     } else {
       const int64_t st[4] = {k->stride[0], k->stride[1], t[1].stride[0], t[1].stride[1]};
       ok = !enter(&at, k->device) &&
-           !leave(&at, kv_rows_append(k->ptr, t[1].ptr, (int)kc->shape[0], off.v, kc->ptr, t[3].ptr, start.v, (int)k->shape[1],
-                                      (int)k->shape[2], (int)kc->shape[2], st, at.stream));
+           !leave(&at, UNLOCKED(kv_rows_append(k->ptr, t[1].ptr, (int)kc->shape[0], off.v, kc->ptr, t[3].ptr, start.v, (int)k->shape[1],
+                                      (int)k->shape[2], (int)kc->shape[2], st, at.stream)));
     }
   }
   ints_free(&off);
@@ -476,8 +485,8 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   int ok = 0;
   if (!ints_from(args[2], s[0], "pos", &pos))
     ok = !enter(&at, kc->device) &&
-         !leave(&at, kv_rows_accept(kc->ptr, t[1].ptr, (int)layers, (int)s[0], (int)s[1], (int)s[3], (int)s[2], pos.v,
-                                    (int)path.shape[1], path.ptr, taken.ptr, at.stream));
+         !leave(&at, UNLOCKED(kv_rows_accept(kc->ptr, t[1].ptr, (int)layers, (int)s[0], (int)s[1], (int)s[3], (int)s[2], pos.v,
+                                    (int)path.shape[1], path.ptr, taken.ptr, at.stream)));
   ints_free(&pos);
   if (!ok) return NULL;
   Py_RETURN_NONE;

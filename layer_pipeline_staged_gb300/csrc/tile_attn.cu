@@ -1139,12 +1139,13 @@ static long long blocks_of(const TileAttnParams& p, int s) {
 
 // Work items of a tree launch: one cluster per (sequence, pair of tiles, kv
 // head), which shares out the sequence's key blocks. The cluster's size is the
-// one with the shortest modelled time in units of a block: the longest CTA, two
-// in a row, or all clusters' work over those that run at once, whichever is
-// most; a CTA costs about kStart blocks to start and finish, and kJoin more
-// where it is joined.
+// one with the shortest modelled time in units of an iteration (a block, or a
+// solo tile's two): the longest CTA, two in a row, or all clusters' work over
+// those that run at once, whichever is most; a CTA costs about kStart of them to
+// start and finish, and kJoin more where it is joined. The smaller of two that
+// are level.
 cudaError_t tile_tree_plan(TileAttnParams& p, bool bf16, int hd, long long* ctas) {
-  constexpr long long kStart = 4, kJoin = 2;
+  constexpr long long kStart = 2, kJoin = 2;
   p.tpt = kRows / p.group;
   int blocks[kOpSeqs], most_rows = 0;
   for (int s = 0; s < p.n_seqs; ++s) {
@@ -1175,7 +1176,8 @@ cudaError_t tile_tree_plan(TileAttnParams& p, bool bf16, int hd, long long* ctas
     long long total = 0, longest = 0, seen = 0, second = 0;
     for (int s = 0; s < p.n_seqs; ++s) {
       if (!p.len[s]) continue;
-      const long long each = (blocks_of(p, s) + size - 1) / size + fixed;
+      const int share = p.solo ? 2 * size : size;
+      const long long each = (blocks_of(p, s) + share - 1) / share + fixed;
       const long long n = ((s + 1 < p.n_seqs ? p.item0[s + 1] : clusters) - p.item0[s]) * p.nkv;
       longest = std::max(longest, each);
       total += n * each;
