@@ -13,8 +13,8 @@ constexpr int kThreads = 256;
 // Block = kTokens consecutive tokens and kThreads of a token's 16-byte units;
 // thread = one unit (kv head, column) of its token, of K and of V, for every
 // kWays-th of the block's tokens. All its loads are issued before its stores.
-// 12185 tokens of 8 heads of 128 (100 MB read and written): a thread a unit with
-// a 64-bit division each took 17.8 us.
+// 12185 tokens of 8 heads of 128 (100 MB read and written) take 16.0 us, 6.2
+// TB/s; a thread a unit with a 64-bit division each took 17.8.
 template <int UNITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
   pdl_launch_dependents();

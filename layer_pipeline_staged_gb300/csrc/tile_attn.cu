@@ -48,14 +48,16 @@
 //     as the products keep shared memory busy (256 KB an iteration at 128 bytes a
 //     cycle), and an item's end about 6000 (its last P.V, and 32 rows a warp
 //     stored row by row);
-//   - 26 drafts over 8176 rows, 8 kv heads (33.5 MB): 16.3 us, of which 2.2 until
-//     the first S, 6.7 for the blocks, 5 for the join and its barriers.
+//   - 26 drafts over 8176 rows, 8 kv heads (33.5 MB): 16 us, of which 2.2 until
+//     the first S, 6.5 for the blocks, 5 for the join and its barriers.
 // Tried and slower: one warp for all MMAs (its waits and commits leave the tensor
 // core idle, 428 us), two without turns (they fall into step, 495), P in two halves
 // (413), two threads a row (a row's exp2 is bound to its quarter of the SM either
 // way, 399), hardware barriers instead of mbarriers (389), output warps of their
-// own (too few registers left for the softmax, 410), one key chunk per CTA with
-// partials in global memory and a merge kernel (tree of 26: 22 us).
+// own (too few registers left for the softmax, 410), waits that only spin (385 to
+// 399) or that suspend for longer (383), S's upper half ahead (413). Trees of 26
+// drafts: one key chunk per CTA with partials in global memory and a merge kernel 22
+// us, parts sent to their CTA by stores 16.2, by bulk copies 17.1.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
