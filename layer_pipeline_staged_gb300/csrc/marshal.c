@@ -221,7 +221,15 @@ sequence:;
   } else if (!ints_room(a, len)) {
     rc = 0;
     for (Py_ssize_t i = 0; i < len && !rc; ++i) {
-      PyObject *x = PyNumber_Index(PySequence_Fast_GET_ITEM(seq, i));
+      if (i >= PySequence_Fast_GET_SIZE(seq)) { /* an item's __index__ is any code */
+        PyErr_Format(PyExc_ValueError, "%s changed while it was read", what);
+        rc = -1;
+        break;
+      }
+      PyObject *item = PySequence_Fast_GET_ITEM(seq, i);
+      Py_INCREF(item);
+      PyObject *x = PyNumber_Index(item);
+      Py_DECREF(item);
       int over = 0;
       const long long y = x ? PyLong_AsLongLongAndOverflow(x, &over) : 0;
       Py_XDECREF(x);

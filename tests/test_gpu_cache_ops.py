@@ -13,6 +13,7 @@ and n keys:
 The row moves copy bits: they are compared exactly.
 """
 import math
+import os
 
 import numpy as np
 import pytest
@@ -629,6 +630,61 @@ def test_host_integers_of_every_kind():
     empty = lps.attention_prompt_packed(q[:0], k[:0], v[:0], [0, 0])
     assert empty.shape == (0, nq, hd)
     assert lps.attention_prompt_packed(q, k, v, [0]).shape == q.shape
+
+
+class _Emptying:
+    """An integer whose __index__ empties the list that holds it."""
+
+    def __init__(self, values):
+        self.values = values
+
+    def __index__(self):
+        self.values.clear()
+        return 0
+
+
+def test_host_integers_that_change_while_they_are_read():
+    q = torch.zeros(4, 2, 64, device="cuda", dtype=torch.bfloat16)
+    values = [0] * 40
+    values[0] = _Emptying(values)
+    with pytest.raises(ValueError, match="changed"):
+        lps.attention_prompt_packed(q, q, q, values)
+
+
+_FIRST_CALL = """
+import torch, layer_pipeline_staged_gb300 as lps
+def t(*shape): return torch.randn(*shape, device="cuda", generator=gen).to(torch.bfloat16)
+gen = torch.Generator("cuda").manual_seed(5)
+q, k, v, kc, vc, tq = t(70, 8, 128), t(70, 2, 128), t(70, 2, 128), t(1, 2, 400, 128), t(1, 2, 400, 128), t(1, 3, 8, 128)
+par = torch.tensor([[-1, 0, -1]], dtype=torch.int32, device="cuda")
+path, taken = torch.tensor([[1, 2]], dtype=torch.int32, device="cuda"), torch.tensor([2], dtype=torch.int32, device="cuda")
+po, to = torch.zeros_like(q), torch.zeros_like(tq)
+def step():
+    lps.attention_prompt_packed(q, k, v, [0, 30, 70], out=po)
+    lps.kv_rows_append(k, v, [0, 70], kc, vc, [200])
+    lps.attention_tree_verify(tq, kc, vc, par, [300], [3], out=to)
+    lps.kv_rows_accept(kc, vc, [300], path, taken)
+first = kc.clone(), vc.clone()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+assert not po.any() and torch.equal(kc, first[0])
+graph.replay()
+got = po.clone(), to.clone(), kc.clone(), vc.clone()
+kc.copy_(first[0]), vc.copy_(first[1]), po.zero_(), to.zero_()
+step()
+assert all(torch.equal(a, b) for a, b in zip(got, (po, to, kc, vc))) and po.any() and to.any()
+print("same")
+"""
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls are made during a capture: what the library sets up once does not break it."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=240)
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stderr[-2000:]
 
 
 # ---- refusals with real buffers --------------------------------------------------------------------
