@@ -133,6 +133,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// 32 columns of 16 TMEM lanes (taddr's on): of lane t / 4 the columns 8i + 2 (t % 4)
+// and the next in r[4i] and r[4i + 1], of lane t / 4 + 8 in r[4i + 2] and r[4i + 3].
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // Wait for this thread's loads; v's uses stay behind the wait.
 template <int N>
 __device__ __forceinline__ void tmem_wait_ld(float* v) {
@@ -881,10 +890,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       }
       const bool seen = row_ok && (!TREE || anc != 0);  // a draft of a broken chain sees nothing
       const bool fix = dirty[no & 1] == no + 1;
-      // 32 columns of o from c on, with the infinities and NaNs of the V blocks made safe
-      auto load_o = [&](int c, float* o) {
-        tmem_ld32(o_addr + c, o);
-        tmem_wait_ld<32>(o);
+      // adds the infinities and NaNs of the V blocks made safe to o's 32 columns from c on
+      auto mend_o = [&](int c, float* o) {
         if (fix && seen) {
           const uint16_t* v =
               static_cast<const uint16_t*>(p.v) + it.tok0 * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head + c;
@@ -902,28 +909,71 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           }
         }
       };
+      auto load_o = [&](int c, float* o) {
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld<32>(o);
+        mend_o(c, o);
+      };
       if (ok && warp_ok && !joined) {
         if (nb > 0) {
-          // a thread writes its row, whole 32-byte sectors at a time where out
-          // is so aligned: a warp's store goes out row by row
           const float inv = seen ? 1.0f / l : 0.f;
           uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
+          if (HD == 128 && p.wide_out) {
+            // A thread has a row, and 32 rows are 32 lines a store. So the rounded
+            // row goes back to TMEM, over columns of o already read, and comes out
+            // four lanes to a row, 32 bytes each: eight whole lines a store (7 prompts
+            // up to 1024, 32/8 heads of 128: 21.5 us so, 22.3 row by row; of 8184
+            // tokens 374 and 377; rows of 64, 30.5 and 30.0, stay as they are).
+            const unsigned long long mine = row_ok ? reinterpret_cast<unsigned long long>(out) : 0;
+            uint16_t* to[4];  // rows 8i + lane / 4
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2)));
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            load_o(c, o);
-            if (row_ok) {
-              uint32_t w[16];
+            for (int c = 0; c < HD; c += 64) {
+              uint32_t w[32];  // word 8q + 2i + e of the row's 32, which lane q of four gets as its (2i + e)th
+              float o[64];
+              tmem_ld32(o_addr + c, o);
+              tmem_ld32(o_addr + c + 32, o + 32);
+              tmem_wait_ld<64>(o);
+              mend_o(c, o);
+              mend_o(c + 32, o + 32);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = seen ? pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-              if (p.wide_out) {
-                st_global32(out + c, w);
-                st_global32(out + c + 16, w + 8);
-              } else {
+              for (int k = 0; k < 32; ++k)
+                w[k % 8 / 2 * 8 + k / 8 * 2 + k % 2] = seen ? pack16<BF16>(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+              tmem_st16(o_addr + c, w);
+              tmem_st16(o_addr + c + 16, w + 16);
+              tmem_wait_st();
+              __syncwarp();
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+              for (int h = 0; h < 2; ++h) tmem_ld_quads(o_addr + (static_cast<uint32_t>(16 * h) << 16) + c, w + 16 * h);
+              tmem_wait_ld<32>(reinterpret_cast<float*>(w));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = w[i / 2 * 16 + e / 2 * 4 + i % 2 * 2 + e % 2];
+                if (to[i]) st_global32(to[i] + c + 16 * (lane & 3), x);
+              }
+            }
+          } else {
+            // a thread writes its row, 32 bytes at a time where out is so aligned
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              load_o(c, o);
+              if (row_ok) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = seen ? pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+                if (HD == 64 && p.wide_out) {
+                  st_global32(out + c, w);
+                  st_global32(out + c + 16, w + 8);
+                } else {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                }
               }
             }
           }
