@@ -41,13 +41,12 @@
 // Waits are bounded and report through the status word.
 //
 // What bounds it, on one GB300 (cuBLAS bf16 1865 TFLOP/s, copy 6793 GB/s):
-//   - an 8184-token prompt, 32/8 heads of 128: 375 us, 1465 TFLOP/s. A paired
+//   - an 8184-token prompt, 32/8 heads of 128: 370 us, 1483 TFLOP/s. A paired
 //     iteration (two tiles x 128 keys) is 2048 cycles of products at the tensor
 //     core's rate and takes 2900 to 3300: a block's softmax is 1160 cycles (the
 //     hardware's exp2 alone 512), hand-overs between the warps 250 to 300 each,
 //     as the products keep shared memory busy (256 KB an iteration at 128 bytes a
-//     cycle), and an item's end about 6000 (its last P.V, and 32 rows a warp
-//     stored row by row);
+//     cycle), and an item's end about 6000 (its last P.V, its rows' way out);
 //   - 26 drafts over 8176 rows, 8 kv heads (33.5 MB): 16 us, of which 2.2 until
 //     the first S, 6.5 for the blocks, 5 for the join and its barriers.
 // Tried and slower: one warp for all MMAs (its waits and commits leave the tensor
@@ -85,7 +84,7 @@ constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
 // call after call: 5.6 -> 4.6 us); of more, its early CTAs only wait on SMs that
 // the last one's could use (7 prompts, 296 CTAs: 22.15 us so, 22.5 started early).
 constexpr int kEarlyCtas = 128;
-constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of 2^8
+constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of about 2^8
 constexpr int kKid = kKidTileAttn << 8;
 
 __device__ int g_status[2];       // sticky: error kinds, first report
@@ -784,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     const int row_tok = r / p.group, row_head = r % p.group;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tS[slot] + lane_off, o_addr = tO[slot] + lane_off;
-    const float sl2 = p.scale_log2;
+    const float sl2 = p.scale_log2, slack = kStale / sl2;  // in units of S, off the chain of the maximum: 372 -> 369 us
     bool ok = true;
     int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
     for (int no = 0; ok && item_there(no); ++no) {
@@ -839,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           if (i == 0) {
             m = top;
-          } else if (__any_sync(0xffffffffu, row_ok && (top - m) * sl2 > kStale)) {  // rows without a query have no say
+          } else if (__any_sync(0xffffffffu, row_ok && top > m + slack)) {  // rows without a query have no say
             // O holds the blocks before this one, whole: S of this block was
             // issued behind their P.V
             const float f = top > m ? ex2((m - top) * sl2) : 1.0f;
