@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     const int row_tok = r / p.group, row_head = r % p.group;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tS[slot] + lane_off, o_addr = tO[slot] + lane_off;
-    const float sl2 = p.scale_log2, slack = kStale / sl2;  // in units of S, off the chain of the maximum: 372 -> 369 us
+    const float sl2 = p.scale_log2, slack = kStale / sl2;  // in units of S
     bool ok = true;
     int ns = 0, no_o = 0;  // S blocks and finished accumulators so far
     for (int no = 0; ok && item_there(no); ++no) {
@@ -806,7 +806,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       }
       const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
       const int nb = blocks_of(it, slot);
-      float m = -INFINITY, l = 0.f;
+      // the row's base, sum, -base sl2 and the maximum that moves the base, which
+      // a row decides for itself: what its warp's other rows see changes nothing
+      float m = -INFINITY, l = 0.f, neg = 0.f, bar = -INFINITY;
+      auto rebase = [&](float to) {
+        m = to;
+        neg = to == -INFINITY ? 0.f : -to * sl2;
+        bar = to + slack;
+      };
       for (int i = 0; i < nb && ok; ++i, ++ns) {
         const int kb = b0 + (solo ? 2 * i + slot : i);
         ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
@@ -835,15 +842,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[e + q], e + 4 + q < kRows ? x[e + 4 + q] : x[e + q]);
           }
-          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          const float block = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (i == 0) {
-            m = top;
-          } else if (__any_sync(0xffffffffu, row_ok && top > m + slack)) {  // rows without a query have no say
+            rebase(block);
+          } else if (__any_sync(0xffffffffu, row_ok && block > bar)) {  // rows without a query have no say
             // O holds the blocks before this one, whole: S of this block was
             // issued behind their P.V
-            const float f = top > m ? ex2((m - top) * sl2) : 1.0f;
+            const bool stale = block > bar;
+            const float f = stale ? ex2((m - block) * sl2) : 1.0f;
             l *= f;
-            m = top;
+            if (stale) rebase(block);
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
               float o[32];
@@ -855,7 +863,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
               tmem_st16(o_addr + c + 16, reinterpret_cast<const uint32_t*>(o) + 16);
             }
           }
-          const float neg = m == -INFINITY ? 0.f : -m * sl2;
           const F2 sl = pack2(sl2, sl2), ng = pack2(neg, neg);
           F2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll

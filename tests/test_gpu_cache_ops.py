@@ -322,6 +322,31 @@ def test_tree_unseen_drafts_change_nothing(pos):
         assert not torch.isfinite(got[:, [1, 3]]).any()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_far_larger_scores_of_other_rows_change_no_bit(hd):
+    """Later tokens of a prompt and another branch's drafts with finite keys whose scores are far above a row's
+    own: the row has the bits that it has without them, rows that see them beside it in its tile or not."""
+    nq, nkv, n, g = 8, 2, 400, _gen(12)
+    q, k, v = (_randn(g, n, h, hd, dtype=torch.bfloat16) for h in (nq, nkv, nkv))
+    clean = lps.attention_prompt_packed(q, k, v, [0, n])
+    for at in (135, 150, 259, 300):
+        k2 = k.clone()
+        k2[at:] *= 40
+        got = lps.attention_prompt_packed(q, k2, v, [0, n])
+        assert torch.equal(got[:at], clean[:at]) and not torch.equal(got[at:], clean[at:])
+        check_prompt(q, k2, v, np.array([0, n], np.int32), got)
+    parents = np.array([[-1, -1, 0, 1, 2, -1]], np.int32)  # 0-2-4 and 1-3, and 5 alone
+    pd = torch.from_numpy(parents).cuda()
+    for pos in (5, 300, 2000):
+        tq, kc, vc, _, p, r = tree_case(9, [pos], [6], 6, nq, nkv, hd, torch.bfloat16)
+        kc[:, :, :pos] *= 0.05
+        clean = lps.attention_tree_verify(tq, kc, vc, pd, p, r)
+        kc[:, :, pos + 1] *= 40
+        got = lps.attention_tree_verify(tq, kc, vc, pd, p, r)
+        assert torch.equal(got[:, [0, 2, 4, 5]], clean[:, [0, 2, 4, 5]]) and not torch.equal(got[:, [1, 3]], clean[:, [1, 3]])
+        check_tree(tq, kc, vc, parents, p, r, got)
+
+
 def test_tree_bad_parents_give_zeros():
     q, kc, vc, _, p, r = tree_case(8, [200, 3], [8, 8], 8, 4, 2, 64, torch.float16)
     parents = np.array([[-1, 0, 5, 2, 1, -2, 6, 3], [-1, 99, 1, 0, -2147483648, 2147483647, 3, 0]], np.int32)
