@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     if (warp == 8) {
       // ---------------- TMA ----------------
       if (lane == 0) {
-        int n = 0, nq[2] = {0, 0}, nf = 0;
+        int n = 0, nq[2] = {0, 0}, nf = 0, asks = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           if (ok && !mbar_wait(bar, parity)) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (ok) {
             mbar_arrive_expect_tx(asked, 16);
             take_next(answer, asked);
-            wait(asked, static_cast<uint32_t>(no & 1));
+            wait(asked, static_cast<uint32_t>(asks++ & 1));
           }
           if (no >= 1) wait(&item_done[place], static_cast<uint32_t>(((no - 1) >> 1) & 1));
           const int idx = ok ? taken(answer) : -1;
@@ -591,8 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           else items[place].idx = -1;
           mbar_arrive(&item_full[place]);
         }
-        // every copy issued lands before the CTA may end
-        bool landed = true;
+        // every copy issued, and the answer to every take-over asked for, lands
+        // before the CTA may end
+        bool landed = asks == 0 || mbar_wait(asked, static_cast<uint32_t>((asks - 1) & 1), kDrainLimitCycles);
         for (int t = 0; t < 2; ++t)
           if (nq[t] > 0) landed &= mbar_wait(&qfull[t], static_cast<uint32_t>((nq[t] - 1) & 1), kDrainLimitCycles);
         for (int m = max(n - NS, 0); m < n; ++m)
