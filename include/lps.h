@@ -562,6 +562,13 @@ int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_
  * invalid; the word is then cleared. It is shared by all calls on the device. */
 int cache_ops_status(void* stream);
 
+/* Test hook, like model_set_wait_limit: the SM cycles that a bounded wait of the
+ * two attention kernels may take, in calls that the calling thread makes from
+ * now on, before the kernel gives up, records an error and returns; 0 restores
+ * the default of about two seconds. A kernel that gives up still waits, with its
+ * own fixed bound, for what it has issued. LPS_EINVAL for cycles < 0. */
+int cache_ops_set_wait_limit(long long cycles);
+
 #ifdef __cplusplus
 }
 #endif

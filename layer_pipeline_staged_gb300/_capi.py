@@ -40,7 +40,7 @@ EXPORTS = (
     "attention_decode_noalloc_scratch_bytes", "model_trace_enable", "model_trace_read", "model_trace_disable",
     "stage_plan_solve", "model_stage_bytes", "model_set_wait_limit", "attention_decode_noalloc_status",
     "model_prefill", "attention_prompt_packed", "attention_tree_verify",
-    "kv_rows_append", "kv_rows_accept", "cache_ops_status",
+    "kv_rows_append", "kv_rows_accept", "cache_ops_status", "cache_ops_set_wait_limit",
 )
 
 
@@ -136,6 +136,7 @@ def load(path: str = LIB_PATH):
         "attention_tree_verify": (i, [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, vp, f, vp]),
         "kv_rows_append": (i, [vp, vp, i, vp, vp, vp, vp, i, i, i, vp, vp]),
         "cache_ops_status": (i, [vp]),
+        "cache_ops_set_wait_limit": (i, [ctypes.c_longlong]),
         "kv_rows_accept": (i, [vp, vp, i, i, i, i, i, vp, i, vp, vp, vp]),
         "stage_plan_solve": (i, [i, i, vp, vp, vp, vp, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_int64)]),
         "model_stage_bytes": (i, [ctypes.POINTER(ModelDesc), vp, vp, ctypes.POINTER(ctypes.c_uint64),

@@ -1,6 +1,6 @@
 // Entry points of the operators over a caller-owned cache: argument checks,
 // tensor maps and launches. Nothing here synchronises, allocates device memory
-// or keeps anything between calls. Lengths, offsets and positions are host
+// or keeps anything between calls (a test's wait limit apart). Lengths, offsets and positions are host
 // arrays that travel in the kernel parameters (so a captured launch keeps the
 // values it was captured with); a tree's parents and an accepted path are
 // device arrays, as a drafter and a sampler on the GPU leave them, and the
@@ -17,6 +17,7 @@
 #include "cache_ops.h"
 #include "kernels.h"
 #include "lps.h"
+#include "ptx.cuh"
 
 namespace lps {
 int host_fail(int code, const char* fn, const std::string& why);
@@ -107,6 +108,9 @@ bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Test hook: the wait limit of the calling thread's later calls.
+thread_local long long g_wait_limit = 0;
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Rows and tokens are counted in 32 bits, a block of keys past the last one included.
@@ -146,6 +150,7 @@ extern "C" int attention_prompt_packed(const void* q, const void* k, const void*
       p.v_row = st[4], p.v_head = st[5], p.o_tok = st[6], p.o_head = st[7];
       p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
       p.wide_out = wide(out, {st[6], st[7]});
+      p.wait_limit = wait_cycles(g_wait_limit);
       p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
       for (int s = 0; s < p.n_seqs; ++s) {
         p.tok0[s] = offsets[s0 + s];
@@ -215,6 +220,7 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     p.k_seq = p.v_seq = p.k_head * n_kv_heads;
     p.parents = parents;
     p.wide_out = wide(out, {st[3], st[4], st[5]});
+    p.wait_limit = wait_cycles(g_wait_limit);
     p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
     const long long kv_n[3] = {max_ctx, n_kv_heads, batch}, kv_st[3] = {p.k_row, p.k_head, p.k_seq};
     if (!encode4(&p.tmap_q, bf16, q, head_dim, {n_q_heads, width, batch}, {st[2], st[1], st[0]}, p.group, p.tpt) ||
@@ -291,6 +297,12 @@ extern "C" int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int ba
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("launch: ") + cudaGetErrorString(e));
     return LPS_OK;
   });
+}
+
+extern "C" int cache_ops_set_wait_limit(long long cycles) {
+  if (cycles < 0) return host_fail(LPS_EINVAL, "cache_ops_set_wait_limit", "cycles must be >= 0");
+  g_wait_limit = cycles;
+  return LPS_OK;
 }
 
 extern "C" int cache_ops_status(void* stream) {

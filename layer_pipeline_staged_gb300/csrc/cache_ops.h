@@ -36,6 +36,7 @@ struct TileAttnParams {
   int nq, nkv, group, n_seqs;
   float scale_log2;    // scale * log2(e)
   int wide_out;        // out's rows are 32-byte aligned
+  long long wait_limit;  // cycles a wait may take before it reports an error
   int tok0[kOpSeqs], len[kOpSeqs], pos[kOpSeqs];
   // set by the plan
   int tpt;             // tokens of a tile: 128 / group

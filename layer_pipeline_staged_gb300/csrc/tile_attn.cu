@@ -527,8 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   auto item_there = [&](int no) -> bool {
     if (no == 0) return true;
     if (TREE) return false;
-    return __all_sync(0xffffffffu, mbar_wait(&item_full[no & 1], static_cast<uint32_t>(((no - 1) >> 1) & 1))) &&
-           items[no & 1].idx >= 0;
+    if (!__all_sync(0xffffffffu, mbar_wait(&item_full[no & 1], static_cast<uint32_t>(((no - 1) >> 1) & 1), p.wait_limit))) {
+      if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (10 << 13));
+      return false;
+    }
+    return items[no & 1].idx >= 0;
   };
   auto through_with = [&](int no) {
     __syncwarp();
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         int n = 0, nq[2] = {0, 0}, nf = 0, asks = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity)) {
+          if (ok && !mbar_wait(bar, parity, p.wait_limit)) {
             report_error(g_status, kErrWaitEmpty | kKid);
             ok = false;
           }
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           const Item it = items[no & 1];
           const int fix0 = fix0_of(it), mine = blocks_of(it, slot), others = blocks_of(it, slot ^ 1);
           auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-            if (ok && !mbar_wait(bar, parity)) {
+            if (ok && !mbar_wait(bar, parity, p.wait_limit)) {
               report_error(g_status, kErrWaitFull | kKid | (what << 13));
               ok = false;
             }
@@ -732,8 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           // place in the load order of V block j of the item: K blocks are ahead of their V
           const int j = kb - it.b0;
           const int n = n0 + (!solo ? 2 * j + 1 : j <= it.nblk - 2 ? 2 * j + 2 : 2 * it.nblk - 1);
-          ok = __all_sync(0xffffffffu, mbar_wait(&vissued[nf % kMaxFix], static_cast<uint32_t>((nf / kMaxFix) & 1)) &&
-                                           mbar_wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1)));
+          ok = __all_sync(0xffffffffu, mbar_wait(&vissued[nf % kMaxFix], static_cast<uint32_t>((nf / kMaxFix) & 1), p.wait_limit) &&
+                                           mbar_wait(&full[n % NS], static_cast<uint32_t>((n / NS) & 1), p.wait_limit));
           if (!ok) {
             if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (5 << 13));
             break;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       };
       for (int i = 0; i < nb && ok; ++i, ++ns) {
         const int kb = b0 + (solo ? 2 * i + slot : i);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[slot], static_cast<uint32_t>(ns & 1), p.wait_limit));
         if (!ok) {
           if (lane == 0) report_error(g_status, kErrWaitFull | kKid | (6 << 13));
           break;
@@ -890,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&pfull[slot]);
       }
       if (nb > 0 && ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot], static_cast<uint32_t>(no_o & 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot], static_cast<uint32_t>(no_o & 1), p.wait_limit));
         if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (7 << 13));
         ++no_o;
         tc_fence_after();
@@ -988,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       } else if (TREE && joined) {
         // the ring is free once the other slot's products are done too
         if (ok && blocks_of(it, slot ^ 1) > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot ^ 1], 0));
+          ok = __all_sync(0xffffffffu, mbar_wait(&ofull[slot ^ 1], 0, p.wait_limit));
           if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
         }
         const bool here = ok && warp_ok && nb > 0;  // this warp has sums
