@@ -25,12 +25,12 @@ from ._capi import (KERNELS, LPS_EBUSY, LPS_ECUDA, LPS_EINVAL, LPS_ENOMEM, LPS_E
                     LPS_OK, LPS_TYPE_BF16, LPS_TYPE_FP16)
 from ._capi import LpsError
 from ._capi import check as _check
-from .ops import attention_prompt_packed, attention_tree_verify, kv_rows_accept, kv_rows_append
+from .ops import attention_prompt_packed, attention_tree_verify, cache_ops_status, kv_rows_accept, kv_rows_append
 
 __all__ = ["LpsError", "StagePlan", "Model", "Pending", "stage_plan_create", "stage_plan_from_counts",
            "stage_plan_solve", "model_stage_bytes", "model_bind", "decode_step", "decode_step_deferred",
            "pending_wait", "pending_free", "decode_step_device", "load", "attention_prompt_packed",
-           "attention_tree_verify", "kv_rows_append", "kv_rows_accept"]
+           "attention_tree_verify", "kv_rows_append", "kv_rows_accept", "cache_ops_status"]
 
 
 def load():

@@ -94,3 +94,23 @@ def test_wait_limit_is_the_calling_threads():
         assert L.cache_ops_set_wait_limit(0) == lps.LPS_OK
     assert rc == [lps.LPS_OK] and torch.equal(got[0], ref)
     assert L.cache_ops_set_wait_limit(-1) == lps.LPS_EINVAL
+
+
+def test_the_package_reports_a_wait_that_gave_up():
+    """cache_ops_status of the package raises once, on the stream it is asked about, and then is clear."""
+    L, call = _capi.load(), CASES["prompt-128"]()
+    side = torch.cuda.Stream()
+    call()
+    lps.cache_ops_status()
+    side.wait_stream(torch.cuda.current_stream())
+    try:
+        assert L.cache_ops_set_wait_limit(1) == lps.LPS_OK
+        with torch.cuda.stream(side):
+            call()
+    finally:
+        assert L.cache_ops_set_wait_limit(0) == lps.LPS_OK
+    with pytest.raises(lps.LpsError, match="output is invalid") as e:
+        lps.cache_ops_status(side)
+    assert e.value.code == lps.LPS_ECUDA
+    lps.cache_ops_status(side)
+    lps.cache_ops_status()
