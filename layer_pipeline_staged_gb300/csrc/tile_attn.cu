@@ -855,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             const bool stale = block > bar;
             const float f = stale ? ex2((m - block) * sl2) : 1.0f;
             l *= f;
-            if (stale) rebase(block);
+            rebase(stale ? block : m);
+            __syncwarp();
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
               float o[32];
@@ -900,9 +901,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       }
       const bool seen = row_ok && (!TREE || anc != 0);  // a draft of a broken chain sees nothing
       const bool fix = dirty[no & 1] == no + 1;
-      // adds the infinities and NaNs of the V blocks made safe to o's 32 columns from c on
+      // adds the infinities and NaNs of the V blocks made safe to o's 32 columns from
+      // c on. TMEM's instructions want the warp together: so it is brought here, and
+      // behind every loop or store that not all lanes take part in.
       auto mend_o = [&](int c, float* o) {
-        if (fix && seen) {
+        if (!fix) return;  // all lanes alike
+        if (seen) {
           const uint16_t* v =
               static_cast<const uint16_t*>(p.v) + it.tok0 * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head + c;
           for (int i = 0; i < nb; ++i) {
@@ -918,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             }
           }
         }
+        __syncwarp();
       };
       auto load_o = [&](int c, float* o) {
         tmem_ld32(o_addr + c, o);
@@ -965,6 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                 for (int e = 0; e < 8; ++e) x[e] = w[i / 2 * 16 + e / 2 * 4 + i % 2 * 2 + e % 2];
                 if (to[i]) st_global32(to[i] + c + 16 * (lane & 3), x);
               }
+              __syncwarp();
             }
           } else {
             // a thread writes its row, 32 bytes at a time where out is so aligned
@@ -985,6 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                     *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
                 }
               }
+              __syncwarp();
             }
           }
         }
@@ -1042,6 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                 x.w = fm != 0.f ? fmaf(fm, o[4 * e + 3], ft * x.w) : ft * x.w;
                 join_o[at] = x;
               }
+              __syncwarp();
             }
           }
         }
