@@ -85,6 +85,11 @@ constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
 // the last one's could use (7 prompts, 296 CTAs: 22.15 us so, 22.5 started early).
 constexpr int kEarlyCtas = 128;
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of about 2^8
+// fp16 weights are made 2^7 times larger, which leaves the sum as it is: they reach
+// 2^15, half of fp16's range, and stay normal down to 2^-21 of the base and above
+// zero down to 2^-32 (2^-14 and 2^-25 without). bf16 has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
 constexpr int kKid = kKidTileAttn << 8;
 
 __device__ int g_status[2];       // sticky: error kinds, first report
@@ -810,12 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       }
       const int lim = TREE ? p.pos[it.s] - 1 : min(tok, len - 1);
       const int nb = blocks_of(it, slot);
-      // the row's base, sum, -base sl2 and the maximum that moves the base, which
-      // a row decides for itself: what its warp's other rows see changes nothing
+      // the row's base, sum, kLift - base sl2 and the maximum that moves the base,
+      // which a row decides for itself: what its warp's other rows see changes nothing
       float m = -INFINITY, l = 0.f, neg = 0.f, bar = -INFINITY;
       auto rebase = [&](float to) {
         m = to;
-        neg = to == -INFINITY ? 0.f : -to * sl2;
+        neg = to == -INFINITY ? 0.f : fmaf(-to, sl2, kLift<BF16>);
         bar = to + slack;
       };
       for (int i = 0; i < nb && ok; ++i, ++ns) {
@@ -1002,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
         }
         const bool here = ok && warp_ok && nb > 0;  // this warp has sums
-        const float2 ml = seen && nb > 0 ? make_float2(m * sl2, l) : make_float2(-INFINITY, 0.f);
+        const float2 ml = seen && nb > 0 ? make_float2(-neg, l) : make_float2(-INFINITY, 0.f);
         if (!solo) {
           join_ml[slot * kRows + r] = ml;
           if (here) {

@@ -64,3 +64,35 @@ def test_a_threads_first_call_on_the_device(op):
     torch.cuda.synchronize()
     assert not errors
     assert all(torch.equal(t, w) for t, w in zip(state, want))
+
+
+# ---- weights far apart ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("above", [14.0, 16.0, 17.5, 20.0])
+def test_many_small_weights_beside_a_large_one(above, hd, dtype):
+    """One key (the first, or one in the middle) whose score is far above those of 8000 others, which are all
+    equal: their share of the output arrives. With v = 0 at the large key and 1 elsewhere the output is that
+    share, s = n e^-above / (1 + n e^-above).
+
+    Tolerance: u = eps / 2; the result is rounded once, u s; a weight above the type's smallest normal number is
+    off by u of itself, a smaller one by half of the smallest number; in fp16 the weights of 2^7 to 2^15 that
+    the largest key gets make that at most 2^-25 2^-7 of the denominator each, together n 2^-32; fp32: the
+    exponent's argument is at most 1.45 above + 7, rounded twice, and exp2 is off by 2^-22, sums over n keys are
+    off by 2 n 2^-24 of themselves."""
+    n = 8001
+    u = torch.finfo(dtype).eps / 2
+    share = (n - 1) * np.exp(-above) / (1 + (n - 1) * np.exp(-above))
+    tol = 2 * u * share + ((n * 2.0 ** -32) if dtype == FP else 0.0) + share * (2.0 ** -21 + 4 * (1.45 * above + 7) * 2.0 ** -24 + 2 * n * 2.0 ** -24)
+    for at in (0, 4000):
+        q = torch.ones(n, 4, hd, device="cuda", dtype=dtype)
+        k, v = torch.zeros(n, 2, hd, device="cuda", dtype=dtype), torch.ones(n, 2, hd, device="cuda", dtype=dtype)
+        k[at], v[at] = above / 8, 0.0
+        scale = 8.0 / hd  # the score of the large key: hd (above / 8) scale
+        out = lps.attention_prompt_packed(q, k, v, [0, n], scale=scale)
+        kc, vc = (t.transpose(0, 1).contiguous()[None] for t in (k, v))
+        tree = lps.attention_tree_verify(q[None, :3].contiguous(), kc, vc, torch.tensor([[-1, 0, 1]], dtype=torch.int32, device="cuda"),
+                                         [n - 3], [3], scale=scale)
+        for got in (out[-1], tree[0, 2]):
+            assert ((got.double() - share).abs() <= tol).all(), (at, got.double().mean().item() / share, tol / share)
