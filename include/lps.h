@@ -500,6 +500,7 @@ long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n
  * holds the tokens offsets[s] .. offsets[s + 1] - 1, token t of it sees the
  * tokens [0, t] of the same sequence:
  *     out[t][h] = sum_j p_j v[j], p = softmax_j(scale * q[t][h] . k[j]).
+ * A token all of whose scores are -inf gets NaN, as the formula does.
  *   q, out   device [tokens][n_q_heads][head_dim]
  *   k, v     device [tokens][n_kv_heads][head_dim]
  *   offsets  host int32[n_seqs + 1], in [0, 2^31 - 2^16], not descending; empty
@@ -517,7 +518,8 @@ int attention_prompt_packed(const void* q, const void* k, const void* v, void* o
  * and rows[b] drafted tokens, whose keys and values the caller has stored in
  * the cache rows pos[b] .. pos[b] + rows[b] - 1 (kv_rows_append). Draft t hangs
  * from draft parents[b][t] < t, or from the last committed token when that is
- * -1; it sees the cache rows [0, pos[b]), itself and its chain of parents.
+ * -1; it sees the cache rows [0, pos[b]), itself and its chain of parents. A
+ * draft all of whose scores are -inf gets NaN, as the formula does.
  *   q, out   device [batch][width][n_q_heads][head_dim]; rows t >= rows[b] are
  *            neither read nor written
  *   pos, rows  host int32[batch]: 0 <= rows[b] <= width, pos[b] + rows[b] <= max_ctx

@@ -386,6 +386,11 @@ __device__ __forceinline__ float weight_of(float2 ml, float top) {
   return ml.y != ml.y ? ml.y : ex2(ml.x - top);
 }
 
+// A row that sees nothing by its mask carries this for (base, sum); one that has
+// merely no weight yet has some other base.
+__device__ __forceinline__ float2 ml_of_nothing() { return make_float2(NAN, 0.f); }
+__device__ __forceinline__ bool sees_nothing(float2 ml) { return ml.y == 0.f && ml.x != ml.x; }
+
 // One row's join over a cluster's C CTAs in order, 8 columns (a unit) at a time
 // from unit u0 on: o = sum_c w_c o_c / sum_c w_c l_c, w_c = 2^(m_c - max m). All
 // loads of a unit are issued before the first is used: a trip to another CTA's
@@ -395,10 +400,12 @@ template <bool BF16, int HD, int C>
 __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t* out, int u0, int step) {
   constexpr int G = C < 8 ? C : 8;  // parts whose loads are under way at once
   float w[C], top = -INFINITY, l = 0.f;
+  bool unseen;
   {
     float2 ml[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) ml[c] = peer_ld2(peer_smem(ml_at, c));
+    unseen = sees_nothing(ml[0]);
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (ml[c].y != 0.f) top = fmaxf(top, ml[c].x);
@@ -408,7 +415,8 @@ __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t
       if (w[c] != 0.f) l = fmaf(w[c], ml[c].y, l);
     }
   }
-  const float inv = l != 0.f ? 1.0f / l : 0.f;  // a draft of a broken chain: zeros
+  // a draft of a broken chain gets zeros; a row all of whose scores are -inf 0 / 0, as without a join
+  const float inv = unseen ? 0.f : l != 0.f ? 1.0f / l : NAN;
   for (int u = u0; u < HD / 8; u += step) {
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1007,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
         }
         const bool here = ok && warp_ok && nb > 0;  // this warp has sums
-        const float2 ml = seen && nb > 0 ? make_float2(-neg, l) : make_float2(-INFINITY, 0.f);
+        const float2 ml = !seen ? ml_of_nothing() : nb > 0 ? make_float2(-neg, l) : make_float2(-INFINITY, 0.f);
         if (!solo) {
           join_ml[slot * kRows + r] = ml;
           if (here) {
@@ -1038,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           const float2 to = swap_ml[(slot ^ 1) * kRows + r];
           const float top = fmaxf(ml.y != 0.f ? ml.x : -INFINITY, to.y != 0.f ? to.x : -INFINITY);
           const float fm = weight_of(ml, top), ft = weight_of(to, top);
-          if (slot == 0) join_ml[r] = make_float2(top, fm * ml.y + ft * to.y);
+          if (slot == 0) join_ml[r] = seen ? make_float2(top, fm * ml.y + ft * to.y) : ml;
           if (ok && warp_ok) {
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 32) {

@@ -96,3 +96,43 @@ def test_many_small_weights_beside_a_large_one(above, hd, dtype):
                                          [n - 3], [3], scale=scale)
         for got in (out[-1], tree[0, 2]):
             assert ((got.double() - share).abs() <= tol).all(), (at, got.double().mean().item() / share, tol / share)
+
+
+# ---- infinities ---------------------------------------------------------------------------------------
+
+def _chain(batch, width):
+    return torch.arange(-1, width - 1, device="cuda", dtype=torch.int32).repeat(batch, 1)
+
+
+# trees whose keys one CTA has alone, that two slots share, that clusters share, and wide ones
+TREES = [(1, 1, 0, 8, 2), (2, 9, 60, 8, 2), (1, 5, 3000, 8, 2), (1, 64, 2000, 8, 2), (60, 64, 40, 16, 4)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_a_row_whose_scores_are_all_minus_infinity(hd, dtype):
+    """0 / 0 by the formula: NaN from a prompt and from every tree, however its keys are shared out; with one
+    finite score among them the row is that key's value. A draft of a broken chain stays zero."""
+    q, k, v = _randn(1, 300, 8, hd, dtype=dtype).abs() + 1, _randn(2, 300, 2, hd, dtype=dtype), _randn(3, 300, 2, hd, dtype=dtype)
+    k[:140] = -float("inf")
+    out = lps.attention_prompt_packed(q, k, v, [0, 300])
+    assert out[:140].isnan().all() and not out[140:].isnan().any()
+    assert torch.equal(out[140].view(2, 4, hd), v[140][:, None].expand(2, 4, hd))
+    for batch, width, pos, nq, nkv in TREES:
+        tq, kc, vc = _randn(4, batch, width, nq, hd, dtype=dtype).abs() + 1, _randn(5, batch, nkv, pos + width, hd, dtype=dtype), _randn(6, batch, nkv, pos + width, hd, dtype=dtype)
+        parents = _chain(batch, width)
+        if width > 2:
+            parents[:, width - 1] = 77  # the last draft's chain is broken
+        kc[:] = -float("inf")
+        out = lps.attention_tree_verify(tq, kc, vc, parents, [pos] * batch, [width] * batch)
+        whole = out[:, :width - 1] if width > 2 else out
+        assert whole.isnan().all()
+        assert width <= 2 or (out[:, width - 1] == 0).all()
+        for at in {0, pos // 2, pos}:  # one key that is seen by all drafts
+            kc2 = kc.clone()
+            kc2[:, :, at] = 0.5
+            out = lps.attention_tree_verify(tq, kc2, vc, parents, [pos] * batch, [width] * batch)
+            want = vc[:, :, at].repeat_interleave(nq // nkv, 1)[:, None].expand(batch, width, nq, hd)
+            whole = slice(0, width - 1 if width > 2 else width)
+            assert torch.equal(out[:, whole], want[:, whole]), (width, pos, at)
+            assert width <= 2 or (out[:, width - 1] == 0).all()
