@@ -486,6 +486,9 @@ long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n
  *     kv head h / (n_q_heads / n_kv_heads), 1 to 16 q heads per kv head;
  *   - device pointers are 16-byte aligned; strides are in elements, multiples
  *     of 8 and at least head_dim; out overlaps no input;
+ *   - an infinity or NaN of V arrives in the rows that see it, however small its
+ *     weight; where the score is -inf the weight is zero, and the product NaN. o is
+ *     summed in fp32 with weights of up to 2^8 a key (fp16: 2^15) and then divided;
  *   - host arrays are read during the call and travel with the launch: a
  *     captured call replays with the values it was captured with;
  *   - a call runs on the calling thread's current device, in `stream` (NULL:

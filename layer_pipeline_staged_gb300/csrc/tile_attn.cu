@@ -27,7 +27,10 @@
 // and 11: the MMAs of slot 0 and 1. Warp 10: V blocks that some row does not see
 // whole are made safe before the MMA reads them, as 0 x inf is not 0: rows past
 // the last key become zero, and so do infinities and NaNs, which the epilogue
-// then adds to the rows that do see them (a path that finite inputs never take).
+// then adds to the rows that do see them. Where a row's result is not finite, V is
+// looked through again and the formula decides (settle): a weight that came to zero
+// in the element type, or a factor that did, leaves NaN of an infinity that counts.
+// Finite inputs take neither path.
 //
 // A prompt's CTA stays on its SM: once the copies of its item are issued, its
 // TMA lane takes over the next CTA of the grid that has not started
@@ -386,21 +389,75 @@ __device__ __forceinline__ float weight_of(float2 ml, float top) {
   return ml.y != ml.y ? ml.y : ex2(ml.x - top);
 }
 
-// A row that sees nothing by its mask carries this for (base, sum); one that has
-// merely no weight yet has some other base.
+// A part of a row with no weight carries a base that says why: the row sees nothing
+// by its mask (NaN), the part has had no keys and left no o (-inf), or all its
+// scores are -inf and o is 0 times V (0).
 __device__ __forceinline__ float2 ml_of_nothing() { return make_float2(NAN, 0.f); }
 __device__ __forceinline__ bool sees_nothing(float2 ml) { return ml.y == 0.f && ml.x != ml.x; }
+__device__ __forceinline__ float2 ml_without_keys() { return make_float2(-INFINITY, 0.f); }
+__device__ __forceinline__ bool has_o(float2 ml) { return ml.y != 0.f || ml.x == 0.f; }
+
+// Whether one of 16-bit words probed into acc is infinite or NaN.
+template <bool BF16>
+__device__ __forceinline__ bool wild(uint32_t acc) {
+  return nonfinite<BF16>(acc) || nonfinite<BF16>(acc >> 16);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t probe4(uint4 x, uint32_t acc) {
+  return probe<BF16>(x.w, probe<BF16>(x.z, probe<BF16>(x.y, probe<BF16>(x.x, acc))));
+}
+
+// The columns of one row's result, 8 (a unit) at a time from unit u0 on, that are not
+// finite although no score of the row is NaN: where V holds infinities or NaNs at keys
+// the row sees, their sum; a key whose score is -inf has a weight of zero, and zero
+// times them is NaN; any other weight is positive. Where V holds none, the sum has
+// gone past the type, and stays.
+template <bool BF16, int HD, bool TREE>
+__device__ __forceinline__ void settle(const TileAttnParams& p, const Item& it, int tok, int head, int lim, unsigned long long anc,
+                                       uint16_t* out, int u0, int step) {
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + it.tok0 * (TREE ? p.q_seq : p.q_tok) + tok * p.q_tok + head * p.q_head;
+  const uint16_t* k = static_cast<const uint16_t*>(p.k) + it.tok0 * (TREE ? p.k_seq : p.k_row) + it.g * p.k_head;
+  const uint16_t* v = static_cast<const uint16_t*>(p.v) + it.tok0 * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head;
+#pragma unroll 1
+  for (int u = u0; u < HD / 8; u += step) {
+    if (!wild<BF16>(probe4<BF16>(*reinterpret_cast<const uint4*>(out + u * 8), 0))) continue;
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint32_t hit = 0;
+#pragma unroll 1
+    for (int key = 0; key < it.kend; ++key) {
+      if (!(seen32<TREE>(key, lim, anc) & 1u)) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(v + key * p.v_row + u * 8);
+      if (!wild<BF16>(probe4<BF16>(x, 0))) continue;
+      float s = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < HD; ++d) s = fmaf(widen<BF16>(q[d]), widen<BF16>(k[key * p.k_row + d]), s);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t y = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+        if (!nonfinite<BF16>(y)) continue;
+        sum[e] += s == -INFINITY ? NAN : widen<BF16>(y);
+        hit |= 1u << e;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if ((hit >> e) & 1u) out[u * 8 + e] = static_cast<uint16_t>(pack16<BF16>(sum[e], 0.f));
+  }
+}
 
 // One row's join over a cluster's C CTAs in order, 8 columns (a unit) at a time
 // from unit u0 on: o = sum_c w_c o_c / sum_c w_c l_c, w_c = 2^(m_c - max m). All
 // loads of a unit are issued before the first is used: a trip to another CTA's
 // shared memory takes some 200 ns, and one per part and unit in turn took 3.5
 // of a call's 14 us.
+// Returns whether the row's result wants to be settled.
 template <bool BF16, int HD, int C>
-__device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t* out, int u0, int step) {
+__device__ __forceinline__ bool join_row(uint32_t ml_at, uint32_t o_at, uint16_t* out, int u0, int step) {
   constexpr int G = C < 8 ? C : 8;  // parts whose loads are under way at once
   float w[C], top = -INFINITY, l = 0.f;
   bool unseen;
+  uint32_t has = 0, acc = 0;  // the parts that have left an o; NaN where a result is not finite
   {
     float2 ml[C];
 #pragma unroll
@@ -412,6 +469,7 @@ __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       w[c] = weight_of(ml[c], top);
+      has |= has_o(ml[c]) ? 1u << c : 0u;
       if (w[c] != 0.f) l = fmaf(w[c], ml[c].y, l);
     }
   }
@@ -431,7 +489,7 @@ __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t
 #pragma unroll
       for (int c = 0; c < G; ++c) {
         const float f = w[g + c];
-        if (f != 0.f) {  // a part that saw nothing has left no o
+        if ((has >> (g + c)) & 1u) {  // whatever its weight: zero times an infinity is to be seen
           o[0] = fmaf(f, x[c].x, o[0]);
           o[1] = fmaf(f, x[c].y, o[1]);
           o[2] = fmaf(f, x[c].z, o[2]);
@@ -443,10 +501,12 @@ __device__ __forceinline__ void join_row(uint32_t ml_at, uint32_t o_at, uint16_t
         }
       }
     }
-    *reinterpret_cast<uint4*>(out + u * 8) =
-        make_uint4(pack16<BF16>(o[0] * inv, o[1] * inv), pack16<BF16>(o[2] * inv, o[3] * inv),
-                   pack16<BF16>(o[4] * inv, o[5] * inv), pack16<BF16>(o[6] * inv, o[7] * inv));
+    const uint4 y = make_uint4(pack16<BF16>(o[0] * inv, o[1] * inv), pack16<BF16>(o[2] * inv, o[3] * inv),
+                               pack16<BF16>(o[4] * inv, o[5] * inv), pack16<BF16>(o[6] * inv, o[7] * inv));
+    *reinterpret_cast<uint4*>(out + u * 8) = y;
+    acc = probe4<BF16>(y, acc);
   }
+  return wild<BF16>(acc) && inv == inv;
 }
 
 template <bool BF16, int HD, bool TREE>
@@ -551,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
     if (lane == 0) mbar_arrive(&item_done[no & 1]);
   };
 
+  bool again = false;  // tree: the thread's row wants to be settled
   if (warp >= 8) {
     regs_dec<kOtherRegs>();
     if (warp == 8) {
@@ -947,6 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           const float inv = seen ? 1.0f / l : 0.f;
           uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
+          uint32_t odds[2] = {0, 0};  // NaN where a result of the row is not finite
           if (HD == 128 && p.wide_out) {
             // A thread has a row, and 32 rows are 32 lines a store. So the rounded
             // row goes back to TMEM, over columns of o already read, and comes out
@@ -969,6 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 w[k % 8 / 2 * 8 + k / 8 * 2 + k % 2] = seen ? pack16<BF16>(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) odds[k & 1] = probe<BF16>(w[k], odds[k & 1]);
               tmem_st16(o_addr + c, w);
               tmem_st16(o_addr + c + 16, w + 16);
               tmem_wait_st();
@@ -1003,9 +1067,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                   for (int u = 0; u < 4; ++u)
                     *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
                 }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) odds[e & 1] = probe<BF16>(w[e], odds[e & 1]);
               }
               __syncwarp();
             }
+          }
+          bool odd = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) odd |= wild<BF16>(odds[k]);
+          if (odd && seen && l == l) {
+            if (TREE) again = true;
+            else settle<BF16, HD, TREE>(p, it, tok, it.g * p.group + row_head, lim, anc, out, 0, 1);
           }
         }
       } else if (TREE && joined) {
@@ -1015,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           if (!ok && lane == 0) report_error(g_status, kErrWaitFull | kKid | (9 << 13));
         }
         const bool here = ok && warp_ok && nb > 0;  // this warp has sums
-        const float2 ml = !seen ? ml_of_nothing() : nb > 0 ? make_float2(-neg, l) : make_float2(-INFINITY, 0.f);
+        const float2 ml = !seen ? ml_of_nothing() : nb > 0 ? make_float2(-neg, l) : ml_without_keys();
         if (!solo) {
           join_ml[slot * kRows + r] = ml;
           if (here) {
@@ -1046,7 +1119,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           const float2 to = swap_ml[(slot ^ 1) * kRows + r];
           const float top = fmaxf(ml.y != 0.f ? ml.x : -INFINITY, to.y != 0.f ? to.x : -INFINITY);
           const float fm = weight_of(ml, top), ft = weight_of(to, top);
-          if (slot == 0) join_ml[r] = seen ? make_float2(top, fm * ml.y + ft * to.y) : ml;
+          const bool has = has_o(ml), other_has = has_o(to);
+          if (slot == 0) {
+            const float sum = fm * ml.y + ft * to.y;
+            join_ml[r] = sum != 0.f ? make_float2(top, sum) : !seen ? ml : make_float2(has || other_has ? 0.f : -INFINITY, 0.f);
+          }
           if (ok && warp_ok) {
 #pragma unroll 1
             for (int c = 0; c < HD / 2; c += 32) {
@@ -1055,11 +1132,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int at = ((mine + c) / 4 + e) * kRows + r;
-                float4 x = ft != 0.f ? swap_o[at] : make_float4(0.f, 0.f, 0.f, 0.f);
-                x.x = fm != 0.f ? fmaf(fm, o[4 * e], ft * x.x) : ft * x.x;
-                x.y = fm != 0.f ? fmaf(fm, o[4 * e + 1], ft * x.y) : ft * x.y;
-                x.z = fm != 0.f ? fmaf(fm, o[4 * e + 2], ft * x.z) : ft * x.z;
-                x.w = fm != 0.f ? fmaf(fm, o[4 * e + 3], ft * x.w) : ft * x.w;
+                float4 x = other_has ? swap_o[at] : make_float4(0.f, 0.f, 0.f, 0.f);
+                x.x = has ? fmaf(fm, o[4 * e], ft * x.x) : ft * x.x;
+                x.y = has ? fmaf(fm, o[4 * e + 1], ft * x.y) : ft * x.y;
+                x.z = has ? fmaf(fm, o[4 * e + 2], ft * x.z) : ft * x.z;
+                x.w = has ? fmaf(fm, o[4 * e + 3], ft * x.w) : ft * x.w;
                 join_o[at] = x;
               }
               __syncwarp();
@@ -1086,16 +1163,25 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                         (it.g * p.group + r % p.group) * p.o_head;
         const int u0 = blockIdx.x % p.cluster + (solo ? half * p.cluster : 0), step = solo ? 2 * p.cluster : p.cluster;
         switch (p.cluster) {
-          case 1: join_row<BF16, HD, 1>(ml_at, o_at, out, u0, step); break;
-          case 2: join_row<BF16, HD, 2>(ml_at, o_at, out, u0, step); break;
-          case 4: join_row<BF16, HD, 4>(ml_at, o_at, out, u0, step); break;
-          case 8: join_row<BF16, HD, 8>(ml_at, o_at, out, u0, step); break;
-          default: join_row<BF16, HD, 16>(ml_at, o_at, out, u0, step); break;
+          case 1: again = join_row<BF16, HD, 1>(ml_at, o_at, out, u0, step); break;
+          case 2: again = join_row<BF16, HD, 2>(ml_at, o_at, out, u0, step); break;
+          case 4: again = join_row<BF16, HD, 4>(ml_at, o_at, out, u0, step); break;
+          case 8: again = join_row<BF16, HD, 8>(ml_at, o_at, out, u0, step); break;
+          default: again = join_row<BF16, HD, 16>(ml_at, o_at, out, u0, step); break;
         }
       }
     }
     __syncwarp();
     cluster_sync();  // the cluster's shared memory has been read
+  }
+  if (TREE && __builtin_expect(again, 0)) {
+    // a thread has the row here, and its warp the parents, that it had in its softmax
+    const Item& it = items[0];
+    const int half = tid >> 7, r = tid & 127, tok = it.t0 + (solo ? 0 : half * p.tpt) + r / p.group, head = it.g * p.group + r % p.group;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * p.o_seq + tok * p.o_tok + head * p.o_head;
+    const int u0 = joined ? blockIdx.x % p.cluster + (solo ? half * p.cluster : 0) : 0;
+    settle<BF16, HD, TREE>(p, it, tok, head, p.pos[it.s] - 1, tree_mask(parents + warp * kTreeMax, tok), out, u0,
+                           joined ? (solo ? 2 * p.cluster : p.cluster) : 1);
   }
 
   tc_fence_before();

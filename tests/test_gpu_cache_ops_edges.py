@@ -136,3 +136,86 @@ def test_a_row_whose_scores_are_all_minus_infinity(hd, dtype):
             whole = slice(0, width - 1 if width > 2 else width)
             assert torch.equal(out[:, whole], want[:, whole]), (width, pos, at)
             assert width <= 2 or (out[:, width - 1] == 0).all()
+
+
+FAR = {BF: 100.0, FP: 30.0}  # a score so far below the largest has a weight of zero in the element type
+
+
+def _far_case(seed, n, nq, nkv, hd, dtype, peak):
+    """q, k, v of one sequence whose key `peak` has a score FAR above all others', which are equal; by the formula
+    every weight is positive."""
+    q = torch.ones(n, nq, hd, device="cuda", dtype=dtype)
+    k = torch.zeros(n, nkv, hd, device="cuda", dtype=dtype)
+    k[peak] = FAR[dtype] / 8
+    return q, k, _randn(seed, n, nkv, hd, dtype=dtype), 8.0 / hd
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("peak,at", [(0, 70), (70, 0), (300, 20), (20, 300), (500, 501), (599, 3), (3, 598)])
+def test_prompt_infinity_seen_with_a_weight_next_to_nothing(peak, at, hd, dtype):
+    """A positive weight times infinity is infinite, however small the weight and wherever the key lies: in a block
+    that all rows see whole or one that they do not, before or behind the key that outweighs it."""
+    n, inf = 600, float("inf")
+    q, k, v, scale = _far_case(7, n, 8, 2, hd, dtype, peak)
+    clean = lps.attention_prompt_packed(q, k, v, [0, n], scale=scale)
+    assert torch.isfinite(clean).all()
+    v2 = v.clone()
+    v2[at, :, 3], v2[at, :, 40] = inf, -inf
+    v2[at, :, 50], v2[max(at - 9, 1), :, 50] = inf, -inf
+    v2[at, :, 60] = float("nan")
+    got = lps.attention_prompt_packed(q, k, v2, [0, n], scale=scale)
+    assert (got[at:, :, 3] == inf).all() and (got[at:, :, 40] == -inf).all()
+    both = max(at, at - 9, 1)
+    assert got[both:, :, [50, 60]].isnan().all()
+    others = [d for d in range(hd) if d not in (3, 40, 50, 60)]
+    assert torch.equal(got[:, :, others], clean[:, :, others]) and torch.equal(got[:at, :, 3], clean[:at, :, 3])
+    # a weight that is zero by the formula, at a score of -inf: 0 x inf
+    k[at] = -inf
+    clean = lps.attention_prompt_packed(q, k, v, [0, n], scale=scale)
+    got = lps.attention_prompt_packed(q, k, v2, [0, n], scale=scale)
+    assert got[at:, :, [3, 40, 50, 60]].isnan().all()
+    assert torch.equal(got[at + 1:, :, others], clean[at + 1:, :, others])
+    # and a NaN score makes the whole row NaN
+    k[at] = float("nan")
+    assert lps.attention_prompt_packed(q, k, v2, [0, n], scale=scale)[at:].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("tree", range(len(TREES)))
+def test_tree_infinity_seen_with_a_weight_next_to_nothing(tree, hd, dtype):
+    """The same over a cache, with the two keys in one CTA's part, in the parts of two slots or of two CTAs."""
+    batch, width, pos, nq, nkv = TREES[tree]
+    n, inf = pos + width, float("inf")
+    parents = _chain(batch, width)
+    for peak, at in {(0, n - 1), (n - 1, 0), (n // 2, n // 3), (n // 3, n // 2), (0, min(130, n - 1)), (min(130, n - 1), 0)}:
+        if peak == at:
+            continue
+        q1, k, v, scale = _far_case(8, n, nq, nkv, hd, dtype, peak)
+        q = q1[:width][None].repeat(batch, 1, 1, 1)
+        kc, vc = (t.transpose(0, 1)[None].repeat(batch, 1, 1, 1) for t in (k, v))
+        call = lambda: lps.attention_tree_verify(q, kc, vc, parents, [pos] * batch, [width] * batch, scale=scale)  # noqa: E731
+        clean = call()
+        assert torch.isfinite(clean).all()
+        vc[:, :, at, 3], vc[:, :, at, 40], vc[:, :, at, 50] = inf, -inf, float("nan")
+        got = call()
+        first = max(0, at - pos)  # the first draft that sees it
+        assert (got[:, first:, :, 3] == inf).all() and (got[:, first:, :, 40] == -inf).all() and got[:, first:, :, 50].isnan().all(), (peak, at)
+        others = [d for d in range(hd) if d not in (3, 40, 50)]
+        assert torch.equal(got[..., others], clean[..., others]) and torch.equal(got[:, :first], clean[:, :first])
+        kc[:, :, at] = -inf
+        got = call()
+        assert got[:, first:, :, [3, 40, 50]].isnan().all(), (peak, at)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_values_near_the_types_end(dtype):
+    """Large finite values stay what they are (a mean of them): o is summed in fp32 with weights of up to 2^8 a key
+    (2^15 in fp16) before it is divided."""
+    top = torch.finfo(dtype).max / (2.0 ** 30 if dtype == BF else 2.0)
+    q, k = _randn(1, 200, 4, 64, dtype=dtype), _randn(2, 200, 2, 64, dtype=dtype)
+    v = torch.full_like(k, top)
+    out = lps.attention_prompt_packed(q, k, v, [0, 200]).double()
+    # the weights are rounded for the product and not for the sum: off by eps / 2, and the result by as much again
+    assert ((out - top).abs() <= 1.01 * torch.finfo(dtype).eps * top).all()
