@@ -17,6 +17,8 @@
 static PyObject *g_bf16, *g_fp16, *g_int32;             /* torch dtypes */
 static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad; /* torch functions */
 static PyObject *g_error;                                /* LpsError */
+static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
+static PyObject *s_level, *s_unpack; /* in it: the current level of forward derivatives (-1: none), unpack_dual */
 static PyObject *s_dtype, *s_get_device, *s_data_ptr, *s_shape, *s_stride, *s_requires_grad, *s_device, *s_is_cuda;
 static PyObject *g_empty_names; /* ("dtype", "device") */
 
@@ -40,6 +42,20 @@ static int ints_of(PyObject *seq, int64_t *out, const char *what) {
     if (out[i] == -1 && PyErr_Occurred()) return -1;
   }
   return (int)n;
+}
+
+/* Whether `obj` carries a forward derivative, which the calls would lose; -1 on an error. Its requires_grad
+ * is false and its memory the primal's, so nothing else tells. */
+static int has_tangent(PyObject *obj) {
+  PyObject *level = PyDict_GetItemWithError(g_dual, s_level); /* borrowed */
+  if (level && PyLong_Check(level) && PyLong_AsLong(level) < 0) return 0;
+  PyObject *unpack = PyErr_Occurred() ? NULL : PyDict_GetItemWithError(g_dual, s_unpack);
+  if (!unpack && !PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "this torch has no forward_ad.unpack_dual");
+  PyObject *dual = unpack ? PyObject_CallOneArg(unpack, obj) : NULL, *tangent = dual ? PySequence_GetItem(dual, 1) : NULL;
+  const int has = tangent ? tangent != Py_None : -1;
+  Py_XDECREF(tangent);
+  Py_XDECREF(dual);
+  return has;
 }
 
 /* The facts of `obj`; strides of axes with one entry are set to dense. */
@@ -70,6 +86,9 @@ static int tensor_of(PyObject *obj, tensor *t, const char *what) {
   t->ptr = PyLong_AsVoidPtr(x);
   Py_DECREF(x);
   if (PyErr_Occurred()) return -1;
+  const int dual = has_tangent(obj);
+  if (dual > 0) PyErr_Format(PyExc_ValueError, "%s carries a forward derivative, and there is none of these operators", what);
+  if (dual) return -1;
   int64_t dense = 1;
   for (int i = t->dim - 1; i >= 0; --i) {
     if (t->shape[i] == 1) t->stride[i] = dense;
@@ -511,6 +530,10 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   g_fp16 = PyObject_GetAttrString(torch, "float16");
   g_int32 = PyObject_GetAttrString(torch, "int32");
   g_empty = PyObject_GetAttrString(torch, "empty");
+  PyObject *dual = PyImport_ImportModule("torch.autograd.forward_ad");
+  g_dual = dual ? PyModule_GetDict(dual) : NULL;
+  Py_XINCREF(g_dual);
+  Py_XDECREF(dual);
   g_grad = PyObject_GetAttrString(torch, "is_grad_enabled");
   /* the calls' tensors are on a GPU, so torch's lazy initialisation has been */
   g_device = c && PyObject_HasAttrString(c, "_cuda_getDevice") ? PyObject_GetAttrString(c, "_cuda_getDevice")
@@ -523,7 +546,7 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     Py_INCREF(Py_None);
     g_stream = Py_None;
   }
-  if (!g_bf16 || !g_fp16 || !g_int32 || !g_empty || !g_grad || !g_device || !g_set || PyErr_Occurred()) return NULL;
+  if (!g_bf16 || !g_fp16 || !g_int32 || !g_empty || !g_dual || !g_grad || !g_device || !g_set || PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
 
@@ -534,6 +557,8 @@ static PyMethodDef methods[] = {{"init", FAST(init), METH_FASTCALL, NULL},     {
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__marshal(void) {
+  s_level = PyUnicode_InternFromString("_current_level");
+  s_unpack = PyUnicode_InternFromString("unpack_dual");
   s_dtype = PyUnicode_InternFromString("dtype");
   s_get_device = PyUnicode_InternFromString("get_device");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");

@@ -54,3 +54,37 @@ def test_status_raises_what_the_library_says(monkeypatch):
     assert e.value.code == lps.LPS_ECUDA and seen == ["the device", 77]
     library.rc = lps.LPS_OK
     assert lps.cache_ops_status(Stream) is None
+
+
+def _calls(torch, mark):
+    """Every operator's call on CPU tensors, with `mark` applied to one tensor argument after the other. Unmarked
+    they are refused because the tensors are not on a GPU."""
+    bf = torch.bfloat16
+    q, k = torch.zeros(4, 4, 64, dtype=bf), torch.zeros(4, 2, 64, dtype=bf)
+    tq, kc = torch.zeros(2, 3, 4, 64, dtype=bf), torch.zeros(2, 2, 8, 64, dtype=bf)
+    par, path, taken = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for fn, tensors, call in (
+            (lps.attention_prompt_packed, [q, k, k.clone(), q.clone()], lambda f, q, k, v, o: f(q, k, v, [0, 4], out=o)),
+            (lps.attention_tree_verify, [tq, kc, kc.clone(), tq.clone()], lambda f, q, k, v, o: f(q, k, v, par, [0, 0], [1, 1], out=o)),
+            (lps.kv_rows_append, [k, k.clone(), kc, kc.clone()], lambda f, k, v, kc, vc: f(k, v, [0, 2, 4], kc, vc, [0, 0])),
+            (lps.kv_rows_accept, [kc, kc.clone()], lambda f, kc, vc: f(kc, vc, [0, 0], path, taken))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(fn, *tensors)
+        for i in range(len(tensors)):
+            marked = [mark(t) if i == j else t for j, t in enumerate(tensors)]
+            yield lambda: call(fn, *marked)
+
+
+def test_forward_derivatives_are_refused():
+    """A dual tensor has requires_grad False and its primal's memory: its tangent would be lost without a word."""
+    torch = pytest.importorskip("torch")
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level():
+        for call in _calls(torch, lambda t: fwd.make_dual(t, torch.ones_like(t))):
+            with pytest.raises(ValueError, match="forward derivative"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="forward derivative"):
+                call()
+        for call in _calls(torch, lambda t: fwd.unpack_dual(fwd.make_dual(t, torch.ones_like(t))).primal):
+            with pytest.raises(ValueError, match="CUDA"):
+                call()
