@@ -19,7 +19,7 @@ static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad; /* torch functi
 static PyObject *g_error;                                /* LpsError */
 static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
 static PyObject *s_level, *s_unpack; /* in it: the current level of forward derivatives (-1: none), unpack_dual */
-static PyObject *s_dtype, *s_get_device, *s_data_ptr, *s_shape, *s_stride, *s_requires_grad, *s_device, *s_is_cuda;
+static PyObject *s_dtype, *s_get_device, *s_data_ptr, *s_shape, *s_stride, *s_requires_grad, *s_device, *s_is_cuda, *s_is_neg;
 static PyObject *g_empty_names; /* ("dtype", "device") */
 
 #define MAX_DIM 5
@@ -82,6 +82,13 @@ static int tensor_of(PyObject *obj, tensor *t, const char *what) {
   if (!(x = PyObject_GetAttr(obj, s_requires_grad))) goto not_tensor;
   t->grad = x == Py_True;
   Py_DECREF(x);
+  if (!(x = PyObject_CallMethodNoArgs(obj, s_is_neg))) goto not_tensor;
+  const int neg = x == Py_True;
+  Py_DECREF(x);
+  if (neg) { /* a lazy view: its memory holds the values before their sign changes */
+    PyErr_Format(PyExc_ValueError, "%s is a negative view: pass its resolve_neg()", what);
+    return -1;
+  }
   if (!(x = PyObject_CallMethodNoArgs(obj, s_data_ptr))) goto not_tensor;
   t->ptr = PyLong_AsVoidPtr(x);
   Py_DECREF(x);
@@ -567,6 +574,7 @@ PyMODINIT_FUNC PyInit__marshal(void) {
   s_requires_grad = PyUnicode_InternFromString("requires_grad");
   s_device = PyUnicode_InternFromString("device");
   s_is_cuda = PyUnicode_InternFromString("is_cuda");
+  s_is_neg = PyUnicode_InternFromString("is_neg");
   g_empty_names = Py_BuildValue("(ss)", "dtype", "device");
   return g_empty_names ? PyModule_Create(&module) : NULL;
 }

@@ -88,3 +88,16 @@ def test_forward_derivatives_are_refused():
         for call in _calls(torch, lambda t: fwd.unpack_dual(fwd.make_dual(t, torch.ones_like(t))).primal):
             with pytest.raises(ValueError, match="CUDA"):
                 call()
+
+
+def test_negative_views_are_refused():
+    """A view whose sign is still to be changed (the imaginary part of a conjugate) holds other values than it shows."""
+    torch = pytest.importorskip("torch")
+    lazy = torch.zeros(2, 2, dtype=torch.complex64).conj().imag
+    assert lazy.is_neg()
+    for call in _calls(torch, torch._neg_view):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            call()
+    for call in _calls(torch, lambda t: torch._neg_view(t).resolve_neg()):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
