@@ -336,6 +336,15 @@ static int leave(const place *p, int rc) {
   return rc < 0 ? -1 : 0;
 }
 
+/* The scale as the library takes it, where 0 stands for 1/sqrt(head_dim): a scale
+ * that only comes to 0 in 32 bits is refused. */
+static int scale_of(PyObject *obj, float *scale) {
+  const double x = PyFloat_AsDouble(obj);
+  if (PyErr_Occurred()) return -1;
+  *scale = (float)x;
+  return *scale == 0.f && x != 0. ? refuse("scale must be 0 or a number that 32 bits hold") : 0;
+}
+
 /* The output: `out` checked against q, or a new dense tensor like q (a new reference). */
 static PyObject *output_like(PyObject *out, const tensor *q, tensor *o) {
   if (out != Py_None) {
@@ -393,8 +402,8 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     if (tensor_of(args[4], &t[3], "out")) return NULL;
     if (!same_shape(&t[3], q)) return refuse("out must have q's shape"), NULL;
   }
-  const double scale = PyFloat_AsDouble(args[5]);
-  if (PyErr_Occurred() || alike(t, given ? 4 : 3, &kind)) return NULL;
+  float scale;
+  if (scale_of(args[5], &scale) || alike(t, given ? 4 : 3, &kind)) return NULL;
   for (int i = 0; i < 3 + given; ++i)
     if (contiguous_heads(&t[i])) return NULL;
   if (!fits(q->shape[0]) || !fits(q->shape[1]) || !fits(k->shape[1])) return refuse("tensors are too large"), NULL;
@@ -407,7 +416,7 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[3].stride[0], t[3].stride[1]};
     if (enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_prompt_packed(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)(off.n - 1), off.v, (int)q->shape[1],
-                                           (int)k->shape[1], (int)q->shape[2], st, (float)scale, at.stream))))
+                                           (int)k->shape[1], (int)q->shape[2], st, scale, at.stream))))
       Py_CLEAR(out);
   }
   ints_free(&off);
@@ -434,8 +443,8 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     if (tensor_of(args[6], &t[3], "out")) return NULL;
     if (!same_shape(&t[3], q)) return refuse("out must have q's shape"), NULL;
   }
-  const double scale = PyFloat_AsDouble(args[7]);
-  if (PyErr_Occurred() || alike(t, given ? 4 : 3, &kind)) return NULL;
+  float scale;
+  if (scale_of(args[7], &scale) || alike(t, given ? 4 : 3, &kind)) return NULL;
   if (!dense(kc) || !dense(&t[2])) return refuse("the caches must be contiguous [batch, kv heads, max_ctx, head_dim]"), NULL;
   if (contiguous_heads(q) || (given && contiguous_heads(&t[3]))) return NULL;
   const int64_t batch = q->shape[0], width = q->shape[1];
@@ -449,7 +458,7 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     const int64_t st[6] = {q->stride[0], q->stride[1], q->stride[2], t[3].stride[0], t[3].stride[1], t[3].stride[2]};
     if (enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_tree_verify(q->ptr, kc->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, (int)width, pos.v, rows.v, par.ptr,
-                                         (int)q->shape[2], (int)kc->shape[1], (int)q->shape[3], (int)kc->shape[2], st, (float)scale,
+                                         (int)q->shape[2], (int)kc->shape[1], (int)q->shape[3], (int)kc->shape[2], st, scale,
                                          at.stream))))
       Py_CLEAR(out);
   }

@@ -101,3 +101,18 @@ def test_negative_views_are_refused():
     for call in _calls(torch, lambda t: torch._neg_view(t).resolve_neg()):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("scale", [1e-46, 2.0 ** -150, 5e-324, -1e-50])
+def test_a_scale_that_32_bits_do_not_hold_is_refused(scale):
+    """It would come to 0, which stands for 1/sqrt(head_dim)."""
+    torch = pytest.importorskip("torch")
+    q, kc = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    par = torch.zeros(2, 3, dtype=torch.int32)
+    for call in (lambda s: lps.attention_prompt_packed(q[0], q[0], q[0], [0, 3], scale=s),
+                 lambda s: lps.attention_tree_verify(q, kc, kc, par, [0, 0], [1, 1], scale=s)):
+        with pytest.raises(ValueError, match="scale"):
+            call(scale)
+        for fits in (0, 0.0, 2.0 ** -149, 0.1):
+            with pytest.raises(ValueError, match="CUDA"):
+                call(fits)
