@@ -511,7 +511,7 @@ long long attention_decode_noalloc_scratch_bytes(int batch, int n_q_heads, int n
  *            neither used nor written; a key a token does not see changes
  *            nothing, whatever it holds
  *   strides  host int64[8]: token and head stride of q, k, v and out; NULL: dense
- *   scale    > 0, or 0 for 1/sqrt(head_dim)
+ *   scale    > 0 and below 2.3e38, or 0 for 1/sqrt(head_dim)
  * LPS_EINVAL for bad types, head counts, offsets, strides, alignment or scale. */
 int attention_prompt_packed(const void* q, const void* k, const void* v, void* out, int type, int n_seqs,
                             const int32_t* offsets, int n_q_heads, int n_kv_heads, int head_dim,

@@ -27,6 +27,8 @@ namespace {
 
 using namespace lps;
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // Runs the body of an entry point; no exception leaves the C boundary.
 template <class F>
 int guarded(const char* fn, F&& body) {
@@ -63,6 +65,7 @@ int check_heads(const char* fn, int type, int nq, int nkv, int hd) {
 
 int check_scale(const char* fn, float scale) {
   if (!(scale >= 0.f) || std::isinf(scale)) return host_fail(LPS_EINVAL, fn, "scale must be finite and >= 0 (0: 1/sqrt(head_dim))");
+  if (std::isinf(scale * kLog2e)) return host_fail(LPS_EINVAL, fn, "scale must be below 2.3e38 (its product with log2(e) is what the kernels use)");
   return LPS_OK;
 }
 
@@ -117,8 +120,6 @@ bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long l
 
 // Test hook: the wait limit of the calling thread's later calls.
 thread_local long long g_wait_limit = 0;
-
-constexpr float kLog2e = 1.44269504088896340736f;
 
 // Rows and tokens are counted in 32 bits, a block of keys past the last one included.
 constexpr int32_t kMaxRows = 0x7fff0000;

@@ -116,3 +116,37 @@ def test_a_scale_that_32_bits_do_not_hold_is_refused(scale):
         for fits in (0, 0.0, 2.0 ** -149, 0.1):
             with pytest.raises(ValueError, match="CUDA"):
                 call(fits)
+
+
+# ---- the library's own refusals, with addresses that are never dereferenced ------------------------------
+
+def _no_gpu():
+    try:
+        import torch
+        return not torch.cuda.is_available()
+    except Exception:
+        return True
+
+
+cpu_only = pytest.mark.skipif(not _no_gpu(), reason="addresses here are placeholders")
+
+
+def _i32(*x):
+    import ctypes
+    return (ctypes.c_int32 * len(x))(*x)
+
+
+def _refused(rc, what):
+    from layer_pipeline_staged_gb300 import _capi
+    assert rc == lps.LPS_EINVAL
+    err = _capi.load().last_error_string().decode()
+    assert what in err, err
+
+
+@cpu_only
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_a_scale_whose_product_overflows_is_refused(scale):
+    L = lps.load()
+    _refused(L.attention_prompt_packed(0x10000, 0x20000, 0x30000, 0x40000, 0, 1, _i32(0, 5), 8, 2, 64, None, scale, None), "scale")
+    _refused(L.attention_tree_verify(0x10000, 0x20000, 0x30000, 0x40000, 0, 1, 4, _i32(3), _i32(4), 0x50000, 8, 2, 64, 64, None, scale,
+                                     None), "scale")

@@ -219,3 +219,20 @@ def test_values_near_the_types_end(dtype):
     out = lps.attention_prompt_packed(q, k, v, [0, 200]).double()
     # the weights are rounded for the product and not for the sum: off by eps / 2, and the result by as much again
     assert ((out - top).abs() <= 1.01 * torch.finfo(dtype).eps * top).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 1e-30])
+def test_scales_next_to_nothing(scale, dtype):
+    """All scores come to nothing: the mean of the values seen, also where scores of -inf come first. The mean is off
+    by one rounding and by fp32 sums over n keys."""
+    n, hd = 700, 64
+    q, k, v = _randn(1, n, 4, hd, dtype=dtype).abs() + 1, _randn(2, n, 2, hd, dtype=dtype), _randn(3, n, 2, hd, dtype=dtype)
+    k[:200] = -float("inf")
+    kc, vc = (t.transpose(0, 1).contiguous()[None] for t in (k, v))
+    prompt = lps.attention_prompt_packed(q, k, v, [0, n], scale=scale)
+    tree = lps.attention_tree_verify(q[None, :5].contiguous(), kc, vc, _chain(1, 5), [n - 5], [5], scale=scale)
+    for got, last in ((prompt[-1], n), (prompt[400], 401), (tree[0, 4], n), (tree[0, 0], n - 4)):
+        want = v[200:last].double().mean(0)[:, None].expand(2, 2, hd).reshape(4, hd)
+        tol = torch.finfo(dtype).eps / 2 * want.abs() + (2 * n + 16) * 2.0 ** -24 * v[200:last].double().abs().mean()
+        assert ((got.double() - want).abs() <= tol + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps).all()
