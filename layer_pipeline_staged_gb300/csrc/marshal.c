@@ -15,7 +15,7 @@
 /* ---- what init() is given ------------------------------------------------- */
 
 static PyObject *g_bf16, *g_fp16, *g_int32;             /* torch dtypes */
-static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad; /* torch functions */
+static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad, *g_written; /* torch functions */
 static PyObject *g_error;                                /* LpsError */
 static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
 static PyObject *s_level, *s_unpack; /* in it: the current level of forward derivatives (-1: none), unpack_dual */
@@ -82,12 +82,14 @@ static int tensor_of(PyObject *obj, tensor *t, const char *what) {
   if (!(x = PyObject_GetAttr(obj, s_requires_grad))) goto not_tensor;
   t->grad = x == Py_True;
   Py_DECREF(x);
-  if (!(x = PyObject_CallMethodNoArgs(obj, s_is_neg))) goto not_tensor;
-  const int neg = x == Py_True;
-  Py_DECREF(x);
-  if (neg) { /* a lazy view: its memory holds the values before their sign changes */
-    PyErr_Format(PyExc_ValueError, "%s is a negative view: pass its resolve_neg()", what);
-    return -1;
+  if (t->dtype != g_int32) {
+    if (!(x = PyObject_CallMethodNoArgs(obj, s_is_neg))) goto not_tensor;
+    const int neg = x == Py_True;
+    Py_DECREF(x);
+    if (neg) { /* a lazy view: its memory holds the values before their sign changes */
+      PyErr_Format(PyExc_ValueError, "%s is a negative view: pass its resolve_neg()", what);
+      return -1;
+    }
   }
   if (!(x = PyObject_CallMethodNoArgs(obj, s_data_ptr))) goto not_tensor;
   t->ptr = PyLong_AsVoidPtr(x);
@@ -364,6 +366,15 @@ static PyObject *output_like(PyObject *out, const tensor *q, tensor *o) {
   return out;
 }
 
+/* Tells autograd that a call writes `a` (and `b`) in place: an earlier operation that
+ * saved one of them for its backward then refuses to run on the new values. */
+static int written(PyObject *a, PyObject *b) {
+  PyObject *both = b ? PyTuple_Pack(2, a, b) : PyTuple_Pack(1, a), *r = both ? PyObject_CallOneArg(g_written, both) : NULL;
+  Py_XDECREF(both);
+  Py_XDECREF(r);
+  return r ? 0 : -1;
+}
+
 static int contiguous_heads(const tensor *t) {
   return t->shape[t->dim - 1] <= 1 || t->stride[t->dim - 1] == 1 ? 0 : refuse("the head dimension must be contiguous");
 }
@@ -414,7 +425,7 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   else out = output_like(args[4], q, &t[3]);
   if (out && off.n > 1 && q->shape[0] > 0) {
     const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[3].stride[0], t[3].stride[1]};
-    if (enter(&at, q->device) ||
+    if ((given && written(out, NULL)) || enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_prompt_packed(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)(off.n - 1), off.v, (int)q->shape[1],
                                            (int)k->shape[1], (int)q->shape[2], st, scale, at.stream))))
       Py_CLEAR(out);
@@ -456,7 +467,7 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (!ints_from(args[4], batch, "pos", &pos) && !ints_from(args[5], batch, "rows", &rows) &&
       (out = output_like(args[6], q, &t[3]))) {
     const int64_t st[6] = {q->stride[0], q->stride[1], q->stride[2], t[3].stride[0], t[3].stride[1], t[3].stride[2]};
-    if (enter(&at, q->device) ||
+    if ((given && written(out, NULL)) || enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_tree_verify(q->ptr, kc->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, (int)width, pos.v, rows.v, par.ptr,
                                          (int)q->shape[2], (int)kc->shape[1], (int)q->shape[3], (int)kc->shape[2], st, scale,
                                          at.stream))))
@@ -496,7 +507,7 @@ static PyObject *append(PyObject *self, PyObject *const *args, Py_ssize_t n) {
       ok = 1;
     } else {
       const int64_t st[4] = {k->stride[0], k->stride[1], t[1].stride[0], t[1].stride[1]};
-      ok = !enter(&at, k->device) &&
+      ok = !written(kc->obj, t[3].obj) && !enter(&at, k->device) &&
            !leave(&at, UNLOCKED(kv_rows_append(k->ptr, t[1].ptr, (int)kc->shape[0], off.v, kc->ptr, t[3].ptr, start.v, (int)k->shape[1],
                                       (int)k->shape[2], (int)kc->shape[2], st, at.stream)));
     }
@@ -527,7 +538,7 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (!fits(layers) || !fits(s[0]) || !fits(s[1]) || !fits(s[2]) || !fits(path.shape[1])) return refuse("tensors are too large"), NULL;
   int ok = 0;
   if (!ints_from(args[2], s[0], "pos", &pos))
-    ok = !enter(&at, kc->device) &&
+    ok = !written(kc->obj, t[1].obj) && !enter(&at, kc->device) &&
          !leave(&at, UNLOCKED(kv_rows_accept(kc->ptr, t[1].ptr, (int)layers, (int)s[0], (int)s[1], (int)s[3], (int)s[2], pos.v,
                                     (int)path.shape[1], path.ptr, taken.ptr, at.stream)));
   ints_free(&pos);
@@ -551,6 +562,13 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   Py_XINCREF(g_dual);
   Py_XDECREF(dual);
   g_grad = PyObject_GetAttrString(torch, "is_grad_enabled");
+  /* what torch.autograd.graph.increment_version calls, without its trip through Python */
+  g_written = c && PyObject_HasAttrString(c, "_increment_version") ? PyObject_GetAttrString(c, "_increment_version") : NULL;
+  if (!g_written) {
+    PyObject *graph = PyImport_ImportModule("torch.autograd.graph");
+    g_written = graph ? PyObject_GetAttrString(graph, "increment_version") : NULL;
+    Py_XDECREF(graph);
+  }
   /* the calls' tensors are on a GPU, so torch's lazy initialisation has been */
   g_device = c && PyObject_HasAttrString(c, "_cuda_getDevice") ? PyObject_GetAttrString(c, "_cuda_getDevice")
              : cuda ? PyObject_GetAttrString(cuda, "current_device") : NULL;
@@ -562,7 +580,7 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     Py_INCREF(Py_None);
     g_stream = Py_None;
   }
-  if (!g_bf16 || !g_fp16 || !g_int32 || !g_empty || !g_dual || !g_grad || !g_device || !g_set || PyErr_Occurred()) return NULL;
+  if (!g_bf16 || !g_fp16 || !g_int32 || !g_empty || !g_dual || !g_grad || !g_written || !g_device || !g_set || PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
 

@@ -236,3 +236,45 @@ def test_scales_next_to_nothing(scale, dtype):
         want = v[200:last].double().mean(0)[:, None].expand(2, 2, hd).reshape(4, hd)
         tol = torch.finfo(dtype).eps / 2 * want.abs() + (2 * n + 16) * 2.0 ** -24 * v[200:last].double().abs().mean()
         assert ((got.double() - want).abs() <= tol + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps).all()
+
+
+# ---- autograd ---------------------------------------------------------------------------------------
+
+def _writers():
+    """Each call that writes a given tensor, and the tensors that it writes."""
+    q, k, v = _randn(1, 20, 4, 64), _randn(2, 20, 2, 64), _randn(3, 20, 2, 64)
+    kc, vc, tq = _randn(4, 1, 2, 50, 64), _randn(5, 1, 2, 50, 64), _randn(6, 1, 3, 4, 64)
+    path, taken = torch.tensor([[1, 2]], dtype=torch.int32, device="cuda"), torch.tensor([2], dtype=torch.int32, device="cuda")
+    po, to = torch.zeros_like(q), torch.zeros_like(tq)
+    return {"prompt": (lambda: lps.attention_prompt_packed(q, k, v, [0, 20], out=po), [po]),
+            "tree": (lambda: lps.attention_tree_verify(tq, kc, vc, _chain(1, 3), [40], [3], out=to), [to]),
+            "append": (lambda: lps.kv_rows_append(k, v, [0, 20], kc, vc, [5]), [kc, vc]),
+            "accept": (lambda: lps.kv_rows_accept(kc, vc, [40], path, taken), [kc, vc])}
+
+
+@pytest.mark.parametrize("op", ["prompt", "tree", "append", "accept"])
+def test_what_a_call_writes_is_known_to_autograd(op):
+    """A tensor that an earlier product saved for its backward and a call then writes: the backward refuses, as after
+    any operation in place, instead of using the new values."""
+    call, outs = _writers()[op]
+    for t in outs:
+        w = torch.ones_like(t, requires_grad=True)
+        loss = (w * t).float().sum()
+        with torch.no_grad():
+            call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():  # whose tensors have no version
+        call, outs = _writers()[op]
+        call()
+    lps.cache_ops_status()
+
+
+def test_forward_derivatives_are_refused_on_the_gpu():
+    import torch.autograd.forward_ad as fwd
+    q, k = _randn(1, 20, 4, 64), _randn(2, 20, 2, 64)
+    with fwd.dual_level():
+        with pytest.raises(ValueError, match="forward derivative"):
+            lps.attention_prompt_packed(fwd.make_dual(q, torch.ones_like(q)), k, k, [0, 20])
+        inside = lps.attention_prompt_packed(q, k, k, [0, 20])
+    assert torch.equal(inside, lps.attention_prompt_packed(q, k, k, [0, 20]))
