@@ -366,7 +366,7 @@ static PyObject *output_like(PyObject *out, const tensor *q, tensor *o) {
   return out;
 }
 
-/* Tells autograd that a call writes `a` (and `b`) in place: an earlier operation that
+/* Tells autograd that a call that has been enqueued writes `a` (and `b`) in place: an earlier operation that
  * saved one of them for its backward then refuses to run on the new values. */
 static int written(PyObject *a, PyObject *b) {
   PyObject *both = b ? PyTuple_Pack(2, a, b) : PyTuple_Pack(1, a), *r = both ? PyObject_CallOneArg(g_written, both) : NULL;
@@ -425,9 +425,10 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   else out = output_like(args[4], q, &t[3]);
   if (out && off.n > 1 && q->shape[0] > 0) {
     const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[3].stride[0], t[3].stride[1]};
-    if ((given && written(out, NULL)) || enter(&at, q->device) ||
+    if (enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_prompt_packed(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)(off.n - 1), off.v, (int)q->shape[1],
-                                           (int)k->shape[1], (int)q->shape[2], st, scale, at.stream))))
+                                           (int)k->shape[1], (int)q->shape[2], st, scale, at.stream))) ||
+        (given && written(out, NULL)))
       Py_CLEAR(out);
   }
   ints_free(&off);
@@ -467,10 +468,11 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (!ints_from(args[4], batch, "pos", &pos) && !ints_from(args[5], batch, "rows", &rows) &&
       (out = output_like(args[6], q, &t[3]))) {
     const int64_t st[6] = {q->stride[0], q->stride[1], q->stride[2], t[3].stride[0], t[3].stride[1], t[3].stride[2]};
-    if ((given && written(out, NULL)) || enter(&at, q->device) ||
+    if (enter(&at, q->device) ||
         leave(&at, UNLOCKED(attention_tree_verify(q->ptr, kc->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, (int)width, pos.v, rows.v, par.ptr,
                                          (int)q->shape[2], (int)kc->shape[1], (int)q->shape[3], (int)kc->shape[2], st, scale,
-                                         at.stream))))
+                                         at.stream))) ||
+        (given && written(out, NULL)))
       Py_CLEAR(out);
   }
   ints_free(&pos);
@@ -507,9 +509,10 @@ static PyObject *append(PyObject *self, PyObject *const *args, Py_ssize_t n) {
       ok = 1;
     } else {
       const int64_t st[4] = {k->stride[0], k->stride[1], t[1].stride[0], t[1].stride[1]};
-      ok = !written(kc->obj, t[3].obj) && !enter(&at, k->device) &&
+      ok = !enter(&at, k->device) &&
            !leave(&at, UNLOCKED(kv_rows_append(k->ptr, t[1].ptr, (int)kc->shape[0], off.v, kc->ptr, t[3].ptr, start.v, (int)k->shape[1],
-                                      (int)k->shape[2], (int)kc->shape[2], st, at.stream)));
+                                      (int)k->shape[2], (int)kc->shape[2], st, at.stream))) &&
+           !written(kc->obj, t[3].obj);
     }
   }
   ints_free(&off);
@@ -538,9 +541,10 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   if (!fits(layers) || !fits(s[0]) || !fits(s[1]) || !fits(s[2]) || !fits(path.shape[1])) return refuse("tensors are too large"), NULL;
   int ok = 0;
   if (!ints_from(args[2], s[0], "pos", &pos))
-    ok = !written(kc->obj, t[1].obj) && !enter(&at, kc->device) &&
+    ok = !enter(&at, kc->device) &&
          !leave(&at, UNLOCKED(kv_rows_accept(kc->ptr, t[1].ptr, (int)layers, (int)s[0], (int)s[1], (int)s[3], (int)s[2], pos.v,
-                                    (int)path.shape[1], path.ptr, taken.ptr, at.stream)));
+                                    (int)path.shape[1], path.ptr, taken.ptr, at.stream))) &&
+         !written(kc->obj, t[1].obj);
   ints_free(&pos);
   if (!ok) return NULL;
   Py_RETURN_NONE;

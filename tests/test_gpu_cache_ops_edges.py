@@ -264,6 +264,17 @@ def test_what_a_call_writes_is_known_to_autograd(op):
             call()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+        version = t._version
+        with pytest.raises(lps.LpsError):  # a refused call writes nothing
+            if op == "prompt":
+                lps.attention_prompt_packed(t, t[:, :3], t[:, :3], [0, 20], out=t)
+            elif op == "tree":
+                lps.attention_tree_verify(t, _randn(4, 1, 2, 50, 64), _randn(5, 1, 2, 50, 64), _chain(1, 3), [49], [3], out=t)
+            elif op == "append":
+                lps.kv_rows_append(_randn(2, 20, 2, 64), _randn(3, 20, 2, 64), [0, 20], t, t.clone(), [31])
+            else:
+                lps.kv_rows_accept(t, t.clone(), [51], torch.zeros(1, 2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+        assert t._version == version
     with torch.inference_mode():  # whose tensors have no version
         call, outs = _writers()[op]
         call()
