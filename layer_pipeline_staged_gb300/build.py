@@ -2,9 +2,10 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library (static CUDA runtime, no libtorch); then the torch wrappers'
-argument marshalling as a Python extension beside it (gcc, no torch headers).
-Run as a module or call ``build()``; the results sit next to this file and are
-git-ignored.
+argument marshalling as a Python extension beside it (gcc, no torch headers;
+its name carries the Python it is for, and it is left out, with a word on
+stderr, where that Python has no headers). Run as a module or call ``build()``;
+the results sit next to this file and are git-ignored.
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblps.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
-MARSHAL = os.path.join(HERE, "_marshal.so")  # Python extension: the torch wrappers' argument marshalling
+# Python extension: the torch wrappers' argument marshalling
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["runtime.cu", "gemv.cu", "attention.cu", "embed.cu", "noalloc.cu", "skinny.cu", "solver.cu", "stage.cu", "tcgemm.cu", "prefill.cu",
            "cache_ops.cu", "cache_rows.cu", "tile_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -76,10 +78,16 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if force or _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "lps.h")]):
+    untagged = os.path.join(HERE, "_marshal.so")  # any Python would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        sys.stderr.write(f"no Python.h in {python}: the torch wrappers of the cache operators are not built\n")
+    elif force or _stale(MARSHAL, [MARSHAL_SRC, os.path.join(INCLUDE, "lps.h")]):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         run([os.environ.get("CC") or "gcc", "-O2", "-std=gnu11", "-Wall", "-Wextra", "-Wno-cast-function-type", "-shared", "-fPIC",
-             f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", MARSHAL_SRC, f"-L{HERE}", "-l:liblps.so", "-Wl,-rpath,$ORIGIN", "-o", tmp])
+             f"-I{python}", f"-I{INCLUDE}", MARSHAL_SRC, f"-L{HERE}", "-l:liblps.so", "-Wl,-rpath,$ORIGIN", "-o", tmp])
         os.replace(tmp, MARSHAL)
     return LIB
 

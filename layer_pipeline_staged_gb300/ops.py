@@ -22,7 +22,11 @@ def _ready():
     _capi.load()
     import torch
 
-    from . import _marshal
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError("the torch wrappers' marshalling is missing for this Python: build it first "
+                           "(python -m layer_pipeline_staged_gb300.build, which needs Python.h)") from e
     _marshal.init(_capi.LpsError, torch)
     _m = _marshal
     return _m

@@ -150,3 +150,31 @@ def test_a_scale_whose_product_overflows_is_refused(scale):
     _refused(L.attention_prompt_packed(0x10000, 0x20000, 0x30000, 0x40000, 0, 1, _i32(0, 5), 8, 2, 64, None, scale, None), "scale")
     _refused(L.attention_tree_verify(0x10000, 0x20000, 0x30000, 0x40000, 0, 1, 4, _i32(3), _i32(4), 0x50000, 8, 2, 64, 64, None, scale,
                                      None), "scale")
+
+
+# ---- the marshalling extension ---------------------------------------------------------------------------
+
+def test_the_extension_is_named_for_its_python():
+    import os
+    import sysconfig
+    assert lps_build.MARSHAL.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and os.path.exists(lps_build.MARSHAL)
+    assert not os.path.exists(os.path.join(lps_build.HERE, "_marshal.so"))
+    ops._ready()
+    assert os.path.samefile(ops._m.__file__, lps_build.MARSHAL)
+
+
+def test_without_python_headers_the_library_is_built(monkeypatch, tmp_path, capsys):
+    """The C library needs no Python: its build goes on without the extension, and the wrappers say what is missing."""
+    import os
+    import sys
+    import sysconfig
+    paths = sysconfig.get_paths()
+    monkeypatch.setattr(lps_build.sysconfig, "get_paths", lambda: dict(paths, include=str(tmp_path)))
+    monkeypatch.setattr(lps_build, "MARSHAL", str(tmp_path / "_marshal.so"))
+    assert lps_build.build() == lps_build.LIB and os.path.exists(lps_build.LIB)
+    assert not os.path.exists(tmp_path / "_marshal.so") and "Python.h" in capsys.readouterr().err
+    monkeypatch.setitem(sys.modules, "layer_pipeline_staged_gb300._marshal", None)
+    monkeypatch.delattr(lps, "_marshal", raising=False)
+    monkeypatch.setattr(ops, "_m", None)
+    with pytest.raises(RuntimeError, match="build it first"):
+        lps.kv_rows_append(None, None, [0], None, None, [])
