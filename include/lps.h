@@ -541,7 +541,7 @@ int attention_tree_verify(const void* q, const void* k_cache, const void* v_cach
  * (tokens offsets[s] .. offsets[s + 1] - 1) goes to row start[s] + i of cache
  * sequence s, for every kv head. No other row changes. Elements of 2 bytes.
  *   k, v     device [tokens][n_kv_heads][head_dim]
- *   caches   device [n_seqs][n_kv_heads][max_ctx][head_dim]
+ *   caches   device [n_seqs][n_kv_heads][max_ctx][head_dim], not overlapping
  *   offsets  host int32[n_seqs + 1], start host int32[n_seqs]:
  *            start[s] + length <= max_ctx
  *   strides  host int64[4]: token and head stride of k, then of v; NULL: dense */
@@ -552,7 +552,8 @@ int kv_rows_append(const void* k, const void* v, int n_seqs, const int32_t* offs
 /* The accepted path of a drafted tree, moved in place behind the committed
  * rows: for i < accepted[b], cache row pos[b] + path[b][i] goes to row
  * pos[b] + i, in every layer, for keys and values.
- *   caches   device [n_layers][batch][n_kv_heads][max_ctx][head_dim], elements of 2 bytes
+ *   caches   device [n_layers][batch][n_kv_heads][max_ctx][head_dim], elements of 2 bytes,
+ *            not overlapping
  *   pos      host int32[batch], 0..max_ctx
  *   path     device int32[batch][width], strictly ascending draft rows (parents
  *            come before their children); accepted: device int32[batch], 0..width

@@ -53,6 +53,12 @@ bool wide(const void* p, std::initializer_list<int64_t> strides) {
   return true;
 }
 
+// Whether two caches of so many rows of hd elements share memory.
+bool overlap(const void* a, const void* b, double rows, int hd) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return static_cast<double>(x < y ? y - x : x - y) < rows * hd * 2;
+}
+
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
 int check_heads(const char* fn, int type, int nq, int nkv, int hd) {
@@ -262,6 +268,8 @@ extern "C" int kv_rows_append(const void* k, const void* v, int n_seqs, const in
     if ((rc = check_strides(FN, st, 4, head_dim))) return rc;
     if (misaligned(k) || misaligned(v) || misaligned(k_cache) || misaligned(v_cache))
       return host_fail(LPS_EINVAL, FN, "k, v and the caches must be 16-byte aligned");
+    if (overlap(k_cache, v_cache, static_cast<double>(n_seqs) * n_kv_heads * max_ctx, head_dim))
+      return host_fail(LPS_EINVAL, FN, "the two caches must not overlap");
     const long long seq_units = static_cast<long long>(n_kv_heads) * max_ctx * (head_dim / 8);
     for (int s0 = 0; s0 < n_seqs; s0 += kOpSeqs) {
       AppendParams p{};
@@ -296,6 +304,8 @@ extern "C" int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int ba
     for (int b = 0; b < batch; ++b)
       if (pos[b] < 0 || pos[b] > max_ctx) return host_fail(LPS_EINVAL, FN, "pos out of [0, max_ctx]");
     if (misaligned(k_cache) || misaligned(v_cache)) return host_fail(LPS_EINVAL, FN, "the caches must be 16-byte aligned");
+    if (overlap(k_cache, v_cache, static_cast<double>(n_layers) * batch * n_kv_heads * max_ctx, head_dim))
+      return host_fail(LPS_EINVAL, FN, "the two caches must not overlap");
     AcceptParams p{};
     p.kc = static_cast<uint4*>(k_cache), p.vc = static_cast<uint4*>(v_cache);
     p.path = path, p.accepted = accepted;

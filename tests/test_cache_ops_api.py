@@ -152,6 +152,16 @@ def test_a_scale_whose_product_overflows_is_refused(scale):
                                      None), "scale")
 
 
+@cpu_only
+def test_caches_that_overlap_are_refused():
+    """Rows of both would be moved at once: which of them stays would be a matter of time."""
+    L, one, base = lps.load(), 2 * 2 * 64 * 64 * 2, 0x1000000  # bytes of [2][2][64][64]
+    for other in (base + 16, base + one - 16, base - 16, base - one + 16):
+        _refused(L.kv_rows_append(0x10000, 0x20000, 2, _i32(0, 5, 9), base, other, _i32(0, 0), 2, 64, 64, None, None), "overlap")
+        _refused(L.kv_rows_accept(base, other, 1, 2, 2, 64, 64, _i32(0, 0), 8, 0x30000, 0x40000, None), "overlap")
+    _refused(L.kv_rows_accept(base, base + one, 3, 2, 2, 64, 64, _i32(0, 0), 8, 0x30000, 0x40000, None), "overlap")
+
+
 # ---- the marshalling extension ---------------------------------------------------------------------------
 
 def test_the_extension_is_named_for_its_python():

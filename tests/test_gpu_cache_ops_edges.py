@@ -289,3 +289,31 @@ def test_forward_derivatives_are_refused_on_the_gpu():
             lps.attention_prompt_packed(fwd.make_dual(q, torch.ones_like(q)), k, k, [0, 20])
         inside = lps.attention_prompt_packed(q, k, k, [0, 20])
     assert torch.equal(inside, lps.attention_prompt_packed(q, k, k, [0, 20]))
+
+
+# ---- caches in one buffer ------------------------------------------------------------------------------
+
+def test_caches_side_by_side_in_one_buffer():
+    """K and V caches as the halves of one tensor touch but do not overlap; shifted by a row they do, and are refused."""
+    both = torch.zeros(2, 2, 2, 50, 64, device="cuda", dtype=FP)
+    k, v = _randn(1, 20, 2, 64, dtype=FP), _randn(2, 20, 2, 64, dtype=FP)
+    lps.kv_rows_append(k, v, [0, 12, 20], both[0], both[1], [3, 40])
+    want = torch.zeros_like(both)
+    for half, t in enumerate((k, v)):
+        want[half, 0, :, 3:15], want[half, 1, :, 40:48] = t[:12].transpose(0, 1), t[12:].transpose(0, 1)
+    assert torch.equal(both, want)
+    path = torch.tensor([[1, 3], [0, 2]], dtype=torch.int32, device="cuda")
+    taken = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    lps.kv_rows_accept(both[0], both[1], [4, 41], path, taken)
+    for b, pos in enumerate((4, 41)):
+        rows = want[:, b, :, [pos + int(x) for x in path[b]]].clone()
+        want[:, b, :, pos:pos + 2] = rows
+    assert torch.equal(both, want)
+    flat = torch.zeros(2 * 2 * 2 * 50 * 64 + 64, device="cuda", dtype=FP)
+    n = 2 * 2 * 50 * 64
+    a, b = flat[:n].view(2, 2, 50, 64), flat[64:64 + n].view(2, 2, 50, 64)
+    with pytest.raises(lps.LpsError, match="overlap"):
+        lps.kv_rows_append(k, v, [0, 12, 20], a, b, [3, 40])
+    with pytest.raises(lps.LpsError, match="overlap"):
+        lps.kv_rows_accept(a, b, [4, 41], path, taken)
+    assert not flat.any()
