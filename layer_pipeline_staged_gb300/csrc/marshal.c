@@ -550,6 +550,24 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+/* host_ints(values, count or -1) -> list: how the calls read their host integers, for tests without a GPU. */
+static PyObject *host_ints(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  ints a;
+  (void)self;
+  if (argc_is(n, 2)) return NULL;
+  const Py_ssize_t want = PyLong_AsSsize_t(args[1]);
+  if (want == -1 && PyErr_Occurred()) return NULL;
+  if (ints_from(args[0], want, "values", &a)) return ints_free(&a), NULL;
+  PyObject *list = PyList_New(a.n);
+  for (Py_ssize_t i = 0; list && i < a.n; ++i) {
+    PyObject *x = PyLong_FromLong(a.v[i]);
+    if (!x) Py_CLEAR(list);
+    else PyList_SET_ITEM(list, i, x);
+  }
+  ints_free(&a);
+  return list;
+}
+
 /* init(LpsError, torch): what the calls need of torch, looked up once. */
 static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
@@ -591,7 +609,8 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
 #define FAST(f) (PyCFunction)(void (*)(void))f
 static PyMethodDef methods[] = {{"init", FAST(init), METH_FASTCALL, NULL},     {"prompt", FAST(prompt), METH_FASTCALL, NULL},
                                 {"tree", FAST(tree), METH_FASTCALL, NULL},     {"append", FAST(append), METH_FASTCALL, NULL},
-                                {"accept", FAST(accept), METH_FASTCALL, NULL}, {NULL, NULL, 0, NULL}};
+                                {"accept", FAST(accept), METH_FASTCALL, NULL}, {"host_ints", FAST(host_ints), METH_FASTCALL, NULL},
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__marshal(void) {

@@ -118,6 +118,70 @@ def test_a_scale_that_32_bits_do_not_hold_is_refused(scale):
                 call(fits)
 
 
+# ---- host integers -------------------------------------------------------------------------------------------
+
+class _Int:
+    def __init__(self, x):
+        self.x = x
+
+    def __index__(self):
+        return self.x
+
+
+def _ints(values, n=-1):
+    return ops._ready().host_ints(values, n)
+
+
+def test_host_integers_are_read_from_every_kind():
+    """Lists, tuples, ranges, arrays of several types, byte orders, strides and directions, CPU tensors, and any
+    object with __index__."""
+    np, torch = pytest.importorskip("numpy"), pytest.importorskip("torch")
+    want, wide = [-5, 0, 2**31 - 1, -2**31], np.zeros((4, 3), np.int64)
+    wide[:, 1] = want
+    for values in (want, tuple(want), np.array(want), np.array(want, np.int32), np.array(want, np.int32)[::-1][::-1], wide[:, 1],
+                   np.array(want[::-1])[::-1], np.array(want, ">i4"), np.array(want, ">i8"), np.array(want, "<i8"), torch.tensor(want),
+                   torch.tensor(want, dtype=torch.int32), torch.tensor(wide[:, 1]), [_Int(x) for x in want], [np.int64(x) for x in want]):
+        assert _ints(values) == want and _ints(values, 4) == want
+    assert _ints(range(0, 51, 10)) == [0, 10, 20, 30, 40, 50]
+    for t in (np.uint8, np.int8, np.uint16, np.int16, np.uint32, np.uint64):
+        assert _ints(np.array([0, 3, 100], t)) == [0, 3, 100]
+    many = list(range(1000))  # more than the call's own room
+    assert _ints(many) == _ints(np.array(many)) == _ints(np.array(many, np.int32)[:], 1000) == many
+    assert _ints([]) == _ints(np.zeros(0, np.int32)) == _ints((), 0) == []
+
+
+def test_what_is_not_a_row_of_host_integers_is_refused():
+    np, torch = pytest.importorskip("numpy"), pytest.importorskip("torch")
+    for values in ([0.0, 1.0], np.array([0.0, 1.0]), np.array([0, 1], np.float16), np.array([False, True]), np.array([[0, 1]]), np.array(3),
+                   [0, 2**31], [-2**31 - 1, 0], np.array([0, 2**31]), np.array([0, 2**32 - 1], np.uint32), np.array([2**63], np.uint64),
+                   [2**70], ["0"], [None], torch.tensor([0.5]), torch.tensor([[1, 2]]), np.array([1j])):
+        with pytest.raises(ValueError):
+            _ints(values)
+    for values in (None, 7, object()):
+        with pytest.raises(TypeError):
+            _ints(values)
+    for values in ([0, 1], np.array([0, 1]), np.array([0, 1], np.int16)):
+        for n in (0, 1, 3):
+            with pytest.raises(ValueError, match="must hold"):
+                _ints(values, n)
+
+    class Emptying:
+        def __index__(self):
+            values.clear()
+            return 0
+
+    values = [Emptying()] + [1] * 40
+    with pytest.raises(ValueError, match="changed"):
+        _ints(values)
+
+    class Failing:
+        def __index__(self):
+            raise KeyError("no")
+
+    with pytest.raises(ValueError, match="integers"):
+        _ints([0, Failing()])
+
+
 # ---- the library's own refusals, with addresses that are never dereferenced ------------------------------
 
 def _no_gpu():
