@@ -302,11 +302,11 @@ def test_caches_side_by_side_in_one_buffer():
     for half, t in enumerate((k, v)):
         want[half, 0, :, 3:15], want[half, 1, :, 40:48] = t[:12].transpose(0, 1), t[12:].transpose(0, 1)
     assert torch.equal(both, want)
-    path = torch.tensor([[1, 3], [0, 2]], dtype=torch.int32, device="cuda")
+    path = torch.tensor([[1, 3, 0, 0], [0, 2, 0, 0]], dtype=torch.int32, device="cuda")  # draft rows below the width
     taken = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
     lps.kv_rows_accept(both[0], both[1], [4, 41], path, taken)
     for b, pos in enumerate((4, 41)):
-        rows = want[:, b, :, [pos + int(x) for x in path[b]]].clone()
+        rows = want[:, b, :, [pos + int(x) for x in path[b, :2]]].clone()
         want[:, b, :, pos:pos + 2] = rows
     assert torch.equal(both, want)
     flat = torch.zeros(2 * 2 * 2 * 50 * 64 + 64, device="cuda", dtype=FP)
