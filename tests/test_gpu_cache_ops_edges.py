@@ -317,3 +317,69 @@ def test_caches_side_by_side_in_one_buffer():
     with pytest.raises(lps.LpsError, match="overlap"):
         lps.kv_rows_accept(a, b, [4, 41], path, taken)
     assert not flat.any()
+
+
+# ---- outputs on 16 and on 32 bytes -----------------------------------------------------------------------
+
+def _spaced(shape, hd, shift, dtype):
+    """A view of `shape` whose rows lie `shift` elements apart (8: on 16 bytes, 16: on 32), and its buffer."""
+    *outer, heads, _ = shape
+    buf = torch.full((*outer, heads * (hd + shift) + shift), 3.0, device="cuda", dtype=dtype)
+    return buf[..., shift:].unflatten(-1, (heads, hd + shift))[..., :hd], buf
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("nq,nkv", [(3, 1), (8, 2), (14, 2)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_output_rows_on_16_and_on_32_bytes(hd, nq, nkv, dtype):
+    """The same bits from every way out, with ragged last tiles, and with an infinity and a NaN of V that are seen;
+    nothing between the rows is touched."""
+    off, inf = [0, 70, 71, 331], float("inf")
+    q, k, v = _randn(1, 331, nq, hd, dtype=dtype), _randn(2, 331, nkv, hd, dtype=dtype), _randn(3, 331, nkv, hd, dtype=dtype)
+    kc, vc, tq = _randn(4, 2, nkv, 300, hd, dtype=dtype), _randn(5, 2, nkv, 300, hd, dtype=dtype), _randn(6, 2, 41, nq, hd, dtype=dtype)
+    par = _chain(2, 41)
+    for plant in (False, True):
+        if plant:
+            v[75, :, 5], v[200, :, hd - 1], vc[0, :, 3, 7], vc[1, :, 255, hd - 2] = inf, float("nan"), -inf, inf
+        want = lps.attention_prompt_packed(q, k, v, off)
+        tree = lps.attention_tree_verify(tq, kc, vc, par, [200, 240], [41, 30], out=torch.full_like(tq, 3.0))
+        if plant:
+            assert (want[75:, :, 5] == inf).all() and want[200:, :, hd - 1].isnan().all()
+            assert (tree[0, :, :, 7] == -inf).all() and (tree[1, 15:30, :, hd - 2] == inf).all()
+        for shift in (8, 16):
+            out, buf = _spaced(q.shape, hd, shift, dtype)
+            lps.attention_prompt_packed(q, k, v, off, out=out)
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+            out.fill_(3.0)
+            assert (buf == 3.0).all()
+            out, buf = _spaced(tq.shape, hd, shift, dtype)
+            lps.attention_tree_verify(tq, kc, vc, par, [200, 240], [41, 30], out=out)
+            assert torch.equal(out.view(torch.int16), tree.view(torch.int16))
+            out.fill_(3.0)
+            assert (buf == 3.0).all()
+
+
+# ---- row moves of either type --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_accept_moves_bits_of_either_type(hd, dtype):
+    kc, vc = (torch.randint(-2**15, 2**15, (3, 4, 3, 90, hd), device="cuda", dtype=torch.int16).view(dtype) for _ in range(2))
+    paths, pos = [[0, 3, 4, 11], [], [5], list(range(1, 12))], [70, 5, 0, 33]
+    want = [kc.clone(), vc.clone()]
+    path = torch.full((4, 12), -1, dtype=torch.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = torch.tensor(p, dtype=torch.int32)
+        for w, c in zip(want, (kc, vc)):
+            for i, x in enumerate(p):
+                w[:, b, :, pos[b] + i] = c[:, b, :, pos[b] + x]
+    lps.kv_rows_accept(kc, vc, pos, path.cuda(), torch.tensor([len(p) for p in paths], dtype=torch.int32, device="cuda"))
+    for got, w in zip((kc, vc), want):
+        assert torch.equal(got.view(torch.int16), w.view(torch.int16))
+
+
+def test_a_range_of_offsets():
+    q, k = _randn(1, 50, 4, 64), _randn(2, 50, 2, 64)
+    got = lps.attention_prompt_packed(q, k, k, range(0, 51, 10))
+    assert torch.equal(got, lps.attention_prompt_packed(q, k, k, [0, 10, 20, 30, 40, 50]))
+    assert not torch.equal(got, lps.attention_prompt_packed(q, k, k, [0, 50]))
