@@ -408,36 +408,39 @@ __device__ __forceinline__ uint32_t probe4(uint4 x, uint32_t acc) {
 }
 
 // The columns of one row's result, 8 (a unit) at a time from unit u0 on, that are not
-// finite although no score of the row is NaN: where V holds infinities or NaNs at keys
-// the row sees, their sum; a key whose score is -inf has a weight of zero, and zero
-// times them is NaN; any other weight is positive. Where V holds none, the sum has
-// gone past the type, and stays.
+// finite although the row has weights and no score of it is NaN: where V holds
+// infinities or NaNs at keys the row sees, their sum; a key whose score is -inf has a
+// weight of zero, and zero times them is NaN; any other weight is positive. Where V
+// holds none, the sum has gone past the type, and stays. As no score is NaN or inf, one
+// is -inf exactly where the key is not finite. A column is looked for until it is NaN.
 template <bool BF16, int HD, bool TREE>
-__device__ __forceinline__ void settle(const TileAttnParams& p, const Item& it, int tok, int head, int lim, unsigned long long anc,
-                                       uint16_t* out, int u0, int step) {
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + it.tok0 * (TREE ? p.q_seq : p.q_tok) + tok * p.q_tok + head * p.q_head;
+__device__ __forceinline__ void settle(const TileAttnParams& p, const Item& it, int lim, unsigned long long anc, uint16_t* out,
+                                       int u0, int step) {
   const uint16_t* k = static_cast<const uint16_t*>(p.k) + it.tok0 * (TREE ? p.k_seq : p.k_row) + it.g * p.k_head;
   const uint16_t* v = static_cast<const uint16_t*>(p.v) + it.tok0 * (TREE ? p.v_seq : p.v_row) + it.g * p.v_head;
 #pragma unroll 1
   for (int u = u0; u < HD / 8; u += step) {
-    if (!wild<BF16>(probe4<BF16>(*reinterpret_cast<const uint4*>(out + u * 8), 0))) continue;
+    uint32_t open = 0, hit = 0;  // columns that are not finite and not known to be NaN; those of which V says more
+#pragma unroll
+    for (int e = 0; e < 8; ++e) open |= nonfinite<BF16>(out[u * 8 + e]) ? 1u << e : 0u;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint32_t hit = 0;
 #pragma unroll 1
-    for (int key = 0; key < it.kend; ++key) {
+    for (int key = 0; key < it.kend && open; ++key) {
       if (!(seen32<TREE>(key, lim, anc) & 1u)) continue;
       const uint4 x = *reinterpret_cast<const uint4*>(v + key * p.v_row + u * 8);
       if (!wild<BF16>(probe4<BF16>(x, 0))) continue;
-      float s = 0.f;
+      uint32_t acc = 0;
 #pragma unroll 1
-      for (int d = 0; d < HD; ++d) s = fmaf(widen<BF16>(q[d]), widen<BF16>(k[key * p.k_row + d]), s);
+      for (int d = 0; d < HD; d += 8) acc = probe4<BF16>(*reinterpret_cast<const uint4*>(k + key * p.k_row + d), acc);
+      const bool weightless = wild<BF16>(acc);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint16_t y = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
         if (!nonfinite<BF16>(y)) continue;
-        sum[e] += s == -INFINITY ? NAN : widen<BF16>(y);
+        sum[e] += weightless ? NAN : widen<BF16>(y);
         hit |= 1u << e;
+        if (sum[e] != sum[e]) open &= ~(1u << e);
       }
     }
 #pragma unroll
@@ -1005,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       };
       if (ok && warp_ok && !joined) {
         if (nb > 0) {
-          const float inv = seen ? 1.0f / l : 0.f;
+          const float inv = !seen ? 0.f : l != 0.f ? 1.0f / l : NAN;  // all scores -inf: 0 / 0
           uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * (TREE ? p.o_seq : p.o_tok) + tok * p.o_tok +
                           (it.g * p.group + row_head) * p.o_head;
           uint32_t odds[2] = {0, 0};  // NaN where a result of the row is not finite
@@ -1076,9 +1079,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
           bool odd = false;
 #pragma unroll
           for (int k = 0; k < 2; ++k) odd |= wild<BF16>(odds[k]);
-          if (odd && seen && l == l) {
+          if (odd && seen && inv == inv) {
             if (TREE) again = true;
-            else settle<BF16, HD, TREE>(p, it, tok, it.g * p.group + row_head, lim, anc, out, 0, 1);
+            else settle<BF16, HD, TREE>(p, it, lim, anc, out, 0, 1);
           }
         }
       } else if (TREE && joined) {
@@ -1177,10 +1180,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
   if (TREE && __builtin_expect(again, 0)) {
     // a thread has the row here, and its warp the parents, that it had in its softmax
     const Item& it = items[0];
-    const int half = tid >> 7, r = tid & 127, tok = it.t0 + (solo ? 0 : half * p.tpt) + r / p.group, head = it.g * p.group + r % p.group;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * p.o_seq + tok * p.o_tok + head * p.o_head;
+    const int half = tid >> 7, r = tid & 127, tok = it.t0 + (solo ? 0 : half * p.tpt) + r / p.group;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + it.tok0 * p.o_seq + tok * p.o_tok + (it.g * p.group + r % p.group) * p.o_head;
     const int u0 = joined ? blockIdx.x % p.cluster + (solo ? half * p.cluster : 0) : 0;
-    settle<BF16, HD, TREE>(p, it, tok, head, p.pos[it.s] - 1, tree_mask(parents + warp * kTreeMax, tok), out, u0,
+    settle<BF16, HD, TREE>(p, it, p.pos[it.s] - 1, tree_mask(parents + warp * kTreeMax, tok), out, u0,
                            joined ? (solo ? 2 * p.cluster : p.cluster) : 1);
   }
 

@@ -209,6 +209,24 @@ def test_tree_infinity_seen_with_a_weight_next_to_nothing(tree, hd, dtype):
         assert got[:, first:, :, [3, 40, 50]].isnan().all(), (peak, at)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_all_infinite_or_nan(bad):
+    """A cache or a long prompt full of them is answered like any other, well within the kernels' waits."""
+    for n, hd in ((8184, 128), (3000, 64)):
+        q, k, v = _randn(1, n, 8, hd), _randn(2, n, 2, hd), torch.full((n, 2, hd), bad, device="cuda", dtype=BF)
+        out = lps.attention_prompt_packed(q, k, v, [0, n])
+        lps.cache_ops_status()
+        assert out.isnan().all() if bad != bad else (out == bad).all()
+        k[n // 2] = -float("inf")  # a NaN score, or one of either infinity, makes NaN of the rows that see it
+        out = lps.attention_prompt_packed(q, k, v, [0, n])
+        lps.cache_ops_status()
+        assert out[n // 2:].isnan().all() and (bad != bad or (out[:n // 2] == bad).all())
+    kc, vc, tq = _randn(3, 2, 2, 100064, 128), torch.full((2, 2, 100064, 128), bad, device="cuda", dtype=BF), _randn(4, 2, 40, 8, 128)
+    out = lps.attention_tree_verify(tq, kc, vc, _chain(2, 40), [100000, 7], [40, 40])
+    lps.cache_ops_status()
+    assert out.isnan().all() if bad != bad else (out == bad).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_values_near_the_types_end(dtype):
     """Large finite values stay what they are (a mean of them): o is summed in fp32 with weights of up to 2^8 a key
