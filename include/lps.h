@@ -523,8 +523,8 @@ int attention_prompt_packed(const void* q, const void* k, const void* v, void* o
  * from draft parents[b][t] < t, or from the last committed token when that is
  * -1; it sees the cache rows [0, pos[b]), itself and its chain of parents. A
  * draft all of whose scores are -inf gets NaN, as the formula does.
- *   q, out   device [batch][width][n_q_heads][head_dim]; rows t >= rows[b] are
- *            neither read nor written
+ *   q, out   device [batch][width][n_q_heads][head_dim]; rows t >= rows[b]
+ *            change nothing and are not written
  *   pos, rows  host int32[batch]: 0 <= rows[b] <= width, pos[b] + rows[b] <= max_ctx
  *   parents  device int32[batch][width]; the drafts of a chain that holds a
  *            parent outside [-1, t) get zeros

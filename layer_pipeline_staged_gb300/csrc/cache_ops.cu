@@ -159,10 +159,10 @@ extern "C" int attention_prompt_packed(const void* q, const void* k, const void*
     for (int s0 = 0; s0 < n_seqs; s0 += kOpSeqs) {
       TileAttnParams p{};
       p.n_seqs = n_seqs - s0 < kOpSeqs ? n_seqs - s0 : kOpSeqs;
-      p.q = q, p.k = k, p.v = v, p.out = out;
-      p.q_tok = st[0], p.q_head = st[1], p.k_row = st[2], p.k_head = st[3];
+      p.k = k, p.v = v, p.out = out;
+      p.k_row = st[2], p.k_head = st[3];
       p.v_row = st[4], p.v_head = st[5], p.o_tok = st[6], p.o_head = st[7];
-      p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+      p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
       p.wide_out = wide(out, {st[6], st[7]});
       p.wait_limit = wait_cycles(g_wait_limit);
       p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
@@ -220,15 +220,15 @@ extern "C" int attention_tree_verify(const void* q, const void* k_cache, const v
     TileAttnParams p{};
     p.n_seqs = batch;
     p.width = width;
-    p.nq = n_q_heads, p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
+    p.nkv = n_kv_heads, p.group = n_q_heads / n_kv_heads;
     for (int b = 0; b < batch; ++b) p.pos[b] = pos[b], p.len[b] = rows[b];
     long long ctas = 0;
     cudaError_t e = tile_tree_plan(p, bf16, head_dim, &ctas);
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, std::string("plan: ") + cudaGetErrorString(e));
     if (ctas == 0) return LPS_OK;
     if (ctas > 0x7fffffffll) return host_fail(LPS_EINVAL, FN, "too many rows for one launch");
-    p.q = q, p.k = k_cache, p.v = v_cache, p.out = out;
-    p.q_seq = st[0], p.q_tok = st[1], p.q_head = st[2], p.o_seq = st[3], p.o_tok = st[4], p.o_head = st[5];
+    p.k = k_cache, p.v = v_cache, p.out = out;
+    p.o_seq = st[3], p.o_tok = st[4], p.o_head = st[5];
     p.k_row = p.v_row = head_dim;
     p.k_head = p.v_head = static_cast<long long>(max_ctx) * head_dim;
     p.k_seq = p.v_seq = p.k_head * n_kv_heads;

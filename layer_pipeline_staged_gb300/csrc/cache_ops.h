@@ -23,17 +23,15 @@ struct TileAttnParams {
   CUtensorMap tmap_q;  // [batch][token][head][hd], boxes of one tile's rows
   CUtensorMap tmap_k;  // [batch][head][row][hd]
   CUtensorMap tmap_v;
-  const void* q;       // element (s, t, h): q + s * q_seq + (tok0 + t) * q_tok + h * q_head
   const void* k;       // element (s, j, g): k + s * k_seq + (tok0 + j) * k_row + g * k_head
   const void* v;
-  void* out;
-  long long q_seq, q_tok, q_head;
+  void* out;           // element (s, t, h): out + s * o_seq + (tok0 + t) * o_tok + h * o_head
   long long k_seq, k_row, k_head;
   long long v_seq, v_row, v_head;
   long long o_seq, o_tok, o_head;
   const int* parents;  // tree: device [n_seqs][width]
   int width;
-  int nq, nkv, group, n_seqs;
+  int nkv, group, n_seqs;
   float scale_log2;    // scale * log2(e)
   int wide_out;        // out's rows are 32-byte aligned
   long long wait_limit;  // cycles a wait may take before it reports an error

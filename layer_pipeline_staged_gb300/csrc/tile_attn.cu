@@ -35,8 +35,9 @@
 // A prompt's CTA stays on its SM: once the copies of its item are issued, its
 // TMA lane takes over the next CTA of the grid that has not started
 // (clusterlaunchcontrol), so the next item's Q, K and V arrive, and its first S
-// is made, while the last item's softmax and epilogue still run. The grid is
-// ordered from the largest item to the smallest.
+// is made, while the last item's softmax and epilogue still run. The grid goes
+// through the sequences from the longest to the shortest, and through each from its
+// largest item to its smallest.
 //
 // A tree's keys are shared out over a thread-block cluster, whose CTAs join
 // their (o, m, l) through distributed shared memory; a prompt tile's are not.
@@ -83,9 +84,15 @@ constexpr int kLaunchRegs = 168;
 constexpr int kMaxStages = 8;
 constexpr int kMaxFix = 4;        // blocks of one item that some row does not see whole (at most 3)
 constexpr int kClusterSizes = 5;  // clusters of 1, 2, 4, 8 and 16 CTAs
-// A launch of up to so many CTAs starts under the stream's last kernel (18 tokens,
-// call after call: 5.6 -> 4.6 us); of more, its early CTAs only wait on SMs that
-// the last one's could use (7 prompts, 296 CTAs: 22.15 us so, 22.5 started early).
+// A prompt launch of up to so many CTAs starts under the stream's last kernel; call
+// after call, 32/8 heads of 128: 64 tokens (8 CTAs) 6.1 us so and 6.6 otherwise, 512
+// (64) 11.2 and 11.9, 1024 (128) 18.6 and 18.9. With more CTAs than SMs, items of one
+// length still gain (2048 tokens, 256 CTAs: 32.3 and 32.7), but of several lengths
+// they lose, as early CTAs hold SMs on which the last launch's could take over items
+// (7 prompts up to 1024, 296 CTAs: 22.9 and 21.9; 4 up to 1024, 448 CTAs, heads of 64:
+// 31.4 and 31.0). A launch of clusters, which take nothing over, always starts so: 1
+// row over 1000 8.1 and 9.0, 26 over 8150 15.8 and 16.3, 64 trees of 64 over 4000 237
+// and 239.
 constexpr int kEarlyCtas = 128;
 constexpr float kStale = 8.0f;    // the base may lag the maximum by a factor of about 2^8
 // fp16 weights are made 2^7 times larger, which leaves the sum as it is: they reach
