@@ -44,12 +44,13 @@ static int ints_of(PyObject *seq, int64_t *out, const char *what) {
   return (int)n;
 }
 
+static int g_duals; /* the running call: tensors may carry forward derivatives (read once, under the interpreter lock) */
+
 /* Whether `obj` carries a forward derivative, which the calls would lose; -1 on an error. Its requires_grad
  * is false and its memory the primal's, so nothing else tells. */
 static int has_tangent(PyObject *obj) {
-  PyObject *level = PyDict_GetItemWithError(g_dual, s_level); /* borrowed */
-  if (level && PyLong_Check(level) && PyLong_AsLong(level) < 0) return 0;
-  PyObject *unpack = PyErr_Occurred() ? NULL : PyDict_GetItemWithError(g_dual, s_unpack);
+  if (!g_duals) return 0;
+  PyObject *unpack = PyDict_GetItemWithError(g_dual, s_unpack); /* borrowed */
   if (!unpack && !PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "this torch has no forward_ad.unpack_dual");
   PyObject *dual = unpack ? PyObject_CallOneArg(unpack, obj) : NULL, *tangent = dual ? PySequence_GetItem(dual, 1) : NULL;
   const int has = tangent ? tangent != Py_None : -1;
@@ -385,6 +386,14 @@ static int argc_is(Py_ssize_t n, Py_ssize_t want) {
   return -1;
 }
 
+/* The start of a call on tensors. */
+static int begin(Py_ssize_t n, Py_ssize_t want) {
+  if (argc_is(n, want)) return -1;
+  PyObject *level = PyDict_GetItemWithError(g_dual, s_level);
+  g_duals = !(level && PyLong_Check(level) && PyLong_AsLong(level) < 0);
+  return PyErr_Occurred() ? -1 : 0;
+}
+
 /* A library call without the interpreter lock: a launch waits while the stream's
  * queue is full, and what the queue waits for may need the lock. */
 #define UNLOCKED(call)                     \
@@ -403,7 +412,7 @@ static PyObject *prompt(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   place at;
   int kind = 0;
   (void)self;
-  if (argc_is(n, 6) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k") || tensor_of(args[2], &t[2], "v")) return NULL;
+  if (begin(n, 6) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k") || tensor_of(args[2], &t[2], "v")) return NULL;
   const tensor *q = &t[0], *k = &t[1];
   if (q->dim != 3 || k->dim != 3) return refuse("q, k and v must be [tokens, heads, head_dim]"), NULL;
   if (k->shape[0] != q->shape[0] || k->shape[2] != q->shape[2] || !same_shape(k, &t[2]))
@@ -442,7 +451,7 @@ static PyObject *tree(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   place at;
   int kind = 0;
   (void)self;
-  if (argc_is(n, 8) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k_cache") ||
+  if (begin(n, 8) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k_cache") ||
       tensor_of(args[2], &t[2], "v_cache") || tensor_of(args[3], &par, "parents"))
     return NULL;
   const tensor *q = &t[0], *kc = &t[1];
@@ -487,7 +496,7 @@ static PyObject *append(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   place at;
   int kind = 0;
   (void)self;
-  if (argc_is(n, 6) || tensor_of(args[0], &t[0], "k") || tensor_of(args[1], &t[1], "v") || tensor_of(args[3], &t[2], "k_cache") ||
+  if (begin(n, 6) || tensor_of(args[0], &t[0], "k") || tensor_of(args[1], &t[1], "v") || tensor_of(args[3], &t[2], "k_cache") ||
       tensor_of(args[4], &t[3], "v_cache"))
     return NULL;
   const tensor *k = &t[0], *kc = &t[2];
@@ -528,7 +537,7 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   place at;
   int kind = 0;
   (void)self;
-  if (argc_is(n, 5) || tensor_of(args[0], &t[0], "k_cache") || tensor_of(args[1], &t[1], "v_cache")) return NULL;
+  if (begin(n, 5) || tensor_of(args[0], &t[0], "k_cache") || tensor_of(args[1], &t[1], "v_cache")) return NULL;
   const tensor *kc = &t[0];
   if ((kc->dim != 4 && kc->dim != 5) || !same_shape(&t[1], kc))
     return refuse("the caches must be [layers, batch, kv heads, max_ctx, head_dim], both alike"), NULL;
