@@ -229,10 +229,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void st_global32(void* at, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+// Stores of 32 and 16 bytes by the lanes with `on`, under a predicate: the warp stays together.
+__device__ __forceinline__ void st_global32(bool on, void* at, const uint32_t* r) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %9, 0;\n\t"
+      "@p st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t}" ::"l"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+__device__ __forceinline__ void st_global16(bool on, void* at, const uint32_t* r) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(static_cast<uint32_t>(on))
+      : "memory");
 }
 
 // x * 0 + acc: acc becomes NaN where x holds an infinity or a NaN.
@@ -987,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
       const bool fix = dirty[no & 1] == no + 1;
       // adds the infinities and NaNs of the V blocks made safe to o's 32 columns from
       // c on. TMEM's instructions want the warp together: so it is brought here, and
-      // behind every loop or store that not all lanes take part in.
+      // stores that not all lanes make are predicated.
       auto mend_o = [&](int c, float* o) {
         if (!fix) return;  // all lanes alike
         if (seen) {
@@ -1055,9 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
                 uint32_t x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = w[i / 2 * 16 + e / 2 * 4 + i % 2 * 2 + e % 2];
-                if (to[i]) st_global32(to[i] + c + 16 * (lane & 3), x);
+                st_global32(to[i] != nullptr, to[i] + c + 16 * (lane & 3), x);
               }
-              __syncwarp();
             }
           } else {
             // a thread writes its row, 32 bytes at a time where out is so aligned
@@ -1065,22 +1076,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_attn_kernel(const __grid_con
             for (int c = 0; c < HD; c += 32) {
               float o[32];
               load_o(c, o);
-              if (row_ok) {
-                uint32_t w[16];
+              uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = seen ? pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-                if (HD == 64 && p.wide_out) {
-                  st_global32(out + c, w);
-                  st_global32(out + c + 16, w + 8);
-                } else {
+              for (int e = 0; e < 16; ++e) w[e] = seen ? pack16<BF16>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+              if (HD == 64 && p.wide_out) {
+                st_global32(row_ok, out + c, w);
+                st_global32(row_ok, out + c + 16, w + 8);
+              } else {
 #pragma unroll
-                  for (int u = 0; u < 4; ++u)
-                    *reinterpret_cast<uint4*>(out + c + u * 8) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) odds[e & 1] = probe<BF16>(w[e], odds[e & 1]);
+                for (int u = 0; u < 4; ++u) st_global16(row_ok, out + c + u * 8, w + 4 * u);
               }
-              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) odds[e & 1] = probe<BF16>(w[e], odds[e & 1]);
             }
           }
           bool odd = false;
