@@ -45,7 +45,7 @@
 // Waits are bounded and report through the status word.
 //
 // What bounds it, on one GB300 (cuBLAS bf16 1865 TFLOP/s, copy 6793 GB/s):
-//   - an 8184-token prompt, 32/8 heads of 128: 370 us, 1483 TFLOP/s. A paired
+//   - an 8184-token prompt, 32/8 heads of 128: 370 to 374 us, 1470 TFLOP/s. A paired
 //     iteration (two tiles x 128 keys) is 2048 cycles of products at the tensor
 //     core's rate and takes 2900 to 3300: a block's softmax is 1160 cycles (the
 //     hardware's exp2 alone 512), hand-overs between the warps 250 to 300 each,
