@@ -10,6 +10,7 @@ the results sit next to this file and are git-ignored.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import os
 import shutil
 import subprocess
@@ -78,9 +79,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    untagged = os.path.join(HERE, "_marshal.so")  # any Python would load it
-    if os.path.exists(untagged):
-        os.remove(untagged)
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(os.path.join(HERE, "_marshal.so"))  # an untagged one, which any Python would load
     python = sysconfig.get_paths()["include"]
     if not os.path.exists(os.path.join(python, "Python.h")):
         sys.stderr.write(f"no Python.h in {python}: the torch wrappers of the cache operators are not built\n")
