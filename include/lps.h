@@ -562,18 +562,150 @@ int kv_rows_append(const void* k, const void* v, int n_seqs, const int32_t* offs
 int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_kv_heads, int head_dim, int max_ctx,
                    const int32_t* pos, int width, const int32_t* path, const int32_t* accepted, void* stream);
 
-/* Synchronize `stream` and read the status word that the two attention kernels
- * set on the current device when one of their bounded waits gives up. LPS_OK:
+/* Synchronize `stream` and read the status words that the attention kernels of
+ * this section set on the current device when one of their bounded waits gives up. LPS_OK:
  * none has since the last check. LPS_ECUDA: at least one call's `out` is
- * invalid; the word is then cleared. It is shared by all calls on the device. */
+ * invalid; the words are then cleared. They are shared by all calls on the device. */
 int cache_ops_status(void* stream);
 
 /* Test hook, like model_set_wait_limit: the SM cycles that a bounded wait of the
- * two attention kernels may take, in calls that the calling thread makes from
+ * attention kernels may take, in calls that the calling thread makes from
  * now on, before the kernel gives up, records an error and returns; 0 restores
  * the default of about two seconds. A kernel that gives up still waits, with its
  * own fixed bound, for what it has issued. LPS_EINVAL for cycles < 0. */
 int cache_ops_set_wait_limit(long long cycles);
+
+/* ---- operators over a paged cache ----------------------------------------------- */
+
+/* A decode step over a cache in pages, with everything that changes from step to
+ * step on the DEVICE, so that one captured step serves every later one: rotary
+ * positions and the append of a step's rows, attention of one token a sequence,
+ * eviction of the rows that attention passes over, and the adjustment of the
+ * logits. The common rules above hold, but for these:
+ *   - a cache is two arrays of pages [n_pages][n_kv_heads][page_size][head_dim],
+ *     dense, of bf16 or fp16; page_size is a multiple of 8, up to 65536. Row j of
+ *     sequence s is row j % page_size of page table[s][j / page_size]; a table is
+ *     a dense device int32[n][table_width], table_width * page_size at most
+ *     2^31 - 2^16. Entries behind a sequence's rows are not looked at;
+ *   - lengths, tables, offsets and positions are device arrays that the kernels
+ *     check: what they hold never makes a call read or write outside the arrays
+ *     it was given. The calls say what becomes of a sequence that breaks the rules;
+ *   - key_weights is a device float array [n_pages][n_kv_heads][page_size], one
+ *     weight a cached key and kv head;
+ *   - a call with a workspace uses it from its start on the stream to its end; calls
+ *     that may overlap need workspaces of their own. Its contents need not be set. */
+#define LPS_TYPE_FP32 2
+
+/* Rotary positions: with angle a = positions[t] * freqs[i], the pair i of every
+ * head's first rot_dim elements becomes
+ *     x' = magnitude (x cos a - y sin a), y' = magnitude (y cos a + x sin a),
+ * (x, y) = elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) where interleaved is
+ * not 0; the other elements are copied. The turn is undone, and a gradient taken
+ * back, by the negative positions. Angles are taken modulo a turn exactly, from
+ * freqs in 64 bits; products are fp32, rounded once.
+ *   q, q_out   device [n_tokens][n_q_heads][head_dim]; k, k_out likewise; an
+ *              output may be its input (the same address and strides) and overlaps
+ *              nothing else
+ *   positions  device int32[n_tokens], any value
+ *   freqs      device double[rot_dim / 2], radians a position
+ *   rot_dim    a multiple of 16 from 0 (copies) to head_dim
+ *   strides    host int64[8]: token and head stride of q, k, q_out, k_out; NULL: dense */
+int rotary_rows(const void* q, const void* k, void* q_out, void* k_out, int type, int n_tokens,
+                const int32_t* positions, const double* freqs, int rot_dim, int interleaved, float magnitude,
+                int n_q_heads, int n_kv_heads, int head_dim, const int64_t* strides, void* stream);
+
+/* rotary_rows with the turned keys, and the values as they are, written to the
+ * cache: sequence s has the tokens offsets[s] .. offsets[s + 1] - 1, and its
+ * last one goes to row lengths[s] - 1 (lengths count the rows after the append).
+ *   v, k, q, q_out  as above (v like k); tokens outside the offsets are neither
+ *              used nor written
+ *   offsets    device int32[n_seqs + 1], not descending; NULL: one token a
+ *              sequence (n_tokens = n_seqs)
+ *   lengths    device int32[n_seqs]; table device int32[n_seqs][table_width]
+ *   positions  device int32[n_tokens], or NULL: the row that the token goes to
+ *   key_weights  set to 0 for the new rows; or NULL
+ *   strides    host int64[8]: token and head stride of q, k, v, q_out; NULL: dense
+ * A token whose row lies outside the table, or on a page outside [0, n_pages), is
+ * not stored; its q_out is still written. No two tokens may go to one row. */
+int rotary_append_paged(const void* q, const void* k, const void* v, void* q_out, int type, int n_tokens, int n_seqs,
+                        const int32_t* offsets, const int32_t* lengths, const int32_t* table, int table_width,
+                        void* k_pages, void* v_pages, int n_pages, int page_size, const int32_t* positions,
+                        const double* freqs, int rot_dim, int interleaved, float magnitude, float* key_weights,
+                        int n_q_heads, int n_kv_heads, int head_dim, const int64_t* strides, void* stream);
+
+/* The workspace bytes of attention_paged_decode on the current device (weights:
+ * not 0 with key_weights), or a negative LPS_E* code. */
+long long attention_paged_decode_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                           int table_width, int weights);
+
+/* Attention of one token a sequence over its rows [0, lengths[b]) (its own among
+ * them, appended before):
+ *     out[b][h] = sum_j p_j v[j], p = softmax_j(scale * q[b][h] . k[j]).
+ * Rows on a page outside [0, n_pages) are not seen. A sequence that sees nothing,
+ * or whose length is not in [0, table_width * page_size], gets zeros; one all of
+ * whose scores are -inf gets NaN, as the formula does. What is not seen changes
+ * nothing, whatever it holds. The weights enter the product with V in 16 bits or
+ * more; an infinity or NaN of V that is seen leaves no finite result where its
+ * weight is not zero in fp32, and NaN where it is.
+ *   q, out     device [batch][n_q_heads][head_dim], batch 1..1024
+ *   lengths    device int32[batch]; table device int32[batch][table_width]
+ *   strides    host int64[4]: batch and head stride of q, then of out; NULL: dense
+ *   scale      > 0 and below 2.3e38, or 0 for 1/sqrt(head_dim)
+ *   key_weights  or NULL; for every row j that is seen, and its kv head g,
+ *              key_weights = decay * key_weights + sum of p_j over the q heads of g
+ *              (decay 0: what was there is not read, whatever it holds). Rows of
+ *              two sequences on one page of one call need not be told apart by
+ *              their weights, and are not: such pages' weights are undefined
+ *   decay      0 to 1
+ *   workspace  device, 16-byte aligned, at least attention_paged_decode_workspace bytes */
+int attention_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, int type, int batch,
+                           const int32_t* lengths, const int32_t* table, int table_width, int n_pages, int page_size,
+                           int n_q_heads, int n_kv_heads, int head_dim, const int64_t* strides, float scale,
+                           float* key_weights, float decay, void* workspace, long long workspace_bytes, void* stream);
+
+/* The workspace bytes of kv_pages_evict, or a negative LPS_E* code. */
+long long kv_pages_evict_workspace(int batch, int n_kv_heads, int budget);
+
+/* Eviction: of a sequence of more than `budget` rows stay, for every kv head, the
+ * last `recent` ones and the heaviest of the others by key_weights (of equal
+ * weights the lowest row; NaN is below every number), `budget` in all. They are
+ * copied in order, with their weights, to the rows 0, 1, .. of the new table, for
+ * keys and values; a sequence of up to `budget` rows is copied whole. The old
+ * pages are only read (they may be shared), and no other row is written.
+ *   lengths    device int32[batch]; table device int32[batch][table_width]
+ *   new_table  device int32[batch][new_width], new_width * page_size >= budget;
+ *              pages that no table of the call has elsewhere
+ *   new_lengths  device int32[batch], written: the rows kept, or -1 for a sequence
+ *              whose length is not in [0, table_width * page_size] or that needs a
+ *              page outside [0, n_pages): nothing of it is copied
+ *   recent     0 to budget
+ *   workspace  device, at least kv_pages_evict_workspace bytes, 4-byte aligned */
+int kv_pages_evict(void* k_pages, void* v_pages, float* key_weights, int n_pages, int page_size, int n_kv_heads,
+                   int head_dim, int batch, const int32_t* lengths, const int32_t* table, int table_width,
+                   const int32_t* new_table, int new_width, int32_t* new_lengths, int budget, int recent,
+                   void* workspace, long long workspace_bytes, void* stream);
+
+/* Logits before a token is chosen, in this order, in fp32, rounded once:
+ *     x = x > 0 ? x / repetition : x * repetition   for tokens of the row's history,
+ *     x = x - frequency * c - presence              for tokens that its output holds c > 0 times,
+ *     x = x + bias                                  for every entry of the token in bias_ids,
+ *     x = -inf                                      for tokens that are not allowed.
+ *   logits, out  device [batch][vocab] of type LPS_TYPE_BF16, _FP16 or _FP32; out may
+ *              be logits (the same address and strides) and overlaps nothing else
+ *   strides    host int64[2]: row stride of logits, then of out; NULL: dense
+ *   tokens     device int32[batch][width]: a row's history is its first lengths[b]
+ *              tokens (a length is taken into [0, width]), of which those from
+ *              prompt_lengths[b] on are its output (NULL: all); tokens outside
+ *              [0, vocab) do not count. width 0: no history
+ *   repetition, frequency, presence  device float[batch], or NULL: 1, 0, 0
+ *   bias_ids, bias  device int32 and float [batch][n_bias]; ids outside [0, vocab) do
+ *              not count, equal ones add up in order. n_bias 0: none
+ *   allowed    device [batch][(vocab + 31) / 32] bits, bit i % 32 of word i / 32 set
+ *              where token i is allowed; or NULL: all are */
+int logits_adjust(const void* logits, void* out, int type, int batch, int vocab, const int64_t* strides,
+                  const int32_t* tokens, int width, const int32_t* lengths, const int32_t* prompt_lengths,
+                  const float* repetition, const float* frequency, const float* presence, const int32_t* bias_ids,
+                  const float* bias, int n_bias, const uint32_t* allowed, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,15 +22,17 @@ from . import _capi
 from ._capi import (KERNELS, LPS_EBUSY, LPS_ECUDA, LPS_EINVAL, LPS_ENOMEM, LPS_ETIMEDOUT,  # noqa: F401
                     LPS_FLAG_KEEP_ATTN_OUT, LPS_FLAG_SERIAL_STEPS, LPS_FLAG_SINGLE_STREAM, LPS_FLAG_VERIFY, LPS_FLAG_PERSISTENT, LPS_FLAG_GRAPH,
                     LPS_NOALLOC_SCRATCH_BYTES,
-                    LPS_OK, LPS_TYPE_BF16, LPS_TYPE_FP16)
+                    LPS_OK, LPS_TYPE_BF16, LPS_TYPE_FP16, LPS_TYPE_FP32)
 from ._capi import LpsError
 from ._capi import check as _check
-from .ops import attention_prompt_packed, attention_tree_verify, cache_ops_status, kv_rows_accept, kv_rows_append
+from .ops import (attention_paged_decode, attention_prompt_packed, attention_tree_verify, cache_ops_status, kv_pages_evict,
+                  kv_rows_accept, kv_rows_append, logits_adjust, rotary_append_paged, rotary_frequencies, rotary_rows)
 
 __all__ = ["LpsError", "StagePlan", "Model", "Pending", "stage_plan_create", "stage_plan_from_counts",
            "stage_plan_solve", "model_stage_bytes", "model_bind", "decode_step", "decode_step_deferred",
            "pending_wait", "pending_free", "decode_step_device", "load", "attention_prompt_packed",
-           "attention_tree_verify", "kv_rows_append", "kv_rows_accept", "cache_ops_status"]
+           "attention_tree_verify", "kv_rows_append", "kv_rows_accept", "cache_ops_status", "rotary_frequencies", "rotary_rows",
+           "rotary_append_paged", "attention_paged_decode", "kv_pages_evict", "logits_adjust"]
 
 
 def load():

@@ -19,6 +19,7 @@ LPS_WEIGHT_INT8_ROWSCALE = 1
 LPS_KV_BF16 = 0
 LPS_TYPE_BF16 = 0
 LPS_TYPE_FP16 = 1
+LPS_TYPE_FP32 = 2
 LPS_NOALLOC_SCRATCH_BYTES = 8 << 20
 LPS_FLAG_SINGLE_STREAM = 1
 LPS_FLAG_KEEP_ATTN_OUT = 2
@@ -41,6 +42,8 @@ EXPORTS = (
     "stage_plan_solve", "model_stage_bytes", "model_set_wait_limit", "attention_decode_noalloc_status",
     "model_prefill", "attention_prompt_packed", "attention_tree_verify",
     "kv_rows_append", "kv_rows_accept", "cache_ops_status", "cache_ops_set_wait_limit",
+    "rotary_rows", "rotary_append_paged", "attention_paged_decode_workspace", "attention_paged_decode",
+    "kv_pages_evict_workspace", "kv_pages_evict", "logits_adjust",
 )
 
 
@@ -99,6 +102,7 @@ def load(path: str = LIB_PATH):
         raise RuntimeError(f"{path} is missing: build it first (python -m layer_pipeline_staged_gb300.build)")
     L = ctypes.CDLL(path)
     vp, i, pp, f = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p), ctypes.c_float
+    ll = ctypes.c_longlong
     sig = {
         "stage_plan_create": (i, [i, vp, i, pp]),
         "stage_plan_from_counts": (i, [vp, i, pp]),
@@ -138,6 +142,13 @@ def load(path: str = LIB_PATH):
         "cache_ops_status": (i, [vp]),
         "cache_ops_set_wait_limit": (i, [ctypes.c_longlong]),
         "kv_rows_accept": (i, [vp, vp, i, i, i, i, i, vp, i, vp, vp, vp]),
+        "rotary_rows": (i, [vp, vp, vp, vp, i, i, vp, vp, i, i, f, i, i, i, vp, vp]),
+        "rotary_append_paged": (i, [vp, vp, vp, vp, i, i, i, vp, vp, vp, i, vp, vp, i, i, vp, vp, i, i, f, vp, i, i, i, vp, vp]),
+        "attention_paged_decode_workspace": (ll, [i, i, i, i, i, i, i]),
+        "attention_paged_decode": (i, [vp, vp, vp, vp, i, i, vp, vp, i, i, i, i, i, i, vp, f, vp, f, vp, ll, vp]),
+        "kv_pages_evict_workspace": (ll, [i, i, i]),
+        "kv_pages_evict": (i, [vp, vp, vp, i, i, i, i, i, vp, vp, i, vp, i, vp, i, i, vp, ll, vp]),
+        "logits_adjust": (i, [vp, vp, i, i, i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, i, vp, vp]),
         "stage_plan_solve": (i, [i, i, vp, vp, vp, vp, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_int64)]),
         "model_stage_bytes": (i, [ctypes.POINTER(ModelDesc), vp, vp, ctypes.POINTER(ctypes.c_uint64),
                                   ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),

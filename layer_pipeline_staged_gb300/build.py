@@ -27,7 +27,8 @@ MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
 # Python extension: the torch wrappers' argument marshalling
 MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["runtime.cu", "gemv.cu", "attention.cu", "embed.cu", "noalloc.cu", "skinny.cu", "solver.cu", "stage.cu", "tcgemm.cu", "prefill.cu",
-           "cache_ops.cu", "cache_rows.cu", "tile_attn.cu"]
+           "cache_ops.cu", "cache_rows.cu", "tile_attn.cu",
+           "page_ops.cu", "paged_attn.cu", "rotary.cu", "page_evict.cu", "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -5,45 +5,16 @@
 // values it was captured with); a tree's parents and an accepted path are
 // device arrays, as a drafter and a sampler on the GPU leave them, and the
 // kernels check them.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_runtime.h>
-
-#include <cmath>
-#include <exception>
 #include <initializer_list>
-#include <string>
 
-#include "cache_ops.h"
 #include "kernels.h"
-#include "lps.h"
+#include "op_host.h"
+#include "page_ops.h"
 #include "ptx.cuh"
-
-namespace lps {
-int host_fail(int code, const char* fn, const std::string& why);
-}  // namespace lps
 
 namespace {
 
 using namespace lps;
-
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// Runs the body of an entry point; no exception leaves the C boundary.
-template <class F>
-int guarded(const char* fn, F&& body) {
-  try {
-    return body();
-  } catch (const std::exception& e) {
-    try {
-      return host_fail(LPS_ENOMEM, fn, e.what());
-    } catch (...) {
-      return LPS_ENOMEM;
-    }
-  } catch (...) {
-    return LPS_ENOMEM;
-  }
-}
 
 // Whether every row of an output starts on 32 bytes.
 bool wide(const void* p, std::initializer_list<int64_t> strides) {
@@ -53,82 +24,8 @@ bool wide(const void* p, std::initializer_list<int64_t> strides) {
   return true;
 }
 
-// Whether two caches of so many rows of hd elements share memory.
-bool overlap(const void* a, const void* b, double rows, int hd) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return static_cast<double>(x < y ? y - x : x - y) < rows * hd * 2;
-}
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
-
-int check_heads(const char* fn, int type, int nq, int nkv, int hd) {
-  if (type != LPS_TYPE_BF16 && type != LPS_TYPE_FP16) return host_fail(LPS_EINVAL, fn, "type must be LPS_TYPE_BF16 or LPS_TYPE_FP16");
-  if (hd != 64 && hd != 128) return host_fail(LPS_EINVAL, fn, "head_dim must be 64 or 128");
-  if (nkv < 1 || nkv > 65535 || nq < 1 || nq % nkv || nq / nkv > kMaxGroup || nq > 65535)
-    return host_fail(LPS_EINVAL, fn, "n_q_heads must be 1 to 16 times n_kv_heads (each at most 65535)");
-  return LPS_OK;
-}
-
-int check_scale(const char* fn, float scale) {
-  if (!(scale >= 0.f) || std::isinf(scale)) return host_fail(LPS_EINVAL, fn, "scale must be finite and >= 0 (0: 1/sqrt(head_dim))");
-  if (std::isinf(scale * kLog2e)) return host_fail(LPS_EINVAL, fn, "scale must be below 2.3e38 (its product with log2(e) is what the kernels use)");
-  return LPS_OK;
-}
-
-// Element strides of a tensor's outer axes: whole 16-byte units, at least one
-// row apart, and inside what a tensor map can hold.
-int check_strides(const char* fn, const int64_t* st, int n, int hd) {
-  for (int i = 0; i < n; ++i)
-    if (st[i] < hd || st[i] % 8 || st[i] >= (1ll << 38))
-      return host_fail(LPS_EINVAL, fn, "strides must be multiples of 8 elements, at least head_dim and below 2^38");
-  return LPS_OK;
-}
-
-// The driver's tensor-map encoder, looked up once per process.
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// [n3][n2][n1][hd] of 2-byte elements with element strides s1..s3, in boxes of
-// 64 elements x b1 x b2 with the 128-byte swizzle. The stride of an axis of one
-// entry is never used and set to one row.
-bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const long long (&n)[3], const long long (&st)[3],
-             int b1, int b2) {
-  if (!encoder()) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(n[0]), static_cast<cuuint64_t>(n[1]),
-                        static_cast<cuuint64_t>(n[2])};
-  cuuint64_t strides[3];
-  for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? st[i] : hd) * 2;
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  auto encode = [&] {
-    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  if (encode()) return true;
-  // The driver's call wants a current context, which a host thread has from its
-  // first runtime call on the device, and this may be it.
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
-}
-
 // Test hook: the wait limit of the calling thread's later calls.
 thread_local long long g_wait_limit = 0;
-
-// Rows and tokens are counted in 32 bits, a block of keys past the last one included.
-constexpr int32_t kMaxRows = 0x7fff0000;
 
 int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
   if (offsets[0] < 0 || offsets[n_seqs] > kMaxRows) return host_fail(LPS_EINVAL, fn, "offsets must lie in [0, 2^31 - 2^16]");
@@ -138,6 +35,8 @@ int check_offsets(const char* fn, int n_seqs, const int32_t* offsets) {
 }
 
 }  // namespace
+
+long long lps::op_wait_limit() { return g_wait_limit; }
 
 extern "C" int attention_prompt_packed(const void* q, const void* k, const void* v, void* out, int type, int n_seqs,
                                        const int32_t* offsets, int n_q_heads, int n_kv_heads, int head_dim,
@@ -327,8 +226,12 @@ extern "C" int cache_ops_status(void* stream) {
   static const char* FN = "cache_ops_status";
   return guarded(FN, [&]() -> int {
     int st[2] = {0, 0};
-    const cudaError_t e = tile_attn_status(st, static_cast<cudaStream_t>(stream));
+    cudaError_t e = tile_attn_status(st, static_cast<cudaStream_t>(stream));
+    int paged[2] = {0, 0};
+    if (e == cudaSuccess) e = paged_attn_status(paged, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return host_fail(LPS_ECUDA, FN, cudaGetErrorString(e));
+    st[0] |= paged[0];
+    if (!st[1]) st[1] = paged[1];
     if (!st[0] && !st[1]) return LPS_OK;
     return host_fail(LPS_ECUDA, FN, "an earlier call's output is invalid: " + describe_status(st[0], st[1]));
   });

@@ -1,4 +1,4 @@
-/* Argument marshalling of the operators over a caller-owned cache: torch
+/* Argument marshalling of the operators over a caller-owned cache and over pages: torch
  * tensors in, the C ABI's pointers, strides and host arrays out. A call's
  * kernels take 2 to 10 microseconds when the work is small; the same
  * marshalling in Python and ctypes took 5 to 7 of a call's 8 to 10 on the host,
@@ -15,7 +15,7 @@
 
 /* ---- what init() is given ------------------------------------------------- */
 
-static PyObject *g_bf16, *g_fp16, *g_int32;             /* torch dtypes */
+static PyObject *g_bf16, *g_fp16, *g_int32, *g_fp32, *g_fp64, *g_uint8; /* torch dtypes */
 static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad, *g_written; /* torch functions */
 static PyObject *g_error;                                /* LpsError */
 static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
@@ -116,6 +116,18 @@ static int refuse(const char *why) {
   return -1;
 }
 
+/* Refuses tensors that want a gradient (`grad`: whether some do) while autograd records. */
+static int no_grad(int grad) {
+  if (grad) {
+    PyObject *on = PyObject_CallNoArgs(g_grad);
+    if (!on) return -1;
+    grad = on == Py_True;
+    Py_DECREF(on);
+    if (grad) return refuse("there is no backward pass: detach the tensors or call under torch.no_grad()");
+  }
+  return 0;
+}
+
 /* The library type that n tensors share, which are on one GPU and need no gradient. */
 static int alike(const tensor *t, int n, int *kind) {
   if (t[0].dtype == g_bf16) *kind = LPS_TYPE_BF16;
@@ -127,14 +139,7 @@ static int alike(const tensor *t, int n, int *kind) {
     if (t[i].dtype != t[0].dtype || t[i].device != t[0].device) return refuse("tensors must share one type and one device");
     grad |= t[i].grad;
   }
-  if (grad) {
-    PyObject *on = PyObject_CallNoArgs(g_grad);
-    if (!on) return -1;
-    grad = on == Py_True;
-    Py_DECREF(on);
-    if (grad) return refuse("there is no backward pass: detach the tensors or call under torch.no_grad()");
-  }
-  return 0;
+  return no_grad(grad);
 }
 
 static int same_shape(const tensor *a, const tensor *b) {
@@ -159,6 +164,30 @@ static int int_rows(const tensor *t, int device, int dim, int64_t n0, int64_t n1
     return -1;
   }
   return 0;
+}
+
+/* The facts of `obj`, a contiguous tensor of `dtype` on `device` of the given shape (-1: any size of that axis); wants no
+ * gradient. `form` says the shape. */
+static int array_of(PyObject *obj, tensor *t, PyObject *dtype, int device, int dim, int64_t n0, int64_t n1, int64_t n2, const char *what,
+                    const char *form) {
+  const int64_t n[3] = {n0, n1, n2};
+  if (tensor_of(obj, t, what)) return -1;
+  int ok = t->dtype == dtype && t->device == device && t->dim == dim && dense(t);
+  for (int i = 0; ok && i < dim; ++i) ok = t->shape[i] <= INT32_MAX && (n[i] < 0 || t->shape[i] == n[i]);
+  if (!ok) {
+    PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s tensor %s on the same device", what,
+                 dtype == g_int32 ? "int32" : dtype == g_fp32 ? "float32" : "float64", form);
+    return -1;
+  }
+  return no_grad(t->grad);
+}
+
+/* array_of for an argument that may be None, which leaves a null pointer. */
+static int maybe_array_of(PyObject *obj, tensor *t, PyObject *dtype, int device, int dim, int64_t n0, int64_t n1, int64_t n2, const char *what,
+                          const char *form) {
+  t->ptr = NULL;
+  t->obj = NULL;
+  return obj == Py_None ? 0 : array_of(obj, t, dtype, device, dim, n0, n1, n2, what, form);
 }
 
 /* Sizes go to the library as int. */
@@ -368,6 +397,18 @@ static PyObject *output_like(PyObject *out, const tensor *q, tensor *o) {
   return out;
 }
 
+/* A new dense tensor [n] of `dtype` on the device of `like` (a new reference). */
+static PyObject *new_array(int64_t n, PyObject *dtype, PyObject *like) {
+  PyObject *shape = Py_BuildValue("(L)", (long long)n), *device = PyObject_GetAttr(like, s_device), *x = NULL;
+  if (shape && device) {
+    PyObject *const args[3] = {shape, dtype, device};
+    x = PyObject_Vectorcall(g_empty, args, 1, g_empty_names);
+  }
+  Py_XDECREF(shape);
+  Py_XDECREF(device);
+  return x;
+}
+
 /* Tells autograd that a call that has been enqueued writes `a` (and `b`) in place: an earlier operation that
  * saved one of them for its backward then refuses to run on the new values. */
 static int written(PyObject *a, PyObject *b) {
@@ -560,6 +601,250 @@ static PyObject *accept(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+/* ---- over pages ---------------------------------------------------------------------- */
+
+/* Both pools of pages [pages, kv heads, page rows, head_dim], of kv heads `nkv` and head_dim `hd` (-1: any). */
+static int pools_of(PyObject *k, PyObject *v, tensor *kp, tensor *vp, int64_t nkv, int64_t hd) {
+  if (tensor_of(k, kp, "k_pages") || tensor_of(v, vp, "v_pages")) return -1;
+  if (kp->dim != 4 || !same_shape(kp, vp) || (nkv >= 0 && kp->shape[1] != nkv) || (hd >= 0 && kp->shape[3] != hd))
+    return refuse("the pages must be two tensors [pages, kv heads, page rows, head_dim] of the call's kv heads and head_dim");
+  if (!dense(kp) || !dense(vp)) return refuse("the pages must be contiguous [pages, kv heads, page rows, head_dim]");
+  for (int i = 0; i < 4; ++i)
+    if (!fits(kp->shape[i])) return refuse("tensors are too large");
+  return 0;
+}
+
+/* frequencies [rot_dim / 2], or None: nothing turns. */
+static int freqs_of(PyObject *obj, tensor *f, int device, int *rot) {
+  *rot = 0;
+  if (maybe_array_of(obj, f, g_fp64, device, 1, -1, 0, 0, "freqs", "[rot_dim / 2]")) return -1;
+  if (f->obj) {
+    if (f->shape[0] > 32768) return refuse("freqs must hold half of a head's elements at most");
+    *rot = (int)(2 * f->shape[0]);
+  }
+  return 0;
+}
+
+/* rows(q, k, positions, freqs, interleaved, magnitude, q_out, k_out) -> (q_out, k_out) */
+static PyObject *rows(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  tensor t[4], pos, f;
+  place at;
+  int kind = 0, rot, given = 2;
+  (void)self;
+  if (begin(n, 8) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k")) return NULL;
+  const tensor *q = &t[0], *k = &t[1];
+  if (q->dim != 3 || k->dim != 3 || k->shape[0] != q->shape[0] || k->shape[2] != q->shape[2])
+    return refuse("q and k must be [tokens, heads, head_dim] of the same tokens and head_dim"), NULL;
+  if ((args[6] == Py_None) != (args[7] == Py_None)) return refuse("out must hold two tensors"), NULL;
+  if (args[6] != Py_None) {
+    if (tensor_of(args[6], &t[2], "out[0]") || tensor_of(args[7], &t[3], "out[1]")) return NULL;
+    if (!same_shape(&t[2], q) || !same_shape(&t[3], k)) return refuse("out must have the shapes of q and k"), NULL;
+    given = 4;
+  }
+  if (alike(t, given, &kind)) return NULL;
+  for (int i = 0; i < given; ++i)
+    if (contiguous_heads(&t[i])) return NULL;
+  if (!fits(q->shape[0]) || !fits(q->shape[1]) || !fits(k->shape[1]) || !fits(q->shape[2])) return refuse("tensors are too large"), NULL;
+  if (array_of(args[2], &pos, g_int32, q->device, 1, q->shape[0], 0, 0, "positions", "[tokens]") || freqs_of(args[3], &f, q->device, &rot))
+    return NULL;
+  const int interleaved = PyObject_IsTrue(args[4]);
+  const double magnitude = PyFloat_AsDouble(args[5]);
+  if (interleaved < 0 || PyErr_Occurred()) return NULL;
+  PyObject *qo = output_like(args[6], q, &t[2]), *ko = qo ? output_like(args[7], k, &t[3]) : NULL, *both = NULL;
+  if (ko) {
+    int ok = q->shape[0] == 0; /* no tokens: there is nothing to point to */
+    if (!ok) {
+      const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[3].stride[0], t[3].stride[1]};
+      ok = !enter(&at, q->device) &&
+           !leave(&at, UNLOCKED(rotary_rows(q->ptr, k->ptr, t[2].ptr, t[3].ptr, kind, (int)q->shape[0], pos.ptr, f.ptr, rot, interleaved,
+                                            (float)magnitude, (int)q->shape[1], (int)k->shape[1], (int)q->shape[2], st, at.stream))) &&
+           (given == 2 || !written(qo, ko));
+    }
+    if (ok) both = PyTuple_Pack(2, qo, ko);
+  }
+  Py_XDECREF(qo);
+  Py_XDECREF(ko);
+  return both;
+}
+
+/* append_paged(q, k, v, offsets, lengths, table, k_pages, v_pages, freqs, positions, interleaved, magnitude, key_weights, q_out) -> q_out */
+static PyObject *append_paged(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  tensor t[6], off, len, tab, f, pos, kw;
+  place at;
+  int kind = 0, rot;
+  (void)self;
+  if (begin(n, 14) || tensor_of(args[0], &t[0], "q") || tensor_of(args[1], &t[1], "k") || tensor_of(args[2], &t[2], "v")) return NULL;
+  const tensor *q = &t[0], *k = &t[1], *kp = &t[3];
+  if (q->dim != 3 || k->dim != 3) return refuse("q, k and v must be [tokens, heads, head_dim]"), NULL;
+  if (k->shape[0] != q->shape[0] || k->shape[2] != q->shape[2] || !same_shape(k, &t[2]))
+    return refuse("k and v must be [tokens, kv heads, head_dim] of q's tokens and head_dim"), NULL;
+  if (pools_of(args[6], args[7], &t[3], &t[4], k->shape[1], k->shape[2])) return NULL;
+  const int given = args[13] != Py_None;
+  if (given) {
+    if (tensor_of(args[13], &t[5], "q_out")) return NULL;
+    if (!same_shape(&t[5], q)) return refuse("q_out must have q's shape"), NULL;
+  }
+  if (alike(t, 5 + given, &kind)) return NULL;
+  if (contiguous_heads(q) || contiguous_heads(k) || contiguous_heads(&t[2]) || (given && contiguous_heads(&t[5]))) return NULL;
+  if (!fits(q->shape[0]) || !fits(q->shape[1]) || !fits(q->shape[2])) return refuse("tensors are too large"), NULL;
+  if (array_of(args[4], &len, g_int32, q->device, 1, -1, 0, 0, "lengths", "[sequences]")) return NULL;
+  const int64_t seqs = len.shape[0];
+  if (maybe_array_of(args[3], &off, g_int32, q->device, 1, seqs + 1, 0, 0, "offsets", "[sequences + 1]") ||
+      array_of(args[5], &tab, g_int32, q->device, 2, seqs, -1, 0, "table", "[sequences, pages]") || freqs_of(args[8], &f, q->device, &rot) ||
+      maybe_array_of(args[9], &pos, g_int32, q->device, 1, q->shape[0], 0, 0, "positions", "[tokens]") ||
+      maybe_array_of(args[12], &kw, g_fp32, q->device, 3, kp->shape[0], kp->shape[1], kp->shape[2], "key_weights", "[pages, kv heads, page rows]"))
+    return NULL;
+  const int interleaved = PyObject_IsTrue(args[10]);
+  const double magnitude = PyFloat_AsDouble(args[11]);
+  if (interleaved < 0 || PyErr_Occurred()) return NULL;
+  PyObject *out = output_like(args[13], q, &t[5]);
+  if (!out) return NULL;
+  if (q->shape[0] == 0 && (off.ptr || seqs == 0)) return out;
+  const int64_t st[8] = {q->stride[0], q->stride[1], k->stride[0], k->stride[1], t[2].stride[0], t[2].stride[1], t[5].stride[0], t[5].stride[1]};
+  if (enter(&at, q->device) ||
+      leave(&at, UNLOCKED(rotary_append_paged(q->ptr, k->ptr, t[2].ptr, t[5].ptr, kind, (int)q->shape[0], (int)seqs, off.ptr, len.ptr, tab.ptr,
+                                              (int)tab.shape[1], kp->ptr, t[4].ptr, (int)kp->shape[0], (int)kp->shape[2], pos.ptr, f.ptr, rot,
+                                              interleaved, (float)magnitude, kw.ptr, (int)q->shape[1], (int)k->shape[1], (int)q->shape[2], st,
+                                              at.stream))) ||
+      written(kp->obj, t[4].obj) || (kw.obj && written(kw.obj, given ? out : NULL)) || (!kw.obj && given && written(out, NULL)))
+    Py_CLEAR(out);
+  return out;
+}
+
+/* decode_paged(q, k_pages, v_pages, table, lengths, out, scale, key_weights, decay) -> out */
+static PyObject *decode_paged(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  tensor t[4], tab, len, kw;
+  place at;
+  int kind = 0;
+  (void)self;
+  if (begin(n, 9) || tensor_of(args[0], &t[0], "q")) return NULL;
+  const tensor *q = &t[0], *kp = &t[1];
+  if (q->dim != 3) return refuse("q must be [batch, q heads, head_dim]"), NULL;
+  if (pools_of(args[1], args[2], &t[1], &t[2], -1, q->shape[2])) return NULL;
+  const int given = args[5] != Py_None;
+  if (given) {
+    if (tensor_of(args[5], &t[3], "out")) return NULL;
+    if (!same_shape(&t[3], q)) return refuse("out must have q's shape"), NULL;
+  }
+  float scale;
+  if (scale_of(args[6], &scale) || alike(t, 3 + given, &kind)) return NULL;
+  if (contiguous_heads(q) || (given && contiguous_heads(&t[3]))) return NULL;
+  const int64_t batch = q->shape[0];
+  if (!fits(batch) || !fits(q->shape[1]) || !fits(q->shape[2])) return refuse("tensors are too large"), NULL;
+  if (array_of(args[3], &tab, g_int32, q->device, 2, batch, -1, 0, "table", "[batch, pages]") ||
+      array_of(args[4], &len, g_int32, q->device, 1, batch, 0, 0, "lengths", "[batch]") ||
+      maybe_array_of(args[7], &kw, g_fp32, q->device, 3, kp->shape[0], kp->shape[1], kp->shape[2], "key_weights", "[pages, kv heads, page rows]"))
+    return NULL;
+  const double decay = PyFloat_AsDouble(args[8]);
+  if (PyErr_Occurred()) return NULL;
+  PyObject *out = output_like(args[5], q, &t[3]), *work = NULL;
+  if (!out) return NULL;
+  const int64_t st[4] = {q->stride[0], q->stride[1], t[3].stride[0], t[3].stride[1]};
+  if (enter(&at, q->device)) return Py_DECREF(out), NULL;
+  /* memory of the allocator: what the call's stream runs next may have it */
+  const long long bytes = attention_paged_decode_workspace((int)batch, (int)q->shape[1], (int)kp->shape[1], (int)q->shape[2], (int)kp->shape[2],
+                                                           (int)tab.shape[1], kw.ptr != NULL);
+  int rc = bytes < 0 ? (int)bytes : 0;
+  PyObject *ptr = NULL;
+  if (!rc && (!(work = new_array(bytes, g_uint8, q->obj)) || !(ptr = PyObject_CallMethodNoArgs(work, s_data_ptr)))) rc = 1;
+  if (!rc) {
+    void *space = PyLong_AsVoidPtr(ptr);
+    rc = UNLOCKED(attention_paged_decode(q->ptr, kp->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, len.ptr, tab.ptr, (int)tab.shape[1],
+                                         (int)kp->shape[0], (int)kp->shape[2], (int)q->shape[1], (int)kp->shape[1], (int)q->shape[2], st, scale,
+                                         kw.ptr, (float)decay, space, bytes, at.stream));
+  }
+  Py_XDECREF(ptr);
+  Py_XDECREF(work);
+  if (leave(&at, rc) || rc || (given && written(out, kw.obj)) || (!given && kw.obj && written(kw.obj, NULL))) Py_CLEAR(out);
+  return out;
+}
+
+/* evict_paged(k_pages, v_pages, key_weights, table, lengths, new_table, budget, recent) -> new lengths */
+static PyObject *evict_paged(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  tensor t[2], kw, tab, len, fresh, out;
+  place at;
+  int kind = 0;
+  (void)self;
+  if (begin(n, 8) || pools_of(args[0], args[1], &t[0], &t[1], -1, -1) || alike(t, 2, &kind)) return NULL;
+  const tensor *kp = &t[0];
+  if (array_of(args[2], &kw, g_fp32, kp->device, 3, kp->shape[0], kp->shape[1], kp->shape[2], "key_weights", "[pages, kv heads, page rows]") ||
+      array_of(args[4], &len, g_int32, kp->device, 1, -1, 0, 0, "lengths", "[batch]"))
+    return NULL;
+  const int64_t batch = len.shape[0];
+  if (array_of(args[3], &tab, g_int32, kp->device, 2, batch, -1, 0, "table", "[batch, pages]") ||
+      array_of(args[5], &fresh, g_int32, kp->device, 2, batch, -1, 0, "new_table", "[batch, pages]"))
+    return NULL;
+  int64_t size[2];
+  for (int i = 0; i < 2; ++i) {
+    PyObject *x = PyNumber_Index(args[6 + i]);
+    size[i] = x ? PyLong_AsLongLong(x) : -1;
+    Py_XDECREF(x);
+    if (PyErr_Occurred()) return NULL;
+    if (size[i] < INT32_MIN || size[i] > INT32_MAX) return refuse("budget and recent must fit 32 bits"), NULL;
+  }
+  PyObject *made = new_array(batch, g_int32, kp->obj), *work = NULL, *ptr = NULL;
+  if (!made || tensor_of(made, &out, "new lengths") || enter(&at, kp->device)) return Py_XDECREF(made), NULL;
+  const long long bytes = kv_pages_evict_workspace((int)batch, (int)kp->shape[1], (int)size[0]);
+  int rc = bytes < 0 ? (int)bytes : 0;
+  if (!rc && (!(work = new_array(bytes, g_uint8, kp->obj)) || !(ptr = PyObject_CallMethodNoArgs(work, s_data_ptr)))) rc = 1;
+  if (!rc) {
+    void *space = PyLong_AsVoidPtr(ptr);
+    rc = UNLOCKED(kv_pages_evict(kp->ptr, t[1].ptr, kw.ptr, (int)kp->shape[0], (int)kp->shape[2], (int)kp->shape[1], (int)kp->shape[3], (int)batch,
+                                 len.ptr, tab.ptr, (int)tab.shape[1], fresh.ptr, (int)fresh.shape[1], out.ptr, (int)size[0], (int)size[1], space,
+                                 bytes, at.stream));
+  }
+  Py_XDECREF(ptr);
+  Py_XDECREF(work);
+  if (leave(&at, rc) || rc || written(kp->obj, t[1].obj) || written(kw.obj, NULL)) Py_CLEAR(made);
+  return made;
+}
+
+/* adjust(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence, bias_ids, bias, allowed, out) -> out */
+static PyObject *adjust(PyObject *self, PyObject *const *args, Py_ssize_t n) {
+  tensor x, o, tok, len, pro, pen[3], ids, bias, bits;
+  place at;
+  static const char *const penalty[3] = {"repetition", "frequency", "presence"};
+  (void)self;
+  if (begin(n, 11) || tensor_of(args[0], &x, "logits")) return NULL;
+  const int kind = x.dtype == g_bf16 ? LPS_TYPE_BF16 : x.dtype == g_fp16 ? LPS_TYPE_FP16 : x.dtype == g_fp32 ? LPS_TYPE_FP32 : -1;
+  if (kind < 0) return refuse("logits must be float32, bfloat16 or float16"), NULL;
+  if (x.dim != 2) return refuse("logits must be [batch, vocabulary]"), NULL;
+  const int64_t batch = x.shape[0], vocab = x.shape[1];
+  if (!fits(batch) || !fits(vocab)) return refuse("tensors are too large"), NULL;
+  const int given = args[10] != Py_None;
+  o.grad = 0;
+  if (given) {
+    if (tensor_of(args[10], &o, "out")) return NULL;
+    if (!same_shape(&o, &x) || o.dtype != x.dtype || o.device != x.device) return refuse("out must be like logits"), NULL;
+  }
+  if (x.device < 0) return refuse("tensors must be on a CUDA device"), NULL;
+  if (no_grad(x.grad | o.grad)) return NULL;
+  if ((vocab > 1 && x.stride[1] != 1) || (given && vocab > 1 && o.stride[1] != 1)) return refuse("rows of logits must be contiguous"), NULL;
+  if (maybe_array_of(args[1], &tok, g_int32, x.device, 2, batch, -1, 0, "tokens", "[batch, history]") ||
+      maybe_array_of(args[2], &len, g_int32, x.device, 1, batch, 0, 0, "lengths", "[batch]") ||
+      maybe_array_of(args[3], &pro, g_int32, x.device, 1, batch, 0, 0, "prompt_lengths", "[batch]") ||
+      maybe_array_of(args[7], &ids, g_int32, x.device, 2, batch, -1, 0, "bias_ids", "[batch, entries]") ||
+      maybe_array_of(args[8], &bias, g_fp32, x.device, 2, batch, ids.obj ? ids.shape[1] : -1, 0, "bias", "[batch, entries] like bias_ids") ||
+      maybe_array_of(args[9], &bits, g_int32, x.device, 2, batch, (vocab + 31) / 32, 0, "allowed", "[batch, (vocabulary + 31) / 32]"))
+    return NULL;
+  for (int i = 0; i < 3; ++i)
+    if (maybe_array_of(args[4 + i], &pen[i], g_fp32, x.device, 1, batch, 0, 0, penalty[i], "[batch]")) return NULL;
+  if (!tok.obj != !len.obj) return refuse("tokens and lengths go together"), NULL;
+  if (!tok.obj && (pro.obj || pen[0].obj || pen[1].obj || pen[2].obj)) return refuse("penalties need tokens and lengths"), NULL;
+  if (!ids.obj != !bias.obj) return refuse("bias_ids and bias go together"), NULL;
+  PyObject *out = output_like(args[10], &x, &o);
+  if (!out || batch == 0 || vocab == 0) return out;
+  const int64_t width = tok.obj ? tok.shape[1] : 0, entries = ids.obj ? ids.shape[1] : 0;
+  const int64_t st[2] = {batch > 1 ? x.stride[0] : vocab, batch > 1 ? o.stride[0] : vocab};
+  if (enter(&at, x.device) ||
+      leave(&at, UNLOCKED(logits_adjust(x.ptr, o.ptr, kind, (int)batch, (int)vocab, st, tok.ptr, (int)width, len.ptr, pro.ptr,
+                                        width ? pen[0].ptr : NULL, width ? pen[1].ptr : NULL, width ? pen[2].ptr : NULL, ids.ptr, bias.ptr,
+                                        (int)entries, bits.ptr, at.stream))) ||
+      (given && written(out, NULL)))
+    Py_CLEAR(out);
+  return out;
+}
+
 /* host_ints(values, count or -1) -> list: how the calls read their host integers, for tests without a GPU. */
 static PyObject *host_ints(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   ints a;
@@ -588,6 +873,9 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   g_bf16 = PyObject_GetAttrString(torch, "bfloat16");
   g_fp16 = PyObject_GetAttrString(torch, "float16");
   g_int32 = PyObject_GetAttrString(torch, "int32");
+  g_fp32 = PyObject_GetAttrString(torch, "float32");
+  g_fp64 = PyObject_GetAttrString(torch, "float64");
+  g_uint8 = PyObject_GetAttrString(torch, "uint8");
   g_empty = PyObject_GetAttrString(torch, "empty");
   PyObject *dual = PyImport_ImportModule("torch.autograd.forward_ad");
   g_dual = dual ? PyModule_GetDict(dual) : NULL;
@@ -612,7 +900,7 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     Py_INCREF(Py_None);
     g_stream = Py_None;
   }
-  if (!g_bf16 || !g_fp16 || !g_int32 || !g_empty || !g_dual || !g_grad || !g_written || !g_device || !g_set || PyErr_Occurred()) return NULL;
+  if (!g_bf16 || !g_fp16 || !g_int32 || !g_fp32 || !g_fp64 || !g_uint8 || !g_empty || !g_dual || !g_grad || !g_written || !g_device || !g_set || PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
 
@@ -620,6 +908,9 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
 static PyMethodDef methods[] = {{"init", FAST(init), METH_FASTCALL, NULL},     {"prompt", FAST(prompt), METH_FASTCALL, NULL},
                                 {"tree", FAST(tree), METH_FASTCALL, NULL},     {"append", FAST(append), METH_FASTCALL, NULL},
                                 {"accept", FAST(accept), METH_FASTCALL, NULL}, {"host_ints", FAST(host_ints), METH_FASTCALL, NULL},
+                                {"rows", FAST(rows), METH_FASTCALL, NULL},     {"append_paged", FAST(append_paged), METH_FASTCALL, NULL},
+                                {"decode_paged", FAST(decode_paged), METH_FASTCALL, NULL}, {"evict_paged", FAST(evict_paged), METH_FASTCALL, NULL},
+                                {"adjust", FAST(adjust), METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -33,6 +33,7 @@ enum : int {
   kKidChunkAttn = 10,  // prefill-chunk attention (and its merge)
   kKidPrep = 11,       // prefill-chunk RMSNorm / split of the activations
   kKidTileAttn = 12,   // packed-prompt and drafted-tree attention
+  kKidPagedAttn = 13,  // paged decode attention
   kKidSkinnyBit = 1 << 12,
 };
 
