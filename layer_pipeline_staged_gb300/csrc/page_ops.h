@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "cache_ops.h"
+
 namespace lps {
 
 constexpr int kPagedBatch = 1024;  // sequences of one attention call (their lengths are kept in shared memory)
@@ -50,8 +52,8 @@ struct PagedAttnParams {
   const int* lengths;          // [batch]
   float* key_weights;          // [n_pages][nkv][page], or NULL
   float* part_o;               // workspace: [ctas][2][group][hd]
-  float4* part_ml;             // [ctas][2][group]: base, sum, whether a key was seen
-  float4* row_ml;              // key_weights: [batch][nq]: base, 1 / sum
+  float4* part_ml;             // [ctas][2][group]: base, sum, whether a key was seen; then,
+                               // with key_weights, of heads that one CTA has whole: [batch][nkv][group]
   float* scores;               // key_weights: [batch][nq][width * page], times log2(e)
   long long wait_limit;
   int batch, width, n_pages, page, box;

@@ -34,6 +34,7 @@ namespace {
 constexpr int kTile = 64;          // keys of a tile
 constexpr int kConsumers = 8;      // warps of 16 keys; two teams
 constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMaxParts = 256;     // CTAs of a launch, and so parts of a head
 constexpr int kKid = kKidPagedAttn << 8;
 
 __device__ int g_status[2];        // sticky: error kinds, first report
@@ -48,7 +49,11 @@ struct Shape {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kHalf = kTile * 128;             // bytes of 64 keys x 64 elements
   static constexpr int kBytes = kTile * HD * 2;         // K (or V) of a tile
-  static constexpr int kStages = HD == 128 ? (NT == 1 ? 5 : 4) : (NT == 1 ? 10 : 8);
+  // Even, so that a stage is always the same team's: a wait for a barrier's phase
+  // n by its parity holds only for who knows that phase n - 1 is over, and a team
+  // knows that of its own tiles alone.
+  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static_assert(kStages % 2 == 0, "a stage belongs to one team");
   static constexpr int kRow = HD + 4;                   // floats of a head's row in the join: other banks for other heads
 };
 
@@ -139,7 +144,7 @@ __device__ __forceinline__ void store_out(void* out, long long at, float x) {
 
 // Rows of sequence b: its length, or 0 where that is not one.
 __device__ __forceinline__ int rows_of(const PagedAttnParams& p, int b) {
-  const int n = p.lengths[b];
+  const int n = __ldcg(p.lengths + b);  // from L2: the join reads it before its wait
   return n > 0 && n <= static_cast<long long>(p.width) * p.page ? n : 0;
 }
 
@@ -191,8 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     sm.seen[0] = sm.seen[1] = 0;
     fence_mbar_init();
   }
-  pdl_launch_dependents();
+  // what the stream ran before is done when the join is let start: it may read
+  // the lengths at once, and only the parts behind its own wait
   pdl_wait();
+  pdl_launch_dependents();
 
   // the tiles of every sequence, and where this CTA's share begins
   long long total, beg, end;
@@ -467,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const int head = g * p.group + h;
       if (whole) {
         store_out<BF16>(p.out, b * p.o_seq + head * p.o_head + d, seen ? acc / sum : 0.f);
-        if (WEIGHTS && d == 0) p.row_ml[static_cast<long long>(b) * p.nq + head] = make_float4(top, 1.f / sum, 0.f, 0.f);
+        if (WEIGHTS && d == 0)
+          p.part_ml[(2ll * p.ctas + static_cast<long long>(b) * p.nkv + g) * p.group + h] = make_float4(top, sum, 1.f, 0.f);
       } else {
         p.part_o[(slot + h) * HD + d] = acc;
         if (d == 0) p.part_ml[slot + h] = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
@@ -477,16 +485,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
 }
 
-// Block = (head, sequence), thread = element: the parts of a head that several
-// CTAs have computed, in their order; zeros where the sequence has no rows.
+constexpr int kJoin = 256;         // threads of the join
+constexpr int kJoinKeys = 1024;    // keys of one of its blocks, with key weights
+
+// Block = (kv head, sequence): the parts of the group's heads that several CTAs
+// have computed, in their order; zeros where the sequence has no rows. With key
+// weights also the block's share of the cached rows: their weights over the
+// group's heads, into the pages' entries.
 template <bool BF16, int HD, bool WEIGHTS>
-__global__ void __launch_bounds__(HD) join_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ long long sums[2][HD / 32];
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ PagedAttnParams p) {
+  __shared__ long long sums[2][kJoin / 32];
+  __shared__ float factor[kMaxGroup][kMaxParts];  // 2^(m of the part - m)
+  __shared__ float top[kMaxGroup], inv[kMaxGroup];
+  __shared__ int seen[kMaxGroup];
   pdl_launch_dependents();
-  pdl_wait();
-  const int tid = threadIdx.x, head = blockIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
   long long before = 0, total = 0;
-  for (int i = tid; i < p.batch; i += HD) {
+  for (int i = tid; i < p.batch; i += kJoin) {
     const int n = (rows_of(p, i) + kTile - 1) / kTile;
     total += n;
     if (i < b) before += n;
@@ -496,64 +511,80 @@ __global__ void __launch_bounds__(HD) join_kernel(const __grid_constant__ PagedA
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
-  if ((tid & 31) == 0) sums[0][tid >> 5] = before, sums[1][tid >> 5] = total;
+  if (lane == 0) sums[0][warp] = before, sums[1][warp] = total;
   __syncthreads();
   before = total = 0;
 #pragma unroll
-  for (int w = 0; w < HD / 32; ++w) before += sums[0][w], total += sums[1][w];
-  const int n = (rows_of(p, b) + kTile - 1) / kTile;
-  const long long at = b * p.o_seq + head * p.o_head + tid;
+  for (int w = 0; w < kJoin / 32; ++w) before += sums[0][w], total += sums[1][w];
+  const int n_rows = rows_of(p, b), n = (n_rows + kTile - 1) / kTile;
+  int c0 = 0, c1 = 0;
+  bool shifted = false;  // the first part is not its CTA's first piece
+  if (n) {
+    total *= p.nkv;
+    const int ctas = sharers(p, total);
+    const long long i0 = before * p.nkv + static_cast<long long>(g) * n;
+    c0 = share_of(total, ctas, i0), c1 = share_of(total, ctas, i0 + n - 1);
+    shifted = share_start(total, ctas, c0) < i0;
+  }
+  const int parts = c1 - c0 + 1;
+  auto slot = [&](int i, int h) { return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h; };
+  pdl_wait();
+  char* out = static_cast<char*>(p.out) + 2 * (b * p.o_seq + static_cast<long long>(g) * p.group * p.o_head);
   if (n == 0) {
-    store_out<BF16>(p.out, at, 0.f);
+    if (blockIdx.z == 0)
+      for (int i = tid; i < p.group * HD; i += kJoin) store_out<BF16>(out, i / HD * p.o_head + i % HD, 0.f);
     return;
   }
-  total *= p.nkv;
-  const int g = head / p.group, h = head - g * p.group;
-  const long long i0 = before * p.nkv + static_cast<long long>(g) * n;
-  const int ctas = sharers(p, total);
-  const int c0 = share_of(total, ctas, i0), c1 = share_of(total, ctas, i0 + n - 1);
-  if (c0 == c1) return;
-  // a CTA's part is its first piece where its share begins in this head
-  auto slot = [&](int c) {
-    return (static_cast<long long>(c) * 2 + (c == c0 && share_start(total, ctas, c) < i0 ? 1 : 0)) * p.group + h;
-  };
-  float top = -INFINITY;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, p.part_ml[slot(c)].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc = 0.f, seen = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const long long s = slot(c);
-    const float4 ml = p.part_ml[s];
-    const float f = exp2_fast(ml.x - base);
-    sum += f * ml.y;
-    seen += ml.z;
-    acc += f * p.part_o[s * HD + tid];
-  }
-  store_out<BF16>(p.out, at, seen > 0.f ? acc / sum : 0.f);
-  if (WEIGHTS && tid == 0) p.row_ml[static_cast<long long>(b) * p.nq + head] = make_float4(top, 1.f / sum, 0.f, 0.f);
-}
+  if (!WEIGHTS && parts == 1) return;
+  if (WEIGHTS && static_cast<long long>(blockIdx.z) * kJoinKeys >= n_rows) return;
 
-// Thread = a cached row of (sequence, kv head): its weights over the group's
-// heads, into the page's entry.
-template <bool BF16>
-__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ PagedAttnParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int n = rows_of(p, b);
-  const long long rows = static_cast<long long>(p.width) * p.page;
-  for (long long key = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; key < n; key += static_cast<long long>(gridDim.x) * 256) {
-    const int j = static_cast<int>(key), pi = j / p.page;
-    const int page = p.table[static_cast<long long>(b) * p.width + pi];
-    if (page < 0 || page >= p.n_pages) continue;
-    float w = 0.f;
-    for (int h = 0; h < p.group; ++h) {
-      const long long row = static_cast<long long>(b) * p.nq + g * p.group + h;
-      const float4 ml = p.row_ml[row];
-      w += exp2_fast(p.scores[row * rows + j] - ml.x + kLift<BF16>) * ml.y;
+  // warp = head: its base, its sum, and what each part is multiplied by
+  for (int h = warp; h < p.group; h += kJoin / 32) {
+    if (parts == 1) {
+      const float4 ml = p.part_ml[(2ll * p.ctas + static_cast<long long>(b) * p.nkv + g) * p.group + h];  // the whole head's
+      if (lane == 0) top[h] = ml.x, inv[h] = 1.f / ml.y;
+      continue;
     }
-    float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
-    *to = p.decay == 0.f ? w : p.decay * *to + w;
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i, h)].x);
+    m = warp_max(m);
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, any = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const float4 ml = p.part_ml[slot(i, h)];
+      const float f = exp2_fast(ml.x - base);
+      factor[h][i] = f;
+      sum += f * ml.y;
+      any += ml.z;
+    }
+    sum = warp_sum(sum);
+    any = warp_sum(any);
+    if (lane == 0) top[h] = m, inv[h] = 1.f / sum, seen[h] = any > 0.f;
+  }
+  __syncthreads();
+  if (parts > 1 && blockIdx.z == 0) {
+    for (int i = tid; i < p.group * HD; i += kJoin) {
+      const int h = i / HD, d = i % HD;
+      float acc = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < parts; ++c) acc += factor[h][c] * p.part_o[slot(c, h) * HD + d];
+      store_out<BF16>(out, h * p.o_head + d, seen[h] ? acc * inv[h] : 0.f);
+    }
+  }
+  if constexpr (WEIGHTS) {
+    const long long rows = static_cast<long long>(p.width) * p.page;
+    const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
+    // a block's lot of kJoinKeys, and what lies a grid further on
+    for (long long lot = static_cast<long long>(blockIdx.z) * kJoinKeys; lot < n_rows; lot += static_cast<long long>(gridDim.z) * kJoinKeys)
+    for (int i = tid; i < kJoinKeys && lot + i < n_rows; i += kJoin) {
+      const int j = static_cast<int>(lot) + i, pi = j / p.page;
+      const int page = p.table[static_cast<long long>(b) * p.width + pi];
+      if (page < 0 || page >= p.n_pages) continue;
+      float w = 0.f;
+      for (int h = 0; h < p.group; ++h) w += exp2_fast(scores[h * rows + j] - top[h] + kLift<BF16>) * inv[h];
+      float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
+      *to = p.decay == 0.f ? w : p.decay * *to + w;
+    }
   }
 }
 
@@ -578,11 +609,9 @@ cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   static_assert(kSmem <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<BF16, HD, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e == cudaSuccess) e = launch(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, p, s);
-  if (e == cudaSuccess) e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(p.nq, p.batch), HD, 0, p, s);
-  if (WEIGHTS && e == cudaSuccess) {
-    const long long rows = static_cast<long long>(p.width) * p.page;
-    e = launch(weights_kernel<BF16>, dim3(static_cast<unsigned>(rows < 256 * 1024 ? (rows + 255) / 256 : 1024), p.nkv, p.batch), 256, 0, p, s);
-  }
+  const long long rows = static_cast<long long>(p.width) * p.page;
+  const unsigned z = WEIGHTS ? static_cast<unsigned>(rows < 65535ll * kJoinKeys ? (rows + kJoinKeys - 1) / kJoinKeys : 65535) : 1;
+  if (e == cudaSuccess) e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(p.nkv, p.batch, z), kJoin, 0, p, s);
   return e;
 }
 
@@ -599,13 +628,15 @@ long long up256(long long x) { return (x + 255) / 256 * 256; }
 cudaError_t paged_attn_ctas(int* ctas) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (*ctas > kMaxParts) *ctas = kMaxParts;
+  return e;
 }
 
 long long paged_attn_workspace(const PagedAttnParams& p, int hd, bool weights) {
   const long long parts = 2ll * p.ctas * p.group;
-  long long n = up256(parts * hd * 4) + up256(parts * 16);
-  if (weights) n += up256(16ll * p.batch * p.nq) + 4ll * p.batch * p.nq * (static_cast<long long>(p.width) * p.page);
+  long long n = up256(parts * hd * 4) + up256(16 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
+  if (weights) n += 4ll * p.batch * p.nq * (static_cast<long long>(p.width) * p.page);
   return n;
 }
 
@@ -615,10 +646,8 @@ void paged_attn_place(PagedAttnParams& p, int hd, bool weights, void* workspace)
   p.part_o = reinterpret_cast<float*>(at);
   at += up256(parts * hd * 4);
   p.part_ml = reinterpret_cast<float4*>(at);
-  at += up256(parts * 16);
   if (!weights) return;
-  p.row_ml = reinterpret_cast<float4*>(at);
-  at += up256(16ll * p.batch * p.nq);
+  at += up256(16 * (parts + static_cast<long long>(p.batch) * p.nq));
   p.scores = reinterpret_cast<float*>(at);
 }
 
