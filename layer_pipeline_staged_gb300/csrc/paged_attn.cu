@@ -33,16 +33,21 @@ namespace {
 
 constexpr int kTile = 64;          // keys of a tile
 constexpr int kConsumers = 8;      // warps of 16 keys; two teams
-constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kProducers = 2;      // warps that feed the ring, one for each team
+constexpr int kWriters = 2;        // warps that finish pieces
+constexpr int kThreads = (kConsumers + kProducers + kWriters) * 32;
 constexpr int kMaxParts = 256;     // CTAs of a launch, and so parts of a head
 constexpr int kKid = kKidPagedAttn << 8;
+constexpr float kStale = 8.0f;     // the base may lag the maximum by a factor of 2^8
+constexpr uint32_t kWhole = ~0u;   // Smem::valid: all keys of the tile are there
 
 __device__ int g_status[2];        // sticky: error kinds, first report
 
-// fp16 weights are made 2^14 times larger, which the sum divides out, so that
-// their second part stays normal.
+// fp16 weights are made 2^7 times larger, which the sum divides out: with a stale
+// base they reach 2^15, half of the type's range, and their second part stays
+// normal further down.
 template <bool BF16>
-constexpr float kLift = BF16 ? 0.0f : 14.0f;
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
 
 template <int HD, int NT>
 struct Shape {
@@ -54,22 +59,31 @@ struct Shape {
   // knows that of its own tiles alone.
   static constexpr int kStages = HD == 128 ? 4 : 8;
   static_assert(kStages % 2 == 0, "a stage belongs to one team");
-  static constexpr int kRow = HD + 4;                   // floats of a head's row in the join: other banks for other heads
+  static constexpr int kSlots = HD == 128 && NT == 2 ? 1 : 2;  // pieces on their way out
+  static constexpr int kRow = HD + 4;                   // floats of a head's row in a slot: other banks for other heads
+  static constexpr int kQRow = HD * 2 + 16;             // bytes of a head's row of q, likewise
+};
+
+template <int HD, int NT>
+struct Slot {
+  using S = Shape<HD, NT>;
+  float o[kConsumers][S::kHeads][S::kRow];
+  float m[kConsumers][S::kHeads], l[kConsumers][S::kHeads];
+  int seen[kConsumers];            // whether the warp has seen a key
 };
 
 template <int HD, int NT>
 struct __align__(1024) Smem {
   using S = Shape<HD, NT>;
   uint8_t kv[S::kStages][2][S::kBytes];
-  float o[kConsumers][S::kHeads][S::kRow];
-  float m[kConsumers][S::kHeads], l[kConsumers][S::kHeads];
-  int tiles[kPagedBatch];          // of each sequence
-  long long warp_sum[kThreads / 32];
-  long long base;                  // first tile of the sequence that the CTA begins in
+  uint8_t q[S::kStages][S::kHeads * S::kQRow];  // of the stages that a team's piece begins with
+  Slot<HD, NT> slot[S::kSlots];
+  int rows[kPagedBatch];           // of each sequence
+  int warp_sum[kThreads / 32];
+  int base;                        // first tile of the sequence that the CTA begins in
   int first;                       // that sequence
-  int seen[2];                     // whether the piece has a key (pieces take turns)
-  uint32_t valid[S::kStages];      // boxes of the tile whose page is one
-  uint64_t full[S::kStages], empty[S::kStages];
+  uint32_t valid[S::kStages];      // boxes of the tile whose page is one, or kWhole
+  uint64_t full[S::kStages], empty[S::kStages], slot_full[S::kSlots], slot_empty[S::kSlots];
 };
 
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar,
@@ -137,6 +151,15 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& 
 }
 
 template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <bool BF16>
 __device__ __forceinline__ void store_out(void* out, long long at, float x) {
   if constexpr (BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
   else static_cast<__half*>(out)[at] = __float2half_rn(x);
@@ -148,34 +171,39 @@ __device__ __forceinline__ int rows_of(const PagedAttnParams& p, int b) {
   return n > 0 && n <= static_cast<long long>(p.width) * p.page ? n : 0;
 }
 
-// The CTAs that have a share, the first tile of CTA c's share of `total` tiles,
-// and the CTA that has tile i.
-__device__ __forceinline__ int sharers(const PagedAttnParams& p, long long total) {
-  return total < p.ctas ? static_cast<int>(total) : p.ctas;
-}
-__device__ __forceinline__ long long share_start(long long total, int ctas, int c) { return total * c / ctas; }
-__device__ __forceinline__ int share_of(long long total, int ctas, long long i) {
-  return static_cast<int>(((i + 1) * ctas - 1) / total);
-}
+// `total` tiles in equal shares (in 32 bits: the entry point bounds them), the
+// first `more` of one tile more.
+struct Shares {
+  int ctas, per, more;
+  __device__ __forceinline__ Shares(int total, int grid) {
+    ctas = max(1, min(total, grid));
+    per = total / ctas;
+    more = total - per * ctas;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int head = more * (per + 1);
+    return tile < head ? tile / (per + 1) : more + (tile - head) / per;
+  }
+};
 
 // A CTA's pieces in order: tiles [t0, t1) of kv head g of sequence b.
 struct Walk {
-  long long at, end, base;  // next tile, the share's end, the first tile of sequence b
+  int at, end, base;  // next tile, the share's end, the first tile of sequence b
   int b, nkv;
-  const int* tiles;
+  const int* rows;
   int g, t0, t1;
+  __device__ __forceinline__ int tiles() const { return (rows[b] + kTile - 1) / kTile; }
   __device__ __forceinline__ bool next() {
     if (at >= end) return false;
-    while (at >= base + static_cast<long long>(nkv) * tiles[b]) {
-      base += static_cast<long long>(nkv) * tiles[b];
+    int n;
+    while (n = tiles(), at >= base + nkv * n) {
+      base += nkv * n;
       ++b;
     }
-    const int n = tiles[b];
-    const unsigned off = static_cast<unsigned>(at - base);  // below nkv * tiles, kept below 2^31 by the entry point
-    g = off / n;
-    t0 = off - g * n;
-    const long long left = end - at;
-    t1 = left < n - t0 ? t0 + static_cast<int>(left) : n;
+    g = (at - base) / n;
+    t0 = at - base - g * n;
+    t1 = min(n, t0 + end - at);
     at += t1 - t0;
     return true;
   }
@@ -193,138 +221,200 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kConsumers / 2);
     }
-    sm.seen[0] = sm.seen[1] = 0;
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&sm.slot_full[i], kConsumers);
+      mbar_init(&sm.slot_empty[i], kWriters);
+    }
     fence_mbar_init();
   }
+  // heads that the group does not have are columns of zeros
+  for (int i = tid; i < static_cast<int>(sizeof sm.q) / 16; i += kThreads) reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the copies' bytes
   // what the stream ran before is done when the join is let start: it may read
   // the lengths at once, and only the parts behind its own wait
   pdl_wait();
   pdl_launch_dependents();
 
   // the tiles of every sequence, and where this CTA's share begins
-  long long total, beg, end;
+  int beg, end;
   {
     const int per = (p.batch + kThreads - 1) / kThreads, lo = min(tid * per, p.batch), hi = min(lo + per, p.batch);
-    long long mine = 0;
+    int mine = 0;
     for (int b = lo; b < hi; ++b) {
-      const int n = (rows_of(p, b) + kTile - 1) / kTile;
-      sm.tiles[b] = n;
-      mine += n;
+      const int n = rows_of(p, b);
+      sm.rows[b] = n;
+      mine += (n + kTile - 1) / kTile;
     }
     mine *= p.nkv;
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
-    long long before = 0;
-    total = 0;
+    int before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w == warp) before = total;
       total += sm.warp_sum[w];
     }
-    const int ctas = sharers(p, total);
+    const Shares shares(total, p.ctas);
     beg = end = total;
-    if (static_cast<int>(blockIdx.x) < ctas) beg = share_start(total, ctas, blockIdx.x), end = share_start(total, ctas, blockIdx.x + 1);
-    long long at = before + incl - mine;
+    if (static_cast<int>(blockIdx.x) < shares.ctas) beg = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
+    int at = before + incl - mine;
     if (beg < end && beg >= at && beg < at + mine) {
       int b = lo;
-      while (beg >= at + static_cast<long long>(p.nkv) * sm.tiles[b]) at += static_cast<long long>(p.nkv) * sm.tiles[b++];
+      for (int n; n = p.nkv * ((sm.rows[b] + kTile - 1) / kTile), beg >= at + n; ++b) at += n;
       sm.first = b;
       sm.base = at;
     }
     __syncthreads();
   }
   if (beg >= end) return;
-  Walk walk{beg, end, sm.base, sm.first, p.nkv, sm.tiles, 0, 0, 0};
+  Walk walk{beg, end, sm.base, sm.first, p.nkv, sm.rows, 0, 0, 0};
   const long long limit = wait_cycles(p.wait_limit);
 
-  if (warp == kConsumers) {
-    // ---- the ring's producer ----
+  if (warp >= kConsumers && warp < kConsumers + kProducers) {
+    // ---- a team's producer ----
+    const int team = warp - kConsumers;
     const uint64_t pol = l2_evict_first();
-    const int boxes = kTile / p.box, box_bytes = p.box * 128, page_boxes = p.page / p.box;
-    int it = 0, stage = 0;
-    bool ok = true;
-    while (ok && walk.next()) {
-      const int n_rows = rows_of(p, walk.b);
-      const int* table = p.table + static_cast<long long>(walk.b) * p.width;
-      const int n_boxes = (n_rows + p.box - 1) / p.box;
-      // a lane holds the page of one box; 32 boxes at a time are looked up, one lot ahead
-      auto look = [&](int box) {
-        if (box >= n_boxes) return make_int2(-1, 0);
-        const int pi = box / page_boxes;
-        return make_int2(table[pi], (box - pi * page_boxes) * p.box);
-      };
-      int2 ahead = look(walk.t0 * boxes + lane);
-      const int lot = 32 / boxes;  // tiles whose boxes one look covers
-      int2 now = ahead;
-      for (int t = walk.t0; t < walk.t1; ++t) {
-        const int i = (t - walk.t0) % lot;
-        if (i == 0) {
-          now = ahead;
-          ahead = look((t + lot) * boxes + lane);
-        }
-        if (it >= S::kStages) {
-          ok = mbar_wait(&sm.empty[stage], (it / S::kStages - 1) & 1, limit);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        const bool good = now.x >= 0 && now.x < p.n_pages;
-        const uint32_t valid = (__ballot_sync(0xffffffffu, good) >> (i * boxes)) & ((1u << boxes) - 1);
-        if (lane == 0) {
-          sm.valid[stage] = valid;
-          mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * 2 * (HD / 64) * box_bytes);
-        }
-        __syncwarp();
-        // lane: one box of K or V, one half of the head
-        constexpr int kParts = 2 * (HD / 64);
-        for (int j = lane; __any_sync(0xffffffffu, j < boxes * kParts); j += 32) {
-          const int bx = j % boxes, part = j / boxes;
-          const int page = __shfl_sync(0xffffffffu, now.x, i * boxes + bx), slot = __shfl_sync(0xffffffffu, now.y, i * boxes + bx);
-          if (j < boxes * kParts && (valid >> bx & 1)) {
-            const int v = part & 1, half = part >> 1;
-            tma_4d(sm.kv[stage][v] + half * S::kHalf + bx * box_bytes, v ? &p.tmap_v : &p.tmap_k, 64 * half, slot, walk.g,
-                   page, &sm.full[stage], pol);
+    const int log_box = 31 - __clz(p.box), log_boxes = 6 - log_box, boxes = 1 << log_boxes;  // boxes of a tile
+    const int page_boxes = p.page >> log_box;
+    // a lane's part of a tile: box `bx` of K or V, of one half of the head
+    constexpr int kParts = 2 * (HD / 64);
+    const int bx = lane & (boxes - 1), part = lane >> log_boxes, v = part & 1;
+    const bool carries = part < kParts;
+    uint8_t* const dst = carries ? sm.kv[0][v] + (part >> 1) * S::kHalf + bx * (p.box * 128) : nullptr;
+    const CUtensorMap* const map = v ? &p.tmap_v : &p.tmap_k;
+    const int x = 64 * (part >> 1);
+    const uint32_t all = (1u << boxes) - 1;
+    // Pages of 32 boxes of a sequence, one a lane: (page, row in the page). The
+    // next lot of a piece, or the first one of the next piece, is on its way while
+    // this one is used.
+    const int lot = 32 >> log_boxes;  // tiles of a lot
+    auto look = [&](const Walk& w, int tile) {
+      const int box = (tile << log_boxes) + lane;
+      if (tile >= w.t1 || box >= (w.rows[w.b] + p.box - 1) >> log_box) return make_int2(-1, 0);
+      const int pi = box / page_boxes;
+      return make_int2(p.table[static_cast<long long>(w.b) * p.width + pi], (box - pi * page_boxes) << log_box);
+    };
+    int it = 0, last = -1;  // tiles of the pieces before; the last one issued
+    bool ok = true, more = walk.next();
+    int2 ahead = more ? look(walk, walk.t0) : make_int2(-1, 0);
+    while (ok && more) {
+      Walk next = walk;
+      more = next.next();
+      const int n_rows = walk.rows[walk.b], n_tiles = walk.t1 - walk.t0;
+      for (int l0 = 0; l0 < n_tiles && ok; l0 += lot) {
+        const int2 now = ahead;
+        if (l0 + lot < n_tiles) ahead = look(walk, walk.t0 + l0 + lot);
+        else if (more) ahead = look(next, next.t0);
+        const uint32_t good = __ballot_sync(0xffffffffu, now.x >= 0 && now.x < p.n_pages);
+        const int l1 = min(n_tiles, l0 + lot);
+        for (int i = l0 + ((it + l0 + team) & 1); i < l1; i += 2) {
+          const int stage = (it + i) % S::kStages, use = (it + i) / S::kStages, t = walk.t0 + i;
+          if (use) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[stage], (use - 1) & 1, limit));
+            if (!ok) break;
           }
+          const uint32_t valid = good >> ((i - l0) << log_boxes) & all;
+          const bool with_q = i < 2;  // the team's first tile of the piece
+          const int from = ((i - l0) << log_boxes) + bx;
+          const int page = __shfl_sync(0xffffffffu, now.x, from), row = __shfl_sync(0xffffffffu, now.y, from);
+          if (lane == 0) {
+            sm.valid[stage] = valid == all && (t + 1) * kTile <= n_rows ? kWhole : valid;
+            mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * kParts * p.box * 128 + (with_q ? p.group * HD * 2 : 0));
+          }
+          __syncwarp();
+          if (carries && (valid >> bx & 1)) tma_4d(dst + stage * (2 * S::kBytes), map, x, row, walk.g, page, &sm.full[stage], pol);
+          if (with_q && lane < p.group)
+            bulk_g2s_plain(sm.q[stage] + lane * S::kQRow,
+                           static_cast<const char*>(p.q) + 2 * (walk.b * p.q_seq + static_cast<long long>(walk.g * p.group + lane) * p.q_head),
+                           HD * 2, &sm.full[stage]);
+          __syncwarp();
+          last = it + i;
         }
-        ++it;
-        if (++stage == S::kStages) stage = 0;
       }
+      it += n_tiles;
+      walk = next;
     }
     if (!ok && lane == 0) report_error(g_status, kErrWaitEmpty | kKid);
-    // what is in flight lands before the CTA ends
-    for (int i = max(0, it - S::kStages); i < it; ++i)
-      if (!mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, ok ? limit : kDrainLimitCycles)) {
+    // what is in flight lands before the CTA ends: the team's last tiles
+    for (int i = last - (S::kStages - 2); i <= last; i += 2)
+      if (i >= 0 && !mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, ok ? limit : kDrainLimitCycles)) {
         if (lane == 0) report_error(g_status, kErrDrain | kKid);
         break;
       }
     return;
   }
 
+  if (warp >= kConsumers + kProducers) {
+    // ---- the writers: eight warps' (o, m, l) of a piece, in warp order; warp = head ----
+    int it = 0;
+    bool alive = true;
+    for (int piece = 0; walk.next(); ++piece) {
+      const int n = walk.t1 - walk.t0, sl = piece % S::kSlots;
+      const int w0 = n == 1 && (it & 1) ? kConsumers / 2 : 0, w1 = n == 1 && !(it & 1) ? kConsumers / 2 : kConsumers;  // the warps that had tiles
+      it += n;
+      if (alive) alive = mbar_wait(&sm.slot_full[sl], (piece / S::kSlots) & 1, limit);
+      if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
+      alive = __all_sync(0xffffffffu, alive);
+      const Slot<HD, NT>& in = sm.slot[sl];
+      const bool mine = lane >= w0 && lane < w1;  // lane = warp of the piece
+      const bool seen = __any_sync(0xffffffffu, mine && in.seen[lane & 7]);
+      const bool whole = n == walk.tiles();
+      const long long part = (static_cast<long long>(blockIdx.x) * 2 + (piece ? 1 : 0)) * p.group;
+      for (int h = warp - kConsumers - kProducers; alive && h < p.group; h += kWriters) {
+        const float m = mine ? in.m[lane][h] : -INFINITY;
+        const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
+        const float f = exp2_fast(m - base);
+        const float sum = warp_sum(mine ? f * in.l[lane][h] : 0.f);
+        constexpr int kEach = HD / 32;  // elements of a lane
+        float acc[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+        for (int w = w0; w < w1; ++w) {
+          const float fw = __shfl_sync(0xffffffffu, f, w);
+          const float* row = in.o[w][h] + lane * kEach;
+          if constexpr (kEach == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(row);
+            acc[0] += fw * x.x, acc[1] += fw * x.y, acc[2] += fw * x.z, acc[3] += fw * x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(row);
+            acc[0] += fw * x.x, acc[1] += fw * x.y;
+          }
+        }
+        if (whole) {
+          const int head = walk.g * p.group + h;
+          uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<char*>(p.out) + 2 * (walk.b * p.o_seq + head * p.o_head + lane * kEach));
+#pragma unroll
+          for (int e = 0; e < kEach; e += 2) to[e / 2] = pack<BF16>(seen ? acc[e] / sum : 0.f, seen ? acc[e + 1] / sum : 0.f);
+          if (WEIGHTS && lane == 0)
+            p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = make_float4(top, sum, 1.f, 0.f);
+        } else {
+          float* to = p.part_o + (part + h) * HD + lane * kEach;
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) to[e] = acc[e];
+          if (lane == 0) p.part_ml[part + h] = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.slot_empty[sl]);
+    }
+    return;
+  }
+
   // ---- softmax and products: warps 0-7 ----
   const int team = warp >> 2, row0 = (warp & 3) * 16;  // the team's tiles, the warp's keys in a tile
   const int g8 = lane >> 2, t4 = lane & 3;             // fragment coordinates
+  const int mtx = lane >> 3, r8 = lane & 7;            // ldmatrix: matrix and row of the lane's address
   const int box_shift = 31 - __clz(p.box);
   bool alive = true;
-  int it = 0, piece = 0;
-  while (walk.next()) {
-    const int n_rows = rows_of(p, walk.b), b = walk.b, g = walk.g;
-    // q of the group as the B operand of S^T: column = head
-    uint32_t qb[HD / 16][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h = 8 * nt + g8;
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const char*>(p.q) +
-                                                            2 * (b * p.q_seq + static_cast<long long>(g * p.group + h) * p.q_head));
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        qb[kk][nt][0] = h < p.group ? q[8 * kk + t4] : 0u;
-        qb[kk][nt][1] = h < p.group ? q[8 * kk + 4 + t4] : 0u;
-      }
-    }
+  int it = 0;
+  for (int piece = 0; walk.next(); ++piece) {
+    const int b = walk.b, g = walk.g, n_tiles = walk.t1 - walk.t0, sl = piece % S::kSlots;
     float m[NT][2], l[NT][2], o[NT][HD / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -334,174 +424,186 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       for (int d = 0; d < HD / 16; ++d) o[nt][d][0] = o[nt][d][1] = o[nt][d][2] = o[nt][d][3] = 0.f;
     }
     bool any = false;
-    for (int t = walk.t0; t < walk.t1; ++t, ++it) {
-      if ((it & 1) != team) continue;
-      const int stage = it % S::kStages;
+    const int skip = (it ^ team) & 1;  // 1: the piece begins with the other team's tile
+    uint32_t qb[HD / 16][NT][2];       // q of the group as the B operand of S^T: column = head
+    for (int i = skip; i < n_tiles; i += 2) {
+      const int t = walk.t0 + i, stage = (it + i) % S::kStages;
       if (alive) {
-        alive = mbar_wait(&sm.full[stage], (it / S::kStages) & 1, limit);
+        alive = mbar_wait(&sm.full[stage], ((it + i) / S::kStages) & 1, limit);
         if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
         alive = __all_sync(0xffffffffu, alive);
       }
-      const int key0 = t * kTile + row0;
-      if (alive && key0 < n_rows) {
-        // which of the warp's 16 keys there are
-        const uint32_t valid = sm.valid[stage];
-        const int mine = lane & 15;
-        const bool is_key = key0 + mine < n_rows && (valid >> ((row0 + mine) >> box_shift) & 1);
-        const uint32_t keys = __ballot_sync(0xffffffffu, is_key) & 0xffffu;
-        const uint32_t kbase = smem_u32(sm.kv[stage][0]), vbase = smem_u32(sm.kv[stage][1]);
-        const int mtx = lane >> 3, r8 = lane & 7;
-        if (keys != 0xffffu) {
-          // what lies in the other rows is of no sequence, and 0 x inf is not 0
-          for (int c = lane; c < 16 * (HD / 8); c += 32) {
-            const int r = c / (HD / 8), ch = c % (HD / 8);
-            if (!(keys >> r & 1))
-              *reinterpret_cast<uint4*>(sm.kv[stage][1] + (ch / 8) * S::kHalf + (row0 + r) * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+      if (i < 2) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; kk += 2) {
+            uint32_t f[4];
+            ldsm_x4(smem_u32(sm.q[stage] + (8 * nt + r8) * S::kQRow + (2 * kk + mtx) * 16), f);
+            qb[kk][nt][0] = f[0], qb[kk][nt][1] = f[1], qb[kk + 1][nt][0] = f[2], qb[kk + 1][nt][1] = f[3];
           }
+      }
+      const int key0 = t * kTile + row0;
+      // which of the warp's 16 keys there are
+      uint32_t keys = alive ? 0xffffu : 0u;
+      const uint32_t valid = sm.valid[stage];
+      if (alive && valid != kWhole) {
+        const int mine = lane & 15;
+        keys = __ballot_sync(0xffffffffu, key0 + mine < walk.rows[b] && (valid >> ((row0 + mine) >> box_shift) & 1)) & 0xffffu;
+        // what lies in the other rows is of no sequence, and 0 x inf is not 0
+        for (int c = lane; c < 16 * (HD / 8); c += 32) {
+          const int r = c / (HD / 8), ch = c % (HD / 8);
+          if (!(keys >> r & 1))
+            *reinterpret_cast<uint4*>(sm.kv[stage][1] + (ch / 8) * S::kHalf + (row0 + r) * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      if (keys) {
+        any = true;
+        const uint32_t kbase = smem_u32(sm.kv[stage][0]), vbase = smem_u32(sm.kv[stage][1]);
+        // S^T in two chains
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+        {
+          const int r = row0 + (mtx & 1) * 8 + r8;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; kk += 2) {
+            uint32_t a[4], c[4];
+            ldsm_x4(kbase + (kk / 4) * S::kHalf + r * 128 + (((2 * (kk % 4) + (mtx >> 1)) ^ r8) << 4), a);
+            ldsm_x4(kbase + (kk / 4) * S::kHalf + r * 128 + (((2 * (kk % 4) + 2 + (mtx >> 1)) ^ r8) << 4), c);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<BF16>(s[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+              mma<BF16>(s2[nt], c, qb[kk + 1][nt][0], qb[kk + 1][nt][1]);
+            }
+          }
+        }
+        bool above = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = (s[nt][e] + s2[nt][e]) * p.scale_log2;
+            s[nt][e] = keys >> (g8 + 8 * (e >> 1)) & 1 ? x : -INFINITY;
+            above = above || s[nt][e] > m[nt][e & 1] + kStale;
+          }
+        if constexpr (WEIGHTS) {
+          const long long rows = static_cast<long long>(p.width) * p.page;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int h = 8 * nt + 2 * t4 + (e & 1), key = key0 + g8 + 8 * (e >> 1);
+              if (h < p.group && keys >> (g8 + 8 * (e >> 1)) & 1)
+                p.scores[(static_cast<long long>(b) * p.nq + g * p.group + h) * rows + key] = s[nt][e];
+            }
           __syncwarp();
         }
-        if (keys) {
-          any = true;
-          float s[NT][4];
+        // the bases follow the maximum when it has outgrown one of them
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-          {
-            const int r = row0 + (mtx & 1) * 8 + r8;
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              uint32_t a[4];
-              ldsm_x4(kbase + (kk / 4) * S::kHalf + r * 128 + (((2 * (kk % 4) + (mtx >> 1)) ^ r8) << 4), a);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<BF16>(s[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
-            }
-          }
-          const bool k0 = keys >> g8 & 1, k1 = keys >> (g8 + 8) & 1;
-          uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (e < 2 ? k0 : k1) ? s[nt][e] * p.scale_log2 : -INFINITY;
-            if constexpr (WEIGHTS) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int h = 8 * nt + 2 * t4 + (e & 1), key = key0 + g8 + 8 * (e >> 1);
-                if (h < p.group && key < n_rows)
-                  p.scores[(static_cast<long long>(b) * p.nq + g * p.group + h) * (static_cast<long long>(p.width) * p.page) + key] = x[e];
-              }
-            }
-            float w[4];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(x[c], x[2 + c]);
+              float top = fmaxf(s[nt][c], s[nt][2 + c]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
               const float was = m[nt][c], now = fmaxf(was, top);
-              const float base = now == -INFINITY ? 0.f : now;
-              if (__any_sync(0xffffffffu, now > was)) {  // the whole warp, so that it stays together
-                const float f = now > was ? exp2_fast(was - base) : 1.f;
-                m[nt][c] = now;
-                l[nt][c] *= f;
+              const float f = now > was ? exp2_fast(was - now) : 1.f;
+              m[nt][c] = now;
+              l[nt][c] *= f;
 #pragma unroll
-                for (int d = 0; d < HD / 16; ++d) o[nt][d][c] *= f, o[nt][d][2 + c] *= f;
-              }
-              w[c] = exp2_fast(x[c] - base + kLift<BF16>);
-              w[2 + c] = exp2_fast(x[2 + c] - base + kLift<BF16>);
-              l[nt][c] += w[c] + w[2 + c];
+              for (int d = 0; d < HD / 16; ++d) o[nt][d][c] *= f, o[nt][d][2 + c] *= f;
             }
-            uint32_t h0, l0, h1, l1;
-            split<BF16>(w[0], w[1], h0, l0);
-            split<BF16>(w[2], w[3], h1, l1);
-            ph[nt][0] = transposed(h0), ph[nt][1] = transposed(h1);
-            pl[nt][0] = transposed(l0), pl[nt][1] = transposed(l1);
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float base = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+            w[e] = exp2_fast(s[nt][e] - base + kLift<BF16>);
+            l[nt][e & 1] += w[e];
           }
-          const int r = row0 + (mtx >> 1) * 8 + r8;
+          uint32_t h0, l0, h1, l1;
+          split<BF16>(w[0], w[1], h0, l0);
+          split<BF16>(w[2], w[3], h1, l1);
+          ph[nt][0] = transposed(h0), ph[nt][1] = transposed(h1);
+          pl[nt][0] = transposed(l0), pl[nt][1] = transposed(l1);
+        }
+        const int r = row0 + (mtx >> 1) * 8 + r8;
 #pragma unroll
-          for (int d = 0; d < HD / 16; ++d) {
-            uint32_t a[4];
-            ldsm_x4_t(vbase + (d / 4) * S::kHalf + r * 128 + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
+        for (int d = 0; d < HD / 16; ++d) {
+          uint32_t a[4];
+          ldsm_x4_t(vbase + (d / 4) * S::kHalf + r * 128 + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<BF16>(o[nt][d], a, ph[nt][0], ph[nt][1]);
-              mma<BF16>(o[nt][d], a, pl[nt][0], pl[nt][1]);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<BF16>(o[nt][d], a, ph[nt][0], ph[nt][1]);
+            mma<BF16>(o[nt][d], a, pl[nt][0], pl[nt][1]);
           }
         }
-        if (keys != 0xffffu) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the next copy's bytes
       }
+      if (valid != kWhole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the next copy's bytes
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[stage]);
     }
+    it += n_tiles;
 
-    // ---- the piece's end: eight warps' (o, m, l) in warp order ----
-    named_bar_sync(1, kConsumers * 32);  // the last piece's have been read
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float sum = l[nt][c];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int h = 8 * nt + 2 * t4 + c;
-        if (g8 == 0) sm.m[warp][h] = m[nt][c], sm.l[warp][h] = sum;
-#pragma unroll
-        for (int d = 0; d < HD / 16; ++d) {
-          sm.o[warp][h][16 * d + g8] = o[nt][d][c];
-          sm.o[warp][h][16 * d + g8 + 8] = o[nt][d][2 + c];
-        }
-      }
-    if (any && lane == 0) sm.seen[piece & 1] = 1;
-    named_bar_sync(1, kConsumers * 32);
-    const bool seen = sm.seen[piece & 1] != 0;
-    if (tid == 0) sm.seen[~piece & 1] = 0;
-    const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles[b];
-    const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (piece ? 1 : 0)) * p.group;
-    for (int i = tid; i < p.group * HD; i += kConsumers * 32) {
-      const int h = i / HD, d = i % HD;
-      float top = sm.m[0][h];
-#pragma unroll
-      for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, sm.m[w][h]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kConsumers; ++w) {
-        const float f = exp2_fast(sm.m[w][h] - base);
-        sum += f * sm.l[w][h];
-        acc += f * sm.o[w][h][d];
-      }
-      const int head = g * p.group + h;
-      if (whole) {
-        store_out<BF16>(p.out, b * p.o_seq + head * p.o_head + d, seen ? acc / sum : 0.f);
-        if (WEIGHTS && d == 0)
-          p.part_ml[(2ll * p.ctas + static_cast<long long>(b) * p.nkv + g) * p.group + h] = make_float4(top, sum, 1.f, 0.f);
-      } else {
-        p.part_o[(slot + h) * HD + d] = acc;
-        if (d == 0) p.part_ml[slot + h] = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
-      }
+    // ---- the piece's end: (o, m, l) to the writers ----
+    if (piece >= S::kSlots && alive) {
+      alive = mbar_wait(&sm.slot_empty[sl], (piece / S::kSlots - 1) & 1, limit);
+      if (!alive && lane == 0) report_error(g_status, kErrWaitEmpty | kKid);
+      alive = __all_sync(0xffffffffu, alive);
     }
-    ++piece;
+    Slot<HD, NT>& out = sm.slot[sl];
+    if (skip < n_tiles) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float sum = l[nt][c];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int h = 8 * nt + 2 * t4 + c;
+          if (g8 == 0) out.m[warp][h] = m[nt][c], out.l[warp][h] = sum;
+          if (h < p.group) {
+#pragma unroll
+            for (int d = 0; d < HD / 16; ++d) {
+              out.o[warp][h][16 * d + g8] = o[nt][d][c];
+              out.o[warp][h][16 * d + g8 + 8] = o[nt][d][2 + c];
+            }
+          }
+        }
+      if (lane == 0) out.seen[warp] = any;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.slot_full[sl]);
   }
 }
 
-constexpr int kJoin = 256;         // threads of the join
-constexpr int kJoinKeys = 1024;    // keys of one of its blocks, with key weights
+constexpr int kJoinKeys = 1024;    // keys of a block that sums key weights
+constexpr int kAhead = 16;         // parts that a thread of the join asks for at once
 
-// Block = (kv head, sequence): the parts of the group's heads that several CTAs
-// have computed, in their order; zeros where the sequence has no rows. With key
-// weights also the block's share of the cached rows: their weights over the
-// group's heads, into the pages' entries.
-template <bool BF16, int HD, bool WEIGHTS>
-__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ long long sums[2][kJoin / 32];
-  __shared__ float factor[kMaxGroup][kMaxParts];  // 2^(m of the part - m)
-  __shared__ float top[kMaxGroup], inv[kMaxGroup];
-  __shared__ int seen[kMaxGroup];
-  pdl_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
-  long long before = 0, total = 0;
-  for (int i = tid; i < p.batch; i += kJoin) {
+// The parts of head (b, g), found from the lengths alone.
+struct Parts {
+  int n_rows, c0, n;  // n: 0 where there are no rows
+  bool shifted;       // the first part is not its CTA's first piece
+  __device__ __forceinline__ long long slot(const PagedAttnParams& p, int i, int h) const {
+    return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h;
+  }
+};
+template <int THREADS>
+__device__ __forceinline__ Parts parts_of(const PagedAttnParams& p, int b, int g) {
+  __shared__ int sums[2][THREADS / 32];
+  const int tid = threadIdx.x;
+  int before = 0, total = 0;
+  for (int i = tid; i < p.batch; i += THREADS) {
     const int n = (rows_of(p, i) + kTile - 1) / kTile;
     total += n;
     if (i < b) before += n;
@@ -511,85 +613,113 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
-  if (lane == 0) sums[0][warp] = before, sums[1][warp] = total;
+  if ((tid & 31) == 0) sums[0][tid >> 5] = before, sums[1][tid >> 5] = total;
   __syncthreads();
   before = total = 0;
 #pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) before += sums[0][w], total += sums[1][w];
-  const int n_rows = rows_of(p, b), n = (n_rows + kTile - 1) / kTile;
-  int c0 = 0, c1 = 0;
-  bool shifted = false;  // the first part is not its CTA's first piece
+  for (int w = 0; w < THREADS / 32; ++w) before += sums[0][w], total += sums[1][w];
+  Parts parts{rows_of(p, b), 0, 0, false};
+  const int n = (parts.n_rows + kTile - 1) / kTile;
   if (n) {
-    total *= p.nkv;
-    const int ctas = sharers(p, total);
-    const long long i0 = before * p.nkv + static_cast<long long>(g) * n;
-    c0 = share_of(total, ctas, i0), c1 = share_of(total, ctas, i0 + n - 1);
-    shifted = share_start(total, ctas, c0) < i0;
+    const Shares shares(total * p.nkv, p.ctas);
+    const int i0 = before * p.nkv + g * n;
+    parts.c0 = shares.owner(i0);
+    parts.n = shares.owner(i0 + n - 1) - parts.c0 + 1;
+    parts.shifted = shares.start(parts.c0) < i0;
   }
-  const int parts = c1 - c0 + 1;
-  auto slot = [&](int i, int h) { return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h; };
+  return parts;
+}
+
+// Block = (query head, sequence), thread = element: the parts of a head that
+// several CTAs have computed, in their order; zeros where the sequence has no
+// rows. All a thread reads is asked for at once, the parts' bases with their o.
+template <bool BF16, int HD, bool WEIGHTS>
+__global__ void __launch_bounds__(HD) join_kernel(const __grid_constant__ PagedAttnParams p) {
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, head = blockIdx.x, b = blockIdx.y, g = head / p.group, h = head - g * p.group;
+  const Parts parts = parts_of<HD>(p, b, g);
+  const long long at = b * p.o_seq + head * p.o_head + tid;
   pdl_wait();
-  char* out = static_cast<char*>(p.out) + 2 * (b * p.o_seq + static_cast<long long>(g) * p.group * p.o_head);
-  if (n == 0) {
-    if (blockIdx.z == 0)
-      for (int i = tid; i < p.group * HD; i += kJoin) store_out<BF16>(out, i / HD * p.o_head + i % HD, 0.f);
+  if (parts.n == 1) return;
+  if (parts.n == 0) {
+    store_out<BF16>(p.out, at, 0.f);
     return;
   }
-  if (!WEIGHTS && parts == 1) return;
-  if (WEIGHTS && static_cast<long long>(blockIdx.z) * kJoinKeys >= n_rows) return;
+  float top = -INFINITY, sum = 0.f, acc = 0.f, seen = 0.f;
+  for (int i0 = 0; i0 < parts.n; i0 += kAhead) {
+    float4 ml[kAhead];
+    float o[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const bool on = i0 + i < parts.n;
+      const long long s = parts.slot(p, on ? i0 + i : 0, h);
+      ml[i] = on ? __ldcg(p.part_ml + s) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      o[i] = on ? __ldcg(p.part_o + s * HD + tid) : 0.f;
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) now = fmaxf(now, ml[i].x);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float f = exp2_fast(top - base);
+    sum *= f, acc *= f, top = now;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= parts.n) break;
+      const float w = exp2_fast(ml[i].x - base);
+      sum += w * ml[i].y;
+      acc += w * o[i];
+      seen += ml[i].z;
+    }
+  }
+  store_out<BF16>(p.out, at, seen > 0.f ? acc / sum : 0.f);
+}
 
-  // warp = head: its base, its sum, and what each part is multiplied by
-  for (int h = warp; h < p.group; h += kJoin / 32) {
-    if (parts == 1) {
+// Block = (kv head, sequence, a share of the cached rows): the rows' weights over
+// the group's heads, into the pages' entries.
+__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ PagedAttnParams p, float lift) {
+  __shared__ float top[kMaxGroup], inv[kMaxGroup];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
+  const Parts parts = parts_of<256>(p, b, g);
+  const int first = static_cast<int>(blockIdx.z) * kJoinKeys;
+  pdl_wait();
+  if (first >= parts.n_rows) return;
+  for (int h = warp; h < p.group; h += 8) {
+    float m, sum;
+    if (parts.n == 1) {
       const float4 ml = p.part_ml[(2ll * p.ctas + static_cast<long long>(b) * p.nkv + g) * p.group + h];  // the whole head's
-      if (lane == 0) top[h] = ml.x, inv[h] = 1.f / ml.y;
-      continue;
+      m = ml.x, sum = ml.y;
+    } else {
+      m = -INFINITY, sum = 0.f;
+      for (int i = lane; i < parts.n; i += 32) m = fmaxf(m, p.part_ml[parts.slot(p, i, h)].x);
+      m = warp_max(m);
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int i = lane; i < parts.n; i += 32) {
+        const float4 ml = p.part_ml[parts.slot(p, i, h)];
+        sum += exp2_fast(ml.x - base) * ml.y;
+      }
+      sum = warp_sum(sum);
     }
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i, h)].x);
-    m = warp_max(m);
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, any = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-      const float4 ml = p.part_ml[slot(i, h)];
-      const float f = exp2_fast(ml.x - base);
-      factor[h][i] = f;
-      sum += f * ml.y;
-      any += ml.z;
-    }
-    sum = warp_sum(sum);
-    any = warp_sum(any);
-    if (lane == 0) top[h] = m, inv[h] = 1.f / sum, seen[h] = any > 0.f;
+    if (lane == 0) top[h] = m, inv[h] = 1.f / sum;
   }
   __syncthreads();
-  if (parts > 1 && blockIdx.z == 0) {
-    for (int i = tid; i < p.group * HD; i += kJoin) {
-      const int h = i / HD, d = i % HD;
-      float acc = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < parts; ++c) acc += factor[h][c] * p.part_o[slot(c, h) * HD + d];
-      store_out<BF16>(out, h * p.o_head + d, seen[h] ? acc * inv[h] : 0.f);
-    }
-  }
-  if constexpr (WEIGHTS) {
-    const long long rows = static_cast<long long>(p.width) * p.page;
-    const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
-    // a block's lot of kJoinKeys, and what lies a grid further on
-    for (long long lot = static_cast<long long>(blockIdx.z) * kJoinKeys; lot < n_rows; lot += static_cast<long long>(gridDim.z) * kJoinKeys)
-    for (int i = tid; i < kJoinKeys && lot + i < n_rows; i += kJoin) {
+  const long long rows = static_cast<long long>(p.width) * p.page;
+  const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
+  // a block's lot of kJoinKeys, and what lies a grid further on
+  for (long long lot = first; lot < parts.n_rows; lot += static_cast<long long>(gridDim.z) * kJoinKeys)
+    for (int i = tid; i < kJoinKeys && lot + i < parts.n_rows; i += 256) {
       const int j = static_cast<int>(lot) + i, pi = j / p.page;
       const int page = p.table[static_cast<long long>(b) * p.width + pi];
       if (page < 0 || page >= p.n_pages) continue;
       float w = 0.f;
-      for (int h = 0; h < p.group; ++h) w += exp2_fast(scores[h * rows + j] - top[h] + kLift<BF16>) * inv[h];
+      for (int h = 0; h < p.group; ++h) w += exp2_fast(scores[h * rows + j] - top[h] + lift) * inv[h];
       float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
       *to = p.decay == 0.f ? w : p.decay * *to + w;
     }
-  }
 }
 
-template <class Kern>
-cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, const PagedAttnParams& p, cudaStream_t s) {
+template <class Kern, class... Args>
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -600,7 +730,7 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, const PagedAt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <bool BF16, int HD, int NT, bool WEIGHTS>
@@ -608,10 +738,13 @@ cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   constexpr size_t kSmem = sizeof(Smem<HD, NT>) + 1024;
   static_assert(kSmem <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<BF16, HD, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-  if (e == cudaSuccess) e = launch(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, p, s);
-  const long long rows = static_cast<long long>(p.width) * p.page;
-  const unsigned z = WEIGHTS ? static_cast<unsigned>(rows < 65535ll * kJoinKeys ? (rows + kJoinKeys - 1) / kJoinKeys : 65535) : 1;
-  if (e == cudaSuccess) e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(p.nkv, p.batch, z), kJoin, 0, p, s);
+  if (e == cudaSuccess) e = launch(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, s, p);
+  if (e == cudaSuccess) e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(p.nq, p.batch), HD, 0, s, p);
+  if (WEIGHTS && e == cudaSuccess) {
+    const long long rows = static_cast<long long>(p.width) * p.page;
+    const unsigned z = static_cast<unsigned>(rows < 65535ll * kJoinKeys ? (rows + kJoinKeys - 1) / kJoinKeys : 65535);
+    e = launch(weights_kernel, dim3(p.nkv, p.batch, z), 256, 0, s, p, kLift<BF16>);
+  }
   return e;
 }
 

@@ -3,8 +3,8 @@
 Tolerance of an output, per element, with u = eps / 2 of the element type, A = sum_j p_j |v_j| and n keys:
   - the result is rounded once:                                                    u |o|
   - a weight enters P.V as hi + lo: hi is cut to 8 bits (fp16: 11), lo rounded to as many: off by 2^-7 2^-9 = 2^-16 of
-    the weight (fp16: 2^-10 2^-11 = 2^-21), and 2^-24 for the part that keeps lo from being 0; fp16 weights, 2^14
-    times larger, end at 2^-25: n 2^-39 max|v|
+    the weight (fp16: 2^-10 2^-11 = 2^-21), and 2^-24 for the part that keeps lo from being 0; fp16 weights, 2^7
+    times larger (and the base at most the maximum), end at 2^-25: n 2^-32 max|v|
   - fp32, as the tensor core sums it (an addition may cut at 2^-23 instead of rounding at 2^-24, and aligned products
     once more: 4 times 2^-24): a score is a sum of hd products, off by 4 hd 2^-24 S with S = scale sum |q k|, which
     moves p by that much, in the numerator and the denominator: 8 hd 2^-24 S; the exponent's argument is rounded three
@@ -41,7 +41,7 @@ def attend64(q, k, v, scale=None):
     c32 = 2 * 2.0 ** -22 + (8 * hd * mag + 3 * (8 * mag + 14) + 8 * n) * 2.0 ** -24
     tol = u * o.abs() + (1 + u) * ((2.0 ** -21 if half else 2.0 ** -16) + 2.0 ** -24 + c32) * a
     if half:
-        tol = tol + n * 2.0 ** -39 * vd.abs().amax() + 2.0 ** -25  # and the result's own subnormals
+        tol = tol + n * 2.0 ** -32 * vd.abs().amax() + 2.0 ** -25  # and the result's own subnormals
     w = p.sum(1)
     return o.view(nq, hd), tol.view(nq, hd), w, ((c32 + group * 2.0 ** -24) * p).sum(1)
 
