@@ -108,6 +108,28 @@ inline bool encode4(CUtensorMap* map, bool bf16, const void* base, int hd, const
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
+// Pages [n_pages][nkv][page][hd], dense, in boxes of `box` rows of both halves of
+// the head, which lie one after the other: [half][row][64 elements].
+inline bool encode_pages(CUtensorMap* map, bool bf16, const void* base, int hd, int page, int nkv, int n_pages, int box) {
+  if (!encoder()) return false;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(hd / 64), static_cast<cuuint64_t>(nkv),
+                        static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(hd) * 2;
+  cuuint64_t strides[4] = {row, 128, row * page, row * page * nkv};
+  cuuint32_t size[5] = {64, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(hd / 64), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  auto encode = [&] {
+    return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                     const_cast<void*>(base), dims, strides, size, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // as in encode4: a host thread's first call has no context yet
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
 // Rows and tokens are counted in 32 bits, a block of keys past the last one included.
 constexpr int32_t kMaxRows = 0x7fff0000;
 

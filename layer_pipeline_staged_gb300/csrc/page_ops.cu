@@ -170,9 +170,8 @@ extern "C" int attention_paged_decode(const void* q, const void* k_pages, const 
     p.decay = decay;
     p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
     const bool bf16 = type == LPS_TYPE_BF16;
-    const long long n[3] = {page_size, n_kv_heads, n_pages};
-    const long long kst[3] = {head_dim, static_cast<long long>(page_size) * head_dim, static_cast<long long>(page_size) * head_dim * n_kv_heads};
-    if (!encode4(&p.tmap_k, bf16, k_pages, head_dim, n, kst, p.box, 1) || !encode4(&p.tmap_v, bf16, v_pages, head_dim, n, kst, p.box, 1))
+    if (!encode_pages(&p.tmap_k, bf16, k_pages, head_dim, page_size, n_kv_heads, n_pages, p.box) ||
+        !encode_pages(&p.tmap_v, bf16, v_pages, head_dim, page_size, n_kv_heads, n_pages, p.box))
       return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
     return launched(FN, launch_paged_attn(p, bf16, head_dim, static_cast<cudaStream_t>(stream)));
   });

@@ -43,7 +43,7 @@ cudaError_t launch_rotary(const RotaryParams& p, bool bf16, cudaStream_t s);
 // share of all the tiles (sequence, kv head, 64 keys); what it computes of a
 // head that others share goes to the workspace, and a second kernel joins it.
 struct PagedAttnParams {
-  CUtensorMap tmap_k;          // [n_pages][nkv][page][hd], boxes of `box` rows of 64 elements
+  CUtensorMap tmap_k;          // [n_pages][nkv][page][hd], boxes of `box` rows
   CUtensorMap tmap_v;
   const void* q;               // element (b, h): q + b * q_seq + h * q_head
   void* out;

@@ -25,6 +25,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "page_ops.h"
 #include "ptx.cuh"
 
@@ -52,7 +54,6 @@ constexpr float kLift = BF16 ? 0.0f : 7.0f;
 template <int HD, int NT>
 struct Shape {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kHalf = kTile * 128;             // bytes of 64 keys x 64 elements
   static constexpr int kBytes = kTile * HD * 2;         // K (or V) of a tile
   // Even, so that a stage is always the same team's: a wait for a barrier's phase
   // n by its parity holds only for who knows that phase n - 1 is over, and a team
@@ -60,14 +61,13 @@ struct Shape {
   static constexpr int kStages = HD == 128 ? 4 : 8;
   static_assert(kStages % 2 == 0, "a stage belongs to one team");
   static constexpr int kSlots = HD == 128 && NT == 2 ? 1 : 2;  // pieces on their way out
-  static constexpr int kRow = HD + 4;                   // floats of a head's row in a slot: other banks for other heads
-  static constexpr int kQRow = HD * 2 + 16;             // bytes of a head's row of q, likewise
+  static constexpr int kQRow = HD * 2 + 16;             // bytes of a head's row of q: other banks for other heads
 };
 
 template <int HD, int NT>
 struct Slot {
   using S = Shape<HD, NT>;
-  float o[kConsumers][S::kHeads][S::kRow];
+  float o[kConsumers][NT][HD][8];  // heads side by side, as the fragments hold them
   float m[kConsumers][S::kHeads], l[kConsumers][S::kHeads];
   int seen[kConsumers];            // whether the warp has seen a key
 };
@@ -78,6 +78,7 @@ struct __align__(1024) Smem {
   uint8_t kv[S::kStages][2][S::kBytes];
   uint8_t q[S::kStages][S::kHeads * S::kQRow];  // of the stages that a team's piece begins with
   Slot<HD, NT> slot[S::kSlots];
+  float factor[kWriters][kConsumers][S::kHeads], sum[kWriters][S::kHeads];  // a writer's notes on its piece
   int rows[kPagedBatch];           // of each sequence
   int warp_sum[kThreads / 32];
   int base;                        // first tile of the sequence that the CTA begins in
@@ -86,12 +87,11 @@ struct __align__(1024) Smem {
   uint64_t full[S::kStages], empty[S::kStages], slot_full[S::kSlots], slot_empty[S::kSlots];
 };
 
-__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar,
-                                       uint64_t pol) {
+__device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int y, int z, int w, uint64_t* bar, uint64_t pol) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
-      "%4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(pol)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(y), "r"(0), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(pol)
       : "memory");
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -150,15 +150,6 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& 
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack(float x, float y) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 template <bool BF16>
 __device__ __forceinline__ void store_out(void* out, long long at, float x) {
   if constexpr (BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
@@ -272,6 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     __syncthreads();
   }
+  // sequences without rows: zeros
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (sm.rows[b] == 0)
+      for (int i = tid; i < p.nq * HD; i += kThreads) store_out<BF16>(p.out, b * p.o_seq + i / HD * p.o_head + i % HD, 0.f);
   if (beg >= end) return;
   Walk walk{beg, end, sm.base, sm.first, p.nkv, sm.rows, 0, 0, 0};
   const long long limit = wait_cycles(p.wait_limit);
@@ -282,13 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const uint64_t pol = l2_evict_first();
     const int log_box = 31 - __clz(p.box), log_boxes = 6 - log_box, boxes = 1 << log_boxes;  // boxes of a tile
     const int page_boxes = p.page >> log_box;
-    // a lane's part of a tile: box `bx` of K or V, of one half of the head
-    constexpr int kParts = 2 * (HD / 64);
-    const int bx = lane & (boxes - 1), part = lane >> log_boxes, v = part & 1;
-    const bool carries = part < kParts;
-    uint8_t* const dst = carries ? sm.kv[0][v] + (part >> 1) * S::kHalf + bx * (p.box * 128) : nullptr;
+    // a lane's part of a tile: box `bx` of K or V
+    const int bx = lane & (boxes - 1), v = lane >> log_boxes;
+    const bool carries = v < 2;
+    const int box_bytes = p.box * HD * 2;
+    uint8_t* const dst = carries ? sm.kv[0][v] + bx * box_bytes : nullptr;
     const CUtensorMap* const map = v ? &p.tmap_v : &p.tmap_k;
-    const int x = 64 * (part >> 1);
     const uint32_t all = (1u << boxes) - 1;
     // Pages of 32 boxes of a sequence, one a lane: (page, row in the page). The
     // next lot of a piece, or the first one of the next piece, is on its way while
@@ -325,10 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           const int page = __shfl_sync(0xffffffffu, now.x, from), row = __shfl_sync(0xffffffffu, now.y, from);
           if (lane == 0) {
             sm.valid[stage] = valid == all && (t + 1) * kTile <= n_rows ? kWhole : valid;
-            mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * kParts * p.box * 128 + (with_q ? p.group * HD * 2 : 0));
+            mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * 2 * box_bytes + (with_q ? p.group * HD * 2 : 0));
           }
           __syncwarp();
-          if (carries && (valid >> bx & 1)) tma_4d(dst + stage * (2 * S::kBytes), map, x, row, walk.g, page, &sm.full[stage], pol);
+          if (carries && (valid >> bx & 1)) tma_5d(dst + stage * (2 * S::kBytes), map, row, walk.g, page, &sm.full[stage], pol);
           if (with_q && lane < p.group)
             bulk_g2s_plain(sm.q[stage] + lane * S::kQRow,
                            static_cast<const char*>(p.q) + 2 * (walk.b * p.q_seq + static_cast<long long>(walk.g * p.group + lane) * p.q_head),
@@ -362,42 +356,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
       alive = __all_sync(0xffffffffu, alive);
       const Slot<HD, NT>& in = sm.slot[sl];
-      const bool mine = lane >= w0 && lane < w1;  // lane = warp of the piece
-      const bool seen = __any_sync(0xffffffffu, mine && in.seen[lane & 7]);
       const bool whole = n == walk.tiles();
       const long long part = (static_cast<long long>(blockIdx.x) * 2 + (piece ? 1 : 0)) * p.group;
-      for (int h = warp - kConsumers - kProducers; alive && h < p.group; h += kWriters) {
-        const float m = mine ? in.m[lane][h] : -INFINITY;
-        const float top = warp_max(m), base = top == -INFINITY ? 0.f : top;
-        const float f = exp2_fast(m - base);
-        const float sum = warp_sum(mine ? f * in.l[lane][h] : 0.f);
-        constexpr int kEach = HD / 32;  // elements of a lane
-        float acc[kEach];
+      const int wr = warp - kConsumers - kProducers;
+      const bool seen = __any_sync(0xffffffffu, lane >= w0 && lane < w1 && in.seen[lane & 7]);
+      // lane = (head, warps w and w + 4): the bases meet, and with them what each warp's part counts
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
-        for (int w = w0; w < w1; ++w) {
-          const float fw = __shfl_sync(0xffffffffu, f, w);
-          const float* row = in.o[w][h] + lane * kEach;
-          if constexpr (kEach == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(row);
-            acc[0] += fw * x.x, acc[1] += fw * x.y, acc[2] += fw * x.z, acc[3] += fw * x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(row);
-            acc[0] += fw * x.x, acc[1] += fw * x.y;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = 8 * nt + (lane & 7), w = lane >> 3;
+        const bool on0 = w >= w0 && w < w1, on1 = w + 4 >= w0 && w + 4 < w1;
+        const float m0 = on0 ? in.m[w][h] : -INFINITY, m1 = on1 ? in.m[w + 4][h] : -INFINITY;
+        float top = fmaxf(m0, m1);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2_fast(m0 - base), f1 = exp2_fast(m1 - base);
+        float sum = (on0 ? f0 * in.l[w][h] : 0.f) + (on1 ? f1 * in.l[w + 4][h] : 0.f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        sm.factor[wr][w][h] = f0;
+        sm.factor[wr][w + 4][h] = f1;
+        if (w == 0) {
+          sm.sum[wr][h] = sum;
+          const float4 ml = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
+          if (alive && wr == 0 && h < p.group) {
+            if (!whole) p.part_ml[part + h] = ml;
+            else if (WEIGHTS) p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = ml;
           }
         }
-        if (whole) {
-          const int head = walk.g * p.group + h;
-          uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<char*>(p.out) + 2 * (walk.b * p.o_seq + head * p.o_head + lane * kEach));
+      }
+      __syncwarp();
+      // lane = elements d, a writer its half of them, four heads at a time
+      constexpr int kEach = HD / kWriters / 32;
 #pragma unroll
-          for (int e = 0; e < kEach; e += 2) to[e / 2] = pack<BF16>(seen ? acc[e] / sum : 0.f, seen ? acc[e + 1] / sum : 0.f);
-          if (WEIGHTS && lane == 0)
-            p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = make_float4(top, sum, 1.f, 0.f);
-        } else {
-          float* to = p.part_o + (part + h) * HD + lane * kEach;
+      for (int h0 = 0; h0 < 8 * NT; h0 += 4) {
+        if (!alive || h0 >= p.group) break;
+        float acc[kEach][4];
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) to[e] = acc[e];
-          if (lane == 0) p.part_ml[part + h] = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
+        for (int e = 0; e < kEach; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+        for (int w = w0; w < w1; ++w) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.factor[wr][w][h0]);
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            const float4 x = *reinterpret_cast<const float4*>(&in.o[w][h0 / 8][(wr * kEach + e) * 32 + lane][h0 % 8]);
+            acc[e][0] += f.x * x.x, acc[e][1] += f.y * x.y, acc[e][2] += f.z * x.z, acc[e][3] += f.w * x.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int h = h0 + j;
+          if (h >= p.group) break;
+          const float sum = sm.sum[wr][h];
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            const int d = (wr * kEach + e) * 32 + lane;
+            if (whole) store_out<BF16>(p.out, walk.b * p.o_seq + (walk.g * p.group + h) * p.o_head + d, seen ? acc[e][j] / sum : 0.f);
+            else p.part_o[(part + h) * HD + d] = acc[e][j];
+          }
         }
       }
       __syncwarp();
@@ -410,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const int team = warp >> 2, row0 = (warp & 3) * 16;  // the team's tiles, the warp's keys in a tile
   const int g8 = lane >> 2, t4 = lane & 3;             // fragment coordinates
   const int mtx = lane >> 3, r8 = lane & 7;            // ldmatrix: matrix and row of the lane's address
-  const int box_shift = 31 - __clz(p.box);
+  // A box lies as [half of the head][row][128 bytes], its 16-byte units swizzled by the row
+  const int box_shift = 31 - __clz(p.box), half = p.box * 128;
+  auto place = [&](int row) { return (row >> box_shift) * (p.box * HD * 2) + (row & (p.box - 1)) * 128; };
+  const int k_row = place(row0 + (mtx & 1) * 8 + r8), v_row = place(row0 + (mtx >> 1) * 8 + r8);
   bool alive = true;
   int it = 0;
   for (int piece = 0; walk.next(); ++piece) {
@@ -454,31 +472,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int c = lane; c < 16 * (HD / 8); c += 32) {
           const int r = c / (HD / 8), ch = c % (HD / 8);
           if (!(keys >> r & 1))
-            *reinterpret_cast<uint4*>(sm.kv[stage][1] + (ch / 8) * S::kHalf + (row0 + r) * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm.kv[stage][1] + place(row0 + r) + (ch / 8) * half + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
       }
       if (keys) {
         any = true;
-        const uint32_t kbase = smem_u32(sm.kv[stage][0]), vbase = smem_u32(sm.kv[stage][1]);
+        const uint32_t kbase = smem_u32(sm.kv[stage][0]) + k_row, vbase = smem_u32(sm.kv[stage][1]) + v_row;
         // S^T in two chains
         float s[NT][4], s2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-        {
-          const int r = row0 + (mtx & 1) * 8 + r8;
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; kk += 2) {
-            uint32_t a[4], c[4];
-            ldsm_x4(kbase + (kk / 4) * S::kHalf + r * 128 + (((2 * (kk % 4) + (mtx >> 1)) ^ r8) << 4), a);
-            ldsm_x4(kbase + (kk / 4) * S::kHalf + r * 128 + (((2 * (kk % 4) + 2 + (mtx >> 1)) ^ r8) << 4), c);
+        for (int kk = 0; kk < HD / 16; kk += 2) {
+          uint32_t a[4], c[4];
+          ldsm_x4(kbase + (kk / 4) * half + (((2 * (kk % 4) + (mtx >> 1)) ^ r8) << 4), a);
+          ldsm_x4(kbase + (kk / 4) * half + (((2 * (kk % 4) + 2 + (mtx >> 1)) ^ r8) << 4), c);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<BF16>(s[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
-              mma<BF16>(s2[nt], c, qb[kk + 1][nt][0], qb[kk + 1][nt][1]);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<BF16>(s[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+            mma<BF16>(s2[nt], c, qb[kk + 1][nt][0], qb[kk + 1][nt][1]);
           }
         }
         bool above = false;
@@ -536,11 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           ph[nt][0] = transposed(h0), ph[nt][1] = transposed(h1);
           pl[nt][0] = transposed(l0), pl[nt][1] = transposed(l1);
         }
-        const int r = row0 + (mtx >> 1) * 8 + r8;
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d) {
           uint32_t a[4];
-          ldsm_x4_t(vbase + (d / 4) * S::kHalf + r * 128 + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
+          ldsm_x4_t(vbase + (d / 4) * half + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma<BF16>(o[nt][d], a, ph[nt][0], ph[nt][1]);
@@ -563,23 +577,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     Slot<HD, NT>& out = sm.slot[sl];
     if (skip < n_tiles) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) {
+          *reinterpret_cast<float2*>(&out.o[warp][nt][16 * d + g8][2 * t4]) = make_float2(o[nt][d][0], o[nt][d][1]);
+          *reinterpret_cast<float2*>(&out.o[warp][nt][16 * d + g8 + 8][2 * t4]) = make_float2(o[nt][d][2], o[nt][d][3]);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float sum = l[nt][c];
           sum += __shfl_xor_sync(0xffffffffu, sum, 4);
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-          const int h = 8 * nt + 2 * t4 + c;
-          if (g8 == 0) out.m[warp][h] = m[nt][c], out.l[warp][h] = sum;
-          if (h < p.group) {
-#pragma unroll
-            for (int d = 0; d < HD / 16; ++d) {
-              out.o[warp][h][16 * d + g8] = o[nt][d][c];
-              out.o[warp][h][16 * d + g8 + 8] = o[nt][d][2 + c];
-            }
-          }
+          if (g8 == 0) out.m[warp][8 * nt + 2 * t4 + c] = m[nt][c], out.l[warp][8 * nt + 2 * t4 + c] = sum;
         }
+      }
       if (lane == 0) out.seen[warp] = any;
     }
     __syncwarp();
@@ -587,135 +599,174 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
 }
 
+constexpr int kJoin = 256;         // threads of the join
 constexpr int kJoinKeys = 1024;    // keys of a block that sums key weights
 constexpr int kAhead = 16;         // parts that a thread of the join asks for at once
 
-// The parts of head (b, g), found from the lengths alone.
+// The parts of a head that several CTAs share.
 struct Parts {
-  int n_rows, c0, n;  // n: 0 where there are no rows
-  bool shifted;       // the first part is not its CTA's first piece
+  int b, g, n_rows, c0, n;  // n: 1 where one CTA has it whole, 0 where there is none
+  bool shifted;             // the first part is not its CTA's first piece
   __device__ __forceinline__ long long slot(const PagedAttnParams& p, int i, int h) const {
     return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h;
   }
 };
-template <int THREADS>
-__device__ __forceinline__ Parts parts_of(const PagedAttnParams& p, int b, int g) {
-  __shared__ int sums[2][THREADS / 32];
-  const int tid = threadIdx.x;
-  int before = 0, total = 0;
-  for (int i = tid; i < p.batch; i += THREADS) {
-    const int n = (rows_of(p, i) + kTile - 1) / kTile;
-    total += n;
-    if (i < b) before += n;
-  }
+
+// With split >= 0: the head that begins in CTA split's share and ends in another's
+// (n > 1, else n is 0). Otherwise the head (b, g). From the lengths alone.
+__device__ __forceinline__ Parts parts_of(const PagedAttnParams& p, int split, int b, int g) {
+  __shared__ int warp_sum[kJoin / 32], found[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + kJoin - 1) / kJoin, lo = min(tid * per, p.batch), hi = min(lo + per, p.batch);
+  int mine = 0;
+  for (int i = lo; i < hi; ++i) mine += (rows_of(p, i) + kTile - 1) / kTile;
+  mine *= p.nkv;
+  int incl = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-  if ((tid & 31) == 0) sums[0][tid >> 5] = before, sums[1][tid >> 5] = total;
+  if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  before = total = 0;
+  int before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) before += sums[0][w], total += sums[1][w];
-  Parts parts{rows_of(p, b), 0, 0, false};
-  const int n = (parts.n_rows + kTile - 1) / kTile;
-  if (n) {
-    const Shares shares(total * p.nkv, p.ctas);
-    const int i0 = before * p.nkv + g * n;
-    parts.c0 = shares.owner(i0);
-    parts.n = shares.owner(i0 + n - 1) - parts.c0 + 1;
-    parts.shifted = shares.start(parts.c0) < i0;
+  for (int w = 0; w < kJoin / 32; ++w) {
+    if (w == warp) before = total;
+    total += warp_sum[w];
   }
+  const Shares shares(total, p.ctas);
+  int at = before + incl - mine;  // the first tile of sequence lo
+  const int tile = split >= 0 ? (split + 1 < shares.ctas ? shares.start(split + 1) : 0) - 1 : 0;  // the last one of the CTA's share
+  if (split >= 0 ? tile >= at && tile < at + mine : lo <= b && b < hi) {
+    for (int i = lo; i < hi; ++i) {
+      const int n = p.nkv * ((rows_of(p, i) + kTile - 1) / kTile);
+      if (split >= 0 ? tile < at + n : i == b) {
+        found[0] = i, found[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Parts parts{b, g, 0, 0, 0, false};
+  if (split >= 0) {
+    if (tile < 0) return parts;
+    parts.b = found[0];
+  }
+  parts.n_rows = rows_of(p, parts.b);
+  const int n = (parts.n_rows + kTile - 1) / kTile;
+  if (n == 0) return parts;
+  if (split >= 0) parts.g = (tile - found[1]) / n;
+  const int i0 = found[1] + parts.g * n;
+  if (split >= 0 && (i0 < shares.start(split) || i0 + n - 1 <= tile)) return parts;
+  parts.c0 = split >= 0 ? split : shares.owner(i0);
+  parts.n = shares.owner(i0 + n - 1) - parts.c0 + 1;
+  parts.shifted = shares.start(parts.c0) < i0;
   return parts;
 }
 
-// Block = (query head, sequence), thread = element: the parts of a head that
-// several CTAs have computed, in their order; zeros where the sequence has no
-// rows. All a thread reads is asked for at once, the parts' bases with their o.
+// Block (CTA c, query head of the group): of the head that begins in CTA c's share
+// and ends in another's, the parts in their order. All that a thread reads is asked
+// for at once, the parts' bases with their o. With key weights, the other blocks:
+// (sequence, kv head, a share of the cached rows), the rows' weights over the
+// group's heads into the pages' entries.
 template <bool BF16, int HD, bool WEIGHTS>
-__global__ void __launch_bounds__(HD) join_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ PagedAttnParams p, int key_blocks) {
   pdl_launch_dependents();
-  const int tid = threadIdx.x, head = blockIdx.x, b = blockIdx.y, g = head / p.group, h = head - g * p.group;
-  const Parts parts = parts_of<HD>(p, b, g);
-  const long long at = b * p.o_seq + head * p.o_head + tid;
-  pdl_wait();
-  if (parts.n == 1) return;
-  if (parts.n == 0) {
-    store_out<BF16>(p.out, at, 0.f);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int joins = p.ctas * p.group;
+  if (!WEIGHTS || static_cast<int>(blockIdx.x) < joins) {
+    constexpr int kSlices = kJoin / HD;  // threads of an element, each with every kSlices-th part
+    __shared__ float slice[kSlices][HD], slice_top[kSlices], slice_sum[kSlices], slice_seen[kSlices];
+    const int h = blockIdx.x % p.group, d = tid % HD, sl = tid / HD;
+    const Parts parts = parts_of(p, blockIdx.x / p.group, 0, 0);
+    pdl_wait();
+    if (parts.n == 0) return;
+    float top = -INFINITY, sum = 0.f, acc = 0.f, seen = 0.f;
+    for (int i0 = sl; i0 < parts.n; i0 += kAhead * kSlices) {
+      float4 ml[kAhead];
+      float o[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int part = i0 + i * kSlices;
+        const bool on = part < parts.n;
+        const long long s = parts.slot(p, on ? part : 0, h);
+        ml[i] = on ? __ldcg(p.part_ml + s) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        o[i] = on ? __ldcg(p.part_o + s * HD + d) : 0.f;
+      }
+      float now = top;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) now = fmaxf(now, ml[i].x);
+      const float base = now == -INFINITY ? 0.f : now;
+      const float f = exp2_fast(top - base);
+      sum *= f, acc *= f, top = now;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i * kSlices >= parts.n) break;
+        const float w = exp2_fast(ml[i].x - base);
+        sum += w * ml[i].y;
+        acc += w * o[i];
+        seen += ml[i].z;
+      }
+    }
+    slice[sl][d] = acc;
+    if (d == 0) slice_top[sl] = top, slice_sum[sl] = sum, slice_seen[sl] = seen;
+    __syncthreads();
+    if (sl) return;
+    for (int i = 1; i < kSlices; ++i) top = fmaxf(top, slice_top[i]);
+    const float base = top == -INFINITY ? 0.f : top;
+    sum = acc = seen = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i) {
+      const float f = exp2_fast(slice_top[i] - base);
+      sum += f * slice_sum[i];
+      acc += f * slice[i][d];
+      seen += slice_seen[i];
+    }
+    store_out<BF16>(p.out, parts.b * p.o_seq + (parts.g * p.group + h) * p.o_head + d, seen > 0.f ? acc / sum : 0.f);
     return;
   }
-  float top = -INFINITY, sum = 0.f, acc = 0.f, seen = 0.f;
-  for (int i0 = 0; i0 < parts.n; i0 += kAhead) {
-    float4 ml[kAhead];
-    float o[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const bool on = i0 + i < parts.n;
-      const long long s = parts.slot(p, on ? i0 + i : 0, h);
-      ml[i] = on ? __ldcg(p.part_ml + s) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      o[i] = on ? __ldcg(p.part_o + s * HD + tid) : 0.f;
-    }
-    float now = top;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) now = fmaxf(now, ml[i].x);
-    const float base = now == -INFINITY ? 0.f : now;
-    const float f = exp2_fast(top - base);
-    sum *= f, acc *= f, top = now;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (i0 + i >= parts.n) break;
-      const float w = exp2_fast(ml[i].x - base);
-      sum += w * ml[i].y;
-      acc += w * o[i];
-      seen += ml[i].z;
-    }
-  }
-  store_out<BF16>(p.out, at, seen > 0.f ? acc / sum : 0.f);
-}
-
-// Block = (kv head, sequence, a share of the cached rows): the rows' weights over
-// the group's heads, into the pages' entries.
-__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ PagedAttnParams p, float lift) {
-  __shared__ float top[kMaxGroup], inv[kMaxGroup];
-  pdl_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
-  const Parts parts = parts_of<256>(p, b, g);
-  const int first = static_cast<int>(blockIdx.z) * kJoinKeys;
-  pdl_wait();
-  if (first >= parts.n_rows) return;
-  for (int h = warp; h < p.group; h += 8) {
-    float m, sum;
-    if (parts.n == 1) {
-      const float4 ml = p.part_ml[(2ll * p.ctas + static_cast<long long>(b) * p.nkv + g) * p.group + h];  // the whole head's
-      m = ml.x, sum = ml.y;
-    } else {
-      m = -INFINITY, sum = 0.f;
-      for (int i = lane; i < parts.n; i += 32) m = fmaxf(m, p.part_ml[parts.slot(p, i, h)].x);
-      m = warp_max(m);
-      const float base = m == -INFINITY ? 0.f : m;
-      for (int i = lane; i < parts.n; i += 32) {
-        const float4 ml = p.part_ml[parts.slot(p, i, h)];
-        sum += exp2_fast(ml.x - base) * ml.y;
+  if constexpr (WEIGHTS) {
+    __shared__ float top[kMaxGroup], inv[kMaxGroup];
+    const int z = (blockIdx.x - joins) % key_blocks, y = (blockIdx.x - joins) / key_blocks;
+    const Parts parts = parts_of(p, -1, y / p.nkv, y % p.nkv);
+    pdl_wait();
+    const long long first = static_cast<long long>(z) * kJoinKeys;
+    if (first >= parts.n_rows) return;
+    for (int h = warp; h < p.group; h += kJoin / 32) {
+      float m, sum;
+      if (parts.n == 1) {
+        const float4 ml = __ldcg(p.part_ml + (2ll * p.ctas + y) * p.group + h);  // the whole head's
+        m = ml.x, sum = ml.y;
+      } else {
+        m = -INFINITY, sum = 0.f;
+        for (int i = lane; i < parts.n; i += 32) m = fmaxf(m, __ldcg(p.part_ml + parts.slot(p, i, h)).x);
+        m = warp_max(m);
+        const float base = m == -INFINITY ? 0.f : m;
+        for (int i = lane; i < parts.n; i += 32) {
+          const float4 ml = __ldcg(p.part_ml + parts.slot(p, i, h));
+          sum += exp2_fast(ml.x - base) * ml.y;
+        }
+        sum = warp_sum(sum);
       }
-      sum = warp_sum(sum);
+      if (lane == 0) top[h] = m, inv[h] = 1.f / sum;
     }
-    if (lane == 0) top[h] = m, inv[h] = 1.f / sum;
+    __syncthreads();
+    const long long rows = static_cast<long long>(p.width) * p.page;
+    const float* scores = p.scores + (static_cast<long long>(parts.b) * p.nq + parts.g * p.group) * rows;
+    // the block's lot of kJoinKeys, and what lies key_blocks further on
+    for (long long lot = first; lot < parts.n_rows; lot += static_cast<long long>(key_blocks) * kJoinKeys)
+      for (int i = tid; i < kJoinKeys && lot + i < parts.n_rows; i += kJoin) {
+        const int j = static_cast<int>(lot) + i, pi = j / p.page;
+        const int page = p.table[static_cast<long long>(parts.b) * p.width + pi];
+        if (page < 0 || page >= p.n_pages) continue;
+        float w = 0.f;
+        for (int h = 0; h < p.group; ++h) w += exp2_fast(__ldcg(scores + h * rows + j) - top[h] + kLift<BF16>) * inv[h];
+        float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + parts.g) * p.page + (j - pi * p.page);
+        *to = p.decay == 0.f ? w : p.decay * *to + w;
+      }
   }
-  __syncthreads();
-  const long long rows = static_cast<long long>(p.width) * p.page;
-  const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
-  // a block's lot of kJoinKeys, and what lies a grid further on
-  for (long long lot = first; lot < parts.n_rows; lot += static_cast<long long>(gridDim.z) * kJoinKeys)
-    for (int i = tid; i < kJoinKeys && lot + i < parts.n_rows; i += 256) {
-      const int j = static_cast<int>(lot) + i, pi = j / p.page;
-      const int page = p.table[static_cast<long long>(b) * p.width + pi];
-      if (page < 0 || page >= p.n_pages) continue;
-      float w = 0.f;
-      for (int h = 0; h < p.group; ++h) w += exp2_fast(scores[h * rows + j] - top[h] + lift) * inv[h];
-      float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
-      *to = p.decay == 0.f ? w : p.decay * *to + w;
-    }
 }
 
 template <class Kern, class... Args>
@@ -739,12 +790,12 @@ cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   static_assert(kSmem <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<BF16, HD, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e == cudaSuccess) e = launch(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, s, p);
-  if (e == cudaSuccess) e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(p.nq, p.batch), HD, 0, s, p);
-  if (WEIGHTS && e == cudaSuccess) {
-    const long long rows = static_cast<long long>(p.width) * p.page;
-    const unsigned z = static_cast<unsigned>(rows < 65535ll * kJoinKeys ? (rows + kJoinKeys - 1) / kJoinKeys : 65535);
-    e = launch(weights_kernel, dim3(p.nkv, p.batch, z), 256, 0, s, p, kLift<BF16>);
-  }
+  if (e != cudaSuccess) return e;
+  // blocks for the keys of every head that the tables have room for, in a bounded grid
+  const long long heads = static_cast<long long>(p.batch) * p.nkv, rows = static_cast<long long>(p.width) * p.page;
+  const long long lots = (rows + kJoinKeys - 1) / kJoinKeys, most = std::max(1ll, (1ll << 15) / heads);
+  const int key_blocks = WEIGHTS ? static_cast<int>(std::min(lots, most)) : 0;
+  e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(static_cast<unsigned>(p.ctas * p.group + heads * key_blocks)), kJoin, 0, s, p, key_blocks);
   return e;
 }
 
