@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "page_ops.h"
 #include "ptx.cuh"
@@ -221,8 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   // heads that the group does not have are columns of zeros
   for (int i = tid; i < static_cast<int>(sizeof sm.q) / 16; i += kThreads) reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the copies' bytes
-  // what the stream ran before is done when the join is let start: it may read
-  // the lengths at once, and only the parts behind its own wait
   pdl_wait();
   pdl_launch_dependents();
 
@@ -254,13 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const Shares shares(total, p.ctas);
     beg = end = total;
     if (static_cast<int>(blockIdx.x) < shares.ctas) beg = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
+    // the sequences in which the share begins and ends; what the join needs to know
     int at = before + incl - mine;
-    if (beg < end && beg >= at && beg < at + mine) {
-      int b = lo;
-      for (int n; n = p.nkv * ((sm.rows[b] + kTile - 1) / kTile), beg >= at + n; ++b) at += n;
-      sm.first = b;
-      sm.base = at;
+    const bool begins = beg < end && beg >= at && beg < at + mine, ends = beg < end && end - 1 >= at && end - 1 < at + mine;
+    if (begins || ends || (blockIdx.x == 0 && WEIGHTS)) {
+      for (int b = lo; b < hi; ++b) {
+        const int tiles = (sm.rows[b] + kTile - 1) / kTile, n = p.nkv * tiles;
+        if (WEIGHTS && blockIdx.x == 0) p.first_tile[b] = at;
+        if (begins && beg >= at && beg < at + n) sm.first = b, sm.base = at;
+        if (ends && end - 1 >= at && end - 1 < at + n) {
+          const int g = (end - 1 - at) / tiles, i0 = at + g * tiles, i1 = i0 + tiles;
+          const bool split = i0 >= beg && i1 > end;  // a head that begins here and ends elsewhere
+          p.border[blockIdx.x] = make_int4(b, g, split ? shares.owner(i1 - 1) - blockIdx.x + 1 : 0, beg < i0);
+        }
+        at += n;
+      }
     }
+    if (beg >= end && tid == 0) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (WEIGHTS && blockIdx.x == 0 && tid == 0) p.first_tile[p.batch] = total;
     __syncthreads();
   }
   // sequences without rows: zeros
@@ -394,24 +404,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         float acc[kEach][4];
 #pragma unroll
         for (int e = 0; e < kEach; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
-        for (int w = w0; w < w1; ++w) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.factor[wr][w][h0]);
+        for (int w = w0; w < w1; w += kConsumers / 2) {  // a team's warps
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            const float4 x = *reinterpret_cast<const float4*>(&in.o[w][h0 / 8][(wr * kEach + e) * 32 + lane][h0 % 8]);
-            acc[e][0] += f.x * x.x, acc[e][1] += f.y * x.y, acc[e][2] += f.z * x.z, acc[e][3] += f.w * x.w;
+          for (int j = 0; j < kConsumers / 2; ++j) {
+            const float4 f = *reinterpret_cast<const float4*>(&sm.factor[wr][w + j][h0]);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              const float4 x = *reinterpret_cast<const float4*>(&in.o[w + j][h0 / 8][(wr * kEach + e) * 32 + lane][h0 % 8]);
+              acc[e][0] += f.x * x.x, acc[e][1] += f.y * x.y, acc[e][2] += f.z * x.z, acc[e][3] += f.w * x.w;
+            }
           }
         }
+        const int d = wr * kEach * 32 + lane;
+        if (whole) {
+          const long long to = walk.b * p.o_seq + (walk.g * p.group + h0) * p.o_head + d;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = h0 + j;
-          if (h >= p.group) break;
-          const float sum = sm.sum[wr][h];
+          for (int j = 0; j < 4; ++j) {
+            if (h0 + j >= p.group) break;
+            const float inv = seen ? 1.f / sm.sum[wr][h0 + j] : 0.f;  // nothing seen: o is 0
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) {
-            const int d = (wr * kEach + e) * 32 + lane;
-            if (whole) store_out<BF16>(p.out, walk.b * p.o_seq + (walk.g * p.group + h) * p.o_head + d, seen ? acc[e][j] / sum : 0.f);
-            else p.part_o[(part + h) * HD + d] = acc[e][j];
+            for (int e = 0; e < kEach; ++e) store_out<BF16>(p.out, to + j * p.o_head + 32 * e, acc[e][j] * inv);
+          }
+        } else {
+          float* to = p.part_o + (part + h0) * HD + d;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (h0 + j >= p.group) break;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) to[j * HD + 32 * e] = acc[e][j];
           }
         }
       }
@@ -468,13 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       if (alive && valid != kWhole) {
         const int mine = lane & 15;
         keys = __ballot_sync(0xffffffffu, key0 + mine < walk.rows[b] && (valid >> ((row0 + mine) >> box_shift) & 1)) & 0xffffu;
-        // what lies in the other rows is of no sequence, and 0 x inf is not 0
-        for (int c = lane; c < 16 * (HD / 8); c += 32) {
-          const int r = c / (HD / 8), ch = c % (HD / 8);
-          if (!(keys >> r & 1))
-            *reinterpret_cast<uint4*>(sm.kv[stage][1] + place(row0 + r) + (ch / 8) * half + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
       }
       if (keys) {
         any = true;
@@ -551,18 +564,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           ph[nt][0] = transposed(h0), ph[nt][1] = transposed(h1);
           pl[nt][0] = transposed(l0), pl[nt][1] = transposed(l1);
         }
+        // what lies in the rows that are no keys is of no sequence, and 0 x inf is
+        // not 0: where there are such rows, V's fragments lose them
+        auto products = [&](auto some) {
+          const uint32_t k01 = keys >> (2 * t4), k89 = k01 >> 8;
+          const uint32_t lo = (k01 & 1 ? 0xffffu : 0u) | (k01 & 2 ? 0xffff0000u : 0u), hi = (k89 & 1 ? 0xffffu : 0u) | (k89 & 2 ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int d = 0; d < HD / 16; ++d) {
-          uint32_t a[4];
-          ldsm_x4_t(vbase + (d / 4) * half + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
+          for (int d = 0; d < HD / 16; ++d) {
+            uint32_t a[4];
+            ldsm_x4_t(vbase + (d / 4) * half + (((2 * (d % 4) + (mtx & 1)) ^ r8) << 4), a);
+            if constexpr (decltype(some)::value) a[0] &= lo, a[1] &= lo, a[2] &= hi, a[3] &= hi;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<BF16>(o[nt][d], a, ph[nt][0], ph[nt][1]);
-            mma<BF16>(o[nt][d], a, pl[nt][0], pl[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<BF16>(o[nt][d], a, ph[nt][0], ph[nt][1]);
+              mma<BF16>(o[nt][d], a, pl[nt][0], pl[nt][1]);
+            }
           }
-        }
+        };
+        if (keys == 0xffffu) products(std::false_type{});
+        else products(std::true_type{});
       }
-      if (valid != kWhole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the next copy's bytes
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[stage]);
     }
@@ -603,67 +624,9 @@ constexpr int kJoin = 256;         // threads of the join
 constexpr int kJoinKeys = 1024;    // keys of a block that sums key weights
 constexpr int kAhead = 16;         // parts that a thread of the join asks for at once
 
-// The parts of a head that several CTAs share.
-struct Parts {
-  int b, g, n_rows, c0, n;  // n: 1 where one CTA has it whole, 0 where there is none
-  bool shifted;             // the first part is not its CTA's first piece
-  __device__ __forceinline__ long long slot(const PagedAttnParams& p, int i, int h) const {
-    return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h;
-  }
-};
-
-// With split >= 0: the head that begins in CTA split's share and ends in another's
-// (n > 1, else n is 0). Otherwise the head (b, g). From the lengths alone.
-__device__ __forceinline__ Parts parts_of(const PagedAttnParams& p, int split, int b, int g) {
-  __shared__ int warp_sum[kJoin / 32], found[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.batch + kJoin - 1) / kJoin, lo = min(tid * per, p.batch), hi = min(lo + per, p.batch);
-  int mine = 0;
-  for (int i = lo; i < hi; ++i) mine += (rows_of(p, i) + kTile - 1) / kTile;
-  mine *= p.nkv;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) {
-    if (w == warp) before = total;
-    total += warp_sum[w];
-  }
-  const Shares shares(total, p.ctas);
-  int at = before + incl - mine;  // the first tile of sequence lo
-  const int tile = split >= 0 ? (split + 1 < shares.ctas ? shares.start(split + 1) : 0) - 1 : 0;  // the last one of the CTA's share
-  if (split >= 0 ? tile >= at && tile < at + mine : lo <= b && b < hi) {
-    for (int i = lo; i < hi; ++i) {
-      const int n = p.nkv * ((rows_of(p, i) + kTile - 1) / kTile);
-      if (split >= 0 ? tile < at + n : i == b) {
-        found[0] = i, found[1] = at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-  Parts parts{b, g, 0, 0, 0, false};
-  if (split >= 0) {
-    if (tile < 0) return parts;
-    parts.b = found[0];
-  }
-  parts.n_rows = rows_of(p, parts.b);
-  const int n = (parts.n_rows + kTile - 1) / kTile;
-  if (n == 0) return parts;
-  if (split >= 0) parts.g = (tile - found[1]) / n;
-  const int i0 = found[1] + parts.g * n;
-  if (split >= 0 && (i0 < shares.start(split) || i0 + n - 1 <= tile)) return parts;
-  parts.c0 = split >= 0 ? split : shares.owner(i0);
-  parts.n = shares.owner(i0 + n - 1) - parts.c0 + 1;
-  parts.shifted = shares.start(parts.c0) < i0;
-  return parts;
+// The place of part i of a head that begins in CTA c0's share, for its query head h.
+__device__ __forceinline__ long long part_slot(const PagedAttnParams& p, int c0, bool shifted, int i, int h) {
+  return (2ll * (c0 + i) + (i == 0 && shifted ? 1 : 0)) * p.group + h;
 }
 
 // Block (CTA c, query head of the group): of the head that begins in CTA c's share
@@ -680,18 +643,20 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
     constexpr int kSlices = kJoin / HD;  // threads of an element, each with every kSlices-th part
     __shared__ float slice[kSlices][HD], slice_top[kSlices], slice_sum[kSlices], slice_seen[kSlices];
     const int h = blockIdx.x % p.group, d = tid % HD, sl = tid / HD;
-    const Parts parts = parts_of(p, blockIdx.x / p.group, 0, 0);
+    const int c0 = blockIdx.x / p.group;
     pdl_wait();
-    if (parts.n == 0) return;
+    const int4 border = __ldcg(p.border + c0);
+    const int n = border.z;
+    if (n == 0) return;
     float top = -INFINITY, sum = 0.f, acc = 0.f, seen = 0.f;
-    for (int i0 = sl; i0 < parts.n; i0 += kAhead * kSlices) {
+    for (int i0 = sl; i0 < n; i0 += kAhead * kSlices) {
       float4 ml[kAhead];
       float o[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int part = i0 + i * kSlices;
-        const bool on = part < parts.n;
-        const long long s = parts.slot(p, on ? part : 0, h);
+        const bool on = part < n;
+        const long long s = part_slot(p, c0, border.w, on ? part : 0, h);
         ml[i] = on ? __ldcg(p.part_ml + s) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         o[i] = on ? __ldcg(p.part_o + s * HD + d) : 0.f;
       }
@@ -703,7 +668,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
       sum *= f, acc *= f, top = now;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (i0 + i * kSlices >= parts.n) break;
+        if (i0 + i * kSlices >= n) break;
         const float w = exp2_fast(ml[i].x - base);
         sum += w * ml[i].y;
         acc += w * o[i];
@@ -724,28 +689,33 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
       acc += f * slice[i][d];
       seen += slice_seen[i];
     }
-    store_out<BF16>(p.out, parts.b * p.o_seq + (parts.g * p.group + h) * p.o_head + d, seen > 0.f ? acc / sum : 0.f);
+    store_out<BF16>(p.out, border.x * p.o_seq + (border.y * p.group + h) * p.o_head + d, seen > 0.f ? acc / sum : 0.f);
     return;
   }
   if constexpr (WEIGHTS) {
     __shared__ float top[kMaxGroup], inv[kMaxGroup];
     const int z = (blockIdx.x - joins) % key_blocks, y = (blockIdx.x - joins) / key_blocks;
-    const Parts parts = parts_of(p, -1, y / p.nkv, y % p.nkv);
-    pdl_wait();
+    const int b = y / p.nkv, g = y - b * p.nkv;
     const long long first = static_cast<long long>(z) * kJoinKeys;
-    if (first >= parts.n_rows) return;
+    pdl_wait();
+    const int n_rows = rows_of(p, b), total = __ldcg(p.first_tile + p.batch), tiles = (n_rows + kTile - 1) / kTile;
+    const int i0 = __ldcg(p.first_tile + b) + g * tiles;
+    if (first >= n_rows) return;
+    const Shares shares(total, p.ctas);
+    const int c0 = shares.owner(i0), n = shares.owner(i0 + tiles - 1) - c0 + 1;
+    const bool shifted = shares.start(c0) < i0;
     for (int h = warp; h < p.group; h += kJoin / 32) {
       float m, sum;
-      if (parts.n == 1) {
+      if (n == 1) {
         const float4 ml = __ldcg(p.part_ml + (2ll * p.ctas + y) * p.group + h);  // the whole head's
         m = ml.x, sum = ml.y;
       } else {
         m = -INFINITY, sum = 0.f;
-        for (int i = lane; i < parts.n; i += 32) m = fmaxf(m, __ldcg(p.part_ml + parts.slot(p, i, h)).x);
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(p.part_ml + part_slot(p, c0, shifted, i, h)).x);
         m = warp_max(m);
         const float base = m == -INFINITY ? 0.f : m;
-        for (int i = lane; i < parts.n; i += 32) {
-          const float4 ml = __ldcg(p.part_ml + parts.slot(p, i, h));
+        for (int i = lane; i < n; i += 32) {
+          const float4 ml = __ldcg(p.part_ml + part_slot(p, c0, shifted, i, h));
           sum += exp2_fast(ml.x - base) * ml.y;
         }
         sum = warp_sum(sum);
@@ -754,16 +724,16 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
     }
     __syncthreads();
     const long long rows = static_cast<long long>(p.width) * p.page;
-    const float* scores = p.scores + (static_cast<long long>(parts.b) * p.nq + parts.g * p.group) * rows;
+    const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
     // the block's lot of kJoinKeys, and what lies key_blocks further on
-    for (long long lot = first; lot < parts.n_rows; lot += static_cast<long long>(key_blocks) * kJoinKeys)
-      for (int i = tid; i < kJoinKeys && lot + i < parts.n_rows; i += kJoin) {
+    for (long long lot = first; lot < n_rows; lot += static_cast<long long>(key_blocks) * kJoinKeys)
+      for (int i = tid; i < kJoinKeys && lot + i < n_rows; i += kJoin) {
         const int j = static_cast<int>(lot) + i, pi = j / p.page;
-        const int page = p.table[static_cast<long long>(parts.b) * p.width + pi];
+        const int page = p.table[static_cast<long long>(b) * p.width + pi];
         if (page < 0 || page >= p.n_pages) continue;
         float w = 0.f;
         for (int h = 0; h < p.group; ++h) w += exp2_fast(__ldcg(scores + h * rows + j) - top[h] + kLift<BF16>) * inv[h];
-        float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + parts.g) * p.page + (j - pi * p.page);
+        float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
         *to = p.decay == 0.f ? w : p.decay * *to + w;
       }
   }
@@ -820,6 +790,7 @@ cudaError_t paged_attn_ctas(int* ctas) {
 long long paged_attn_workspace(const PagedAttnParams& p, int hd, bool weights) {
   const long long parts = 2ll * p.ctas * p.group;
   long long n = up256(parts * hd * 4) + up256(16 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
+  n += up256(16ll * p.ctas) + up256(4ll * (p.batch + 1));
   if (weights) n += 4ll * p.batch * p.nq * (static_cast<long long>(p.width) * p.page);
   return n;
 }
@@ -830,8 +801,11 @@ void paged_attn_place(PagedAttnParams& p, int hd, bool weights, void* workspace)
   p.part_o = reinterpret_cast<float*>(at);
   at += up256(parts * hd * 4);
   p.part_ml = reinterpret_cast<float4*>(at);
-  if (!weights) return;
-  at += up256(16 * (parts + static_cast<long long>(p.batch) * p.nq));
+  at += up256(16 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
+  p.border = reinterpret_cast<int4*>(at);
+  at += up256(16ll * p.ctas);
+  p.first_tile = reinterpret_cast<int*>(at);
+  at += up256(4ll * (p.batch + 1));
   p.scores = reinterpret_cast<float*>(at);
 }
 
