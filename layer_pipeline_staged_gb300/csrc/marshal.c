@@ -15,8 +15,9 @@
 
 /* ---- what init() is given ------------------------------------------------- */
 
-static PyObject *g_bf16, *g_fp16, *g_int32, *g_fp32, *g_fp64, *g_uint8; /* torch dtypes */
+static PyObject *g_bf16, *g_fp16, *g_int32, *g_fp32, *g_fp64; /* torch dtypes */
 static PyObject *g_empty, *g_stream, *g_device, *g_set, *g_grad, *g_written; /* torch functions */
+static PyObject *g_alloc, *g_free;                       /* torch's caching allocator: (bytes, stream) -> address, (address) */
 static PyObject *g_error;                                /* LpsError */
 static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
 static PyObject *s_level, *s_unpack; /* in it: the current level of forward derivatives (-1: none), unpack_dual */
@@ -418,6 +419,28 @@ static int written(PyObject *a, PyObject *b) {
   return r ? 0 : -1;
 }
 
+/* Memory for a call's workspace from torch's caching allocator, for `stream` on the current device: what that stream
+ * runs next may have it once `give` has returned it, and in a capture it is the graph's. */
+static PyObject *take(long long bytes, void *stream, void **space) {
+  PyObject *const args[2] = {PyLong_FromLongLong(bytes), PyLong_FromVoidPtr(stream)};
+  PyObject *x = args[0] && args[1] ? PyObject_Vectorcall(g_alloc, args, 2, NULL) : NULL;
+  Py_XDECREF(args[0]);
+  Py_XDECREF(args[1]);
+  *space = x ? PyLong_AsVoidPtr(x) : NULL;
+  if (x && PyErr_Occurred()) Py_CLEAR(x);
+  return x;
+}
+static int give(PyObject *x) {
+  if (!x) return 0;
+  PyObject *t, *v, *tb;
+  PyErr_Fetch(&t, &v, &tb);
+  PyObject *r = PyObject_CallOneArg(g_free, x);
+  Py_DECREF(x);
+  Py_XDECREF(r);
+  if (t) PyErr_Restore(t, v, tb);
+  return r ? 0 : -1;
+}
+
 static int contiguous_heads(const tensor *t) {
   return t->shape[t->dim - 1] <= 1 || t->stride[t->dim - 1] == 1 ? 0 : refuse("the head dimension must be contiguous");
 }
@@ -737,24 +760,21 @@ static PyObject *decode_paged(PyObject *self, PyObject *const *args, Py_ssize_t 
     return NULL;
   const double decay = PyFloat_AsDouble(args[8]);
   if (PyErr_Occurred()) return NULL;
-  PyObject *out = output_like(args[5], q, &t[3]), *work = NULL;
+  PyObject *out = output_like(args[5], q, &t[3]);
   if (!out) return NULL;
   const int64_t st[4] = {q->stride[0], q->stride[1], t[3].stride[0], t[3].stride[1]};
   if (enter(&at, q->device)) return Py_DECREF(out), NULL;
-  /* memory of the allocator: what the call's stream runs next may have it */
   const long long bytes = attention_paged_decode_workspace((int)batch, (int)q->shape[1], (int)kp->shape[1], (int)q->shape[2], (int)kp->shape[2],
                                                            (int)tab.shape[1], kw.ptr != NULL);
   int rc = bytes < 0 ? (int)bytes : 0;
-  PyObject *ptr = NULL;
-  if (!rc && (!(work = new_array(bytes, g_uint8, q->obj)) || !(ptr = PyObject_CallMethodNoArgs(work, s_data_ptr)))) rc = 1;
-  if (!rc) {
-    void *space = PyLong_AsVoidPtr(ptr);
+  void *space = NULL;
+  PyObject *work = rc ? NULL : take(bytes, at.stream, &space);
+  if (!rc && !work) rc = 1;
+  if (!rc)
     rc = UNLOCKED(attention_paged_decode(q->ptr, kp->ptr, t[2].ptr, t[3].ptr, kind, (int)batch, len.ptr, tab.ptr, (int)tab.shape[1],
                                          (int)kp->shape[0], (int)kp->shape[2], (int)q->shape[1], (int)kp->shape[1], (int)q->shape[2], st, scale,
                                          kw.ptr, (float)decay, space, bytes, at.stream));
-  }
-  Py_XDECREF(ptr);
-  Py_XDECREF(work);
+  if (give(work) && !rc) rc = 1;
   if (leave(&at, rc) || rc || (given && written(out, kw.obj)) || (!given && kw.obj && written(kw.obj, NULL))) Py_CLEAR(out);
   return out;
 }
@@ -782,19 +802,18 @@ static PyObject *evict_paged(PyObject *self, PyObject *const *args, Py_ssize_t n
     if (PyErr_Occurred()) return NULL;
     if (size[i] < INT32_MIN || size[i] > INT32_MAX) return refuse("budget and recent must fit 32 bits"), NULL;
   }
-  PyObject *made = new_array(batch, g_int32, kp->obj), *work = NULL, *ptr = NULL;
+  PyObject *made = new_array(batch, g_int32, kp->obj);
   if (!made || tensor_of(made, &out, "new lengths") || enter(&at, kp->device)) return Py_XDECREF(made), NULL;
   const long long bytes = kv_pages_evict_workspace((int)batch, (int)kp->shape[1], (int)size[0]);
   int rc = bytes < 0 ? (int)bytes : 0;
-  if (!rc && (!(work = new_array(bytes, g_uint8, kp->obj)) || !(ptr = PyObject_CallMethodNoArgs(work, s_data_ptr)))) rc = 1;
-  if (!rc) {
-    void *space = PyLong_AsVoidPtr(ptr);
+  void *space = NULL;
+  PyObject *work = rc ? NULL : take(bytes, at.stream, &space);
+  if (!rc && !work) rc = 1;
+  if (!rc)
     rc = UNLOCKED(kv_pages_evict(kp->ptr, t[1].ptr, kw.ptr, (int)kp->shape[0], (int)kp->shape[2], (int)kp->shape[1], (int)kp->shape[3], (int)batch,
                                  len.ptr, tab.ptr, (int)tab.shape[1], fresh.ptr, (int)fresh.shape[1], out.ptr, (int)size[0], (int)size[1], space,
                                  bytes, at.stream));
-  }
-  Py_XDECREF(ptr);
-  Py_XDECREF(work);
+  if (give(work) && !rc) rc = 1;
   if (leave(&at, rc) || rc || written(kp->obj, t[1].obj) || written(kw.obj, NULL)) Py_CLEAR(made);
   return made;
 }
@@ -875,7 +894,6 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   g_int32 = PyObject_GetAttrString(torch, "int32");
   g_fp32 = PyObject_GetAttrString(torch, "float32");
   g_fp64 = PyObject_GetAttrString(torch, "float64");
-  g_uint8 = PyObject_GetAttrString(torch, "uint8");
   g_empty = PyObject_GetAttrString(torch, "empty");
   PyObject *dual = PyImport_ImportModule("torch.autograd.forward_ad");
   g_dual = dual ? PyModule_GetDict(dual) : NULL;
@@ -889,6 +907,8 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     g_written = graph ? PyObject_GetAttrString(graph, "increment_version") : NULL;
     Py_XDECREF(graph);
   }
+  g_alloc = c && PyObject_HasAttrString(c, "_cuda_cudaCachingAllocator_raw_alloc") ? PyObject_GetAttrString(c, "_cuda_cudaCachingAllocator_raw_alloc") : NULL;
+  g_free = c && PyObject_HasAttrString(c, "_cuda_cudaCachingAllocator_raw_delete") ? PyObject_GetAttrString(c, "_cuda_cudaCachingAllocator_raw_delete") : NULL;
   /* the calls' tensors are on a GPU, so torch's lazy initialisation has been */
   g_device = c && PyObject_HasAttrString(c, "_cuda_getDevice") ? PyObject_GetAttrString(c, "_cuda_getDevice")
              : cuda ? PyObject_GetAttrString(cuda, "current_device") : NULL;
@@ -896,11 +916,15 @@ static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   g_stream = c && PyObject_HasAttrString(c, "_cuda_getCurrentRawStream") ? PyObject_GetAttrString(c, "_cuda_getCurrentRawStream") : NULL;
   Py_XDECREF(cuda);
   Py_XDECREF(c);
-  if (!g_stream && !PyErr_Occurred()) { /* a torch without CUDA: every call is refused before it asks for a stream */
-    Py_INCREF(Py_None);
-    g_stream = Py_None;
+  if (!PyErr_Occurred()) { /* a torch without CUDA: every call is refused before it asks for a stream or for memory */
+    PyObject **const lacks[3] = {&g_stream, &g_alloc, &g_free};
+    for (int i = 0; i < 3; ++i)
+      if (!*lacks[i]) {
+        Py_INCREF(Py_None);
+        *lacks[i] = Py_None;
+      }
   }
-  if (!g_bf16 || !g_fp16 || !g_int32 || !g_fp32 || !g_fp64 || !g_uint8 || !g_empty || !g_dual || !g_grad || !g_written || !g_device || !g_set || PyErr_Occurred()) return NULL;
+  if (!g_bf16 || !g_fp16 || !g_int32 || !g_fp32 || !g_fp64 || !g_empty || !g_dual || !g_grad || !g_written || !g_device || !g_set || PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
 

@@ -52,7 +52,7 @@ extern "C" int rotary_rows(const void* q, const void* k, void* q_out, void* k_ou
   static const char* FN = "rotary_rows";
   return guarded(FN, [&]() -> int {
     if (!q || !k || !q_out || !k_out || !positions) return host_fail(LPS_EINVAL, FN, "q, k, their outputs and positions are required");
-    if (n_tokens < 0) return host_fail(LPS_EINVAL, FN, "n_tokens must be >= 0");
+    if (n_tokens < 0 || n_tokens > kMaxRows) return host_fail(LPS_EINVAL, FN, "n_tokens must be in [0, 2^31 - 2^16]");
     int rc = check_plain_heads(FN, type, n_q_heads, n_kv_heads, head_dim);
     if (rc || (rc = check_turn(FN, freqs, rot_dim, head_dim, magnitude))) return rc;
     const int64_t qd = static_cast<int64_t>(n_q_heads) * head_dim, kd = static_cast<int64_t>(n_kv_heads) * head_dim;
@@ -83,7 +83,7 @@ extern "C" int rotary_append_paged(const void* q, const void* k, const void* v, 
   return guarded(FN, [&]() -> int {
     if (!q || !k || !v || !q_out || !lengths || !table || !k_pages || !v_pages)
       return host_fail(LPS_EINVAL, FN, "q, k, v, q_out, lengths, table and the pages are required");
-    if (n_tokens < 0 || n_seqs < 1) return host_fail(LPS_EINVAL, FN, "n_tokens must be >= 0 and n_seqs >= 1");
+    if (n_tokens < 0 || n_tokens > kMaxRows || n_seqs < 1) return host_fail(LPS_EINVAL, FN, "n_tokens must be in [0, 2^31 - 2^16] and n_seqs >= 1");
     if (!offsets && n_tokens != n_seqs) return host_fail(LPS_EINVAL, FN, "without offsets there is one token a sequence");
     int rc = check_plain_heads(FN, type, n_q_heads, n_kv_heads, head_dim);
     if (rc || (rc = check_turn(FN, freqs, rot_dim, head_dim, magnitude)) || (rc = check_pages(FN, n_pages, page_size, table_width)))
@@ -236,7 +236,7 @@ extern "C" int logits_adjust(const void* logits, void* out, int type, int batch,
       return host_fail(LPS_EINVAL, FN, "type must be LPS_TYPE_BF16, LPS_TYPE_FP16 or LPS_TYPE_FP32");
     if (batch < 1 || batch > 65535) return host_fail(LPS_EINVAL, FN, "batch must be in 1..65535");
     if (vocab < 1 || vocab > kMaxRows) return host_fail(LPS_EINVAL, FN, "vocab must be in [1, 2^31 - 2^16]");
-    if (width < 0 || n_bias < 0) return host_fail(LPS_EINVAL, FN, "width and n_bias must be >= 0");
+    if (width < 0 || width > kMaxRows || n_bias < 0 || n_bias > kMaxRows) return host_fail(LPS_EINVAL, FN, "width and n_bias must be in [0, 2^31 - 2^16]");
     if (width > 0 && (!tokens || !lengths)) return host_fail(LPS_EINVAL, FN, "a history needs tokens and lengths");
     if (width == 0 && (repetition || frequency || presence)) return host_fail(LPS_EINVAL, FN, "penalties need a history");
     if (n_bias > 0 && (!bias_ids || !bias)) return host_fail(LPS_EINVAL, FN, "biases need bias_ids and bias");

@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "launch.h"
 #include "page_ops.h"
 #include "ptx.cuh"
 
@@ -739,33 +740,19 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
   }
 }
 
-template <class Kern, class... Args>
-cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <bool BF16, int HD, int NT, bool WEIGHTS>
 cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   constexpr size_t kSmem = sizeof(Smem<HD, NT>) + 1024;
   static_assert(kSmem <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<BF16, HD, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-  if (e == cudaSuccess) e = launch(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, s, p);
+  static std::atomic<uint64_t> told;
+  cudaError_t e = allow_smem(attn_kernel<BF16, HD, NT, WEIGHTS>, kSmem, told);
+  if (e == cudaSuccess) e = launch_early(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, s, p);
   if (e != cudaSuccess) return e;
   // blocks for the keys of every head that the tables have room for, in a bounded grid
   const long long heads = static_cast<long long>(p.batch) * p.nkv, rows = static_cast<long long>(p.width) * p.page;
   const long long lots = (rows + kJoinKeys - 1) / kJoinKeys, most = std::max(1ll, (1ll << 15) / heads);
   const int key_blocks = WEIGHTS ? static_cast<int>(std::min(lots, most)) : 0;
-  e = launch(join_kernel<BF16, HD, WEIGHTS>, dim3(static_cast<unsigned>(p.ctas * p.group + heads * key_blocks)), kJoin, 0, s, p, key_blocks);
+  e = launch_early(join_kernel<BF16, HD, WEIGHTS>, dim3(static_cast<unsigned>(p.ctas * p.group + heads * key_blocks)), kJoin, 0, s, p, key_blocks);
   return e;
 }
 
@@ -780,9 +767,7 @@ long long up256(long long x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 cudaError_t paged_attn_ctas(int* ctas) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(ctas, cudaDevAttrMultiProcessorCount, dev);
+  const cudaError_t e = sm_count(ctas);
   if (*ctas > kMaxParts) *ctas = kMaxParts;
   return e;
 }
