@@ -236,7 +236,8 @@ extern "C" int logits_adjust(const void* logits, void* out, int type, int batch,
       return host_fail(LPS_EINVAL, FN, "type must be LPS_TYPE_BF16, LPS_TYPE_FP16 or LPS_TYPE_FP32");
     if (batch < 1 || batch > 65535) return host_fail(LPS_EINVAL, FN, "batch must be in 1..65535");
     if (vocab < 1 || vocab > kMaxRows) return host_fail(LPS_EINVAL, FN, "vocab must be in [1, 2^31 - 2^16]");
-    if (width < 0 || width > kMaxRows || n_bias < 0 || n_bias > kMaxRows) return host_fail(LPS_EINVAL, FN, "width and n_bias must be in [0, 2^31 - 2^16]");
+    if (width < 0 || width >= (1 << 30) || n_bias < 0 || n_bias >= (1 << 30))
+      return host_fail(LPS_EINVAL, FN, "width and n_bias must be in [0, 2^30)");
     if (width > 0 && (!tokens || !lengths)) return host_fail(LPS_EINVAL, FN, "a history needs tokens and lengths");
     if (width == 0 && (repetition || frequency || presence)) return host_fail(LPS_EINVAL, FN, "penalties need a history");
     if (n_bias > 0 && (!bias_ids || !bias)) return host_fail(LPS_EINVAL, FN, "biases need bias_ids and bias");
