@@ -18,7 +18,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelect = 1024;  // threads of the selection
 constexpr int kWarps = kSelect / 32;
-constexpr int kKeys = 49152;   // keys of a sequence that shared memory holds; those behind are read again
+constexpr int kBins = 2048;
+constexpr int kKeys = 32768;   // weights that a block of the selection keeps
+constexpr long long kAlone = 16384;  // rows that are no work for two blocks
 constexpr int kCopy = 256;     // threads of a block that copies
 constexpr int kRows = 64;      // its rows
 
@@ -29,16 +31,19 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A thread-block cluster per (kv head, sequence), a run of the rows per block: the
-// rows that stay, in order. The lightest weight that stays is found by its bits,
-// eight at a time from the top: a histogram of the rows that agree so far, summed
-// over the cluster, and the digit in which the count is reached.
+// A thread-block cluster per (kv head, sequence), a run of the rows per block: the rows
+// that stay, in order. The lightest weight that stays
+// is found by its bits from the top, 11, 11 and 10: a histogram of the rows that
+// agree so far, summed over the cluster, and the digit in which the count is reached.
+// Latency bounds it, and not least the instructions' own way from memory: its loops
+// stay loops (unrolled, with the weights in registers, 1000 rows of 8 heads took 11.3 us
+// with the copy, and 8.2 so).
 __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__ EvictParams p, int held) {
-  extern __shared__ uint32_t keys[];  // [held]
-  __shared__ int hist[2][256];        // passes take turns: a block may be a pass ahead of those that read its sums
-  __shared__ int all[256];
-  __shared__ int2 counted[kWarps];    // heavier rows and equal ones of each warp's run
-  __shared__ int2 block_counted;      // of the block
+  extern __shared__ uint4 held_keys[];  // [held / 4]: the orders of the block's first rows; those behind are read again
+  uint32_t* keys = reinterpret_cast<uint32_t*>(held_keys);
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ int sums[kWarps];
+  __shared__ int2 block_counted;      // the block's heavier rows and equal ones
   __shared__ int digit, above;
   pdl_launch_dependents();
   pdl_wait();
@@ -49,10 +54,43 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__
   const int* table = p.table + static_cast<long long>(b) * p.width;
   const int* fresh = p.fresh + static_cast<long long>(b) * p.fresh_width;
   int* rows = p.rows + (static_cast<long long>(b) * p.nkv + g) * p.budget;
+  auto meet = [&] {
+    if (blocks > 1) cluster.sync();
+    else __syncthreads();
+  };
+  for (int i = t; i < static_cast<int>(sizeof hist) / 16; i += kSelect) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
 
-  // every block of the cluster finds the same
   bool ok = n >= 0 && n <= static_cast<long long>(p.width) * p.page;
   const int kept = min(n, p.budget);
+  const bool choose = ok && n > p.budget;
+  const int others = choose ? n - p.recent : 0, want = p.budget - p.recent;  // 0 <= want < others
+  // the block's run [b0, b0 + mine) of the rows
+  const int share = (others + 8 * blocks - 1) / (8 * blocks) * 8, b0 = min(rank * share, others), mine = min(share, others - b0);
+  // A page's rows come in eights, and so do the block's: a thread takes eight of one
+  // page. A row on a page that is none is as light as can be, as is what fills an eight.
+  const int in_smem = min(mine, held);
+#pragma unroll 2
+  for (int i = 8 * t; i < in_smem; i += 8 * kSelect) {
+    const int pi = (b0 + i) / p.page, page = table[pi];
+    float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), y = x;
+    if (page >= 0 && page < p.n_pages) {
+      const float4* w = reinterpret_cast<const float4*>(p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (b0 + i - pi * p.page));
+      x = w[0], y = w[1];
+    }
+    uint4 k = make_uint4(order_of(x.x), order_of(x.y), order_of(x.z), order_of(x.w));
+    uint4 l = make_uint4(order_of(y.x), order_of(y.y), order_of(y.z), order_of(y.w));
+    const int left = in_smem - i;
+    if (left < 8) {
+      l.w = 0, l.z = left > 6 ? l.z : 0, l.y = left > 5 ? l.y : 0, l.x = left > 4 ? l.x : 0;
+      k.w = left > 3 ? k.w : 0, k.z = left > 2 ? k.z : 0, k.y = left > 1 ? k.y : 0;
+    }
+    held_keys[i / 4] = k, held_keys[i / 4 + 1] = l;
+  }
+  auto read = [&](int i) {
+    const int row = b0 + i, pi = row / p.page, page = table[pi];
+    return order_of(p.key_weights[(static_cast<long long>(page) * p.nkv + g) * p.page + (row - pi * p.page)]);
+  };
+  // every block of the cluster looks at all pages, and finds the same
   if (ok) {
     for (int i = t; i < (n + p.page - 1) / p.page; i += kSelect) ok = ok && table[i] >= 0 && table[i] < p.n_pages;
     for (int i = t; i < (kept + p.page - 1) / p.page; i += kSelect) ok = ok && fresh[i] >= 0 && fresh[i] < p.n_pages;
@@ -61,102 +99,107 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__
   if (g == 0 && rank == 0 && t == 0) p.new_lengths[b] = ok ? kept : -1;
   if (!ok) return;
   const int first = rank * kSelect + t, step = blocks * kSelect;
-  if (n <= p.budget) {
+  if (!choose) {
     for (int i = first; i < n; i += step) rows[i] = i;
     return;
   }
-  const int others = n - p.recent, want = p.budget - p.recent;  // 0 <= want < others
   for (int i = first; i < p.recent; i += step) rows[want + i] = others + i;
   if (want == 0) return;
-
-  auto read = [&](int row) {
-    const int pi = row / p.page;
-    return order_of(p.key_weights[(static_cast<long long>(table[pi]) * p.nkv + g) * p.page + (row - pi * p.page)]);
-  };
-  // the block's run [b0, b0 + mine) of the rows
-  const int share = (others + blocks - 1) / blocks, b0 = min(rank * share, others), mine = min(share, others - b0);
-  const int in_smem = min(mine, held);
-#pragma unroll 8
-  for (int i = t; i < in_smem; i += kSelect) keys[i] = read(b0 + i);
-  auto key_of = [&](int i) { return i < in_smem ? keys[i] : read(b0 + i); };
+  auto key_of = [&](int i) { return i < in_smem ? keys[i] : read(i); };
 
   uint32_t least = 0;  // the weight of the last one that stays, and how many equal ones do
-  int equal = want, pass = 0;
-  for (int shift = 24; shift >= 0; shift -= 8, ++pass) {
-    int* h = hist[pass & 1];
-    if (t < 256) h[t] = 0;
+  int equal = want;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = max(21 - 11 * pass, 0);
+    const uint32_t bins = pass == 2 ? 1023 : kBins - 1, known = pass == 0 ? 0 : ~0u << (pass == 1 ? 21 : 10);  // bits that agree
+    int* h = hist[pass];
+    auto count = [&](uint32_t k) {
+      if ((k & known) == least) atomicAdd(&h[k >> shift & bins], 1);
+    };
+#pragma unroll 1
+    for (int i = t; i < (in_smem + 3) / 4; i += kSelect) {
+      const uint4 k = held_keys[i];
+      count(k.x), count(k.y), count(k.z), count(k.w);
+    }
+#pragma unroll 1
+    for (int i = held + t; i < mine; i += kSelect) count(read(i));
+    meet();
+    // thread: two bins, from the highest on
+    int2 x = make_int2(0, 0);
+    for (int r = 0; r < blocks; ++r) {
+      const int2 v = reinterpret_cast<const int2*>(blocks > 1 ? cluster.map_shared_rank(h, r) : h)[kSelect - 1 - t];
+      x.x += v.y, x.y += v.x;
+    }
+    int before = x.x + x.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) sums[warp] = before;
     __syncthreads();
-#pragma unroll 4
-    for (int i = t; i < mine; i += kSelect) {
-      const uint32_t k = key_of(i);
-      if (shift == 24 || (k ^ least) >> (shift + 8) == 0) atomicAdd(&h[k >> shift & 255], 1);
-    }
-    cluster.sync();
-    if (t < 256) {
-      int sum = 0;
-      for (int r = 0; r < blocks; ++r) sum += cluster.map_shared_rank(h, r)[t];
-      all[t] = sum;
-    }
-    __syncthreads();
-    if (warp == 0) {  // lane: eight digits, from the highest on
-      int x[8], sum = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += x[j] = all[255 - 8 * lane - j];
-      int before = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
-      }
-      before -= sum;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (before < equal && before + x[j] >= equal) digit = 255 - 8 * lane - j, above = before;
-        before += x[j];
-      }
-    }
+    before += __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) - x.x - x.y;
+    if (before < equal && before + x.x >= equal) digit = kBins - 1 - 2 * t, above = before;
+    before += x.x;
+    if (before < equal && before + x.y >= equal) digit = kBins - 2 - 2 * t, above = before;
     __syncthreads();
     least |= static_cast<uint32_t>(digit) << shift;
     equal -= above;
   }
 
-  // a warp's run of the block's rows: how many stay before it, then each row's place
-  const int run = (mine + kSelect - 1) / kSelect * 32, r0 = min(warp * run, mine), r1 = min(r0 + run, mine);
-  int heavier = 0, ties = 0;
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < r1 ? key_of(i) : 0;
-    heavier += __popc(__ballot_sync(0xffffffffu, i < r1 && k > least));
-    ties += __popc(__ballot_sync(0xffffffffu, i < r1 && k == least));
+  // the heavier rows and the equal ones before the block's, for a block that is not the first
+  int heavy = 0, tie = 0;
+  if (blocks > 1) {
+    int x = 0, y = 0;
+#pragma unroll 1
+    for (int i = t; i < mine; i += kSelect) {
+      const uint32_t k = key_of(i);
+      x += k > least, y += k == least;
+    }
+    x = __reduce_add_sync(0xffffffffu, x), y = __reduce_add_sync(0xffffffffu, y);
+    if (t == 0) block_counted = make_int2(0, 0);
+    __syncthreads();
+    if (lane == 0) atomicAdd(&block_counted.x, x), atomicAdd(&block_counted.y, y);
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int2 o = *cluster.map_shared_rank(&block_counted, r);
+      heavy += o.x, tie += o.y;
+    }
   }
-  if (lane == 0) counted[warp] = make_int2(heavier, ties);
-  __syncthreads();
-  if (warp == 0) {
-    int2 c = counted[lane];
+  // Each row's place, a thread eight rows in turn: heavier rows in the lower half of a
+  // sum and equal ones in the upper, at most 8192 of each
+#pragma unroll 1
+  for (int c0 = 0; c0 < mine; c0 += 8 * kSelect) {
+    const int i0 = c0 + 8 * t;
+    uint32_t more = 0, same = 0;  // a bit a row
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c.x += __shfl_xor_sync(0xffffffffu, c.x, o), c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
-    if (lane == 0) block_counted = c;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t k = i0 + e < mine ? key_of(i0 + e) : 0;
+      more |= static_cast<uint32_t>(i0 + e < mine && k > least) << e;
+      same |= static_cast<uint32_t>(i0 + e < mine && k == least) << e;
+    }
+    const int packed = __popc(more) | __popc(same) << 16;
+    int before = packed;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    __syncthreads();  // the last sums have been read
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+    const int all = sums[lane];
+    before += static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? all : 0)) - packed;
+    int at_tie = tie + (before >> 16), at = heavy + (before & 0xffff) + min(at_tie, equal);  // of equal ones the first stay
+    for (uint32_t left = more | same; left; left &= left - 1) {
+      const int e = __ffs(left) - 1;
+      if (more >> e & 1 || at_tie++ < equal) rows[at++] = b0 + i0 + e;
+    }
+    const int total = __reduce_add_sync(0xffffffffu, all);
+    heavy += total & 0xffff, tie += total >> 16;
   }
-  cluster.sync();
-  int at = 0, tie = 0;
-  auto pass_by = [&](int2 c) {
-    at += c.x + max(0, min(c.y, equal - tie));
-    tie += c.y;
-  };
-  for (int r = 0; r < rank; ++r) pass_by(*cluster.map_shared_rank(&block_counted, r));
-  for (int w = 0; w < warp; ++w) pass_by(counted[w]);
-  const unsigned below = (1u << lane) - 1;
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < r1 ? key_of(i) : 0;
-    const unsigned same = __ballot_sync(0xffffffffu, i < r1 && k == least);
-    const bool stays = i < r1 && (k > least || (k == least && tie + __popc(same & below) < equal));
-    const unsigned stay = __ballot_sync(0xffffffffu, stays);
-    if (stays) rows[at + __popc(stay & below)] = b0 + i;
-    at += __popc(stay);
-    tie += __popc(same);
-  }
-  cluster.sync();  // the counts are read before their block ends
+  if (blocks > 1) cluster.sync();  // the counts are read before their block ends
 }
 
 // Block = kRows kept rows of (kv head, sequence): where they come from and go to,
@@ -199,18 +242,20 @@ __global__ void __launch_bounds__(kCopy) copy_kernel(const __grid_constant__ Evi
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
-  static std::atomic<uint64_t> told;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
+  static std::atomic<uint64_t> told;
   if (e == cudaSuccess) e = allow_smem(select_kernel, kKeys * 4, told);
   if (e != cudaSuccess) return e;
   // a head's rows are shared out over as many blocks as the SMs have room for one by
-  // one, while each has a few thousand rows
+  // one, while each has a few thousand rows; but none has more than it keeps, if eight
+  // are enough for that
   const long long most = static_cast<long long>(p.width) * p.page, heads = static_cast<long long>(p.nkv) * p.batch;
   int blocks_of_head = 1;
-  while (blocks_of_head < 8 && 2 * blocks_of_head * heads <= sms && most >= 2048ll * blocks_of_head) blocks_of_head *= 2;
+  while (blocks_of_head < 8 && ((2 * blocks_of_head * heads <= sms && most >= kAlone * blocks_of_head) || most > static_cast<long long>(kKeys) * blocks_of_head))
+    blocks_of_head *= 2;
   const long long share = (most + blocks_of_head - 1) / blocks_of_head;
-  const int held = static_cast<int>(share < kKeys ? share : kKeys);
+  const int held = static_cast<int>(share + 8 < kKeys ? (share + 15) / 8 * 8 : kKeys);  // a share is in eights
   e = launch_early_clusters(select_kernel, dim3(blocks_of_head, p.nkv, p.batch), kSelect, held * 4, blocks_of_head, s, p, held);
   if (e != cudaSuccess) return e;
   const int blocks = (p.budget + kRows - 1) / kRows;

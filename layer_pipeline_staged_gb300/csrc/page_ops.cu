@@ -213,6 +213,7 @@ extern "C" int kv_pages_evict(void* k_pages, void* v_pages, float* key_weights, 
     if (recent < 0 || recent > budget) return host_fail(LPS_EINVAL, FN, "recent must be in 0..budget");
     if (static_cast<long long>(new_width) * page_size < budget) return host_fail(LPS_EINVAL, FN, "the new table must have room for budget rows");
     if (lengths == new_lengths || table == new_table) return host_fail(LPS_EINVAL, FN, "the new lengths and table must not be the old ones");
+    if (misaligned(key_weights)) return host_fail(LPS_EINVAL, FN, "key_weights must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(workspace) & 3 || workspace_bytes < 4ll * batch * n_kv_heads * budget)
       return host_fail(LPS_EINVAL, FN, "workspace must be 4-byte aligned and hold what kv_pages_evict_workspace asks for");
     EvictParams p{};

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 64;
+constexpr int kRows = 512;  // (token, head) rows whose places are held at once
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack(uint32_t w) {
@@ -38,64 +39,43 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Block = TOK consecutive tokens at a time, every grid's number of blocks again:
-// their angles' cosines and sines once into shared memory, then an item (token,
-// head, 16 elements) per thread, kBatch of which are on their way at once; the
-// first ones while the angles are worked out.
+// Block = TOK consecutive tokens: their angles' cosines and sines, and where each
+// (token, head) comes from and goes to, once into shared memory; then an item (row,
+// 16 elements) per thread, kBatch of which are on their way at once, the first ones
+// while the angles are worked out.
 template <bool BF16, int HD, int TOK>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  __shared__ unsigned long long per[kMaxPairs];  // turns a position, in units of 2^-64
+  constexpr int kBatch = 3, kUnits = HD / 16;  // an item: two 16-byte chunks of a row
   // (cos, sin) times the magnitude, of pair 8 u + e at [e][u]: lanes with other units read other banks
-  __shared__ float2 turn[TOK][8][HD / 16];
-  __shared__ long long row[TOK];                 // page * nkv * page rows + row in the page, or -1: not stored
-  __shared__ int live[TOK], where[TOK];
-  constexpr int kBatch = TOK == 1 ? 2 : 3;
-  constexpr int kUnits = HD / 16;  // a thread's item: two 16-byte chunks of a row
+  __shared__ float2 turn[TOK][8][kUnits];
+  __shared__ const char* src[kRows];  // of the (token, head) rows; bit 0: it turns, 1 and 2: its token
+  __shared__ char* dst[kRows];        // NULL: not stored
+  __shared__ long long row[TOK];      // page * nkv * page rows + row in the page, or -1: not stored
+  __shared__ int where[TOK], live[TOK];
   pdl_launch_dependents();
   pdl_wait();
-  const int t = threadIdx.x, pairs = p.rot >> 1;
-  if (t < pairs) {
-    const double f = p.freqs[t] * 0.15915494309189533577;  // / (2 pi): turns a position
-    per[t] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
-  }
-  const int heads = p.nq + p.nkv + (p.k_pages ? p.nkv : 0);
-  const int per_tok = heads * kUnits, rot_units = p.rot / 16, items = TOK * per_tok;
+  const int t = threadIdx.x, pairs = p.rot >> 1, tok0 = blockIdx.x * TOK;
+  const int heads = p.nq + p.nkv + (p.k_pages ? p.nkv : 0), all_rows = min(TOK, p.tokens - tok0) * heads;
 
-  for (int tok0 = blockIdx.x * TOK; tok0 < p.tokens; tok0 += gridDim.x * TOK) {
-    // an item's place: its token, head and chunks of the row (a pair's partners lie
-    // rot / 2 elements apart, or side by side)
-    struct Item {
-      int ti, h, u, c0, c1;
-      bool on, turned;
-    };
-    auto item_of = [&](int i) {
-      Item it;
-      it.ti = 0;
-#pragma unroll
-      for (int k = 1; k < TOK; ++k) it.ti += i >= k * per_tok;
-      const int j = i - it.ti * per_tok;
-      it.h = j / kUnits, it.u = j % kUnits;
-      it.on = i < items && tok0 + it.ti < p.tokens;
-      it.turned = it.u < rot_units && it.h < p.nq + p.nkv;
-      const bool apart = it.turned && !p.interleaved;
-      it.c0 = apart ? it.u : 2 * it.u, it.c1 = apart ? it.u + rot_units : 2 * it.u + 1;
-      return it;
-    };
-    auto fetch = [&](const Item& it, uint4& a, uint4& b) {
-      if (!it.on) return;
-      const long long tok = tok0 + it.ti;
-      const char* src;
-      if (it.h < p.nq) src = static_cast<const char*>(p.q) + 2 * (tok * p.q_tok + it.h * p.q_head);
-      else if (it.h < p.nq + p.nkv) src = static_cast<const char*>(p.k) + 2 * (tok * p.k_tok + (it.h - p.nq) * p.k_head);
-      else src = static_cast<const char*>(p.v) + 2 * (tok * p.v_tok + (it.h - p.nq - p.nkv) * p.v_head);
-      a = reinterpret_cast<const uint4*>(src)[it.c0], b = reinterpret_cast<const uint4*>(src)[it.c1];
-    };
-    uint4 a[kBatch], b[kBatch];
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) fetch(item_of(t + e * kThreads), a[e], b[e]);
+  // A thread's units are one: its chunks of a row that turns (a pair's partners lie
+  // rot / 2 elements apart, or side by side) and of one that does not
+  const int u = t % kUnits, lane_row = t / kUnits;
+  constexpr int kStep = kThreads / kUnits;  // rows of a step
+  const bool in_rot = u < p.rot / 16, apart = in_rot && !p.interleaved;
+  const int plain = 32 * u, t0 = apart ? 16 * u : plain, t1 = apart ? 16 * (u + p.rot / 16) : plain + 16;
 
-    __syncthreads();  // the last tokens' angles have been used
-    if (t < TOK) {    // where each token goes, and what turns it
+  for (int r0 = 0; r0 < all_rows; r0 += kRows) {
+    const int rows = min(kRows, all_rows - r0);
+    for (int r = t; r < rows; r += kThreads) {
+      const int ti = TOK == 1 ? 0 : (r0 + r) / heads, h = r0 + r - ti * heads;
+      const long long tok = tok0 + ti;
+      const void* from = h < p.nq ? p.q : h < p.nq + p.nkv ? p.k : p.v;
+      const int g = h < p.nq ? h : h < p.nq + p.nkv ? h - p.nq : h - p.nq - p.nkv;
+      const long long by_tok = h < p.nq ? p.q_tok : h < p.nq + p.nkv ? p.k_tok : p.v_tok;
+      const long long by_head = h < p.nq ? p.q_head : h < p.nq + p.nkv ? p.k_head : p.v_head;
+      src[r] = static_cast<const char*>(from) + 2 * (tok * by_tok + g * by_head) + (h < p.nq + p.nkv) + 2 * ti;
+    }
+    if (r0 == 0 && t < TOK) {  // where each token goes, and what turns it
       const int tok = tok0 + t;
       bool on = tok < p.tokens;
       int pos = 0;
@@ -126,66 +106,87 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       where[t] = pos;
     }
     __syncthreads();
-    for (int i = t; i < TOK * kMaxPairs; i += kThreads) {
-      const int ti = i / kMaxPairs, pair = i % kMaxPairs;
-      if (pair < pairs) {
-        const long long angle = static_cast<long long>(per[pair] * static_cast<unsigned long long>(static_cast<long long>(where[ti])));
-        float sn, cs;
-        sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.6566128730773925781e-10f, &sn, &cs);  // * 2^-31
-        turn[ti][pair & 7][pair >> 3] = make_float2(cs * p.magnitude, sn * p.magnitude);
+
+    uint4 a[kBatch], b[kBatch];
+    auto fetch = [&](int r, uint4& x, uint4& y) {
+      if (r >= rows) return;
+      const uintptr_t from = reinterpret_cast<uintptr_t>(src[r]);
+      const char* at = reinterpret_cast<const char*>(from & ~static_cast<uintptr_t>(15));
+      x = *reinterpret_cast<const uint4*>(at + (from & 1 ? t0 : plain));
+      y = *reinterpret_cast<const uint4*>(at + (from & 1 ? t1 : plain + 16));
+    };
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) fetch(lane_row + e * kStep, a[e], b[e]);
+
+    if (r0 == 0) {
+      for (int i = t; i < TOK * kMaxPairs; i += kThreads) {
+        const int ti = i / kMaxPairs, pair = i % kMaxPairs;
+        if (pair < pairs) {
+          const double f = p.freqs[pair] * 0.15915494309189533577;  // / (2 pi): turns a position
+          const unsigned long long per = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+          const long long angle = static_cast<long long>(per * static_cast<unsigned long long>(static_cast<long long>(where[ti])));
+          float sn, cs;
+          sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * 4.6566128730773925781e-10f, &sn, &cs);  // * 2^-31
+          turn[ti][pair & 7][pair >> 3] = make_float2(cs * p.magnitude, sn * p.magnitude);
+        }
       }
+    }
+    for (int r = t; r < rows; r += kThreads) {
+      const int ti = TOK == 1 ? 0 : (r0 + r) / heads, h = r0 + r - ti * heads;
+      const long long tok = tok0 + ti;
+      char* to = nullptr;
+      if (h < p.nq) {
+        to = static_cast<char*>(p.q_out) + 2 * (tok * p.qo_tok + h * p.qo_head);
+      } else if (p.k_pages) {
+        const bool is_k = h < p.nq + p.nkv;
+        if (row[ti] >= 0) {
+          const long long at = row[ti] + static_cast<long long>(h - p.nq - (is_k ? 0 : p.nkv)) * p.page;
+          to = static_cast<char*>(is_k ? p.k_pages : p.v_pages) + 2 * at * HD;
+          if (is_k && p.key_weights && live[ti]) p.key_weights[at] = 0.f;
+        }
+      } else {
+        to = static_cast<char*>(p.k_out) + 2 * (tok * p.ko_tok + (h - p.nq) * p.ko_head);
+      }
+      dst[r] = live[ti] ? to : nullptr;
     }
     __syncthreads();
 
-    for (int i0 = 0; i0 < items; i0 += kBatch * kThreads) {
+    for (int i0 = lane_row; i0 - lane_row < rows; i0 += kBatch * kStep) {
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) {
-        const Item it = item_of(i0 + t + e * kThreads);
-        if (!it.on || !live[it.ti]) continue;
-        if (it.turned) {
+        const int r = i0 + e * kStep;
+        if (r >= rows) continue;
+        char* to = dst[r];
+        const uintptr_t from = reinterpret_cast<uintptr_t>(src[r]);
+        if ((from & 1) && in_rot) {
           uint32_t* aw = reinterpret_cast<uint32_t*>(&a[e]);
           uint32_t* bw = reinterpret_cast<uint32_t*>(&b[e]);
-          const auto& cs = turn[it.ti];
+          const auto& cs = turn[TOK == 1 ? 0 : from >> 1 & 3];
           if (p.interleaved) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float2 x = unpack<BF16>(aw[w]), y = unpack<BF16>(bw[w]), m = cs[w][it.u], n = cs[4 + w][it.u];
+              const float2 x = unpack<BF16>(aw[w]), y = unpack<BF16>(bw[w]), m = cs[w][u], n = cs[4 + w][u];
               aw[w] = pack<BF16>(x.x * m.x - x.y * m.y, x.y * m.x + x.x * m.y);
               bw[w] = pack<BF16>(y.x * n.x - y.y * n.y, y.y * n.x + y.x * n.y);
             }
           } else {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float2 x = unpack<BF16>(aw[w]), y = unpack<BF16>(bw[w]), m = cs[2 * w][it.u], n = cs[2 * w + 1][it.u];
+              const float2 x = unpack<BF16>(aw[w]), y = unpack<BF16>(bw[w]), m = cs[2 * w][u], n = cs[2 * w + 1][u];
               aw[w] = pack<BF16>(x.x * m.x - y.x * m.y, x.y * n.x - y.y * n.y);
               bw[w] = pack<BF16>(y.x * m.x + x.x * m.y, y.y * n.x + x.y * n.y);
             }
           }
         }
-        const long long tok = tok0 + it.ti;
-        if (it.h < p.nq) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(p.q_out) + 2 * (tok * p.qo_tok + it.h * p.qo_head));
-          dst[it.c0] = a[e], dst[it.c1] = b[e];
-        } else {
-          const bool is_k = it.h < p.nq + p.nkv;
-          const int g = it.h - p.nq - (is_k ? 0 : p.nkv);
-          if (is_k && p.k_out) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(p.k_out) + 2 * (tok * p.ko_tok + g * p.ko_head));
-            dst[it.c0] = a[e], dst[it.c1] = b[e];
-          }
-          if (p.k_pages && row[it.ti] >= 0) {
-            const long long r = row[it.ti] + static_cast<long long>(g) * p.page;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(is_k ? p.k_pages : p.v_pages) + 2 * r * HD);
-            dst[it.c0] = a[e], dst[it.c1] = b[e];
-            if (is_k && it.u == 0 && p.key_weights) p.key_weights[r] = 0.f;
-          }
+        if (to) {
+          *reinterpret_cast<uint4*>(to + (from & 1 ? t0 : plain)) = a[e];
+          *reinterpret_cast<uint4*>(to + (from & 1 ? t1 : plain + 16)) = b[e];
         }
       }
-      if (i0 + kBatch * kThreads < items) {
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) fetch(item_of(i0 + kBatch * kThreads + t + e * kThreads), a[e], b[e]);
-      }
+      for (int e = 0; e < kBatch; ++e) fetch(i0 + (kBatch + e) * kStep, a[e], b[e]);
     }
+    __syncthreads();  // the next rows' places
   }
 }
 

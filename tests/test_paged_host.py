@@ -97,7 +97,7 @@ def test_workspace_refused(args):
 @pytest.mark.parametrize("kw", [dict(kp=None), dict(vp=None), dict(kw=None), dict(len=None), dict(table=None), dict(fresh=None), dict(new=None),
                                 dict(ws=None), dict(batch=0), dict(batch=65536), dict(budget=0), dict(budget=33), dict(recent=-1),
                                 dict(recent=33), dict(fw=0), dict(new=A[3]), dict(fresh=A[4]), dict(ws=A[7] + 2), dict(bytes=2 * 2 * 32 * 4 - 1),
-                                dict(kp=A[0] + 8), dict(vp=A[0] + 16), *[h for h in HEADS if "type" not in h], *PAGES])
+                                dict(kp=A[0] + 8), dict(vp=A[0] + 16), dict(kw=A[2] + 8), *[h for h in HEADS if "type" not in h], *PAGES])
 def test_evict_refused(kw):
     assert evict(**kw) == lps.LPS_EINVAL and "kv_pages_evict" in _capi.load().last_error_string().decode()
     assert _capi.load().kv_pages_evict_workspace(1, 2, 0) == lps.LPS_EINVAL
