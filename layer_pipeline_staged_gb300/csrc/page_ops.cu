@@ -116,7 +116,7 @@ int paged_shape(const char* fn, PagedAttnParams& p, int batch, int nq, int nkv, 
   int rc = check_heads(fn, LPS_TYPE_BF16, nq, nkv, hd);
   if (rc || (rc = check_pages(fn, 1, page_size, width))) return rc;
   const long long rows = static_cast<long long>(width) * page_size;
-  if ((rows + 63) / 64 * nkv > 0x7fffffffll / batch) return host_fail(LPS_EINVAL, fn, "too many rows, kv heads and sequences for one launch");
+  if (((rows + 63) / 64 + 1) * nkv > 0x7fffffffll / batch) return host_fail(LPS_EINVAL, fn, "too many rows, kv heads and sequences for one launch");
   p.batch = batch, p.nq = nq, p.nkv = nkv, p.group = nq / nkv, p.page = page_size, p.width = width;
   const cudaError_t e = paged_attn_ctas(&p.ctas);
   return e == cudaSuccess ? LPS_OK : host_fail(LPS_ECUDA, fn, cudaGetErrorString(e));

@@ -52,11 +52,11 @@ struct PagedAttnParams {
   const int* lengths;          // [batch]
   float* key_weights;          // [n_pages][nkv][page], or NULL
   float* part_o;               // workspace: [ctas][2][group][hd]
-  float4* part_ml;             // [ctas][2][group]: base, sum, whether a key was seen; then,
+  float2* part_ml;             // [ctas][2][group]: base, and sum (-1: no key was seen); then,
                                // with key_weights, of heads that one CTA has whole: [batch][nkv][group]
   int4* border;                // [ctas]: the head that begins in the CTA's share and ends in another's: sequence,
                                // kv head, its parts (0: there is none), whether the share begins before it
-  int* first_tile;             // key_weights: [batch + 1], and then the number of tiles
+  int* first_unit;             // key_weights: [batch + 1]: of each sequence, then their number
   float* scores;               // key_weights: [batch][nq][width * page], times log2(e)
   long long wait_limit;
   int batch, width, n_pages, page, box;

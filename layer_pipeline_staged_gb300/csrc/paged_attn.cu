@@ -83,7 +83,7 @@ struct __align__(1024) Smem {
   float factor[kWriters][kConsumers][S::kHeads], sum[kWriters][S::kHeads];  // a writer's notes on its piece
   int rows[kPagedBatch];           // of each sequence
   int warp_sum[kThreads / 32];
-  int base;                        // first tile of the sequence that the CTA begins in
+  int base;                        // first unit of the sequence that the CTA begins in
   int first;                       // that sequence
   uint32_t valid[S::kStages];      // boxes of the tile whose page is one, or kWhole
   uint64_t full[S::kStages], empty[S::kStages], slot_full[S::kSlots], slot_empty[S::kSlots];
@@ -164,8 +164,13 @@ __device__ __forceinline__ int rows_of(const PagedAttnParams& p, int b) {
   return n > 0 && n <= static_cast<long long>(p.width) * p.page ? n : 0;
 }
 
-// `total` tiles in equal shares (in 32 bits: the entry point bounds them), the
-// first `more` of one tile more.
+// What is shared out are units: a head has one for itself (its start and end take
+// about as long as a tile) and then one per tile; in 32 bits, the entry point bounds
+// them. Without heads' own units, a CTA with a share of one-tile heads took 1.5 times
+// as long as the others (32 mixed sequences 62 us).
+__device__ __forceinline__ int units_of(int tiles) { return tiles ? tiles + 1 : 0; }
+
+// `total` units in equal shares, the first `more` of one unit more.
 struct Shares {
   int ctas, per, more;
   __device__ __forceinline__ Shares(int total, int grid) {
@@ -174,31 +179,33 @@ struct Shares {
     more = total - per * ctas;
   }
   __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
-  __device__ __forceinline__ int owner(int tile) const {
+  __device__ __forceinline__ int owner(int unit) const {
     const int head = more * (per + 1);
-    return tile < head ? tile / (per + 1) : more + (tile - head) / per;
+    return unit < head ? unit / (per + 1) : more + (unit - head) / per;
   }
 };
 
 // A CTA's pieces in order: tiles [t0, t1) of kv head g of sequence b.
 struct Walk {
-  int at, end, base;  // next tile, the share's end, the first tile of sequence b
+  int at, end, base;  // next unit, the share's end, the first unit of sequence b
   int b, nkv;
   const int* rows;
   int g, t0, t1;
   __device__ __forceinline__ int tiles() const { return (rows[b] + kTile - 1) / kTile; }
   __device__ __forceinline__ bool next() {
-    if (at >= end) return false;
-    int n;
-    while (n = tiles(), at >= base + nkv * n) {
-      base += nkv * n;
-      ++b;
+    while (at < end) {
+      int n;
+      while (n = units_of(tiles()), at >= base + nkv * n) {
+        base += nkv * n;
+        ++b;
+      }
+      g = (at - base) / n;
+      const int off = at - base - g * n, to = min(n, off + end - at);
+      at += to - off;
+      t0 = max(off - 1, 0), t1 = to - 1;
+      if (t0 < t1) return true;  // else the share ends with the head's own unit
     }
-    g = (at - base) / n;
-    t0 = at - base - g * n;
-    t1 = min(n, t0 + end - at);
-    at += t1 - t0;
-    return true;
+    return false;
   }
 };
 
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     for (int b = lo; b < hi; ++b) {
       const int n = rows_of(p, b);
       sm.rows[b] = n;
-      mine += (n + kTile - 1) / kTile;
+      mine += units_of((n + kTile - 1) / kTile);
     }
     mine *= p.nkv;
     int incl = mine;
@@ -259,19 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const bool begins = beg < end && beg >= at && beg < at + mine, ends = beg < end && end - 1 >= at && end - 1 < at + mine;
     if (begins || ends || (blockIdx.x == 0 && WEIGHTS)) {
       for (int b = lo; b < hi; ++b) {
-        const int tiles = (sm.rows[b] + kTile - 1) / kTile, n = p.nkv * tiles;
-        if (WEIGHTS && blockIdx.x == 0) p.first_tile[b] = at;
+        const int units = units_of((sm.rows[b] + kTile - 1) / kTile), n = p.nkv * units;
+        if (WEIGHTS && blockIdx.x == 0) p.first_unit[b] = at;
         if (begins && beg >= at && beg < at + n) sm.first = b, sm.base = at;
         if (ends && end - 1 >= at && end - 1 < at + n) {
-          const int g = (end - 1 - at) / tiles, i0 = at + g * tiles, i1 = i0 + tiles;
-          const bool split = i0 >= beg && i1 > end;  // a head that begins here and ends elsewhere
+          const int g = (end - 1 - at) / units, i0 = at + g * units, i1 = i0 + units;
+          const bool split = i0 + 1 >= beg && i0 + 1 < end && i1 > end;  // a head whose first tile is here and whose last is elsewhere
           p.border[blockIdx.x] = make_int4(b, g, split ? shares.owner(i1 - 1) - blockIdx.x + 1 : 0, beg < i0);
         }
         at += n;
       }
     }
     if (beg >= end && tid == 0) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (WEIGHTS && blockIdx.x == 0 && tid == 0) p.first_tile[p.batch] = total;
+    if (WEIGHTS && blockIdx.x == 0 && tid == 0) p.first_unit[p.batch] = total;
     __syncthreads();
   }
   // sequences without rows: zeros
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         sm.factor[wr][w + 4][h] = f1;
         if (w == 0) {
           sm.sum[wr][h] = sum;
-          const float4 ml = make_float4(top, sum, seen ? 1.f : 0.f, 0.f);
+          const float2 ml = make_float2(top, seen ? sum : -1.f);
           if (alive && wr == 0 && h < p.group) {
             if (!whole) p.part_ml[part + h] = ml;
             else if (WEIGHTS) p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = ml;
@@ -622,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 constexpr int kJoin = 256;         // threads of the join
-constexpr int kJoinKeys = 1024;    // keys of a block that sums key weights
-constexpr int kAhead = 16;         // parts that a thread of the join asks for at once
+constexpr int kJoinKeys = 1024;    // keys of one of its blocks that sum key weights
+constexpr int kAhead = 8;          // parts that a thread of the join asks for at once
 
 // The place of part i of a head that begins in CTA c0's share, for its query head h.
 __device__ __forceinline__ long long part_slot(const PagedAttnParams& p, int c0, bool shifted, int i, int h) {
@@ -636,7 +643,7 @@ __device__ __forceinline__ long long part_slot(const PagedAttnParams& p, int c0,
 // (sequence, kv head, a share of the cached rows), the rows' weights over the
 // group's heads into the pages' entries.
 template <bool BF16, int HD, bool WEIGHTS>
-__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ PagedAttnParams p, int key_blocks) {
+__global__ void __launch_bounds__(kJoin, 4) join_kernel(const __grid_constant__ PagedAttnParams p, int key_blocks) {
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int joins = p.ctas * p.group;
@@ -651,14 +658,14 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
     if (n == 0) return;
     float top = -INFINITY, sum = 0.f, acc = 0.f, seen = 0.f;
     for (int i0 = sl; i0 < n; i0 += kAhead * kSlices) {
-      float4 ml[kAhead];
+      float2 ml[kAhead];
       float o[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int part = i0 + i * kSlices;
         const bool on = part < n;
         const long long s = part_slot(p, c0, border.w, on ? part : 0, h);
-        ml[i] = on ? __ldcg(p.part_ml + s) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        ml[i] = on ? __ldcg(p.part_ml + s) : make_float2(-INFINITY, -1.f);
         o[i] = on ? __ldcg(p.part_o + s * HD + d) : 0.f;
       }
       float now = top;
@@ -670,10 +677,11 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (i0 + i * kSlices >= n) break;
+        if (ml[i].y < 0.f) continue;  // no key seen
         const float w = exp2_fast(ml[i].x - base);
         sum += w * ml[i].y;
         acc += w * o[i];
-        seen += ml[i].z;
+        seen = 1.f;
       }
     }
     slice[sl][d] = acc;
@@ -699,43 +707,58 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Pag
     const int b = y / p.nkv, g = y - b * p.nkv;
     const long long first = static_cast<long long>(z) * kJoinKeys;
     pdl_wait();
-    const int n_rows = rows_of(p, b), total = __ldcg(p.first_tile + p.batch), tiles = (n_rows + kTile - 1) / kTile;
-    const int i0 = __ldcg(p.first_tile + b) + g * tiles;
+    const int n_rows = rows_of(p, b);
     if (first >= n_rows) return;
-    const Shares shares(total, p.ctas);
-    const int c0 = shares.owner(i0), n = shares.owner(i0 + tiles - 1) - c0 + 1;
-    const bool shifted = shares.start(c0) < i0;
-    for (int h = warp; h < p.group; h += kJoin / 32) {
-      float m, sum;
-      if (n == 1) {
-        const float4 ml = __ldcg(p.part_ml + (2ll * p.ctas + y) * p.group + h);  // the whole head's
-        m = ml.x, sum = ml.y;
-      } else {
-        m = -INFINITY, sum = 0.f;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(p.part_ml + part_slot(p, c0, shifted, i, h)).x);
-        m = warp_max(m);
-        const float base = m == -INFINITY ? 0.f : m;
-        for (int i = lane; i < n; i += 32) {
-          const float4 ml = __ldcg(p.part_ml + part_slot(p, c0, shifted, i, h));
-          sum += exp2_fast(ml.x - base) * ml.y;
-        }
-        sum = warp_sum(sum);
-      }
-      if (lane == 0) top[h] = m, inv[h] = 1.f / sum;
-    }
-    __syncthreads();
+    // the block's keys' pages and scores are asked for before the heads' sums are known
     const long long rows = static_cast<long long>(p.width) * p.page;
     const float* scores = p.scores + (static_cast<long long>(b) * p.nq + g * p.group) * rows;
-    // the block's lot of kJoinKeys, and what lies key_blocks further on
-    for (long long lot = first; lot < n_rows; lot += static_cast<long long>(key_blocks) * kJoinKeys)
-      for (int i = tid; i < kJoinKeys && lot + i < n_rows; i += kJoin) {
-        const int j = static_cast<int>(lot) + i, pi = j / p.page;
-        const int page = p.table[static_cast<long long>(b) * p.width + pi];
-        if (page < 0 || page >= p.n_pages) continue;
-        float w = 0.f;
-        for (int h = 0; h < p.group; ++h) w += exp2_fast(__ldcg(scores + h * rows + j) - top[h] + kLift<BF16>) * inv[h];
-        float* to = p.key_weights + (static_cast<long long>(page) * p.nkv + g) * p.page + (j - pi * p.page);
-        *to = p.decay == 0.f ? w : p.decay * *to + w;
+    const int* table = p.table + static_cast<long long>(b) * p.width;
+    constexpr int kKeys = kJoinKeys / kJoin, kEarly = 4;
+    float x[kKeys][kEarly];
+    int page[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const long long key = first + i * kJoin + tid;
+      page[i] = key < n_rows ? table[static_cast<int>(key) / p.page] : -1;
+#pragma unroll
+      for (int h = 0; h < kEarly; ++h) x[i][h] = key < n_rows && h < p.group ? __ldcg(scores + h * rows + key) : 0.f;
+    }
+    const int total = __ldcg(p.first_unit + p.batch), units = units_of((n_rows + kTile - 1) / kTile), i0 = __ldcg(p.first_unit + b) + g * units;
+    const Shares shares(total, p.ctas);
+    const int c0 = shares.owner(i0 + 1), n = shares.owner(i0 + units - 1) - c0 + 1;
+    const bool shifted = shares.start(c0) < i0;
+    for (int h = warp; h < p.group; h += kJoin / 32) {
+      float m = -INFINITY, sum = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float2 ml = __ldcg(p.part_ml + (n == 1 ? (2ll * p.ctas + y) * p.group + h : part_slot(p, c0, shifted, i, h)));  // one part: the whole head's
+        const float now = fmaxf(m, ml.x), base = now == -INFINITY ? 0.f : now;
+        sum = sum * exp2_fast(m - base) + exp2_fast(ml.x - base) * fmaxf(ml.y, 0.f);
+        m = now;
+      }
+      const float all = warp_max(m), base = all == -INFINITY ? 0.f : all;
+      sum = warp_sum(sum * exp2_fast(m - base));
+      if (lane == 0) top[h] = all, inv[h] = 1.f / sum;
+    }
+    __syncthreads();
+    auto put = [&](long long key, int at, const float (&early)[kEarly]) {
+      if (at < 0 || at >= p.n_pages) return;
+      float w = 0.f;
+#pragma unroll
+      for (int h = 0; h < kEarly; ++h)
+        if (h < p.group) w += exp2_fast(early[h] - top[h] + kLift<BF16>) * inv[h];
+      for (int h = kEarly; h < p.group; ++h) w += exp2_fast(__ldcg(scores + h * rows + key) - top[h] + kLift<BF16>) * inv[h];
+      float* to = p.key_weights + (static_cast<long long>(at) * p.nkv + g) * p.page + static_cast<int>(key) % p.page;
+      *to = p.decay == 0.f ? w : p.decay * *to + w;
+    };
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) put(first + i * kJoin + tid, page[i], x[i]);
+    // what lies key_blocks further on, where the grid is smaller than the tables
+    for (long long lot = first + static_cast<long long>(key_blocks) * kJoinKeys; lot < n_rows; lot += static_cast<long long>(key_blocks) * kJoinKeys)
+      for (long long key = lot + tid; key < min(lot + kJoinKeys, static_cast<long long>(n_rows)); key += kJoin) {
+        float late[kEarly];
+#pragma unroll
+        for (int h = 0; h < kEarly; ++h) late[h] = h < p.group ? __ldcg(scores + h * rows + key) : 0.f;
+        put(key, table[static_cast<int>(key) / p.page], late);
       }
   }
 }
@@ -774,7 +797,7 @@ cudaError_t paged_attn_ctas(int* ctas) {
 
 long long paged_attn_workspace(const PagedAttnParams& p, int hd, bool weights) {
   const long long parts = 2ll * p.ctas * p.group;
-  long long n = up256(parts * hd * 4) + up256(16 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
+  long long n = up256(parts * hd * 4) + up256(8 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
   n += up256(16ll * p.ctas) + up256(4ll * (p.batch + 1));
   if (weights) n += 4ll * p.batch * p.nq * (static_cast<long long>(p.width) * p.page);
   return n;
@@ -785,11 +808,11 @@ void paged_attn_place(PagedAttnParams& p, int hd, bool weights, void* workspace)
   const long long parts = 2ll * p.ctas * p.group;
   p.part_o = reinterpret_cast<float*>(at);
   at += up256(parts * hd * 4);
-  p.part_ml = reinterpret_cast<float4*>(at);
-  at += up256(16 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
+  p.part_ml = reinterpret_cast<float2*>(at);
+  at += up256(8 * (parts + (weights ? static_cast<long long>(p.batch) * p.nq : 0)));
   p.border = reinterpret_cast<int4*>(at);
   at += up256(16ll * p.ctas);
-  p.first_tile = reinterpret_cast<int*>(at);
+  p.first_unit = reinterpret_cast<int*>(at);
   at += up256(4ll * (p.batch + 1));
   p.scores = reinterpret_cast<float*>(at);
 }
