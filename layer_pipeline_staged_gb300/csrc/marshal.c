@@ -1,10 +1,10 @@
 /* Argument marshalling of the operators over a caller-owned cache and over pages: torch
  * tensors in, the C ABI's pointers, strides and host arrays out. A call's
  * kernels take 2 to 10 microseconds when the work is small; the same
- * marshalling in Python and ctypes took 5 to 7 of a call's 8 to 10 on the host,
- * this one takes about 2.5, 1 of it for the checks of lazy tensors and for
- * autograd's version counters. It knows tensors by their public attributes only
- * (no torch headers). What a tensor can tell is checked here (shape, type,
+ * marshalling in Python and ctypes took 5 to 7 of a call's 8 to 10 on the host, and more
+ * with the ten tensors of a call over pages. What a tensor is comes from torch's C++
+ * interface (tensors.h) where that has been built for the torch at hand, and from its
+ * public attributes otherwise. What a tensor can tell is checked here (shape, type,
  * device, strides), the rest by the library; ops.py documents the calls. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -12,6 +12,7 @@
 #include <string.h>
 
 #include "lps.h"
+#include "tensors.h"
 
 /* ---- what init() is given ------------------------------------------------- */
 
@@ -23,8 +24,12 @@ static PyObject *g_dual;  /* the __dict__ of torch.autograd.forward_ad */
 static PyObject *s_level, *s_unpack; /* in it: the current level of forward derivatives (-1: none), unpack_dual */
 static PyObject *s_dtype, *s_get_device, *s_data_ptr, *s_shape, *s_stride, *s_requires_grad, *s_device, *s_is_cuda, *s_is_neg;
 static PyObject *g_empty_names; /* ("dtype", "device") */
+static const tensor_api *g_fast; /* or NULL */
 
-#define MAX_DIM 5
+#define MAX_DIM LPS_TENSORS_DIM
+
+static PyObject *g_other; /* stands for every dtype that no call takes */
+static PyObject **const g_types[] = {&g_other, &g_bf16, &g_fp16, &g_fp32, &g_fp64, &g_int32}; /* by LPS_T_* */
 
 typedef struct {
   PyObject *obj, *dtype; /* borrowed: dtypes live as long as torch */
@@ -63,6 +68,19 @@ static int has_tangent(PyObject *obj) {
 
 /* The facts of `obj`; strides of axes with one entry are set to dense. */
 static int tensor_of(PyObject *obj, tensor *t, const char *what) {
+  tensor_facts f;
+  if (g_fast && !g_fast->facts(obj, &f)) {
+    t->obj = obj;
+    t->dtype = *g_types[f.dtype];
+    t->dim = f.dim;
+    memcpy(t->shape, f.shape, sizeof t->shape);
+    memcpy(t->stride, f.stride, sizeof t->stride);
+    t->device = f.device;
+    t->grad = f.grad;
+    t->ptr = f.ptr;
+    if (f.neg) goto neg;
+    goto known;
+  }
   PyObject *x = PyObject_GetAttr(obj, s_dtype);
   if (!x) goto not_tensor;
   t->obj = obj;
@@ -89,15 +107,13 @@ static int tensor_of(PyObject *obj, tensor *t, const char *what) {
     if (!(x = PyObject_CallMethodNoArgs(obj, s_is_neg))) goto not_tensor;
     const int neg = x == Py_True;
     Py_DECREF(x);
-    if (neg) { /* a lazy view: its memory holds the values before their sign changes */
-      PyErr_Format(PyExc_ValueError, "%s is a negative view: pass its resolve_neg()", what);
-      return -1;
-    }
+    if (neg) goto neg;
   }
   if (!(x = PyObject_CallMethodNoArgs(obj, s_data_ptr))) goto not_tensor;
   t->ptr = PyLong_AsVoidPtr(x);
   Py_DECREF(x);
   if (PyErr_Occurred()) return -1;
+known:;
   const int dual = has_tangent(obj);
   if (dual > 0) PyErr_Format(PyExc_ValueError, "%s carries a forward derivative, and there is none of these operators", what);
   if (dual) return -1;
@@ -107,6 +123,9 @@ static int tensor_of(PyObject *obj, tensor *t, const char *what) {
     dense *= t->shape[i];
   }
   return 0;
+neg: /* a lazy view: its memory holds the values before their sign changes */
+  PyErr_Format(PyExc_ValueError, "%s is a negative view: pass its resolve_neg()", what);
+  return -1;
 not_tensor:
   if (PyErr_ExceptionMatches(PyExc_AttributeError)) PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
   return -1;
@@ -379,28 +398,37 @@ static int scale_of(PyObject *obj, float *scale) {
   return *scale == 0.f && x != 0. ? refuse("scale must be 0 or a number that 32 bits hold") : 0;
 }
 
+/* A new dense tensor (a new reference) by the fast way, or NULL without an error. */
+static PyObject *fast_empty(const int64_t *shape, int dim, PyObject *dtype, int device) {
+  for (int i = 1; g_fast && i < (int)(sizeof g_types / sizeof *g_types); ++i)
+    if (dtype == *g_types[i]) return g_fast->empty(shape, dim, i, device);
+  return NULL;
+}
+
 /* The output: `out` checked against q, or a new dense tensor like q (a new reference). */
 static PyObject *output_like(PyObject *out, const tensor *q, tensor *o) {
   if (out != Py_None) {
     Py_INCREF(out);
     return out;
   }
-  PyObject *shape = PyObject_GetAttr(q->obj, s_shape), *device = PyObject_GetAttr(q->obj, s_device);
-  if (shape && device) {
-    PyObject *const args[3] = {shape, q->dtype, device};
-    out = PyObject_Vectorcall(g_empty, args, 1, g_empty_names);
-  } else {
-    out = NULL;
+  if (!(out = fast_empty(q->shape, q->dim, q->dtype, q->device))) {
+    PyObject *shape = PyObject_GetAttr(q->obj, s_shape), *device = PyObject_GetAttr(q->obj, s_device);
+    if (shape && device) {
+      PyObject *const args[3] = {shape, q->dtype, device};
+      out = PyObject_Vectorcall(g_empty, args, 1, g_empty_names);
+    }
+    Py_XDECREF(shape);
+    Py_XDECREF(device);
   }
-  Py_XDECREF(shape);
-  Py_XDECREF(device);
   if (out && tensor_of(out, o, "out")) Py_CLEAR(out);
   return out;
 }
 
 /* A new dense tensor [n] of `dtype` on the device of `like` (a new reference). */
-static PyObject *new_array(int64_t n, PyObject *dtype, PyObject *like) {
-  PyObject *shape = Py_BuildValue("(L)", (long long)n), *device = PyObject_GetAttr(like, s_device), *x = NULL;
+static PyObject *new_array(int64_t n, PyObject *dtype, const tensor *like) {
+  PyObject *x = fast_empty(&n, 1, dtype, like->device);
+  if (x) return x;
+  PyObject *shape = Py_BuildValue("(L)", (long long)n), *device = PyObject_GetAttr(like->obj, s_device);
   if (shape && device) {
     PyObject *const args[3] = {shape, dtype, device};
     x = PyObject_Vectorcall(g_empty, args, 1, g_empty_names);
@@ -413,6 +441,10 @@ static PyObject *new_array(int64_t n, PyObject *dtype, PyObject *like) {
 /* Tells autograd that a call that has been enqueued writes `a` (and `b`) in place: an earlier operation that
  * saved one of them for its backward then refuses to run on the new values. */
 static int written(PyObject *a, PyObject *b) {
+  if (g_fast && !g_fast->written(a)) {
+    if (!b || !g_fast->written(b)) return 0;
+    a = b, b = NULL; /* the Python way has its error */
+  }
   PyObject *both = b ? PyTuple_Pack(2, a, b) : PyTuple_Pack(1, a), *r = both ? PyObject_CallOneArg(g_written, both) : NULL;
   Py_XDECREF(both);
   Py_XDECREF(r);
@@ -802,7 +834,7 @@ static PyObject *evict_paged(PyObject *self, PyObject *const *args, Py_ssize_t n
     if (PyErr_Occurred()) return NULL;
     if (size[i] < INT32_MIN || size[i] > INT32_MAX) return refuse("budget and recent must fit 32 bits"), NULL;
   }
-  PyObject *made = new_array(batch, g_int32, kp->obj);
+  PyObject *made = new_array(batch, g_int32, kp);
   if (!made || tensor_of(made, &out, "new lengths") || enter(&at, kp->device)) return Py_XDECREF(made), NULL;
   const long long bytes = kv_pages_evict_workspace((int)batch, (int)kp->shape[1], (int)size[0]);
   int rc = bytes < 0 ? (int)bytes : 0;
@@ -882,10 +914,14 @@ static PyObject *host_ints(PyObject *self, PyObject *const *args, Py_ssize_t n) 
   return list;
 }
 
-/* init(LpsError, torch): what the calls need of torch, looked up once. */
+/* init(LpsError, torch, tensors' api or None): what the calls need of torch, looked up once. */
 static PyObject *init(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   (void)self;
-  if (argc_is(n, 2)) return NULL;
+  if (argc_is(n, 3)) return NULL;
+  g_fast = NULL;
+  if (args[2] != Py_None && !(g_fast = PyCapsule_GetPointer(args[2], "layer_pipeline_staged_gb300.tensor_api"))) return NULL;
+  Py_INCREF(Py_None);
+  g_other = Py_None;
   PyObject *torch = args[1], *cuda = PyObject_GetAttrString(torch, "cuda"), *c = PyObject_GetAttrString(torch, "_C");
   Py_INCREF(args[0]);
   g_error = args[0];

@@ -32,9 +32,18 @@ def _ready():
     except ImportError as e:
         raise RuntimeError("the torch wrappers' marshalling is missing for this Python: build it first "
                            "(python -m layer_pipeline_staged_gb300.build, which needs Python.h)") from e
-    _marshal.init(_capi.LpsError, torch)
+    _marshal.init(_capi.LpsError, torch, _tensors(torch))
     _m = _marshal
     return _m
+
+
+def _tensors(torch):
+    """The tensors' facts by torch's C++ interface, if they have been built for this torch; None: by its Python one."""
+    try:
+        from . import _tensors as t
+    except ImportError:
+        return None
+    return t.api if torch.__version__.split("+")[0] == t.torch_version.split("+")[0] else None
 
 
 def attention_prompt_packed(q, k, v, offsets, out=None, scale=0.0):
