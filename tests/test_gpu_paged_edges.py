@@ -1,0 +1,232 @@
+"""The operators over pages where callers meet them: host threads, streams, graphs that take turns, autograd's bookkeeping, both
+ways of reading tensors, equal bits for equal calls, and tensors that do not fit."""
+import threading
+
+import pytest
+
+import layer_pipeline_staged_gb300 as lps
+from layer_pipeline_staged_gb300 import ops
+
+torch = pytest.importorskip("torch")
+from paged import Paged, gen, i32, randn  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+class Step:
+    """Inputs of every operator over pages, and one call of each."""
+
+    def __init__(self, seed=1, lens=(200, 3, 0, 65)):
+        g = gen(seed)
+        self.c = Paged(list(lens), 2, 64, 16, BF, seed=seed, spare=40)
+        n = len(lens)
+        self.q, self.k, self.v = (randn(g, n, h, 64, dtype=BF) for h in (8, 2, 2))
+        self.kp, self.vp = self.c.kp.clone(), self.c.vp.clone()
+        self.w = torch.rand(self.c.pages, 2, 16, generator=g, device="cuda")
+        self.f = lps.rotary_frequencies(64).cuda()
+        self.pos = i32(range(n))
+        self.fresh = i32(self.c.free[:4 * n].reshape(n, 4))
+        self.x = randn(g, n, 1000, dtype=torch.float32)
+        self.tokens = torch.randint(0, 1000, (n, 300), generator=g, device="cuda", dtype=torch.int32)
+        self.ids = torch.randint(0, 1000, (n, 20), generator=g, device="cuda", dtype=torch.int32)
+        self.bias = randn(g, n, 20, dtype=torch.float32)
+        self.count, self.half = torch.full((n,), 300, device="cuda", dtype=torch.int32), torch.full((n,), 0.5, device="cuda")
+
+    def rows(self):
+        return lps.rotary_rows(self.q, self.k, self.pos, self.f)
+
+    def append(self):
+        kp, vp = self.kp.clone(), self.vp.clone()
+        return lps.rotary_append_paged(self.q, self.k, self.v, None, self.c.lengths, self.c.table, kp, vp, self.f), kp, vp
+
+    def attend(self):
+        w = self.w.clone()
+        return lps.attention_paged_decode(self.q, self.kp, self.vp, self.c.table, self.c.lengths, key_weights=w), w
+
+    def evict(self):
+        kp, vp, w = self.kp.clone(), self.vp.clone(), self.w.clone()
+        return lps.kv_pages_evict(kp, vp, w, self.c.table, self.c.lengths, self.fresh, 50, 10), kp, vp, w
+
+    def logits(self):
+        return (lps.logits_adjust(self.x, tokens=self.tokens, lengths=self.count, repetition=self.half + 1, frequency=self.half,
+                                  presence=self.half, bias_ids=self.ids, bias=self.bias),)
+
+    def all(self):
+        return [t for f in (self.rows, self.append, self.attend, self.evict, self.logits) for t in f()]
+
+
+def same(a, b):
+    return len(a) == len(b) and all(torch.equal(x.nan_to_num(nan=-9.0) if x.is_floating_point() else x,
+                                                y.nan_to_num(nan=-9.0) if y.is_floating_point() else y) for x, y in zip(a, b))
+
+
+def test_equal_calls_give_equal_bits():
+    s = Step(lens=(2000, 3, 0, 65, 900, 1000))
+    want = s.all()
+    for _ in range(5):
+        assert same(s.all(), want)
+
+
+def test_a_host_threads_first_calls_and_threads_side_by_side():
+    steps = [Step(seed) for seed in (1, 2, 3)]
+    want = [s.all() for s in steps]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got = steps[i].all()
+                torch.cuda.current_stream().synchronize()
+                if not same(got, want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    lps.cache_ops_status()
+
+
+def test_inputs_made_on_another_stream():
+    """The calls run on the current stream, behind what that stream waits for."""
+    s = Step()
+    want = s.all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+        t = Step()
+        got = t.all()
+    torch.cuda.current_stream().wait_stream(side)
+    assert same(got, want)
+
+
+def test_graphs_that_take_turns_in_one_pool():
+    """Two captured steps that share a memory pool, replayed in turn and one after the other without a pause."""
+    steps = [Step(1), Step(2, (70, 500, 1))]
+    want = [s.all() for s in steps]
+    graphs, out = [], []
+    pool = torch.cuda.graph_pool_handle()
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            o = s.all()
+            keep = [t.clone() for t in o]
+        graphs.append(g)
+        out.append((o, keep))
+    for order in ((0, 1, 0, 1), (1, 0), (0, 0, 1)):
+        for i in order:
+            graphs[i].replay()
+            got = [t.clone() for t in out[i][1]]
+            assert same(got, want[i])
+
+
+def test_both_ways_of_reading_tensors_agree():
+    s = Step()
+    want = s.all()
+    m = ops._ready()
+    assert ops._tensors(torch) is not None, "the quick way has not been built for this torch"
+    try:
+        m.init(lps.LpsError, torch, None)
+        assert same(s.all(), want)
+        with pytest.raises(ValueError, match="type"):
+            lps.rotary_rows(s.q.half(), s.k, s.pos, s.f)
+    finally:
+        m.init(lps.LpsError, torch, ops._tensors(torch))
+    assert same(s.all(), want)
+
+    class Kind(torch.Tensor):
+        pass
+
+    q = s.q.as_subclass(Kind)  # read by its attributes
+    assert torch.equal(lps.attention_paged_decode(q, s.kp, s.vp, s.c.table, s.c.lengths), s.attend()[0])
+
+
+def test_autograd_knows_and_is_refused():
+    s = Step()
+    versions = [t._version for t in (s.kp, s.vp, s.w)]
+    lps.rotary_append_paged(s.q, s.k, s.v, None, s.c.lengths, s.c.table, s.kp, s.vp, s.f, key_weights=s.w)
+    assert [t._version for t in (s.kp, s.vp, s.w)] == [v + 1 for v in versions]
+    out = torch.empty_like(s.q)
+    lps.attention_paged_decode(s.q, s.kp, s.vp, s.c.table, s.c.lengths, key_weights=s.w, out=out)
+    assert out._version == 1 and s.w._version == versions[2] + 2 and s.kp._version == versions[0] + 1
+    lps.kv_pages_evict(s.kp, s.vp, s.w, s.c.table, s.c.lengths, s.fresh, 50)
+    assert s.kp._version == versions[0] + 2 and s.w._version == versions[2] + 3
+    x = s.x.clone()
+    lps.logits_adjust(x, tokens=s.tokens, lengths=s.count, out=x)
+    assert x._version == 1
+    q = s.q.clone()
+    lps.rotary_rows(q, s.k, s.pos, s.f, out=(q, torch.empty_like(s.k)))
+    assert q._version == 1
+
+    leaf = s.q.clone().requires_grad_()
+    for call in (lambda: lps.rotary_rows(leaf, s.k, s.pos, s.f), lambda: lps.attention_paged_decode(leaf, s.kp, s.vp, s.c.table, s.c.lengths),
+                 lambda: lps.attention_paged_decode(s.q, s.kp, s.vp, s.c.table, s.c.lengths, key_weights=s.w.clone().requires_grad_()),
+                 lambda: lps.logits_adjust(s.x.clone().requires_grad_()),
+                 lambda: lps.logits_adjust(s.x, bias_ids=s.ids, bias=s.bias.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="backward"):
+            call()
+        with torch.no_grad():
+            call()
+    want = s.all()
+    with torch.inference_mode():
+        assert same(s.all(), want)
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    s = Step()
+    c, wide = s.c, s.c.table.long()
+    ok = dict(table=c.table, lengths=c.lengths)
+
+    def attend(q=s.q, kp=s.kp, vp=s.vp, key_weights=None, out=None, **kw):
+        a = dict(ok, **kw)
+        return lps.attention_paged_decode(q, kp, vp, a["table"], a["lengths"], key_weights=key_weights, out=out)
+
+    attend()
+    for kw in (dict(q=s.q[:3]), dict(q=s.q[:, :7]), dict(q=s.q[..., :32]), dict(kp=s.kp[:, :1]), dict(kp=s.kp.transpose(1, 2)), dict(kp=s.kp[::2], vp=s.vp[::2]),
+               dict(vp=s.vp.half()), dict(table=wide), dict(table=c.table[:, ::2]), dict(table=c.table[:3]), dict(table=c.table.cpu()),
+               dict(lengths=c.lengths[:3]), dict(lengths=c.lengths.cpu()), dict(lengths=c.lengths.float()), dict(key_weights=s.w[:-1]),
+               dict(key_weights=s.w.half()), dict(key_weights=s.w.double()), dict(out=s.q[:, :4]), dict(out=s.q.float())):
+        with pytest.raises((ValueError, lps.LpsError)):
+            attend(**kw)
+    with pytest.raises(ValueError, match="freqs"):
+        lps.rotary_rows(s.q, s.k, s.pos, s.f.float())
+    with pytest.raises(lps.LpsError, match="rot_dim"):
+        lps.rotary_rows(s.q, s.k, s.pos, s.f[:20])
+    with pytest.raises(ValueError, match="positions"):
+        lps.rotary_rows(s.q, s.k, s.pos[:2], s.f)
+    with pytest.raises(lps.LpsError, match="one token a sequence"):
+        lps.rotary_append_paged(s.q, s.k, s.v, None, c.lengths[:2], c.table[:2], s.kp, s.vp, s.f)
+    flat = torch.zeros(s.w.numel() + 1, device="cuda")[1:].view(s.w.shape)
+    with pytest.raises(lps.LpsError, match="aligned"):
+        lps.kv_pages_evict(s.kp, s.vp, flat, c.table, c.lengths, s.fresh, 50)
+    with pytest.raises(lps.LpsError, match="room"):
+        lps.kv_pages_evict(s.kp, s.vp, s.w, c.table, c.lengths, s.fresh, 65)
+    with pytest.raises(TypeError):
+        lps.kv_pages_evict(s.kp, s.vp, s.w, c.table, c.lengths, s.fresh, 50.5)
+    for kw in (dict(tokens=s.tokens), dict(lengths=s.count), dict(repetition=s.half), dict(bias=s.bias), dict(allowed=s.tokens),
+               dict(tokens=s.tokens.long(), lengths=s.count), dict(bias_ids=s.ids, bias=s.bias[:, :3]), dict(out=s.x.half())):
+        with pytest.raises(ValueError):
+            lps.logits_adjust(s.x, **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        lps.logits_adjust(s.x.t())
+    with pytest.raises(ValueError, match="float32"):
+        lps.logits_adjust(s.x.double())
+
+
+def test_empty_calls():
+    s = Step()
+    q, k = lps.rotary_rows(s.q[:0], s.k[:0], s.pos[:0], s.f)
+    assert q.shape == (0, 8, 64) and k.shape == (0, 2, 64)
+    off = torch.zeros(5, device="cuda", dtype=torch.int32)
+    kp = s.kp.clone()
+    assert lps.rotary_append_paged(s.q[:0], s.k[:0], s.v[:0], off, s.c.lengths, s.c.table, kp, s.vp, s.f).shape == (0, 8, 64)
+    assert torch.equal(kp.nan_to_num(), s.kp.nan_to_num())
+    assert lps.logits_adjust(s.x[:0]).shape == (0, 1000) and lps.logits_adjust(s.x[:, :0]).shape == (4, 0)
+    assert torch.equal(lps.logits_adjust(s.x, tokens=s.tokens[:, :0], lengths=s.count, repetition=s.half), s.x)
+    assert torch.equal(lps.logits_adjust(s.x, bias_ids=s.ids[:, :0], bias=s.bias[:, :0]), s.x)

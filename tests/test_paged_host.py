@@ -158,3 +158,12 @@ def test_tensors_off_the_gpu_and_of_other_kinds_are_refused():
                     call(*[wrong if m == n else t for m, t in enumerate(tensors)])
             with fwd.dual_level(), pytest.raises(ValueError, match="forward derivative"):
                 call(*[fwd.make_dual(t, torch.ones_like(t)) if m == n else t for m, t in enumerate(tensors)])
+
+
+def test_the_quick_way_of_reading_tensors_is_for_one_torch(monkeypatch):
+    from layer_pipeline_staged_gb300 import ops
+    if lps_build._torch() is None:
+        pytest.skip("this torch has no headers")
+    assert ops._tensors(torch) is not None
+    monkeypatch.setattr(torch, "__version__", "0.1.2+other")
+    assert ops._tensors(torch) is None
