@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kTile = 64;          // keys of a tile
 constexpr int kConsumers = 8;      // warps of 16 keys; two teams
-constexpr int kProducers = 2;      // warps that feed the ring, one for each team
+constexpr int kProducers = 2;      // warps that feed the ring, one with K and one with V
 constexpr int kWriters = 2;        // warps that finish pieces
 constexpr int kThreads = (kConsumers + kProducers + kWriters) * 32;
 constexpr int kMaxParts = 256;     // CTAs of a launch, and so parts of a head
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], kProducers);
       mbar_init(&sm.empty[i], kConsumers / 2);
     }
     for (int i = 0; i < S::kSlots; ++i) {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   pdl_launch_dependents();
 
   // the tiles of every sequence, and where this CTA's share begins
-  int beg, end;
+  int beg, end, total = 0;
   {
     const int per = (p.batch + kThreads - 1) / kThreads, lo = min(tid * per, p.batch), hi = min(lo + per, p.batch);
     int mine = 0;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
-    int before = 0, total = 0;
+    int before = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w == warp) before = total;
@@ -261,19 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const Shares shares(total, p.ctas);
     beg = end = total;
     if (static_cast<int>(blockIdx.x) < shares.ctas) beg = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
-    // the sequences in which the share begins and ends; what the join needs to know
+    // the sequence in which the share begins
     int at = before + incl - mine;
-    const bool begins = beg < end && beg >= at && beg < at + mine, ends = beg < end && end - 1 >= at && end - 1 < at + mine;
-    if (begins || ends || (blockIdx.x == 0 && WEIGHTS)) {
+    const bool begins = beg < end && beg >= at && beg < at + mine;
+    if (begins || (blockIdx.x == 0 && WEIGHTS)) {
       for (int b = lo; b < hi; ++b) {
-        const int units = units_of((sm.rows[b] + kTile - 1) / kTile), n = p.nkv * units;
+        const int n = p.nkv * units_of((sm.rows[b] + kTile - 1) / kTile);
         if (WEIGHTS && blockIdx.x == 0) p.first_unit[b] = at;
         if (begins && beg >= at && beg < at + n) sm.first = b, sm.base = at;
-        if (ends && end - 1 >= at && end - 1 < at + n) {
-          const int g = (end - 1 - at) / units, i0 = at + g * units, i1 = i0 + units;
-          const bool split = i0 + 1 >= beg && i0 + 1 < end && i1 > end;  // a head whose first tile is here and whose last is elsewhere
-          p.border[blockIdx.x] = make_int4(b, g, split ? shares.owner(i1 - 1) - blockIdx.x + 1 : 0, beg < i0);
-        }
         at += n;
       }
     }
@@ -290,16 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const long long limit = wait_cycles(p.wait_limit);
 
   if (warp >= kConsumers && warp < kConsumers + kProducers) {
-    // ---- a team's producer ----
-    const int team = warp - kConsumers;
+    // ---- the producer of K or of V (and q): what is on its way first takes half the time ----
+    const int v = warp - kConsumers;
     const uint64_t pol = l2_evict_first();
     const int log_box = 31 - __clz(p.box), log_boxes = 6 - log_box, boxes = 1 << log_boxes;  // boxes of a tile
     const int page_boxes = p.page >> log_box;
-    // a lane's part of a tile: box `bx` of K or V
-    const int bx = lane & (boxes - 1), v = lane >> log_boxes;
-    const bool carries = v < 2;
+    // a lane's part of a tile: box `lane`
     const int box_bytes = p.box * HD * 2;
-    uint8_t* const dst = carries ? sm.kv[0][v] + bx * box_bytes : nullptr;
+    uint8_t* const dst = sm.kv[0][v] + (lane & (boxes - 1)) * box_bytes;
     const CUtensorMap* const map = v ? &p.tmap_v : &p.tmap_k;
     const uint32_t all = (1u << boxes) - 1;
     // Pages of 32 boxes of a sequence, one a lane: (page, row in the page). The
@@ -325,26 +318,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         else if (more) ahead = look(next, next.t0);
         const uint32_t good = __ballot_sync(0xffffffffu, now.x >= 0 && now.x < p.n_pages);
         const int l1 = min(n_tiles, l0 + lot);
-        for (int i = l0 + ((it + l0 + team) & 1); i < l1; i += 2) {
+        for (int i = l0; i < l1; ++i) {
           const int stage = (it + i) % S::kStages, use = (it + i) / S::kStages, t = walk.t0 + i;
           if (use) {
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[stage], (use - 1) & 1, limit));
             if (!ok) break;
           }
           const uint32_t valid = good >> ((i - l0) << log_boxes) & all;
-          const bool with_q = i < 2;  // the team's first tile of the piece
-          const int from = ((i - l0) << log_boxes) + bx;
+          const bool with_q = v == 1 && i < 2;  // a team's first tile of the piece
+          const int from = ((i - l0) << log_boxes) + (lane & (boxes - 1));
           const int page = __shfl_sync(0xffffffffu, now.x, from), row = __shfl_sync(0xffffffffu, now.y, from);
           if (lane == 0) {
-            sm.valid[stage] = valid == all && (t + 1) * kTile <= n_rows ? kWhole : valid;
-            mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * 2 * box_bytes + (with_q ? p.group * HD * 2 : 0));
+            if (v == 0) sm.valid[stage] = valid == all && (t + 1) * kTile <= n_rows ? kWhole : valid;
+            mbar_arrive_expect_tx(&sm.full[stage], __popc(valid) * box_bytes + (with_q ? p.group * HD * 2 : 0));
           }
           __syncwarp();
-          if (carries && (valid >> bx & 1)) tma_5d(dst + stage * (2 * S::kBytes), map, row, walk.g, page, &sm.full[stage], pol);
           if (with_q && lane < p.group)
             bulk_g2s_plain(sm.q[stage] + lane * S::kQRow,
                            static_cast<const char*>(p.q) + 2 * (walk.b * p.q_seq + static_cast<long long>(walk.g * p.group + lane) * p.q_head),
                            HD * 2, &sm.full[stage]);
+          if (lane < boxes && (valid >> lane & 1)) tma_5d(dst + stage * (2 * S::kBytes), map, row, walk.g, page, &sm.full[stage], pol);
           __syncwarp();
           last = it + i;
         }
@@ -353,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       walk = next;
     }
     if (!ok && lane == 0) report_error(g_status, kErrWaitEmpty | kKid);
-    // what is in flight lands before the CTA ends: the team's last tiles
-    for (int i = last - (S::kStages - 2); i <= last; i += 2)
+    // what is in flight lands before the CTA ends
+    for (int i = last - (S::kStages - 1); i <= last; ++i)
       if (i >= 0 && !mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, ok ? limit : kDrainLimitCycles)) {
         if (lane == 0) report_error(g_status, kErrDrain | kKid);
         break;
@@ -366,8 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     // ---- the writers: eight warps' (o, m, l) of a piece, in warp order; warp = head ----
     int it = 0;
     bool alive = true;
+    const bool tells = warp == kConsumers + kProducers && lane == 0;  // the join of a head that begins here and ends elsewhere
+    if (tells) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int piece = 0; walk.next(); ++piece) {
       const int n = walk.t1 - walk.t0, sl = piece % S::kSlots;
+      if (tells && walk.t0 == 0 && n < walk.tiles()) {
+        const int units = walk.tiles() + 1, i0 = walk.base + walk.g * units;
+        p.border[blockIdx.x] = make_int4(walk.b, walk.g, Shares(total, p.ctas).owner(i0 + units - 1) - blockIdx.x + 1, beg < i0);
+      }
       const int w0 = n == 1 && (it & 1) ? kConsumers / 2 : 0, w1 = n == 1 && !(it & 1) ? kConsumers / 2 : kConsumers;  // the warps that had tiles
       it += n;
       if (alive) alive = mbar_wait(&sm.slot_full[sl], (piece / S::kSlots) & 1, limit);
