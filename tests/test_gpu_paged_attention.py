@@ -285,3 +285,32 @@ def test_an_empty_cache_and_math():
     q = randn(gen(12), 2, 4, 64, dtype=torch.float16)
     assert (lps.attention_paged_decode(q, c.kp, c.vp, c.table, c.lengths) == 0).all()
     assert math.isfinite(float(q.sum()))
+
+
+@pytest.mark.parametrize("nq,nkv,hd,lens", [(32, 8, 128, [9000]), (32, 8, 128, [1000, 8191, 0, 333, 64, 2000]), (4, 2, 64, [5000, 70]), (32, 32, 64, [700] * 9),
+                                            (28, 4, 128, [20000, 1]), (12, 4, 128, [3000] * 3), (8, 1, 128, [12000]), (3, 1, 128, [9000, 100])])
+def test_heads_in_parts_are_joined_every_time(nq, nkv, hd, lens):
+    """Whichever CTA finishes last, and in every replay: hundreds of calls of few and of many parts a head, two graphs in turn."""
+    c = Paged(lens, nkv, hd, 16, torch.bfloat16)
+    q = randn(gen(13), len(lens), nq, hd, dtype=torch.bfloat16)
+    want = lps.attention_paged_decode(q, c.kp, c.vp, c.table, c.lengths)
+    check(c, q, want)
+    out = torch.empty_like(q)
+    wrong = torch.zeros((), device="cuda", dtype=torch.int64)
+    for _ in range(300):
+        out.fill_(float("nan"))
+        lps.attention_paged_decode(q, c.kp, c.vp, c.table, c.lengths, out=out)
+        wrong += (out != want).any()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                out.fill_(float("nan"))
+                lps.attention_paged_decode(q, c.kp, c.vp, c.table, c.lengths, out=out)
+                wrong += (out != want).any()
+        graphs.append(g)
+    for i in range(100):
+        graphs[i % 2].replay()
+    assert int(wrong) == 0
+    lps.cache_ops_status()
