@@ -230,3 +230,66 @@ def test_empty_calls():
     assert lps.logits_adjust(s.x[:0]).shape == (0, 1000) and lps.logits_adjust(s.x[:, :0]).shape == (4, 0)
     assert torch.equal(lps.logits_adjust(s.x, tokens=s.tokens[:, :0], lengths=s.count, repetition=s.half), s.x)
     assert torch.equal(lps.logits_adjust(s.x, bias_ids=s.ids[:, :0], bias=s.bias[:, :0]), s.x)
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from test_gpu_paged_edges import Step, same
+s = Step()
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    out = [t.clone() for t in s.all()]
+g.replay()
+torch.cuda.synchronize()
+assert same(out, s.all())
+print("fine")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=os.path.dirname(tests), tests=tests)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("page", [1000, 4096])
+def test_caches_of_one_page_a_sequence(page):
+    """A contiguous cache [sequences, kv heads, max_ctx, head_dim] is pages of max_ctx rows: what the operators on it give."""
+    lens, nkv, hd = [min(page, 900), 1, 300], 2, 128
+    g = gen(4)
+    kc, vc = (randn(g, 3, nkv, page, hd, dtype=BF) for _ in range(2))
+    q = randn(g, 3, 8, hd, dtype=BF)
+    table, chain = i32([[0], [1], [2]]), torch.full((3, 1), -1, device="cuda", dtype=torch.int32)
+    out = lps.attention_paged_decode(q, kc, vc, table, i32(lens))
+    tree = lps.attention_tree_verify(q[:, None], kc, vc, chain, [n - 1 for n in lens], [1, 1, 1])[:, 0]
+    assert (out.float() - tree.float()).abs().max() <= 2 * 2.0 ** -8 * tree.float().abs().max()  # two results, rounded once, and weights of 8 bits
+    k, v = randn(g, 5, nkv, hd, dtype=BF), randn(g, 5, nkv, hd, dtype=BF)
+    a, b, c, d = kc.clone(), vc.clone(), kc.clone(), vc.clone()
+    lps.kv_rows_append(k, v, [0, 2, 2, 5], a, b, [10, 0, 296])
+    lps.rotary_append_paged(randn(g, 5, 8, hd, dtype=BF), k, v, i32([0, 2, 2, 5]), i32([12, 0, 299]), table, c, d, None)
+    assert torch.equal(a, c) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("tokens", [3, 400])
+def test_many_heads_a_token(tokens):
+    """More (token, head) rows than a block places at once: every head as if alone."""
+    g, f = gen(6), lps.rotary_frequencies(64).cuda()
+    q, k, v = randn(g, tokens, 700, 64, dtype=BF), randn(g, tokens, 130, 64, dtype=BF), randn(g, tokens, 130, 64, dtype=BF)
+    pos = torch.arange(50, 50 + tokens, device="cuda", dtype=torch.int32)
+    qo, ko = lps.rotary_rows(q, k, pos, f)
+    for h in (0, 1, 511, 512, 699):
+        one, _ = lps.rotary_rows(q[:, h:h + 1].contiguous(), k[:, :1], pos, f)
+        assert torch.equal(qo[:, h:h + 1], one)
+    kp, vp = (torch.zeros(tokens // 8 + 1, 130, 8, 64, device="cuda", dtype=BF) for _ in range(2))
+    table = torch.arange(kp.shape[0], device="cuda", dtype=torch.int32)[None]
+    qa = lps.rotary_append_paged(q, k, v, i32([0, tokens]), i32([tokens]), table, kp, vp, f, positions=pos)
+    assert torch.equal(qa, qo)
+    assert torch.equal(kp.transpose(1, 2).reshape(-1, 130, 64)[:tokens], ko) and torch.equal(vp.transpose(1, 2).reshape(-1, 130, 64)[:tokens], v)
+    same_q, same_k = lps.rotary_rows(q, k, pos, None)  # nothing turns
+    assert torch.equal(same_q, q) and torch.equal(same_k, k)
