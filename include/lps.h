@@ -592,6 +592,8 @@ int cache_ops_set_wait_limit(long long cycles);
  *     it was given. The calls say what becomes of a sequence that breaks the rules;
  *   - key_weights is a device float array [n_pages][n_kv_heads][page_size], one
  *     weight a cached key and kv head;
+ *   - arrays of integers, floats and doubles need the alignment of their elements
+ *     (kv_pages_evict's key_weights 16 bytes), logits that of theirs;
  *   - a call with a workspace uses it from its start on the stream to its end; calls
  *     that may overlap need workspaces of their own. Its contents need not be set. */
 #define LPS_TYPE_FP32 2
@@ -634,7 +636,8 @@ int rotary_append_paged(const void* q, const void* k, const void* v, void* q_out
                         int n_q_heads, int n_kv_heads, int head_dim, const int64_t* strides, void* stream);
 
 /* The workspace bytes of attention_paged_decode on the current device (weights:
- * not 0 with key_weights), or a negative LPS_E* code. */
+ * not 0 with key_weights: 4 bytes a q head and row that the tables have room for, on
+ * top of some megabytes), or a negative LPS_E* code. */
 long long attention_paged_decode_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
                                            int table_width, int weights);
 
@@ -699,9 +702,10 @@ int kv_pages_evict(void* k_pages, void* v_pages, float* key_weights, int n_pages
  *              [0, vocab) do not count. width 0: no history
  *   repetition, frequency, presence  device float[batch], or NULL: 1, 0, 0
  *   bias_ids, bias  device int32 and float [batch][n_bias]; ids outside [0, vocab) do
- *              not count, equal ones add up in order. n_bias 0: none
+ *              not count, equal ones add up one after another. n_bias 0: none
  *   allowed    device [batch][(vocab + 31) / 32] bits, bit i % 32 of word i / 32 set
- *              where token i is allowed; or NULL: all are */
+ *              where token i is allowed; or NULL: all are
+ * width and n_bias are below 2^30. */
 int logits_adjust(const void* logits, void* out, int type, int batch, int vocab, const int64_t* strides,
                   const int32_t* tokens, int width, const int32_t* lengths, const int32_t* prompt_lengths,
                   const float* repetition, const float* frequency, const float* presence, const int32_t* bias_ids,

@@ -4,24 +4,36 @@
 // For query head h of sequence b, with x_j = scale log2(e) q.k_j over the rows
 // j < lengths[b] on valid pages,
 //     o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m),
-// in one pass over K and V with the running maximum m. The lengths lie on the
-// device, so the split is made there: all tiles (sequence, kv head, 64 keys) in
-// one row, an equal share for every CTA, one CTA per SM. A CTA's share is a run
-// of pieces, each of one (sequence, kv head); a piece that is not the whole
-// head leaves (o, m, sum) in the workspace, and join_kernel puts them together
-// in order. Every sum has one order given by the lengths: equal calls give
-// equal bits.
+// in one pass over K and V. m follows the running maximum when that has grown by
+// more than 2^8 (o and the sum carry any common factor exactly as well). The
+// lengths lie on the device, so the split is made there: the tiles (64 keys) of all
+// (sequence, kv head) and a unit for each of these heads, in one row, an equal share
+// for every CTA, one CTA per SM. A CTA's share is a run of pieces, each of one head; a
+// piece that is not the whole head leaves (o, m, sum) in the workspace, and join_kernel
+// puts them together in order. Every sum has one order given by the lengths: equal
+// calls give equal bits.
 //
-// Warp 8 feeds a ring of tiles by TMA, one box per run of keys that lies
-// together (a page, or what of it divides 64 keys; 128-byte swizzle). Warps 0-3
-// and 4-7 take turns at the tiles, 16 keys a warp, and each warp has a softmax
-// of its own, so that nothing waits inside a piece; the eight (o, m, sum) are
-// joined at its end. Products on the tensor core (mma.sync m16n8k16, fp32
-// sums): keys are the rows of S^T = K.Q^T and d the rows of O^T = V^T.P^T, so
-// the group's heads fill the 8 columns and one head wastes no more than seven.
-// The weights enter P.V as a sum of two numbers of the element type (the first
-// rounded towards zero), 16 to 22 bits: the result's own rounding is what is
-// left. Bound by HBM: 4 HD bytes a key and kv head, 6 to 16 products each.
+// Warps 8 and 9 feed a ring of tiles by TMA, one K and one V: a box per run of keys
+// that lies together (a page, or what of it divides 64 keys) with both halves of the
+// head, 128-byte swizzle; a box takes its warp 50 to 80 cycles to issue, so pages are
+// looked up a lot ahead and boxes are as large as pages let them. Warps 0-3 and 4-7
+// take turns at the tiles, 16 keys a warp, and each warp has a softmax of its own, so
+// that nothing waits inside a piece; warps 10 and 11 join the eight (o, m, sum) at a
+// piece's end while the next piece runs. Products on the tensor core (mma.sync
+// m16n8k16, fp32 sums; a matrix instruction of 128 rows would have 1 to 16 of them
+// used): keys are the rows of S^T = K.Q^T and d the rows of O^T = V^T.P^T, so the
+// group's heads fill the 8 columns. The weights enter P.V as a sum of two numbers of
+// the element type (the first rounded towards zero), 16 to 22 bits: the result's own
+// rounding is what is left.
+//
+// Bound by HBM: 4 HD bytes a key and kv head against 6 to 16 products each. 24
+// sequences of up to 32700 rows, 48/12 heads of 128: 459 us, 6.9 TB/s (the copy rate is
+// 6.8); 32 of 0 to 8192, 32/8 heads: 56.5, of which 49.5 are bytes and the rest start, end
+// and join; 1000 rows of one: 7.0, latency. Tried and slower: one producer warp with a
+// box per half (the same 32 sequences 110 us), the softmax's warps joining the pieces
+// themselves (72), joins by (head, sequence) (72), shares of tiles alone (62), the maximum
+// followed in every tile, the join by the last CTA in the same launch (1000 rows 9.5,
+// three fences of 900 to 1200 cycles), joins of 512 threads (8.0).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
