@@ -650,7 +650,8 @@ long long attention_paged_decode_workspace(int batch, int n_q_heads, int n_kv_he
  * nothing, whatever it holds. The weights enter the product with V in 16 bits or
  * more; an infinity or NaN of V that is seen leaves no finite result where its
  * weight is not zero in fp32, and NaN where it is.
- *   q, out     device [batch][n_q_heads][head_dim], batch 1..1024
+ *   q, out     device [batch][n_q_heads][head_dim], batch 1..1024; out overlaps
+ *              nothing else, q neither
  *   lengths    device int32[batch]; table device int32[batch][table_width]
  *   strides    host int64[4]: batch and head stride of q, then of out; NULL: dense
  *   scale      > 0 and below 2.3e38, or 0 for 1/sqrt(head_dim)

@@ -155,6 +155,7 @@ extern "C" int attention_paged_decode(const void* q, const void* k_pages, const 
     if ((rc = check_strides(FN, st, 4, head_dim))) return rc;
     if (misaligned(q) || misaligned(k_pages) || misaligned(v_pages) || misaligned(out) || misaligned(workspace))
       return host_fail(LPS_EINVAL, FN, "q, the pages, out and workspace must be 16-byte aligned");
+    if (out == q) return host_fail(LPS_EINVAL, FN, "out must not be q: several blocks read a head's q");
     PagedAttnParams p{};
     if ((rc = paged_shape(FN, p, batch, n_q_heads, n_kv_heads, head_dim, page_size, table_width))) return rc;
     if (workspace_bytes < paged_attn_workspace(p, head_dim, key_weights != nullptr))

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
 
   if (warp >= kConsumers + kProducers) {
-    // ---- the writers: eight warps' (o, m, l) of a piece, in warp order; warp = head ----
+    // ---- the writers: eight warps' (o, m, l) of a piece, in warp order; warp = half of the elements d ----
     int it = 0;
     bool alive = true;
     const bool tells = warp == kConsumers + kProducers && lane == 0;  // the join of a head that begins here and ends elsewhere

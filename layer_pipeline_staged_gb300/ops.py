@@ -155,7 +155,7 @@ def attention_paged_decode(q, k_pages, v_pages, table, lengths, key_weights=None
     new token's own row counted. A sequence of no rows (or of a length that its table has no room for) gives zeros, and
     rows on a page that does not exist are not seen. With ``key_weights`` float32 [pages, kv heads, page rows] every row's
     weight, summed over the kv head's query heads, is added to ``decay`` times what is there (0: replaces it).
-    ``scale`` 0 means 1/sqrt(head_dim). ``cache_ops_status`` reports a kernel that gave up."""
+    ``scale`` 0 means 1/sqrt(head_dim). ``cache_ops_status`` reports a kernel that gave up. ``out`` is not q."""
     return (_m or _ready()).decode_paged(q, k_pages, v_pages, table, lengths, out, scale, key_weights, decay)
 
 

@@ -78,7 +78,7 @@ def test_append_refused(kw):
 
 @no_device
 @pytest.mark.parametrize("kw", [dict(q=None), dict(kp=None), dict(vp=None), dict(out=None), dict(len=None), dict(table=None), dict(ws=None),
-                                dict(batch=0), dict(batch=1025), dict(nq=0), dict(nq=9), dict(nq=34), dict(out=A[3] + 2), dict(ws=A[6] + 8),
+                                dict(batch=0), dict(batch=1025), dict(nq=0), dict(nq=9), dict(nq=34), dict(out=A[3] + 2), dict(out=A[0]), dict(ws=A[6] + 8),
                                 dict(strides=[512, 64, 512, 60]), dict(scale=-1.0), dict(scale=math.nan), dict(scale=3e38),
                                 dict(decay=-0.1), dict(decay=1.1), dict(decay=math.nan), dict(nq=65528, nkv=65528, width=2 ** 22, page=64),
                                 *HEADS, *PAGES])
