@@ -293,3 +293,32 @@ def test_many_heads_a_token(tokens):
     assert torch.equal(kp.transpose(1, 2).reshape(-1, 130, 64)[:tokens], ko) and torch.equal(vp.transpose(1, 2).reshape(-1, 130, 64)[:tokens], v)
     same_q, same_k = lps.rotary_rows(q, k, pos, None)  # nothing turns
     assert torch.equal(same_q, q) and torch.equal(same_k, k)
+
+
+def test_pools_and_logits_past_two_to_the_31_elements():
+    nkv, hd, page = 2, 128, 64
+    pages = 2 ** 31 // (nkv * hd * page) + 20
+    kp, vp = (torch.zeros(pages, nkv, page, hd, device="cuda", dtype=BF) for _ in range(2))
+    w = torch.zeros(pages, nkv, page, device="cuda")
+    g, f = gen(7), lps.rotary_frequencies(hd).cuda()
+    q, k, v = randn(g, 100, 4, hd, dtype=BF), randn(g, 100, nkv, hd, dtype=BF), randn(g, 100, nkv, hd, dtype=BF)
+    old, new = i32([[pages - 1, pages - 3]]), i32([[pages - 2]])
+    lps.rotary_append_paged(q, k, v, i32([0, 100]), i32([100]), old, kp, vp, f, key_weights=w)
+    kr = lps.rotary_rows(q, k, torch.arange(100, device="cuda", dtype=torch.int32), f)[1]
+    assert torch.equal(kp[pages - 1].transpose(0, 1), kr[:64]) and torch.equal(vp[pages - 3, :, :36].transpose(0, 1), v[64:])
+    w[pages - 1, 0, 5:30] = 2.0
+    w[pages - 3, 1, 3:20] = 1.0
+    assert lps.kv_pages_evict(kp, vp, w, old, i32([100]), new, 30, 2).tolist() == [30]
+    assert torch.equal(kp[pages - 2, 0, :30], torch.cat((kr[0:3, 0], kr[5:30, 0], kr[98:, 0])))
+    assert torch.equal(vp[pages - 2, 1, :30], torch.cat((v[0:11, 1], v[67:84, 1], v[98:, 1])))
+    assert torch.equal(w[pages - 2, 0, :30], torch.cat((w.new_zeros(3), w.new_full((25,), 2.0), w.new_zeros(2))))
+    assert not kp[0].any() and not vp[1].any()
+    del kp, vp, w
+    torch.cuda.empty_cache()
+    x = torch.zeros(40000, 65536, device="cuda", dtype=BF)
+    x[39999, 7] = 3.0
+    n = torch.ones(40000, device="cuda", dtype=torch.int32)
+    seven = torch.full((40000, 1), 7, device="cuda", dtype=torch.int32)
+    out = lps.logits_adjust(x, tokens=seven, lengths=n, presence=torch.ones(40000, device="cuda"), out=x)
+    assert float(out[39999, 7]) == 2.0 and float(out[39998, 7]) == -1.0 and float(out[0, 7]) == -1.0
+    assert int((out[39990:] != 0).sum()) == 10 and int((out[:10] != 0).sum()) == 10
