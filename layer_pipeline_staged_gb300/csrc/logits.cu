@@ -8,13 +8,14 @@
 //
 // Only the mask concerns every token. A block takes a run of the vocabulary; it
 // counts the row's history for its run in shared memory and lists the tokens it
-// meets for the first time; the listed ones are worked out by themselves, the run is
-// streamed through with the mask alone, and the listed ones' results are written
-// over it. Every block of a row reads all of its history, from L2, and that is what
-// bounds long ones: 64 rows of 128256 in fp32 take 10 us without a history and 19.3 with
-// up to 8192 tokens. Penalties worked out for every token took 26; the history's reading
-// shared out over a cluster, with counts in the owner's memory, 33; runs of 16384 tokens
-// 20.8, of 8192 with half the threads 23.7; the stream before the counting 21.7.
+// meets for the first time, while the run comes to L2; the run is streamed through with
+// the mask alone, and the listed ones are then read again from the output, worked out
+// and written over. Every block of a row reads all of its history, from L2, and that is
+// what bounds long ones: 64 rows of 128256 in fp32 take 9.1 us without a history and 15.7
+// with up to 8192 tokens. Penalties worked out for every token took 26; the history's
+// reading shared out over a cluster, with counts in the owner's memory, 33; the stream
+// before the counting 21.7; the listed ones worked out before the stream, with words of
+// 32 bits that then held the results, 19.3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,9 +27,29 @@
 namespace lps {
 namespace {
 
-constexpr int kEach = 16;  // tokens of a thread
-// a token's word: in the prompt or output, in bias_ids, count in the output
-constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kCount = kBiased - 1;
+// A token's word: whether prompt or output hold it, whether bias_ids do, and its count in
+// the output. Two words share 32 bits where the history is shorter than 2^14 tokens, and
+// so no count passes 14 bits: the blocks that an SM holds are bounded by shared memory.
+template <bool WIDE>
+struct Words {
+  static constexpr uint32_t kSeen = WIDE ? 1u << 31 : 1u << 15, kBiased = kSeen >> 1, kCount = kBiased - 1;
+  static constexpr int kBytes = WIDE ? 4 : 2;
+  uint32_t* w;
+  __device__ __forceinline__ uint32_t get(unsigned at) const {
+    return WIDE ? w[at] : reinterpret_cast<const uint16_t*>(w)[at];
+  }
+  // the word as it was
+  __device__ __forceinline__ uint32_t add_one(unsigned at) const {
+    if (WIDE) return atomicAdd(w + at, 1u);
+    const int by = (at & 1) * 16;
+    return atomicAdd(w + (at >> 1), 1u << by) >> by & 0xffff;
+  }
+  __device__ __forceinline__ uint32_t set(unsigned at, uint32_t bit) const {
+    if (WIDE) return atomicOr(w + at, bit);
+    const int by = (at & 1) * 16;
+    return atomicOr(w + (at >> 1), bit << by) >> by & 0xffff;
+  }
+};
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -42,15 +63,17 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t n) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
 }
 
-// Block = (run of THREADS * kEach tokens, row). Places are counted from the 16-byte
+// Block = (run of THREADS * EACH tokens, row). Places are counted from the 16-byte
 // boundary at or before the row's first logit, `shift` elements before it, so that
 // vectors lie on their boundaries wherever the row begins.
-template <class T, int THREADS>
+template <class T, int THREADS, int EACH, bool WIDE>
 __global__ void __launch_bounds__(THREADS) logits_kernel(const __grid_constant__ LogitsParams p) {
-  constexpr int V = 16 / sizeof(T), kVecs = kEach / V, kRun = THREADS * kEach, kAhead = 8;
-  extern __shared__ uint32_t words[];                             // [kRun]: a token's word, then its result
-  uint16_t* listed = reinterpret_cast<uint16_t*>(words + kRun);   // [kRun]: places of the tokens that have a word
-  __shared__ int n_listed, twice;                                 // whether a token has several biases
+  constexpr int V = 16 / sizeof(T), kVecs = EACH / V, kRun = THREADS * EACH, kAhead = 8;
+  using W = Words<WIDE>;
+  extern __shared__ uint4 space[];
+  const W words{reinterpret_cast<uint32_t*>(space)};                                // [kRun]
+  uint16_t* listed = reinterpret_cast<uint16_t*>(space + kRun * W::kBytes / 16);    // places of the tokens that have a word
+  __shared__ int n_listed, twice;                                                   // whether a token has several biases
   pdl_launch_dependents();
   pdl_wait();
   const int t = threadIdx.x, b = blockIdx.y, run = blockIdx.x * kRun;
@@ -82,7 +105,7 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const __grid_constant__
     for (int j = 0; j < kAhead; ++j) tok[j] = p.tokens && j * THREADS + t < p.width ? tokens[j * THREADS + t] : -1;
     const int len = p.tokens ? min(max(p.lengths[b], 0), p.width) : 0, prompt = p.prompts ? p.prompts[b] : 0;
 #pragma unroll
-    for (int i = 0; i < kEach / 4; ++i) reinterpret_cast<uint4*>(words)[i * THREADS + t] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < EACH * W::kBytes / 16; ++i) space[i * THREADS + t] = make_uint4(0, 0, 0, 0);
     if (t == 0) n_listed = twice = 0;
     __syncthreads();
     auto list = [&](unsigned at, uint32_t was) {
@@ -93,7 +116,7 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const __grid_constant__
       for (int j = 0; j < kAhead; ++j) {
         const int i = i0 + j * THREADS;
         const unsigned at = static_cast<unsigned>(tok[j]) - first;
-        if (at < places && at >= unused && i < len) list(at, i >= prompt ? atomicAdd(words + at, 1u) : atomicOr(words + at, kSeen));
+        if (at < places && at >= unused && i < len) list(at, i >= prompt ? words.add_one(at) : words.set(at, W::kSeen));
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -104,31 +127,9 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const __grid_constant__
     for (int i = t; i < p.n_bias; i += THREADS) {
       const unsigned at = static_cast<unsigned>(ids[i]) - first;
       if (at >= places || at < unused) continue;
-      const uint32_t was = atomicOr(words + at, kBiased);
+      const uint32_t was = words.set(at, W::kBiased);
       list(at, was);
-      if (was & kBiased) twice = 1;
-    }
-    __syncthreads();
-
-    const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f, pres = p.presence ? p.presence[b] : 0.f;
-    for (int i = t; i < n_listed; i += THREADS) {
-      const int at = listed[i], e = run + at - shift;
-      const uint32_t c = words[at], n = c & kCount;
-      float x = to_float(in[e]);
-      if (c & ~kBiased) x = x > 0.f ? x / rep : x * rep;
-      if (n) x -= fmaf(freq, static_cast<float>(n), pres);
-      if (twice && c & kBiased) {  // its entries, in order
-#pragma unroll 8
-        for (int k = 0; k < p.n_bias; ++k) x += ids[k] == e ? bias[k] : 0.f;
-      }
-      words[at] = __float_as_uint(x);
-    }
-    __syncthreads();  // the listed logits have been read, for those that write over them
-    if (!twice) {
-      for (int i = t; i < p.n_bias; i += THREADS) {
-        const unsigned at = static_cast<unsigned>(ids[i]) - first;
-        if (at < places && at >= unused) words[at] = __float_as_uint(__uint_as_float(words[at]) + bias[i]);
-      }
+      if (was & W::kBiased) twice = 1;
     }
   }
 
@@ -163,36 +164,85 @@ __global__ void __launch_bounds__(THREADS) logits_kernel(const __grid_constant__
     }
   }
 
+  // The stream has left a listed token's own logit in `out`, or -inf for good.
   if (counted) {
     __syncthreads();
+    const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f, pres = p.presence ? p.presence[b] : 0.f;
+    auto is_allowed = [&](int e) { return !allowed || allowed[e >> 5] >> (e & 31) & 1; };
+    auto penalized = [&](float x, uint32_t c) {
+      if (c & ~W::kBiased) x = x > 0.f ? x / rep : x * rep;
+      if (c & W::kCount) x -= fmaf(freq, static_cast<float>(c & W::kCount), pres);
+      return x;
+    };
+#pragma unroll 2
     for (int i = t; i < n_listed; i += THREADS) {
       const int at = listed[i], e = run + at - shift;
-      from_float(out[e], !allowed || allowed[e >> 5] >> (e & 31) & 1 ? __uint_as_float(words[at]) : -INFINITY);
+      const uint32_t c = words.get(at);
+      if (c & W::kBiased && !twice) continue;
+      const float was = to_float(out[e]);
+      if (!is_allowed(e)) continue;
+      float x = penalized(was, c);
+      if (c & W::kBiased) {  // its entries, in order
+#pragma unroll 8
+        for (int k = 0; k < p.n_bias; ++k) x += ids[k] == e ? bias[k] : 0.f;
+      }
+      from_float(out[e], x);
+    }
+    if (!twice) {
+      for (int i = t; i < p.n_bias; i += THREADS) {
+        const unsigned at = static_cast<unsigned>(ids[i]) - first;
+        if (at < places && at >= unused && is_allowed(ids[i])) from_float(out[ids[i]], penalized(to_float(out[ids[i]]), words.get(at)) + bias[i]);
+      }
     }
   }
 }
 
-template <class T, int THREADS>
+long long history(const LogitsParams& p) { return static_cast<long long>(p.tokens ? p.width : 0) + (p.bias_ids ? p.n_bias : 0); }
+
+template <class T, int THREADS, int EACH, bool WIDE>
 cudaError_t launch_t(const LogitsParams& p, cudaStream_t s) {
-  constexpr int kRun = THREADS * kEach;
+  constexpr int kRun = THREADS * EACH;
   static_assert(kRun <= 65536, "a place in 16 bits");
   static std::atomic<uint64_t> told;
-  const cudaError_t e = allow_smem(logits_kernel<T, THREADS>, kRun * 6, told);
+  const cudaError_t e = allow_smem(logits_kernel<T, THREADS, EACH, WIDE>, kRun * (Words<WIDE>::kBytes + 2), told);
   if (e != cudaSuccess) return e;
   // a row may begin up to a vector's elements behind a boundary
   const long long runs = (static_cast<long long>(p.vocab) + 16 / sizeof(T) - 1 + kRun - 1) / kRun;
-  return launch_early(logits_kernel<T, THREADS>, dim3(static_cast<unsigned>(runs), p.batch), THREADS,
-                      p.tokens || p.bias_ids ? kRun * 6 : 0, s, p);
+  const long long entries = history(p);
+  const int list = static_cast<int>(entries < kRun ? entries : kRun);
+  return launch_early(logits_kernel<T, THREADS, EACH, WIDE>, dim3(static_cast<unsigned>(runs), p.batch), THREADS,
+                      list ? kRun * Words<WIDE>::kBytes + 2 * list : 0, s, p);
 }
 
+// Threads of a block and tokens of a thread. Every block of a row reads all of its
+// history, so a long one wants long runs, of many threads; runs that are short use more
+// SMs, and of those the small calls have too many. us, rows of 128256, histories of up to
+// so many tokens:
+//                        128 x 16   512 x 16   512 x 32   1024 x 32
+//   6 rows, fp32, 300         4.2        4.9        6.0        7.4
+//   6 rows, fp32, 4000        7.3        5.5        6.5        7.4
+//   12 rows, fp32, 20000     25.1       13.8       12.8       11.4
+//   64 rows, fp32, 300       11.9       12.9       13.0       13.5
+//   64 rows, fp32, 8192                 19.2       17.6       15.7
+//   30 rows, bf16, 1000       7.5        7.2        8.3        8.8
+//   100 rows, bf16, 1000     14.8       14.7       12.3       13.2
+//   64 rows, bf16, 8000      28.3       15.8       13.6       11.3
+// Narrower words put four blocks of 512 x 16 on an SM: 32768 of its tokens at once. With
+// more of them than that, a thread of 16-bit logits takes as many bytes as one of fp32.
 template <class T>
 cudaError_t launch_type(const LogitsParams& p, cudaStream_t s) {
-  // long runs where they fill the SMs (every block of a row reads all of its history),
-  // else short ones, for more SMs
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  return static_cast<double>(p.batch) * p.vocab > 8192.0 * sms ? launch_t<T, 512>(p, s) : launch_t<T, 128>(p, s);
+  const double of_sm = static_cast<double>(p.batch) * p.vocab / sms;
+  const long long entries = history(p);
+  const bool wide = p.tokens && p.width >= 1 << 14;
+  if (of_sm <= 8192 && entries <= 1024) return launch_t<T, 128, 16, false>(p, s);
+  if ((of_sm > 8192 && entries > 8192) || (of_sm > 32768 && entries > 4096))
+    return wide ? launch_t<T, 1024, 32, true>(p, s) : launch_t<T, 1024, 32, false>(p, s);
+  if constexpr (sizeof(T) == 2)
+    if (of_sm > 32768) return launch_t<T, 512, 32, false>(p, s);
+  return wide ? launch_t<T, 512, 16, true>(p, s) : launch_t<T, 512, 16, false>(p, s);
 }
 
 }  // namespace

@@ -9,6 +9,7 @@ from layer_pipeline_staged_gb300 import ops
 
 torch = pytest.importorskip("torch")
 from paged import Paged, gen, i32, randn  # noqa: E402
+from test_gpu_paged_ops import ORDER, adjust64, logits_inputs, same_logits  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -322,3 +323,29 @@ def test_pools_and_logits_past_two_to_the_31_elements():
     out = lps.logits_adjust(x, tokens=seven, lengths=n, presence=torch.ones(40000, device="cuda"), out=x)
     assert float(out[39999, 7]) == 2.0 and float(out[39998, 7]) == -1.0 and float(out[0, 7]) == -1.0
     assert int((out[39990:] != 0).sum()) == 10 and int((out[:10] != 0).sum()) == 10
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("batch,vocab,width,entries", [(2, 1000, 1500, 0), (3, 5000, 16383, 4), (3, 40001, 16384, 4), (20, 65537, 100, 5),
+                                                       (20, 65537, 9000, 5), (20, 65537, 16400, 600), (80, 65537, 60, 3), (80, 65537, 5000, 0)])
+def test_logits_of_few_and_many_rows_with_short_and_long_histories(batch, vocab, width, entries, dtype):
+    x, d = logits_inputs(batch, vocab, width, entries, dtype, 2)
+    d["allowed"] |= i32([[0x0FF0FF0F] * d["allowed"].shape[1]])
+    kw = {k: v for k, v in d.items() if v is not None}
+    ref = adjust64(x, *(kw.get(k) for k in ORDER))
+    got = lps.logits_adjust(x, **kw)
+    same_logits(got, *ref)
+    same = x.clone()
+    assert lps.logits_adjust(same, **kw, out=same) is same and torch.equal(same, got)
+
+
+@pytest.mark.parametrize("width", [16383, 16384, 70000])
+def test_logits_of_a_history_of_one_token(width):
+    """As many counts as the history has room for, of a token whose neighbours are in the history too."""
+    x = torch.zeros(2, 9000, device="cuda")
+    tokens = torch.full((2, width), 4001, device="cuda", dtype=torch.int32)
+    tokens[1, :2] = i32([4000, 4002])
+    out = lps.logits_adjust(x, tokens=tokens, lengths=i32([width, width]), frequency=torch.ones(2, device="cuda"),
+                            bias_ids=i32([[4002], [4003]]), bias=torch.full((2, 1), 0.5, device="cuda"))
+    assert out[0, 3999:4004].tolist() == [0.0, 0.0, -width, 0.5, 0.0] and out[1, 3999:4004].tolist() == [0.0, -1.0, 2.0 - width, -1.0, 0.5]
+    assert int((out != 0).sum()) == 2 + 4
