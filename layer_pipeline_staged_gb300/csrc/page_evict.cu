@@ -4,7 +4,7 @@
 // all and in order; they are copied, with their weights, to the rows 0, 1, ..
 // of the new table's pages. The old pages are only read, so pages that several
 // sequences share stay whole. One kernel finds the rows, a second one copies
-// them. 8 sequences of up to 8192 rows, 8 heads of 128, brought to 4096: 48.7 us, of
+// them. 8 sequences of up to 8192 rows, 8 heads of 128, brought to 4096: 48.0 us, of
 // which the copy is 37 (6.5 TB/s) and the selection, bound by latency, the rest.
 #include <cooperative_groups.h>
 
@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 // candidates, two bits a round, takes 16 rounds of two barriers: 13 us instead of 6).
 // Latency bounds it, and not least the instructions' own way from memory: its loops
 // stay loops (unrolled, with the weights in registers, 1000 rows of 8 heads took 11.3 us
-// with the copy, and 8.2 to 9 so).
+// with the copy, and 8.2 to 8.8 so).
 __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__ EvictParams p, int held) {
   extern __shared__ uint4 held_keys[];  // [held / 4]: the orders of the block's first rows; those behind are read again
   uint32_t* keys = reinterpret_cast<uint32_t*>(held_keys);
@@ -71,6 +71,10 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__
   // A page's rows come in eights, and so do the block's: a thread takes eight of one
   // page. A row on a page that is none is as light as can be, as is what fills an eight.
   const int in_smem = min(mine, held);
+  // the first pages to be looked at are asked for before the weights
+  const int pages = ok ? (n + p.page - 1) / p.page : 0, fresh_pages = ok ? (kept + p.page - 1) / p.page : 0;
+  const int page0 = t < pages ? table[t] : 0, fresh0 = t < fresh_pages ? fresh[t] : 0;
+  __syncthreads();
 #pragma unroll 2
   for (int i = 8 * t; i < in_smem; i += 8 * kSelect) {
     const int pi = (b0 + i) / p.page, page = table[pi];
@@ -87,16 +91,18 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__
       k.w = left > 3 ? k.w : 0, k.z = left > 2 ? k.z : 0, k.y = left > 1 ? k.y : 0;
     }
     held_keys[i / 4] = k, held_keys[i / 4 + 1] = l;
+    // the first digit is counted on the way (what fills an eight goes to the lowest bin: above it are only rows)
+    atomicAdd(&hist[0][k.x >> 21], 1), atomicAdd(&hist[0][k.y >> 21], 1), atomicAdd(&hist[0][k.z >> 21], 1), atomicAdd(&hist[0][k.w >> 21], 1);
+    atomicAdd(&hist[0][l.x >> 21], 1), atomicAdd(&hist[0][l.y >> 21], 1), atomicAdd(&hist[0][l.z >> 21], 1), atomicAdd(&hist[0][l.w >> 21], 1);
   }
   auto read = [&](int i) {
     const int row = b0 + i, pi = row / p.page, page = table[pi];
     return order_of(p.key_weights[(static_cast<long long>(page) * p.nkv + g) * p.page + (row - pi * p.page)]);
   };
   // every block of the cluster looks at all pages, and finds the same
-  if (ok) {
-    for (int i = t; i < (n + p.page - 1) / p.page; i += kSelect) ok = ok && table[i] >= 0 && table[i] < p.n_pages;
-    for (int i = t; i < (kept + p.page - 1) / p.page; i += kSelect) ok = ok && fresh[i] >= 0 && fresh[i] < p.n_pages;
-  }
+  ok = ok && page0 >= 0 && page0 < p.n_pages && fresh0 >= 0 && fresh0 < p.n_pages;
+  for (int i = t + kSelect; i < pages; i += kSelect) ok = ok && table[i] >= 0 && table[i] < p.n_pages;
+  for (int i = t + kSelect; i < fresh_pages; i += kSelect) ok = ok && fresh[i] >= 0 && fresh[i] < p.n_pages;
   ok = __syncthreads_and(ok);
   if (g == 0 && rank == 0 && t == 0) p.new_lengths[b] = ok ? kept : -1;
   if (!ok) return;
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const __grid_constant__
       if ((k & known) == least) atomicAdd(&h[k >> shift & bins], 1);
     };
 #pragma unroll 1
-    for (int i = t; i < (in_smem + 3) / 4; i += kSelect) {
+    for (int i = pass ? t : in_smem; i < (in_smem + 3) / 4; i += kSelect) {
       const uint4 k = held_keys[i];
       count(k.x), count(k.y), count(k.z), count(k.w);
     }
