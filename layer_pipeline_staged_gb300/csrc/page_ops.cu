@@ -172,7 +172,7 @@ extern "C" int attention_paged_decode(const void* q, const void* k_pages, const 
     p.scale_log2 = kLog2e * (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(head_dim)));
     const bool bf16 = type == LPS_TYPE_BF16;
     if (!encode_pages(&p.tmap_k, bf16, k_pages, head_dim, page_size, n_kv_heads, n_pages, p.box) ||
-        !encode_pages(&p.tmap_v, bf16, v_pages, head_dim, page_size, n_kv_heads, n_pages, p.box))
+        !encode_beside(&p.tmap_v, p.tmap_k, v_pages))
       return host_fail(LPS_ECUDA, FN, "cuTensorMapEncodeTiled failed");
     return launched(FN, launch_paged_attn(p, bf16, head_dim, static_cast<cudaStream_t>(stream)));
   });
