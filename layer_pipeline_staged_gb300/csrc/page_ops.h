@@ -63,6 +63,7 @@ struct PagedAttnParams {
   int nq, nkv, group;
   int ctas;
   float scale_log2, decay;
+  int cluster;  // the members of a head's cluster, where it is one's
 };
 // CTAs of the current device's launch, and the workspace's bytes (weights: with key_weights).
 cudaError_t paged_attn_ctas(int* ctas);

@@ -10,7 +10,9 @@
 // (sequence, kv head) and a unit for each of these heads, in one row, an equal share
 // for every CTA, one CTA per SM. A CTA's share is a run of pieces, each of one head; a
 // piece that is not the whole head leaves (o, m, sum) in the workspace, and join_kernel
-// puts them together in order. Every sum has one order given by the lengths: equal
+// puts them together in order. Where the tables have room for few rows of few heads, a
+// head is a thread-block cluster's instead: its CTAs take equal runs of the tiles and put
+// them together through each other's shared memory, in one launch. Every sum has one order given by the lengths: equal
 // calls give equal bits.
 //
 // Warps 8 and 9 feed a ring of tiles by TMA, one K and one V: a box per run of keys
@@ -29,11 +31,12 @@
 // Bound by HBM: 4 HD bytes a key and kv head against 6 to 16 products each. 24
 // sequences of up to 32700 rows, 48/12 heads of 128: 459 us, 6.9 TB/s (the copy rate is
 // 6.8); 32 of 0 to 8192, 32/8 heads: 56.5, of which 49.5 are bytes and the rest start, end
-// and join; 1000 rows of one: 7.0, latency. Tried and slower: one producer warp with a
+// and join; 1000 rows of one: 5.1, latency (7.0 without the cluster). Tried and slower: one producer warp with a
 // box per half (the same 32 sequences 110 us), the softmax's warps joining the pieces
 // themselves (72), joins by (head, sequence) (72), shares of tiles alone (62), the maximum
 // followed in every tile, the join by the last CTA in the same launch (1000 rows 9.5,
 // three fences of 900 to 1200 cycles), joins of 512 threads (8.0).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,11 +50,15 @@
 namespace lps {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kTile = 64;          // keys of a tile
 constexpr int kConsumers = 8;      // warps of 16 keys; two teams
 constexpr int kProducers = 2;      // warps that feed the ring, one with K and one with V
 constexpr int kWriters = 2;        // warps that finish pieces
 constexpr int kThreads = (kConsumers + kProducers + kWriters) * 32;
+constexpr int kMembers = 8;        // of a cluster at most
+constexpr long long kClusterRows = 1024;  // of a member at most
 constexpr int kMaxParts = 256;     // CTAs of a launch, and so parts of a head
 constexpr int kKid = kKidPagedAttn << 8;
 constexpr float kStale = 8.0f;     // the base may lag the maximum by a factor of 2^8
@@ -98,6 +105,7 @@ struct __align__(1024) Smem {
   int base;                        // first unit of the sequence that the CTA begins in
   int first;                       // that sequence
   uint32_t valid[S::kStages];      // boxes of the tile whose page is one, or kWhole
+  float2 part_ml[S::kHeads];       // of a cluster's member: its keys' base and sum (-1: none seen); its o takes the first stage's place
   uint64_t full[S::kStages], empty[S::kStages], slot_full[S::kSlots], slot_empty[S::kSlots];
 };
 
@@ -203,6 +211,7 @@ struct Walk {
   int b, nkv;
   const int* rows;
   int g, t0, t1;
+  __device__ __forceinline__ int n_rows() const { return rows[b]; }
   __device__ __forceinline__ int tiles() const { return (rows[b] + kTile - 1) / kTile; }
   __device__ __forceinline__ bool next() {
     while (at < end) {
@@ -221,7 +230,21 @@ struct Walk {
   }
 };
 
-template <bool BF16, int HD, int NT, bool WEIGHTS>
+// The one piece of a cluster's member.
+struct OnePiece {
+  int rows, b, g, t0, t1;
+  bool left;
+  __device__ __forceinline__ int n_rows() const { return rows; }
+  __device__ __forceinline__ bool next() {
+    const bool is = left && t0 < t1;
+    left = false;
+    return is;
+  }
+};
+
+// CLUSTER: a (sequence, kv head) is a thread-block cluster's, which shares its tiles out
+// and joins them through each other's shared memory: no second launch.
+template <bool BF16, int HD, int NT, bool WEIGHTS, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using S = Shape<HD, NT>;
   extern __shared__ uint8_t raw[];
@@ -242,12 +265,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   // heads that the group does not have are columns of zeros
   for (int i = tid; i < static_cast<int>(sizeof sm.q) / 16; i += kThreads) reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // zeros before the copies' bytes
+  if (CLUSTER && tid < S::kHeads) sm.part_ml[tid] = make_float2(-INFINITY, -1.f);
   pdl_wait();
   pdl_launch_dependents();
 
+  // A cluster's member: an equal share of its head's tiles
+  OnePiece one{};
+  if constexpr (CLUSTER) {
+    const int head = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    one.b = head / p.nkv, one.g = head % p.nkv;
+    one.rows = rows_of(p, one.b);
+    const int tiles = (one.rows + kTile - 1) / kTile;
+    one.t0 = rank * tiles / p.cluster, one.t1 = (rank + 1) * tiles / p.cluster;
+    one.left = true;
+    __syncthreads();
+  }
   // the tiles of every sequence, and where this CTA's share begins
-  int beg, end, total = 0;
-  {
+  int beg = 0, end = 0, total = 0;
+  if constexpr (!CLUSTER) {
     const int per = (p.batch + kThreads - 1) / kThreads, lo = min(tid * per, p.batch), hi = min(lo + per, p.batch);
     int mine = 0;
     for (int b = lo; b < hi; ++b) {
@@ -288,14 +323,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (WEIGHTS && blockIdx.x == 0 && tid == 0) p.first_unit[p.batch] = total;
     __syncthreads();
   }
-  // sequences without rows: zeros
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-    if (sm.rows[b] == 0)
-      for (int i = tid; i < p.nq * HD; i += kThreads) store_out<BF16>(p.out, b * p.o_seq + i / HD * p.o_head + i % HD, 0.f);
-  if (beg >= end) return;
-  Walk walk{beg, end, sm.base, sm.first, p.nkv, sm.rows, 0, 0, 0};
+  if constexpr (!CLUSTER) {
+    // sequences without rows: zeros
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+      if (sm.rows[b] == 0)
+        for (int i = tid; i < p.nq * HD; i += kThreads) store_out<BF16>(p.out, b * p.o_seq + i / HD * p.o_head + i % HD, 0.f);
+    if (beg >= end) return;
+  }
+  using Pieces = std::conditional_t<CLUSTER, OnePiece, Walk>;
+  Pieces walk;
+  if constexpr (CLUSTER) walk = one;
+  else walk = Walk{beg, end, sm.base, sm.first, p.nkv, sm.rows, 0, 0, 0};
   const long long limit = wait_cycles(p.wait_limit);
 
+  auto roles = [&] {
   if (warp >= kConsumers && warp < kConsumers + kProducers) {
     // ---- the producer of K or of V (and q): what is on its way first takes half the time ----
     const int v = warp - kConsumers;
@@ -311,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     // next lot of a piece, or the first one of the next piece, is on its way while
     // this one is used.
     const int lot = 32 >> log_boxes;  // tiles of a lot
-    auto look = [&](const Walk& w, int tile) {
+    auto look = [&](const Pieces& w, int tile) {
       const int box = (tile << log_boxes) + lane;
-      if (tile >= w.t1 || box >= (w.rows[w.b] + p.box - 1) >> log_box) return make_int2(-1, 0);
+      if (tile >= w.t1 || box >= (w.n_rows() + p.box - 1) >> log_box) return make_int2(-1, 0);
       const int pi = box / page_boxes;
       return make_int2(p.table[static_cast<long long>(w.b) * p.width + pi], (box - pi * page_boxes) << log_box);
     };
@@ -321,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     bool ok = true, more = walk.next();
     int2 ahead = more ? look(walk, walk.t0) : make_int2(-1, 0);
     while (ok && more) {
-      Walk next = walk;
+      Pieces next = walk;
       more = next.next();
-      const int n_rows = walk.rows[walk.b], n_tiles = walk.t1 - walk.t0;
+      const int n_rows = walk.n_rows(), n_tiles = walk.t1 - walk.t0;
       for (int l0 = 0; l0 < n_tiles && ok; l0 += lot) {
         const int2 now = ahead;
         if (l0 + lot < n_tiles) ahead = look(walk, walk.t0 + l0 + lot);
@@ -372,12 +413,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     int it = 0;
     bool alive = true;
     const bool tells = warp == kConsumers + kProducers && lane == 0;  // the join of a head that begins here and ends elsewhere
-    if (tells) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!CLUSTER && tells) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int piece = 0; walk.next(); ++piece) {
       const int n = walk.t1 - walk.t0, sl = piece % S::kSlots;
-      if (tells && walk.t0 == 0 && n < walk.tiles()) {
-        const int units = walk.tiles() + 1, i0 = walk.base + walk.g * units;
-        p.border[blockIdx.x] = make_int4(walk.b, walk.g, Shares(total, p.ctas).owner(i0 + units - 1) - blockIdx.x + 1, beg < i0);
+      bool whole = false;
+      if constexpr (!CLUSTER) {
+        whole = n == walk.tiles();
+        if (tells && walk.t0 == 0 && !whole) {
+          const int units = walk.tiles() + 1, i0 = walk.base + walk.g * units;
+          p.border[blockIdx.x] = make_int4(walk.b, walk.g, Shares(total, p.ctas).owner(i0 + units - 1) - blockIdx.x + 1, beg < i0);
+        }
       }
       const int w0 = n == 1 && (it & 1) ? kConsumers / 2 : 0, w1 = n == 1 && !(it & 1) ? kConsumers / 2 : kConsumers;  // the warps that had tiles
       it += n;
@@ -385,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
       alive = __all_sync(0xffffffffu, alive);
       const Slot<HD, NT>& in = sm.slot[sl];
-      const bool whole = n == walk.tiles();
       const long long part = (static_cast<long long>(blockIdx.x) * 2 + (piece ? 1 : 0)) * p.group;
       const int wr = warp - kConsumers - kProducers;
       const bool seen = __any_sync(0xffffffffu, lane >= w0 && lane < w1 && in.seen[lane & 7]);
@@ -409,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           sm.sum[wr][h] = sum;
           const float2 ml = make_float2(top, seen ? sum : -1.f);
           if (alive && wr == 0 && h < p.group) {
-            if (!whole) p.part_ml[part + h] = ml;
+            if (CLUSTER) sm.part_ml[h] = ml;
+            else if (!whole) p.part_ml[part + h] = ml;
             else if (WEIGHTS) p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = ml;
           }
         }
@@ -445,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             for (int e = 0; e < kEach; ++e) store_out<BF16>(p.out, to + j * p.o_head + 32 * e, acc[e][j] * inv);
           }
         } else {
-          float* to = p.part_o + (part + h0) * HD + d;
+          float* to = (CLUSTER ? reinterpret_cast<float*>(sm.kv) + h0 * HD : p.part_o + (part + h0) * HD) + d;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (h0 + j >= p.group) break;
@@ -506,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const uint32_t valid = sm.valid[stage];
       if (alive && valid != kWhole) {
         const int mine = lane & 15;
-        keys = __ballot_sync(0xffffffffu, key0 + mine < walk.rows[b] && (valid >> ((row0 + mine) >> box_shift) & 1)) & 0xffffu;
+        keys = __ballot_sync(0xffffffffu, key0 + mine < walk.n_rows() && (valid >> ((row0 + mine) >> box_shift) & 1)) & 0xffffu;
       }
       if (keys) {
         any = true;
@@ -637,6 +682,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.slot_full[sl]);
   }
+  };
+  roles();
+
+  if constexpr (CLUSTER) {
+    // the members' parts in their order, an element of the head's output a thread
+    __syncwarp();
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int i = (blockIdx.x % p.cluster) * kThreads + tid; i < p.group * HD; i += p.cluster * kThreads) {
+      float2 ml[kMembers];
+      float o[kMembers];
+#pragma unroll
+      for (int r = 0; r < kMembers; ++r) {
+        const bool on = r < p.cluster;
+        ml[r] = on ? *cluster.map_shared_rank(&sm.part_ml[i / HD], r) : make_float2(-INFINITY, -1.f);
+        o[r] = on ? *cluster.map_shared_rank(reinterpret_cast<float*>(sm.kv) + i, r) : 0.f;
+      }
+      float top = -INFINITY, sum = 0.f, acc = 0.f;
+      bool seen = false;
+#pragma unroll
+      for (int r = 0; r < kMembers; ++r) top = fmaxf(top, ml[r].x);
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int r = 0; r < kMembers; ++r) {
+        if (ml[r].y < 0.f) continue;  // no key seen, and o is none
+        const float w = exp2_fast(ml[r].x - base);
+        sum += w * ml[r].y;
+        acc += w * o[r];
+        seen = true;
+      }
+      if (WEIGHTS && i % HD == 0)
+        p.part_ml[(2ll * p.ctas + static_cast<long long>(one.b) * p.nkv + one.g) * p.group + i / HD] = make_float2(top, seen ? sum : -1.f);
+      store_out<BF16>(p.out, one.b * p.o_seq + (one.g * p.group + i / HD) * p.o_head + i % HD, seen ? acc / sum : 0.f);
+    }
+    cluster.sync();  // a member's parts are read before it ends
+  }
 }
 
 constexpr int kJoin = 256;         // threads of the join
@@ -657,7 +738,7 @@ template <bool BF16, int HD, bool WEIGHTS>
 __global__ void __launch_bounds__(kJoin, 4) join_kernel(const __grid_constant__ PagedAttnParams p, int key_blocks) {
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int joins = p.ctas * p.group;
+  const int joins = p.cluster ? 0 : p.ctas * p.group;
   if (!WEIGHTS || static_cast<int>(blockIdx.x) < joins) {
     constexpr int kSlices = kJoin / HD;  // threads of an element, each with every kSlices-th part
     __shared__ float slice[kSlices][HD], slice_top[kSlices], slice_sum[kSlices], slice_seen[kSlices];
@@ -734,10 +815,14 @@ __global__ void __launch_bounds__(kJoin, 4) join_kernel(const __grid_constant__ 
 #pragma unroll
       for (int h = 0; h < kEarly; ++h) x[i][h] = key < n_rows && h < p.group ? __ldcg(scores + h * rows + key) : 0.f;
     }
-    const int total = __ldcg(p.first_unit + p.batch), units = units_of((n_rows + kTile - 1) / kTile), i0 = __ldcg(p.first_unit + b) + g * units;
-    const Shares shares(total, p.ctas);
-    const int c0 = shares.owner(i0 + 1), n = shares.owner(i0 + units - 1) - c0 + 1;
-    const bool shifted = shares.start(c0) < i0;
+    int c0 = 0, n = 1;  // the head's parts: a cluster has put them together
+    bool shifted = false;
+    if (!p.cluster) {
+      const int total = __ldcg(p.first_unit + p.batch), units = units_of((n_rows + kTile - 1) / kTile), i0 = __ldcg(p.first_unit + b) + g * units;
+      const Shares shares(total, p.ctas);
+      c0 = shares.owner(i0 + 1), n = shares.owner(i0 + units - 1) - c0 + 1;
+      shifted = shares.start(c0) < i0;
+    }
     for (int h = warp; h < p.group; h += kJoin / 32) {
       float m = -INFINITY, sum = 0.f;
       for (int i = lane; i < n; i += 32) {
@@ -778,16 +863,35 @@ template <bool BF16, int HD, int NT, bool WEIGHTS>
 cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   constexpr size_t kSmem = sizeof(Smem<HD, NT>) + 1024;
   static_assert(kSmem <= 232448, "shared memory");
-  static std::atomic<uint64_t> told;
-  cudaError_t e = allow_smem(attn_kernel<BF16, HD, NT, WEIGHTS>, kSmem, told);
-  if (e == cudaSuccess) e = launch_early(attn_kernel<BF16, HD, NT, WEIGHTS>, dim3(p.ctas), kThreads, kSmem, s, p);
-  if (e != cudaSuccess) return e;
-  // blocks for the keys of every head that the tables have room for, in a bounded grid
   const long long heads = static_cast<long long>(p.batch) * p.nkv, rows = static_cast<long long>(p.width) * p.page;
+  // A head is a cluster's where every cluster has a place at once (clusters of eight leave
+  // much of the chip unused: 16 of them took 11.1 us for 2000 rows each instead of 7.4 in
+  // fours), and the tables have room for so few rows that a member's run costs no more than
+  // the second launch. us with clusters and with shares, heads of 128: 1 sequence of 300
+  // rows, 8 heads 4.8 and 6.7; of 4000 7.6 and 9.0; of 8000 10.7 and 10.6, of 16000 17.0 and
+  // 13.7; 2 of 4000 10.4 and 10.0; 8 of 2000 10.7 and 13.5; 16 of 500 7.4 and 11.0.
+  PagedAttnParams one = p;
+  one.cluster = 2 * kMembers * heads <= p.ctas ? kMembers : kMembers / 2;
+  while (one.cluster > 1 && one.cluster * heads * 8 > p.ctas * 7) one.cluster /= 2;
+  if (one.cluster * heads * 8 > p.ctas * 7 || rows > kClusterRows * one.cluster) one.cluster = 0;
+  cudaError_t e;
+  if (one.cluster) {
+    static std::atomic<uint64_t> told;
+    e = allow_smem(attn_kernel<BF16, HD, NT, WEIGHTS, true>, kSmem, told);
+    if (e == cudaSuccess)
+      e = launch_early_clusters(attn_kernel<BF16, HD, NT, WEIGHTS, true>, dim3(static_cast<unsigned>(one.cluster * heads)), kThreads, kSmem, one.cluster, s, one);
+    if (e != cudaSuccess || !WEIGHTS) return e;
+  } else {
+    static std::atomic<uint64_t> told;
+    e = allow_smem(attn_kernel<BF16, HD, NT, WEIGHTS, false>, kSmem, told);
+    if (e == cudaSuccess) e = launch_early(attn_kernel<BF16, HD, NT, WEIGHTS, false>, dim3(p.ctas), kThreads, kSmem, s, one);
+    if (e != cudaSuccess) return e;
+  }
+  // blocks for the keys of every head that the tables have room for, in a bounded grid
   const long long lots = (rows + kJoinKeys - 1) / kJoinKeys, most = std::max(1ll, (1ll << 15) / heads);
   const int key_blocks = WEIGHTS ? static_cast<int>(std::min(lots, most)) : 0;
-  e = launch_early(join_kernel<BF16, HD, WEIGHTS>, dim3(static_cast<unsigned>(p.ctas * p.group + heads * key_blocks)), kJoin, 0, s, p, key_blocks);
-  return e;
+  const long long joins = one.cluster ? 0 : p.ctas * p.group;
+  return launch_early(join_kernel<BF16, HD, WEIGHTS>, dim3(static_cast<unsigned>(joins + heads * key_blocks)), kJoin, 0, s, one, key_blocks);
 }
 
 template <bool BF16, int HD>
