@@ -572,7 +572,8 @@ int cache_ops_status(void* stream);
  * attention kernels may take, in calls that the calling thread makes from
  * now on, before the kernel gives up, records an error and returns; 0 restores
  * the default of about two seconds. A kernel that gives up still waits, with its
- * own fixed bound, for what it has issued. LPS_EINVAL for cycles < 0. */
+ * own fixed bound, for what it has issued. With 1, attention_paged_decode gives up every
+ * other wait without a look, so that a test can be sure of it. LPS_EINVAL for cycles < 0. */
 int cache_ops_set_wait_limit(long long cycles);
 
 /* ---- operators over a paged cache ----------------------------------------------- */

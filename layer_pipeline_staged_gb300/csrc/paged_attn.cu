@@ -61,6 +61,7 @@ constexpr int kMembers = 8;        // of a cluster at most
 constexpr long long kClusterRows = 1024;  // of a member at most
 constexpr int kMaxParts = 256;     // CTAs of a launch, and so parts of a head
 constexpr int kKid = kKidPagedAttn << 8;
+constexpr long long kGiveUp = 1;   // as the wait limit: every wait but those for what is in flight gives up without a look
 constexpr float kStale = 8.0f;     // the base may lag the maximum by a factor of 2^8
 constexpr uint32_t kWhole = ~0u;   // Smem::valid: all keys of the tile are there
 
@@ -336,6 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   else walk = Walk{beg, end, sm.base, sm.first, p.nkv, sm.rows, 0, 0, 0};
   const long long limit = wait_cycles(p.wait_limit);
 
+  // A warp that gives up a wait says so and ends its role: it arrives nowhere any more,
+  // so no barrier's phase is ever completed without what it stands for (no stage is filled
+  // again while its copy may be under way, and no writer takes a piece that is not whole),
+  // and the waits of the others run out as well.
+  auto arrived = [&](uint64_t* bar, int parity, int kind) {
+    const bool ok = __all_sync(0xffffffffu, limit != kGiveUp && mbar_wait(bar, parity, limit));
+    if (!ok && lane == 0) report_error(g_status, kind | kKid);
+    return ok;
+  };
+
   auto roles = [&] {
   if (warp >= kConsumers && warp < kConsumers + kProducers) {
     // ---- the producer of K or of V (and q): what is on its way first takes half the time ----
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         for (int i = l0; i < l1; ++i) {
           const int stage = (it + i) % S::kStages, use = (it + i) / S::kStages, t = walk.t0 + i;
           if (use) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[stage], (use - 1) & 1, limit));
+            ok = arrived(&sm.empty[stage], (use - 1) & 1, kErrWaitEmpty);
             if (!ok) break;
           }
           const uint32_t valid = good >> ((i - l0) << log_boxes) & all;
@@ -398,20 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       it += n_tiles;
       walk = next;
     }
-    if (!ok && lane == 0) report_error(g_status, kErrWaitEmpty | kKid);
-    // what is in flight lands before the CTA ends
-    for (int i = last - (S::kStages - 1); i <= last; ++i)
-      if (i >= 0 && !mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, ok ? limit : kDrainLimitCycles)) {
-        if (lane == 0) report_error(g_status, kErrDrain | kKid);
-        break;
-      }
+    // What is in flight lands before the CTA ends, whatever limit the waits have and
+    // whoever gave up. (A phase that the other producer has not armed does not end; this
+    // one's copies have long landed when that wait runs out.)
+    bool landed = true;
+    for (int i = max(last - (S::kStages - 1), 0); i <= last; ++i)
+      landed &= mbar_wait(&sm.full[i % S::kStages], (i / S::kStages) & 1, kDrainLimitCycles);
+    if (!__all_sync(0xffffffffu, landed) && lane == 0) report_error(g_status, kErrDrain | kKid);
     return;
   }
 
   if (warp >= kConsumers + kProducers) {
     // ---- the writers: eight warps' (o, m, l) of a piece, in warp order; warp = half of the elements d ----
     int it = 0;
-    bool alive = true;
     const bool tells = warp == kConsumers + kProducers && lane == 0;  // the join of a head that begins here and ends elsewhere
     if (!CLUSTER && tells) p.border[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int piece = 0; walk.next(); ++piece) {
@@ -426,9 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       const int w0 = n == 1 && (it & 1) ? kConsumers / 2 : 0, w1 = n == 1 && !(it & 1) ? kConsumers / 2 : kConsumers;  // the warps that had tiles
       it += n;
-      if (alive) alive = mbar_wait(&sm.slot_full[sl], (piece / S::kSlots) & 1, limit);
-      if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
-      alive = __all_sync(0xffffffffu, alive);
+      if (!arrived(&sm.slot_full[sl], (piece / S::kSlots) & 1, kErrWaitFull)) return;
       const Slot<HD, NT>& in = sm.slot[sl];
       const long long part = (static_cast<long long>(blockIdx.x) * 2 + (piece ? 1 : 0)) * p.group;
       const int wr = warp - kConsumers - kProducers;
@@ -452,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         if (w == 0) {
           sm.sum[wr][h] = sum;
           const float2 ml = make_float2(top, seen ? sum : -1.f);
-          if (alive && wr == 0 && h < p.group) {
+          if (wr == 0 && h < p.group) {
             if (CLUSTER) sm.part_ml[h] = ml;
             else if (!whole) p.part_ml[part + h] = ml;
             else if (WEIGHTS) p.part_ml[(2ll * p.ctas + static_cast<long long>(walk.b) * p.nkv + walk.g) * p.group + h] = ml;
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       constexpr int kEach = HD / kWriters / 32;
 #pragma unroll
       for (int h0 = 0; h0 < 8 * NT; h0 += 4) {
-        if (!alive || h0 >= p.group) break;
+        if (h0 >= p.group) break;
         float acc[kEach][4];
 #pragma unroll
         for (int e = 0; e < kEach; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
@@ -513,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const int box_shift = 31 - __clz(p.box), half = p.box * 128;
   auto place = [&](int row) { return (row >> box_shift) * (p.box * HD * 2) + (row & (p.box - 1)) * 128; };
   const int k_row = place(row0 + (mtx & 1) * 8 + r8), v_row = place(row0 + (mtx >> 1) * 8 + r8);
-  bool alive = true;
   int it = 0;
   for (int piece = 0; walk.next(); ++piece) {
     const int b = walk.b, g = walk.g, n_tiles = walk.t1 - walk.t0, sl = piece % S::kSlots;
@@ -530,11 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     uint32_t qb[HD / 16][NT][2];       // q of the group as the B operand of S^T: column = head
     for (int i = skip; i < n_tiles; i += 2) {
       const int t = walk.t0 + i, stage = (it + i) % S::kStages;
-      if (alive) {
-        alive = mbar_wait(&sm.full[stage], ((it + i) / S::kStages) & 1, limit);
-        if (!alive && lane == 0) report_error(g_status, kErrWaitFull | kKid);
-        alive = __all_sync(0xffffffffu, alive);
-      }
+      if (!arrived(&sm.full[stage], ((it + i) / S::kStages) & 1, kErrWaitFull)) return;
       if (i < 2) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -547,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       }
       const int key0 = t * kTile + row0;
       // which of the warp's 16 keys there are
-      uint32_t keys = alive ? 0xffffu : 0u;
+      uint32_t keys = 0xffffu;
       const uint32_t valid = sm.valid[stage];
-      if (alive && valid != kWhole) {
+      if (valid != kWhole) {
         const int mine = lane & 15;
         keys = __ballot_sync(0xffffffffu, key0 + mine < walk.n_rows() && (valid >> ((row0 + mine) >> box_shift) & 1)) & 0xffffu;
       }
@@ -654,11 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     it += n_tiles;
 
     // ---- the piece's end: (o, m, l) to the writers ----
-    if (piece >= S::kSlots && alive) {
-      alive = mbar_wait(&sm.slot_empty[sl], (piece / S::kSlots - 1) & 1, limit);
-      if (!alive && lane == 0) report_error(g_status, kErrWaitEmpty | kKid);
-      alive = __all_sync(0xffffffffu, alive);
-    }
+    if (piece >= S::kSlots && !arrived(&sm.slot_empty[sl], (piece / S::kSlots - 1) & 1, kErrWaitEmpty)) return;
     Slot<HD, NT>& out = sm.slot[sl];
     if (skip < n_tiles) {
 #pragma unroll
