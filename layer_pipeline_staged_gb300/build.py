@@ -5,7 +5,7 @@ shared library (static CUDA runtime, no libtorch); with them the torch wrappers'
 argument marshalling as a Python extension beside it (gcc, no torch headers;
 its name carries the Python it is for, and it is left out, with a word on
 stderr, where that Python has no headers) and what makes it quicker for one
-torch (g++, that torch's headers; left out where there are none). Run as a module or call ``build()``;
+torch (g++, that torch's headers; left out where there are none or it does not compile). Run as a module or call ``build()``;
 the results sit next to this file and are git-ignored.
 """
 from __future__ import annotations
@@ -103,10 +103,22 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             tensors = [[os.environ.get("CXX") or "g++", "-O1", "-std=c++17", "-shared", "-fPIC", f"-I{python}", f"-isystem{include}",
                         "-isystem" + os.path.join(include, "torch", "csrc", "api", "include"), f"-I{CSRC}", TENSORS_SRC,
                         "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]]
+
+    def run_or_leave_out(cmd):
+        try:
+            run(cmd)
+            os.replace(cmd[-1], TENSORS)
+        except (RuntimeError, OSError) as e:
+            for f in (cmd[-1], TENSORS):  # an older one may not fit the marshalling
+                with contextlib.suppress(FileNotFoundError):
+                    os.remove(f)
+            sys.stderr.write(f"{e}\nthe torch wrappers read tensors through torch's Python interface\n")
+
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        list(ex.map(run, tensors + jobs))
-    for cmd in tensors:
-        os.replace(cmd[-1], TENSORS)
+        quicker = [ex.submit(run_or_leave_out, cmd) for cmd in tensors]
+        list(ex.map(run, jobs))
+        for f in quicker:
+            f.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])

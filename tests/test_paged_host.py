@@ -3,6 +3,7 @@ refusal is decided from the arguments alone. The addresses passed here are never
 first), so the refusals run only where there is no device."""
 import ctypes
 import math
+import os
 
 import pytest
 
@@ -167,3 +168,17 @@ def test_the_quick_way_of_reading_tensors_is_for_one_torch(monkeypatch):
     assert ops._tensors(torch) is not None
     monkeypatch.setattr(torch, "__version__", "0.1.2+other")
     assert ops._tensors(torch) is None
+
+
+@pytest.mark.parametrize("cxx", ["/bin/false", "/no/such/compiler"])
+def test_a_build_without_the_quick_way_of_reading_tensors(monkeypatch, tmp_path, capfd, cxx):
+    """It is left out where it does not compile, an older one too, and the library is built all the same."""
+    if lps_build._torch() is None:
+        pytest.skip("this torch has no headers")
+    older = tmp_path / "_tensors.so"
+    older.write_bytes(b"")
+    os.utime(older, (0, 0))
+    monkeypatch.setattr(lps_build, "TENSORS", str(older))
+    monkeypatch.setenv("CXX", cxx)
+    assert lps_build.build() == lps_build.LIB and os.path.exists(lps_build.LIB)
+    assert list(tmp_path.iterdir()) == [] and "Python interface" in capfd.readouterr().err
