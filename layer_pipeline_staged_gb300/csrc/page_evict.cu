@@ -21,7 +21,6 @@ constexpr int kSelect = 1024;  // threads of the selection
 constexpr int kWarps = kSelect / 32;
 constexpr int kBins = 2048;
 constexpr int kKeys = 32768;   // weights that a block of the selection keeps
-constexpr long long kAlone = 16384;  // rows that are no work for two blocks
 constexpr int kCopy = 256;     // threads of a block that copies
 constexpr int kRows = 64;      // its rows
 
@@ -255,13 +254,26 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> told;
   if (e == cudaSuccess) e = allow_smem(select_kernel, kKeys * 4, told);
   if (e != cudaSuccess) return e;
-  // a head's rows are shared out over as many blocks as the SMs have room for one by
-  // one, while each has a few thousand rows; but none has more than it keeps, if eight
-  // are enough for that
+  // A head's rows are one block's, or shared out over two, four or eight. us for caches
+  // just as long as their tables, brought to 1024 rows, heads of 128 (a block holds 32768):
+  //                                 1      2      4      8
+  //   8 heads, 16384 rows        13.7   14.5   14.6   17.9
+  //   8 heads, 20000 rows        15.8   17.0   15.1   18.3
+  //   8 heads, 28672 rows        18.9   17.6   15.8   18.6
+  //   8 heads, 65536 rows               26.1   20.4   20.6
+  //   8 heads, 131072 rows                     28.3   25.1
+  //   32 heads, 24576 rows       19.5   19.9   18.8   51.8
+  //   72 heads, 24576 rows       24.6   25.2   35.7   91.2
+  //   72 heads, 32768 rows       28.6   26.8   37.6   93.1
+  //   120 heads, 40000 rows             59.1   86.8  160.2
+  // A larger cluster pays where every block has a place at once and the rows are many;
+  // but no block has more rows than it holds, if eight are enough for that.
   const long long most = static_cast<long long>(p.width) * p.page, heads = static_cast<long long>(p.nkv) * p.batch;
   int blocks_of_head = 1;
-  while (blocks_of_head < 8 && ((2 * blocks_of_head * heads <= sms && most >= kAlone * blocks_of_head) || most > static_cast<long long>(kKeys) * blocks_of_head))
-    blocks_of_head *= 2;
+  if (most >= 28672 && 2 * heads <= sms) blocks_of_head = 2;
+  if (most >= 20000 && 4 * heads <= sms) blocks_of_head = 4;
+  if (most >= 65536 && 8 * heads <= sms) blocks_of_head = 8;
+  while (blocks_of_head < 8 && most > static_cast<long long>(kKeys) * blocks_of_head) blocks_of_head *= 2;
   const long long share = (most + blocks_of_head - 1) / blocks_of_head;
   const int held = static_cast<int>(share + 8 < kKeys ? (share + 15) / 8 * 8 : kKeys);  // a share is in eights
   e = launch_early_clusters(select_kernel, dim3(blocks_of_head, p.nkv, p.batch), kSelect, held * 4, blocks_of_head, s, p, held);
