@@ -215,20 +215,27 @@ cudaError_t launch_t(const LogitsParams& p, cudaStream_t s) {
 }
 
 // Threads of a block and tokens of a thread. Every block of a row reads all of its
-// history, so a long one wants long runs, of many threads; runs that are short use more
-// SMs, and of those the small calls have too many. us, rows of 128256, histories of up to
-// so many tokens:
+// history, so a long one wants long runs, of many threads; short runs use more SMs and
+// leave less to wait for at the end. us, rows of 128256, histories of up to so many tokens:
 //                        128 x 16   512 x 16   512 x 32   1024 x 32
-//   6 rows, fp32, 300         4.2        4.9        6.0        7.4
-//   6 rows, fp32, 4000        7.3        5.5        6.5        7.4
-//   12 rows, fp32, 20000     25.1       13.8       12.8       11.4
-//   64 rows, fp32, 300       11.9       12.9       13.0       13.5
-//   64 rows, fp32, 8192                 19.2       17.6       15.7
-//   30 rows, bf16, 1000       7.5        7.2        8.3        8.8
-//   100 rows, bf16, 1000     14.8       14.7       12.3       13.2
-//   64 rows, bf16, 8000      28.3       15.8       13.6       11.3
-// Narrower words put four blocks of 512 x 16 on an SM: 32768 of its tokens at once. With
-// more of them than that, a thread of 16-bit logits takes as many bytes as one of fp32.
+//   8 rows, fp32, 300          4.8        5.7        6.0
+//   6 rows, fp32, 4000         7.3        5.5        6.5        7.4
+//   12 rows, fp32, 300         5.1        6.3        6.8
+//   12 rows, fp32, 20000      25.1       13.8       12.8       11.4
+//   64 rows, fp32, 300        11.9       12.9       13.1       13.5
+//   64 rows, fp32, 1000       12.7       13.3       13.4
+//   32 rows, fp32, 2000       10.5        9.0       11.0       11.4
+//   64 rows, fp32, 8192                  19.2       17.6       15.7
+//   24 rows, bf16, 300         6.5        6.9        6.9        7.9
+//   32 rows, bf16, 1000        7.9        7.3        8.3        8.7
+//   40 rows, bf16, 300         7.3        7.9        8.5        9.4
+//   44 rows, bf16, 2000       10.2        8.8        9.6        9.7
+//   64 rows, bf16, 300         9.9       10.2        9.4        9.7
+//   64 rows, bf16, 8000       28.3       15.8       13.6       11.3
+// Short runs suit fp32 up to 1024 entries whatever the rows (1 to 128 of them); of 16-bit
+// logits, where the stream takes half as long, up to 20480 tokens an SM (fp16 as bf16;
+// around 35000 they would gain a tenth). Four blocks of 512 x 16 lie on an SM; with more
+// tokens than 40960 an SM, a thread of 16-bit logits takes as many bytes as one of fp32.
 template <class T>
 cudaError_t launch_type(const LogitsParams& p, cudaStream_t s) {
   int sms = 0;
@@ -237,11 +244,11 @@ cudaError_t launch_type(const LogitsParams& p, cudaStream_t s) {
   const double of_sm = static_cast<double>(p.batch) * p.vocab / sms;
   const long long entries = history(p);
   const bool wide = p.tokens && p.width >= 1 << 14;
-  if (of_sm <= 8192 && entries <= 1024) return launch_t<T, 128, 16, false>(p, s);
+  if ((sizeof(T) == 4 || of_sm <= 20480) && entries <= 1024) return launch_t<T, 128, 16, false>(p, s);
   if ((of_sm > 8192 && entries > 8192) || (of_sm > 32768 && entries > 4096))
     return wide ? launch_t<T, 1024, 32, true>(p, s) : launch_t<T, 1024, 32, false>(p, s);
   if constexpr (sizeof(T) == 2)
-    if (of_sm > 32768) return launch_t<T, 512, 32, false>(p, s);
+    if (of_sm > 40960) return launch_t<T, 512, 32, false>(p, s);
   return wide ? launch_t<T, 512, 16, true>(p, s) : launch_t<T, 512, 16, false>(p, s);
 }
 

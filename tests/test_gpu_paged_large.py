@@ -1,5 +1,6 @@
 """The operators over pages where tables have room for many rows: evictions by clusters, of more rows than they hold, and key weights
-behind the grid of the kernel that sums them; and the order of weights that are no numbers."""
+behind the grid of the kernel that sums them, logits by the rows and histories that choose a block's run; and the order of weights that
+are no numbers."""
 import numpy as np
 import pytest
 
@@ -8,6 +9,7 @@ import layer_pipeline_staged_gb300 as lps
 torch = pytest.importorskip("torch")
 from paged import Paged, gen, i32, randn  # noqa: E402
 from test_gpu_paged_attention import attend64, close  # noqa: E402
+from test_gpu_paged_ops import ORDER, adjust64, logits_inputs, same_logits  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +121,15 @@ def test_key_weights_behind_the_grid(decay):
     assert torch.equal(new.transpose(1, 2)[~seen], old.transpose(1, 2)[~seen])
     assert (new != old).transpose(1, 2)[seen].any(-1).all()
     lps.cache_ops_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF, torch.float16])
+@pytest.mark.parametrize("batch,vocab,width,entries", [(24, 128256, 300, 8), (27, 128256, 1016, 8), (27, 128256, 1017, 8), (44, 128256, 500, 0),
+                                                       (50, 128256, 0, 30), (50, 128256, 5000, 3), (100, 65537, 1000, 0), (12, 128255, 9000, 1)])
+def test_logits_of_many_rows(batch, vocab, width, entries, dtype):
+    x, d = logits_inputs(batch, vocab, width, entries, dtype)
+    kw = {k: v for k, v in d.items() if v is not None}
+    ref = adjust64(x, *(kw.get(k) for k in ORDER))
+    same_logits(lps.logits_adjust(x, **kw), *ref)
+    assert lps.logits_adjust(x, **kw, out=x) is x
+    same_logits(x, *ref)
