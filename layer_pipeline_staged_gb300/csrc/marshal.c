@@ -793,7 +793,7 @@ static PyObject *decode_paged(PyObject *self, PyObject *const *args, Py_ssize_t 
   const double decay = PyFloat_AsDouble(args[8]);
   if (PyErr_Occurred()) return NULL;
   PyObject *out = output_like(args[5], q, &t[3]);
-  if (!out) return NULL;
+  if (!out || batch == 0) return out;
   const int64_t st[4] = {q->stride[0], q->stride[1], t[3].stride[0], t[3].stride[1]};
   if (enter(&at, q->device)) return Py_DECREF(out), NULL;
   const long long bytes = attention_paged_decode_workspace((int)batch, (int)q->shape[1], (int)kp->shape[1], (int)q->shape[2], (int)kp->shape[2],
@@ -835,6 +835,7 @@ static PyObject *evict_paged(PyObject *self, PyObject *const *args, Py_ssize_t n
     if (size[i] < INT32_MIN || size[i] > INT32_MAX) return refuse("budget and recent must fit 32 bits"), NULL;
   }
   PyObject *made = new_array(batch, g_int32, kp);
+  if (made && batch == 0) return made;
   if (!made || tensor_of(made, &out, "new lengths") || enter(&at, kp->device)) return Py_XDECREF(made), NULL;
   const long long bytes = kv_pages_evict_workspace((int)batch, (int)kp->shape[1], (int)size[0]);
   int rc = bytes < 0 ? (int)bytes : 0;
