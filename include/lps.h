@@ -565,7 +565,8 @@ int kv_rows_accept(void* k_cache, void* v_cache, int n_layers, int batch, int n_
 /* Synchronize `stream` and read the status words that the attention kernels of
  * this section set on the current device when one of their bounded waits gives up. LPS_OK:
  * none has since the last check. LPS_ECUDA: at least one call's `out` is
- * invalid; the words are then cleared. They are shared by all calls on the device. */
+ * invalid, and so are the key_weights of the rows that an attention_paged_decode with
+ * key_weights saw; the words are then cleared. They are shared by all calls on the device. */
 int cache_ops_status(void* stream);
 
 /* Test hook, like model_set_wait_limit: the SM cycles that a bounded wait of the
@@ -658,9 +659,10 @@ long long attention_paged_decode_workspace(int batch, int n_q_heads, int n_kv_he
  *   scale      > 0 and below 2.3e38, or 0 for 1/sqrt(head_dim)
  *   key_weights  or NULL; for every row j that is seen, and its kv head g,
  *              key_weights = decay * key_weights + sum of p_j over the q heads of g
- *              (decay 0: what was there is not read, whatever it holds). Rows of
- *              two sequences on one page of one call need not be told apart by
- *              their weights, and are not: such pages' weights are undefined
+ *              (decay 0: what was there is not read, whatever it holds). A page that
+ *              two of the call's sequences (or one of them twice) have has undefined
+ *              weights after the call, not the same ones in equal calls: a shared prefix
+ *              is not to be thinned out by weights that such calls have left
  *   decay      0 to 1
  *   workspace  device, 16-byte aligned, at least attention_paged_decode_workspace bytes */
 int attention_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, int type, int batch,
@@ -676,7 +678,8 @@ long long kv_pages_evict_workspace(int batch, int n_kv_heads, int budget);
  * weights the lowest row; NaN is below every number), `budget` in all. They are
  * copied in order, with their weights, to the rows 0, 1, .. of the new table, for
  * keys and values; a sequence of up to `budget` rows is copied whole. The old
- * pages are only read (they may be shared), and no other row is written.
+ * pages are only read (they may be shared; what attention_paged_decode leaves as the
+ * key_weights of a page that sequences share is another matter), and no other row is written.
  *   lengths    device int32[batch]; table device int32[batch][table_width]
  *   new_table  device int32[batch][new_width], new_width * page_size >= budget;
  *              pages that no table of the call has elsewhere

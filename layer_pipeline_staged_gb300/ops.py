@@ -6,7 +6,7 @@ computes. Every call is enqueued on the current stream of its tensors' device an
 Lengths, offsets and positions are host integers (a list, a numpy array or a CPU tensor) for the contiguous cache, and
 int32 tensors on the device for the pages, so that a captured call replays with what they hold then. A tensor that
 does not fit is a ValueError, a refusal of the library an LpsError. The attention kernels bound every wait; one that
-gives up leaves an invalid ``out``, which ``cache_ops_status`` says.
+gives up leaves an invalid ``out`` (and ``key_weights``, for the rows that the call saw), which ``cache_ops_status`` says.
 """
 from __future__ import annotations
 
@@ -84,7 +84,7 @@ def kv_rows_accept(k_cache, v_cache, pos, path, accepted) -> None:
 def cache_ops_status(stream=None) -> None:
     """Wait for ``stream`` (a ``torch.cuda.Stream``; None: the current one) and raise LpsError when a wait inside
     an attention kernel has given up on its device since the last check: at least one call's ``out`` is then
-    invalid. Calls on every stream of the device share the report, which the check clears."""
+    invalid (and the ``key_weights`` of what it saw). Calls on every stream of the device share the report, which the check clears."""
     import torch
 
     s = torch.cuda.current_stream() if stream is None else stream
@@ -154,7 +154,9 @@ def attention_paged_decode(q, k_pages, v_pages, table, lengths, key_weights=None
     ``q`` [batch, q heads, head_dim], pages and ``table`` as for ``rotary_append_paged``, ``lengths`` int32 [batch] with the
     new token's own row counted. A sequence of no rows (or of a length that its table has no room for) gives zeros, and
     rows on a page that does not exist are not seen. With ``key_weights`` float32 [pages, kv heads, page rows] every row's
-    weight, summed over the kv head's query heads, is added to ``decay`` times what is there (0: replaces it).
+    weight, summed over the kv head's query heads, is added to ``decay`` times what is there (0: replaces it); the weights of
+    a page that two of the call's sequences share are undefined after it, and the call's workspace takes 4 bytes a query head
+    and row that the table has room for.
     ``scale`` 0 means 1/sqrt(head_dim). ``cache_ops_status`` reports a kernel that gave up. ``out`` is not q."""
     return (_m or _ready()).decode_paged(q, k_pages, v_pages, table, lengths, out, scale, key_weights, decay)
 
@@ -164,8 +166,8 @@ def kv_pages_evict(k_pages, v_pages, key_weights, table, lengths, new_table, bud
     each kv head its own, copied in order with their weights to rows 0, 1, .. of ``new_table``'s pages.
 
     Returns the new lengths, int32 [batch]: ``min(length, budget)``, or -1 for a sequence whose length or pages break the
-    rules, of which nothing is copied. The old pages are only read; the new ones must be none of them. Equal weights:
-    the lowest row stays. Positions were turned into the keys before: the next token keeps its own."""
+    rules, of which nothing is copied. The old pages are only read and may be shared (whose weights
+    ``attention_paged_decode`` does not keep apart); the new ones must be none of them. Equal weights: the lowest row stays. Positions were turned into the keys before: the next token keeps its own."""
     return (_m or _ready()).evict_paged(k_pages, v_pages, key_weights, table, lengths, new_table, budget, recent)
 
 
