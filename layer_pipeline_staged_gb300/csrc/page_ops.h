@@ -41,7 +41,9 @@ cudaError_t launch_rotary(const RotaryParams& p, bool bf16, cudaStream_t s);
 
 // One query row a sequence against its pages. A CTA takes an equal, contiguous
 // share of all the tiles (sequence, kv head, 64 keys); what it computes of a
-// head that others share goes to the workspace, and a second kernel joins it.
+// head that others share goes to the workspace, and a second kernel joins it. Or,
+// where the tables have room for few rows of few heads, a head is a cluster's, which
+// joins it in the same launch; the second kernel then only sums key weights, if any.
 struct PagedAttnParams {
   CUtensorMap tmap_k;          // [n_pages][nkv][page][hd], boxes of `box` rows
   CUtensorMap tmap_v;
@@ -53,7 +55,7 @@ struct PagedAttnParams {
   float* key_weights;          // [n_pages][nkv][page], or NULL
   float* part_o;               // workspace: [ctas][2][group][hd]
   float2* part_ml;             // [ctas][2][group]: base, and sum (-1: no key was seen); then,
-                               // with key_weights, of heads that one CTA has whole: [batch][nkv][group]
+                               // with key_weights, of heads that one CTA (or cluster) has whole: [batch][nkv][group]
   int4* border;                // [ctas]: the head that begins in the CTA's share and ends in another's: sequence,
                                // kv head, its parts (0: there is none), whether the share begins before it
   int* first_unit;             // key_weights: [batch + 1]: of each sequence, then their number

@@ -12,8 +12,9 @@
 // piece that is not the whole head leaves (o, m, sum) in the workspace, and join_kernel
 // puts them together in order. Where the tables have room for few rows of few heads, a
 // head is a thread-block cluster's instead: its CTAs take equal runs of the tiles and put
-// them together through each other's shared memory, in one launch. Every sum has one order given by the lengths: equal
-// calls give equal bits.
+// them together through each other's shared memory, in one launch. Every sum has one order, given by the lengths, the
+// batch and the tables' room: equal calls give equal bits (but for the key weights of pages that sequences share, which
+// several blocks then write).
 //
 // Warps 8 and 9 feed a ring of tiles by TMA, one K and one V: a box per run of keys
 // that lies together (a page, or what of it divides 64 keys) with both halves of the
@@ -181,7 +182,7 @@ __device__ __forceinline__ void store_out(void* out, long long at, float x) {
 
 // Rows of sequence b: its length, or 0 where that is not one.
 __device__ __forceinline__ int rows_of(const PagedAttnParams& p, int b) {
-  const int n = __ldcg(p.lengths + b);  // from L2: the join reads it before its wait
+  const int n = __ldcg(p.lengths + b);
   return n > 0 && n <= static_cast<long long>(p.width) * p.page ? n : 0;
 }
 
@@ -867,8 +868,9 @@ cudaError_t launch_t(const PagedAttnParams& p, cudaStream_t s) {
   // much of the chip unused: 16 of them took 11.1 us for 2000 rows each instead of 7.4 in
   // fours), and the tables have room for so few rows that a member's run costs no more than
   // the second launch. us with clusters and with shares, heads of 128: 1 sequence of 300
-  // rows, 8 heads 4.8 and 6.7; of 4000 7.6 and 9.0; of 8000 10.7 and 10.6, of 16000 17.0 and
-  // 13.7; 2 of 4000 10.4 and 10.0; 8 of 2000 10.7 and 13.5; 16 of 500 7.4 and 11.0.
+  // rows, 8 heads 4.8 and 6.7; of 4000 7.6 and 9.0; of 8000 10.7 and 10.6 (about 1000 rows a
+  // member is where they meet), of 16000 17.0 and 13.7; 2 of 4000 10.4 and 10.0; 8 of 2000
+  // 10.7 and 13.5; 16 of 500 7.4 and 11.0.
   PagedAttnParams one = p;
   one.cluster = 2 * kMembers * heads <= p.ctas ? kMembers : kMembers / 2;
   while (one.cluster > 1 && one.cluster * heads * 8 > p.ctas * 7) one.cluster /= 2;
