@@ -5,6 +5,8 @@ import layer_pipeline_staged_gb300 as lps
 
 torch = pytest.importorskip("torch")
 from paged import Paged, gen, i32, randn  # noqa: E402
+from test_gpu_paged_attention import attend64, close  # noqa: E402
+from test_gpu_paged_large import kept  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,34 @@ def test_a_batch_of_no_sequences(width):
     assert torch.equal(w, was)
     for x, y in ((kp, c.kp), (vp, c.vp)):
         assert torch.equal(x.nan_to_num(), y.nan_to_num())
+
+
+@pytest.mark.parametrize("width", [None, 700])
+def test_sequences_that_share_pages(width):
+    """Two sequences with one prefix, and one that has a page of its own twice: each as if alone, by a cluster a head and by shares;
+    then an eviction from the shared pages, which stay as they were."""
+    nkv, hd, page = 2, 64, 16
+    c = Paged([100, 70, 48], nkv, hd, page, BF, spare=12, width=width)
+    table = c.table.clone()
+    table[1, :3] = table[0, :3]  # 48 rows of the first
+    table[2, 2] = table[2, 0]
+    q = randn(gen(2), 3, 8, hd, dtype=BF)
+    k, v = ([x[0], torch.cat((x[0][:, :48], x[1][:, 48:]), 1), torch.cat((x[2][:, :32], x[2][:, :16]), 1)] for x in (c.k, c.v))
+    out = lps.attention_paged_decode(q, c.kp, c.vp, table, c.lengths)
+    for b in range(3):
+        o, tol, _, _ = attend64(q[b], k[b], v[b])
+        close(out[b], o, tol, f"sequence {b}")
+    weights = torch.rand(c.pages, nkv, page, generator=gen(3), device="cuda")
+    kp, vp, w, fresh = c.kp.clone(), c.vp.clone(), weights.clone(), i32(c.free[:9].reshape(3, 3))
+    assert lps.kv_pages_evict(kp, vp, w, table, c.lengths, fresh, 40, 10).tolist() == [40, 40, 40]
+    old = table[table >= 0].unique().long()
+    for x, was in ((kp, c.kp), (vp, c.vp), (w, weights)):
+        assert torch.equal(x[old].nan_to_num(), was[old].nan_to_num())
+    for b, n in enumerate(c.lens):
+        r = torch.arange(n, device="cuda")
+        of_row = weights[table[b].long()[r // page], :, r % page].cpu().numpy()
+        i = torch.arange(40, device="cuda")
+        at = fresh[b].long()[i // page]
+        for h in range(nkv):
+            rows = torch.from_numpy(kept(of_row[:, h], n, 40, 10)).cuda()
+            assert torch.equal(kp[at, h, i % page], k[b][h, rows]) and torch.equal(vp[at, h, i % page], v[b][h, rows])
